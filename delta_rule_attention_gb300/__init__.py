@@ -17,6 +17,12 @@ import threading
 
 import torch
 
+from . import block
+from .block import (  # noqa: F401
+    falcon_clip_grad_norm, falcon_selective_scan_bwd, falcon_selective_scan_fwd,
+    falcon_selective_scan_step, falcon_short_conv_bwd, falcon_short_conv_fwd,
+    falcon_short_conv_step)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfalcon_gb300.so")
 
@@ -41,7 +47,7 @@ EXPORTS = (
     "falcon1a_bwd_chunked", "falcon3a_fwd_chunked", "falcon2a_fwd_chunked",
     "falcon_normalized_workspace_bytes", "falcon1a_fwd_chunked_normalized",
     "falcon2_fwd_chunked",
-)
+) + block.EXPORTS
 FALCON_ERR_SCRATCH_LIMIT = -10
 FALCON_FIXED_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -126,6 +132,7 @@ def load_library(path: str | None = None):
         lib.falcon_strerror.argtypes = [ctypes.c_int]
         lib.falcon_version.restype = ctypes.c_int
         lib.falcon_version.argtypes = []
+        block.declare(lib)
         _lib = lib
         return lib
 

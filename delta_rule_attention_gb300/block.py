@@ -1,0 +1,435 @@
+"""Binding of the selective state space block's entry points: the short causal
+convolution, the selective scan and gradient clipping (include/falcon.h).
+
+Argument marshalling only, as in the package's other functions: the names are
+the C names, the work is in the CUDA kernels, a nonzero return code raises
+``FalconError``.  Activations may be views with any row strides as long as
+consecutive channels are adjacent; parameters and states are dense.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+FALCON_ACT_IDENTITY = 0
+FALCON_ACT_SILU = 1
+_ACT = {"identity": FALCON_ACT_IDENTITY, "silu": FALCON_ACT_SILU}
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+EXPORTS = (
+    "falcon_short_conv_fwd", "falcon_short_conv_bwd_workspace_bytes", "falcon_short_conv_bwd",
+    "falcon_short_conv_step", "falcon_selective_scan_fwd",
+    "falcon_selective_scan_bwd_workspace_bytes", "falcon_selective_scan_bwd",
+    "falcon_selective_scan_step", "falcon_clip_workspace_bytes", "falcon_clip_grad_norm",
+)
+
+_i64, _i32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
+_f32, _sz = ctypes.c_float, ctypes.c_size_t
+
+
+class falcon_strides(ctypes.Structure):
+    _fields_ = [("batch", _i64), ("head", _i64), ("time", _i64)]
+
+
+class falcon_conv_shape(ctypes.Structure):
+    _fields_ = [("B", _i64), ("H", _i64), ("T", _i64), ("m", _i32), ("width", _i32),
+                ("dtype", _i32), ("activation", _i32)]
+
+
+class falcon_scan_shape(ctypes.Structure):
+    _fields_ = [("B", _i64), ("T", _i64), ("D", _i32), ("G", _i32), ("N", _i32),
+                ("dtype", _i32), ("softplus", _i32)]
+
+
+class falcon_grad(ctypes.Structure):
+    _fields_ = [("grad", _vp), ("out", _vp), ("count", _i64), ("dtype", _i32)]
+
+
+def declare(lib):
+    """Sets the argument types of this module's entry points."""
+    conv, scan = ctypes.POINTER(falcon_conv_shape), ctypes.POINTER(falcon_scan_shape)
+    st, grads = ctypes.POINTER(falcon_strides), ctypes.POINTER(falcon_grad)
+    sig = {
+        "falcon_short_conv_fwd": [conv, _vp, st, _vp, _vp, _vp, _vp, _vp, st, _vp, _vp],
+        "falcon_short_conv_bwd_workspace_bytes": [conv],
+        "falcon_short_conv_bwd": [conv, _vp, st, _vp, _vp, _vp, _vp, _vp, st, _vp, _vp, st,
+                                  _vp, _vp, _vp, _vp, _sz, _vp],
+        "falcon_short_conv_step": [_i64, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _i64,
+                                   _vp, _vp, _vp, _vp],
+        "falcon_selective_scan_fwd": [scan, _vp, st, _vp, st, _vp, _vp, st, _vp, st, _vp, _vp,
+                                      st, _vp, _vp, _vp, _vp, st, _vp, _vp],
+        "falcon_selective_scan_bwd_workspace_bytes": [scan],
+        "falcon_selective_scan_bwd": [scan, _vp, st, _vp, st, _vp, _vp, st, _vp, st, _vp, _vp,
+                                      st, _vp, _vp, _vp, _vp, st, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+        "falcon_selective_scan_step": [_i64, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64,
+                                       _vp, _vp, st, _vp, st, _vp, _vp, _i64, _vp, _vp, _i64,
+                                       _vp, _vp, _vp, _vp],
+        "falcon_clip_workspace_bytes": [grads, _i64],
+        "falcon_clip_grad_norm": [grads, _i64, _f32, _f32, _vp, _vp, _sz, _vp],
+    }
+    for name in EXPORTS:
+        fn = getattr(lib, name)
+        fn.argtypes = sig[name]
+        fn.restype = _sz if name.endswith("_bytes") else ctypes.c_int
+
+
+def _library():
+    from . import load_library
+    return load_library()
+
+
+def _check(rc, what):
+    if rc != 0:
+        from . import FalconError
+        raise FalconError(rc, what)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _current(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _rows(t, name, dtype, shape):
+    """A CUDA tensor of this type and shape whose last dimension is adjacent."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be a CUDA tensor with adjacent channels")
+    return t
+
+
+def _dense(t, name, dtype, shape):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t
+
+
+def _dtype(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    return t.dtype
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors are on {device} and {t.device}")
+
+
+def _workspace(need, workspace, device):
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _conv_rows(t):
+    """Strides of [B,T,m] or [B,H,T,m]."""
+    s = t.stride()
+    return falcon_strides(s[0], 0, s[1]) if t.dim() == 3 else falcon_strides(s[0], s[1], s[2])
+
+
+def _conv_setup(x, weight, bias, state, lengths, activation):
+    dt = _dtype(x, "x")
+    if x.dim() not in (3, 4):
+        raise ValueError("x must be [B,T,m] or [B,H,T,m]")
+    if activation not in _ACT:
+        raise ValueError(f"activation must be one of {sorted(_ACT)}")
+    _rows(x, "x", dt, x.shape)
+    B, T, m = x.shape[0], x.shape[-2], x.shape[-1]
+    H = 1 if x.dim() == 3 else x.shape[1]
+    C = H * m
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [channels, width]")
+    W = weight.shape[1]
+    _dense(weight, "weight", torch.float32, (C, W))
+    _dense(bias, "bias", torch.float32, (C,))
+    _dense(state, "state", dt, (B, W - 1, C))
+    _dense(lengths, "lengths", torch.int32, (B,))
+    _same_device(x.device, weight, bias, state, lengths)
+    return falcon_conv_shape(B, H, T, m, W, _DTYPE[dt], _ACT[activation]), dt, B, C, W
+
+
+def falcon_short_conv_fwd(x, weight, bias=None, state=None, lengths=None, activation="silu",
+                          y=None, state_out=None, stream=None):
+    """Depthwise causal convolution over time.  x [B,T,m], or [B,H,T,m] with
+    H*m channels (bf16 or fp32, any row strides); weight [channels, width] fp32,
+    width 2, 3 or 4; bias [channels] fp32; state [B, width-1, channels] in x's
+    dtype (the inputs before token 0); lengths [B] int32; activation "silu" or
+    "identity".  Returns (y, state_out): y of x's shape, dense unless passed in,
+    and the last width-1 inputs of every row."""
+    lib = _library()
+    shape, dt, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
+    y = torch.empty(x.shape, dtype=dt, device=x.device) if y is None else \
+        _rows(y, "y", dt, x.shape)
+    state_out = torch.empty((B, W - 1, C), dtype=dt, device=x.device) if state_out is None else \
+        _dense(state_out, "state_out", dt, (B, W - 1, C))
+    rc = lib.falcon_short_conv_fwd(shape, _at(x), _conv_rows(x), _at(weight), _at(bias),
+                                   _at(state), _at(lengths), _at(y), _conv_rows(y),
+                                   _at(state_out), _current(stream, x.device))
+    _check(rc, "falcon_short_conv_fwd")
+    return y, state_out
+
+
+def falcon_short_conv_bwd(x, weight, dy, bias=None, state=None, lengths=None, dstate_out=None,
+                          activation="silu", grads=None, workspace=None, stream=None):
+    """Gradients of <dy, y> + <dstate_out, state_out> of falcon_short_conv_fwd.
+    Returns a dict with dx (dense, x's shape), dweight, dbias (fp32) and dstate;
+    ``grads`` may pass preallocated outputs."""
+    lib = _library()
+    shape, dt, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
+    _rows(dy, "dy", dt, x.shape)
+    _dense(dstate_out, "dstate_out", dt, (B, W - 1, C))
+    dev = x.device
+    _same_device(dev, dy, dstate_out)
+    g = {} if grads is None else grads
+    if "dx" not in g:
+        g["dx"] = torch.empty(x.shape, dtype=dt, device=dev)
+    if "dweight" not in g:
+        g["dweight"] = torch.empty((C, W), dtype=torch.float32, device=dev)
+    if "dbias" not in g:
+        g["dbias"] = torch.empty((C,), dtype=torch.float32, device=dev)
+    if "dstate" not in g:
+        g["dstate"] = torch.empty((B, W - 1, C), dtype=dt, device=dev)
+    _rows(g["dx"], "dx", dt, x.shape)
+    _dense(g["dweight"], "dweight", torch.float32, (C, W))
+    _dense(g["dbias"], "dbias", torch.float32, (C,))
+    _dense(g["dstate"], "dstate", dt, (B, W - 1, C))
+    workspace, have = _workspace(int(lib.falcon_short_conv_bwd_workspace_bytes(shape)),
+                                 workspace, dev)
+    rc = lib.falcon_short_conv_bwd(
+        shape, _at(x), _conv_rows(x), _at(weight), _at(bias), _at(state), _at(lengths), _at(dy),
+        _conv_rows(dy), _at(dstate_out), _at(g["dx"]), _conv_rows(g["dx"]), _at(g["dweight"]),
+        _at(g["dbias"]), _at(g["dstate"]), _at(workspace), have, _current(stream, dev))
+    _check(rc, "falcon_short_conv_bwd")
+    return g
+
+
+def falcon_short_conv_step(x, weight, state, bias=None, slots=None, fresh=None,
+                           activation="silu", y=None, stream=None):
+    """One token of N sequences: x [N,channels]; state [pool, width-1, channels]
+    (x's dtype) is updated in place; slots [N] int32 names each row's state (row i
+    uses state i when absent), fresh [N] uint8 marks sequences that start here.
+    Returns y [N,channels]."""
+    lib = _library()
+    dt = _dtype(x, "x")
+    if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("x must be [N, channels] and weight [channels, width]")
+    if activation not in _ACT:
+        raise ValueError(f"activation must be one of {sorted(_ACT)}")
+    N, C = x.shape
+    W = weight.shape[1]
+    _rows(x, "x", dt, x.shape)
+    _dense(weight, "weight", torch.float32, (C, W))
+    _dense(bias, "bias", torch.float32, (C,))
+    pool = _pool(state, "state", slots, N)
+    _dense(state, "state", dt, (pool, W - 1, C))
+    _dense(slots, "slots", torch.int32, (N,))
+    _dense(fresh, "fresh", torch.uint8, (N,))
+    _same_device(x.device, weight, bias, state, slots, fresh)
+    y = torch.empty((N, C), dtype=dt, device=x.device) if y is None else \
+        _dense(y, "y", dt, (N, C))
+    rc = lib.falcon_short_conv_step(N, C, W, _DTYPE[dt], _ACT[activation], _at(x), x.stride(0),
+                                    _at(weight), _at(bias), _at(state), pool, _at(slots),
+                                    _at(fresh), _at(y), _current(stream, x.device))
+    _check(rc, "falcon_short_conv_step")
+    return y
+
+
+def _pool(state, name, slots, N):
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        raise ValueError(f"{name} must be a pool of states, [pool, ., .]")
+    if slots is None and state.shape[0] != N:
+        raise ValueError(f"{name} must hold one state a row where no slots are given")
+    return state.shape[0]
+
+
+def _time_rows(t):
+    s = t.stride()
+    return falcon_strides(s[0], 0, s[1])
+
+
+def _group_rows(t):
+    s = t.stride()
+    return falcon_strides(s[0], s[2], s[1])
+
+
+def _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus):
+    dt = _dtype(u, "u")
+    if u.dim() != 3:
+        raise ValueError("u must be [B,T,D]")
+    B, T, C = u.shape
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be [D, N]")
+    if not isinstance(Bm, torch.Tensor) or Bm.dim() != 4:
+        raise ValueError("Bm and Cm must be [B,T,G,N]")
+    N, G = A.shape[1], Bm.shape[2]
+    _rows(u, "u", dt, (B, T, C))
+    _rows(delta, "delta", dt, (B, T, C))
+    _rows(Bm, "Bm", dt, (B, T, G, N))
+    _rows(Cm, "Cm", dt, (B, T, G, N))
+    if z is not None:
+        _rows(z, "z", dt, (B, T, C))
+    _dense(A, "A", torch.float32, (C, N))
+    _dense(D, "D", torch.float32, (C,))
+    _dense(delta_bias, "delta_bias", torch.float32, (C,))
+    _dense(h0, "h0", torch.float32, (B, C, N))
+    _dense(lengths, "lengths", torch.int32, (B,))
+    _same_device(u.device, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths)
+    return falcon_scan_shape(B, T, C, G, N, _DTYPE[dt], 1 if softplus else 0), dt
+
+
+def falcon_selective_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, h0=None,
+                              lengths=None, softplus=True, y=None, h_out=None, stream=None):
+    """Selective scan h_t = exp(s_t A) h_{t-1} + s_t u_t Bm_t, y_t = (<Cm_t, h_t> +
+    D u_t) silu(z_t), s_t = softplus(delta_t + delta_bias).  u, delta, z [B,T,D]
+    and Bm, Cm [B,T,G,N] (bf16 or fp32, any row strides); A [D,N], D, delta_bias
+    [D] and h0 [B,D,N] fp32; lengths [B] int32.  Returns (y, h_T)."""
+    lib = _library()
+    shape, dt = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
+    dev = u.device
+    y = torch.empty(u.shape, dtype=dt, device=dev) if y is None else _rows(y, "y", dt, u.shape)
+    hs = (shape.B, shape.D, shape.N)
+    h_out = torch.empty(hs, dtype=torch.float32, device=dev) if h_out is None else \
+        _dense(h_out, "h_out", torch.float32, hs)
+    rc = lib.falcon_selective_scan_fwd(
+        shape, _at(u), _time_rows(u), _at(delta), _time_rows(delta), _at(A), _at(Bm),
+        _group_rows(Bm), _at(Cm), _group_rows(Cm), _at(D), _at(z),
+        None if z is None else _time_rows(z), _at(delta_bias), _at(h0), _at(lengths), _at(y),
+        _time_rows(y), _at(h_out), _current(stream, dev))
+    _check(rc, "falcon_selective_scan_fwd")
+    return y, h_out
+
+
+def falcon_selective_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, h0=None,
+                              lengths=None, dh_T=None, softplus=True, grads=None,
+                              workspace=None, stream=None):
+    """Gradients of <dy, y> + <dh_T, h_T> of falcon_selective_scan_fwd.  Returns a
+    dict with du, ddelta, dz, dB, dC (u's dtype, dense) and dA, dD, ddelta_bias,
+    dh0 (fp32); dz, dD and ddelta_bias are None where z, D or delta_bias is.
+    ``grads`` may pass preallocated outputs."""
+    lib = _library()
+    shape, dt = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
+    dev = u.device
+    _rows(dy, "dy", dt, u.shape)
+    hs = (shape.B, shape.D, shape.N)
+    _dense(dh_T, "dh_T", torch.float32, hs)
+    _same_device(dev, dy, dh_T)
+    f32 = torch.float32
+    bc = tuple(Bm.shape)
+    want = {"du": (dt, tuple(u.shape)), "ddelta": (dt, tuple(u.shape)),
+            "dA": (f32, tuple(A.shape)), "dB": (dt, bc), "dC": (dt, bc),
+            "dD": None if D is None else (f32, tuple(D.shape)),
+            "dz": None if z is None else (dt, tuple(u.shape)),
+            "ddelta_bias": None if delta_bias is None else (f32, tuple(delta_bias.shape)),
+            "dh0": (f32, hs)}
+    g = {} if grads is None else grads
+    for name, spec in want.items():
+        if spec is None:
+            g[name] = None
+        elif name in g:
+            _dense(g[name], name, *spec)
+        else:
+            g[name] = torch.empty(spec[1], dtype=spec[0], device=dev)
+    workspace, have = _workspace(int(lib.falcon_selective_scan_bwd_workspace_bytes(shape)),
+                                 workspace, dev)
+    rc = lib.falcon_selective_scan_bwd(
+        shape, _at(u), _time_rows(u), _at(delta), _time_rows(delta), _at(A), _at(Bm),
+        _group_rows(Bm), _at(Cm), _group_rows(Cm), _at(D), _at(z),
+        None if z is None else _time_rows(z), _at(delta_bias), _at(h0), _at(lengths), _at(dy),
+        _time_rows(dy), _at(dh_T), _at(g["du"]), _at(g["ddelta"]), _at(g["dA"]), _at(g["dB"]),
+        _at(g["dC"]), _at(g["dD"]), _at(g["dz"]), _at(g["ddelta_bias"]), _at(g["dh0"]),
+        _at(workspace), have, _current(stream, dev))
+    _check(rc, "falcon_selective_scan_bwd")
+    return g
+
+
+def falcon_selective_scan_step(u, delta, A, Bm, Cm, h, D=None, z=None, delta_bias=None,
+                               slots=None, fresh=None, softplus=True, y=None, stream=None):
+    """One token of N sequences: u, delta, z [N,D], Bm, Cm [N,G,S]; h [pool,D,S]
+    fp32 is updated in place; slots and fresh as in falcon_short_conv_step.
+    Returns y [N,D]."""
+    lib = _library()
+    dt = _dtype(u, "u")
+    if u.dim() != 2 or not isinstance(A, torch.Tensor) or A.dim() != 2 or \
+            not isinstance(Bm, torch.Tensor) or Bm.dim() != 3:
+        raise ValueError("u must be [N,D], A [D,S] and Bm, Cm [N,G,S]")
+    N, C = u.shape
+    S, G = A.shape[1], Bm.shape[1]
+    _rows(u, "u", dt, (N, C))
+    _rows(delta, "delta", dt, (N, C))
+    _rows(Bm, "Bm", dt, (N, G, S))
+    _rows(Cm, "Cm", dt, (N, G, S))
+    if z is not None:
+        _rows(z, "z", dt, (N, C))
+    _dense(A, "A", torch.float32, (C, S))
+    _dense(D, "D", torch.float32, (C,))
+    _dense(delta_bias, "delta_bias", torch.float32, (C,))
+    pool = _pool(h, "h", slots, N)
+    _dense(h, "h", torch.float32, (pool, C, S))
+    _dense(slots, "slots", torch.int32, (N,))
+    _dense(fresh, "fresh", torch.uint8, (N,))
+    _same_device(u.device, delta, A, Bm, Cm, h, D, z, delta_bias, slots, fresh)
+    y = torch.empty((N, C), dtype=dt, device=u.device) if y is None else \
+        _dense(y, "y", dt, (N, C))
+    b, c = Bm.stride(), Cm.stride()
+    rc = lib.falcon_selective_scan_step(
+        N, C, G, S, _DTYPE[dt], 1 if softplus else 0, _at(u), u.stride(0), _at(delta),
+        delta.stride(0), _at(A), _at(Bm), falcon_strides(b[0], b[1], 0), _at(Cm),
+        falcon_strides(c[0], c[1], 0), _at(D), _at(z), 0 if z is None else z.stride(0),
+        _at(delta_bias), _at(h), pool, _at(slots), _at(fresh), _at(y),
+        _current(stream, u.device))
+    _check(rc, "falcon_selective_scan_step")
+    return y
+
+
+def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, workspace=None,
+                          stream=None):
+    """Scales a list of dense gradients (bf16 or fp32, mixed, any shapes) by
+    min(1, max_norm / (n + eps)), n their global 2-norm: in place, or into the
+    tensors of ``out`` (same shapes and dtypes).  Returns n, a 0-d fp32 tensor on
+    the gradients' device; the host does not wait for it."""
+    lib = _library()
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    into = grads if out is None else list(out)
+    if len(into) != len(grads):
+        raise ValueError("out must hold one tensor a gradient")
+    dev = grads[0].device
+    table = (falcon_grad * len(grads))()
+    for i, (g, o) in enumerate(zip(grads, into)):
+        if g.dtype not in _DTYPE or o.dtype != g.dtype:
+            raise TypeError("gradients must be bfloat16 or float32, outputs of the same dtype")
+        if g.device != dev or o.device != dev or not g.is_cuda:
+            raise ValueError("gradients and outputs must be CUDA tensors of one device")
+        if o.shape != g.shape or not g.is_contiguous() or not o.is_contiguous():
+            raise ValueError("gradients and outputs must be contiguous and of the same shapes")
+        e = table[i]
+        e.grad, e.out, e.count, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), _DTYPE[g.dtype]
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    workspace, have = _workspace(int(lib.falcon_clip_workspace_bytes(table, len(grads))),
+                                 workspace, dev)
+    rc = lib.falcon_clip_grad_norm(table, len(grads), float(max_norm), float(eps), _at(norm),
+                                   _at(workspace), have, _current(stream, dev))
+    _check(rc, "falcon_clip_grad_norm")
+    return norm

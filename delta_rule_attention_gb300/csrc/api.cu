@@ -313,6 +313,8 @@ int decode(int rule, int64_t N, int32_t m, int32_t dv, int32_t dtype, int32_t ph
 }  // namespace
 
 namespace falcon {
+int check_sm103_device() { return check_device(); }
+
 // Falcon-1 chunked forward over a workspace of workspace_bytes whose device
 // address `resolve` gives once the device check has passed.
 int fwd_chunked_resolved(const falcon_shape* s, const void* q, const void* k, const void* v,

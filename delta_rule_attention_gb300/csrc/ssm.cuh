@@ -1,0 +1,197 @@
+// Shared by the kernels of the selective state space block: argument blocks,
+// vector loads of bf16 or fp32 rows, softplus and silu in fp32.
+#pragma once
+
+#include "common.cuh"
+
+namespace falcon {
+
+int check_sm103_device();  // FALCON_OK on an sm_103 device (api.cu)
+
+template <int V>
+struct FloatV {
+  float v[V];
+};
+
+// V consecutive elements (V * sizeof(element) bytes, aligned to that size).
+template <typename E, int V>
+__device__ __forceinline__ FloatV<V> load_vec(const E* p) {
+  FloatV<V> r;
+  if constexpr (sizeof(E) == 4) {
+    if constexpr (V == 1) {
+      r.v[0] = *p;
+    } else {
+      static_assert(V == 4, "fp32 rows move four channels or one");
+      const float4 q = *reinterpret_cast<const float4*>(p);
+      r.v[0] = q.x, r.v[1] = q.y, r.v[2] = q.z, r.v[3] = q.w;
+    }
+  } else {
+    if constexpr (V == 1) {
+      r.v[0] = __bfloat162float(*p);
+    } else {
+      uint32_t w[V / 2];
+      if constexpr (V == 2) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+      } else if constexpr (V == 4) {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        w[0] = q.x, w[1] = q.y;
+      } else {
+        static_assert(V == 8, "bf16 rows move 1, 2, 4 or 8 channels");
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+      }
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        r.v[2 * i] = __uint_as_float(w[i] << 16);
+        r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 q = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&q);
+}
+
+template <typename E, int V>
+__device__ __forceinline__ void store_vec(E* p, const FloatV<V>& x) {
+  if constexpr (sizeof(E) == 4) {
+    if constexpr (V == 1)
+      *p = x.v[0];
+    else
+      *reinterpret_cast<float4*>(p) = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
+  } else {
+    if constexpr (V == 1)
+      *p = __float2bfloat16_rn(x.v[0]);
+    else if constexpr (V == 2)
+      *reinterpret_cast<uint32_t*>(p) = pack_bf16(x.v[0], x.v[1]);
+    else if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(p) =
+          make_uint2(pack_bf16(x.v[0], x.v[1]), pack_bf16(x.v[2], x.v[3]));
+    else
+      *reinterpret_cast<uint4*>(p) =
+          make_uint4(pack_bf16(x.v[0], x.v[1]), pack_bf16(x.v[2], x.v[3]),
+                     pack_bf16(x.v[4], x.v[5]), pack_bf16(x.v[6], x.v[7]));
+  }
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// exp(s A), A2 = A log2(e).  ex2.approx comes out low by 2e-8 to 5e-8 of its
+// value on average, which a state with a long memory adds up; the constant in
+// the exponent's fma cancels the mean at no cost (relative error of a state
+// after 2048 tokens with steps of 0.001 .. 0.1 and A of -1 .. -16: 2.3e-7, against
+// 4.9e-7 without it and 3.2e-7 with expf).
+constexpr float kDecayLift = 2.2e-8f;
+__device__ __forceinline__ float decay(float s, float A2) {
+  return exp2_approx(fmaf(s, A2, kDecayLift));
+}
+
+// 1 / (1 + e^{-x}).  The exponent is held below 2^126, so that the reciprocal
+// of a large denominator stays a normal number.
+__device__ __forceinline__ float sigmoid(float x) {
+  return rcp_approx(1.f + exp2_approx(fminf(-x * kLog2e, 126.f)));
+}
+
+// softplus(x) = max(x, 0) + log1p(e), e = e^{-|x|} in (0, 1].
+// log1p(e) = 2 atanh(w), w = e / (2 + e) in (0, 1/3], by the odd series of atanh
+// up to w^15 (the first term left out is below 2e-9 of the sum): the result
+// keeps its relative precision where it is small, which a logarithm of 1 + e
+// would not.
+__device__ __forceinline__ float softplus(float x) {
+  const float e = exp2_approx(-fabsf(x) * kLog2e);
+  const float w = e * rcp_approx(2.f + e);
+  const float q = w * w;
+  float p = 2.f / 15.f;
+  p = fmaf(p, q, 2.f / 13.f);
+  p = fmaf(p, q, 2.f / 11.f);
+  p = fmaf(p, q, 2.f / 9.f);
+  p = fmaf(p, q, 2.f / 7.f);
+  p = fmaf(p, q, 2.f / 5.f);
+  p = fmaf(p, q, 2.f / 3.f);
+  p = fmaf(p, q, 2.f);
+  return fmaxf(x, 0.f) + w * p;
+}
+
+struct ConvArgs {
+  int64_t B, H, T;
+  int m, width, dtype, act;
+  int64_t C;  // H * m
+  falcon_strides xs, ys, dys, dxs;
+  const void *x, *state, *dy, *dstate_out;
+  const float *weight, *bias;
+  const int32_t* lengths;
+  void *y, *state_out, *dx, *dstate;
+  float *dweight, *dbias;
+  float* ws;
+};
+cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t stream);
+size_t conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C, int width);
+cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t stream);
+
+struct ConvStepArgs {
+  int64_t N, pool, x_stride;
+  int C, width, dtype, act;
+  const void* x;
+  const float *weight, *bias;
+  void* state;
+  const int32_t* slots;
+  const uint8_t* fresh;
+  void* y;
+};
+cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t stream);
+
+struct ScanArgs {
+  int64_t B, T;
+  int D, G, N, dtype, softplus;
+  falcon_strides us, ds, bs, cs, zs, ys, dys;
+  const void *u, *delta, *Bm, *Cm, *z, *dy;
+  const float *A, *Dskip, *delta_bias, *h0, *dh_T;
+  const int32_t* lengths;
+  void *y, *du, *ddelta, *dB, *dC, *dz;
+  float *h_out, *dA, *dDskip, *ddelta_bias, *dh0;
+  void* ws;
+};
+cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream);
+size_t scan_bwd_workspace_bytes(const falcon_scan_shape& s);
+cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t stream);
+
+struct ScanStepArgs {
+  int64_t N, pool, u_stride, delta_stride, z_stride;
+  int D, G, S, dtype, softplus;
+  falcon_strides bs, cs;
+  const void *u, *delta, *Bm, *Cm, *z;
+  const float *A, *Dskip, *delta_bias;
+  float* h;
+  const int32_t* slots;
+  const uint8_t* fresh;
+  void* y;
+};
+cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream);
+
+size_t clip_workspace_bytes(const falcon_grad* grads, int64_t tensors);
+cudaError_t launch_clip(const falcon_grad* grads, int64_t tensors, float max_norm, float eps,
+                        float* norm, void* ws, cudaStream_t stream);
+
+// Row length of batch entry b.
+__device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b, int64_t T) {
+  if (!lengths) return T;
+  const int64_t n = lengths[b];
+  return n < 0 ? 0 : (n < T ? n : T);
+}
+
+}  // namespace falcon

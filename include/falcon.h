@@ -405,6 +405,195 @@ int falcon1a_decode_step(int64_t N, int32_t m, int32_t dv, int32_t dtype,
                          const float *lambda, float *S, float *x_prev,
                          const uint8_t *fresh, void *o, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A selective state space block: the short causal convolution, the selective
+ * scan, and the clipping of a training step's gradients.  The convolution is
+ * also what the paper's layers put before q, k and v ("short conv" in the
+ * experiment setup), so its tensors may be laid out head by head, ready for
+ * the calls above.
+ *
+ * Conventions of these calls where they differ from the ones above
+ *   - Activations are FALCON_BF16 or FALCON_F32, read and written through
+ *     strides (in elements; consecutive channels are adjacent), so that parts
+ *     of one projection's rows need no copy.  Parameters (filters, biases, A,
+ *     D), scan states and their gradients are dense float32.  Arithmetic is
+ *     float32; a result is rounded once, when it is stored.
+ *   - Pointers need the alignment of their element only.  Calls whose pointers
+ *     are 16-byte aligned, with sizes and strides that keep rows so, move
+ *     several channels per access; others move one.
+ *   - `lengths` [B] int32, nullable: row b holds tokens 0 .. lengths[b] - 1
+ *     (clamped to 0 .. T).  Later tokens are not read; their outputs and
+ *     gradients are written as zeros.  A row of length 0 passes its state on.
+ *   - `slots` [N] int32, nullable: row i of a single-token step uses state
+ *     slots[i] of a pool of `pool` states (NULL: state i).  A row whose slot is
+ *     outside 0 .. pool - 1 touches no state and its output is zero.  Two rows
+ *     of a call must not name the same slot.
+ *   - `fresh` [N] bytes, nullable: nonzero marks a sequence that starts at this
+ *     token: its old state counts as zero.
+ *   - Outputs must not overlap inputs unless a call says so. */
+
+/* Element strides of a tensor [B,H,T,m] (or [B,T,D], [B,T,G,N]: `head` is then
+ * unused, or the group's stride). */
+typedef struct {
+  int64_t batch, head, time;
+} falcon_strides;
+
+#define FALCON_ACT_IDENTITY 0
+#define FALCON_ACT_SILU 1
+
+/* B rows of T tokens with H*m channels; channel c = h*m + i has a filter of
+ * `width` taps (2, 3 or 4).  H = 1 is the plain [B,T,m] layout. */
+typedef struct {
+  int64_t B, H, T;
+  int32_t m, width, dtype, activation;
+} falcon_conv_shape;
+
+/* Depthwise causal convolution over time:
+ *   y_t = act(bias + sum_{j < width} weight_j x_{t - width + 1 + j}),
+ * act the identity or silu(p) = p / (1 + e^{-p}); the inputs before token 0
+ * are the carried ones.
+ *   x          [B,H,T,m] dtype, strides x_strides
+ *   weight     [H*m, width] f32;  bias [H*m] f32, nullable (zeros)
+ *   state      [B, width-1, H*m] dtype, nullable (zeros): the inputs before
+ *              token 0, oldest first
+ *   y          [B,H,T,m] dtype, out, strides y_strides
+ *   state_out  [B, width-1, H*m] dtype, out, nullable: the last width-1 inputs of
+ *              each row (the carried ones where the row is shorter)
+ * Errors: FALCON_ERR_NULL_PTR, _BAD_SHAPE, _BAD_DTYPE, _MISALIGNED, _BAD_ARG
+ * (activation code, negative stride), _DEVICE; _CUDA. */
+int falcon_short_conv_fwd(const falcon_conv_shape *shape, const void *x,
+                          const falcon_strides *x_strides, const float *weight,
+                          const float *bias, const void *state,
+                          const int32_t *lengths, void *y,
+                          const falcon_strides *y_strides, void *state_out,
+                          cudaStream_t stream);
+
+/* Gradients of <dy, y> + <dstate_out, state_out> of the call above.
+ *   dy [B,H,T,m] dtype;  dstate_out [B, width-1, H*m] dtype, nullable (zeros)
+ *   dx [B,H,T,m] dtype, out;  dweight [H*m, width] f32, out;
+ *   dbias [H*m] f32, out, nullable;  dstate [B, width-1, H*m] dtype, out, nullable
+ *   workspace: at least falcon_short_conv_bwd_workspace_bytes(shape) bytes,
+ *   16-byte aligned (per-block sums of dweight and dbias, added in a fixed order). */
+size_t falcon_short_conv_bwd_workspace_bytes(const falcon_conv_shape *shape);
+int falcon_short_conv_bwd(const falcon_conv_shape *shape, const void *x,
+                          const falcon_strides *x_strides, const float *weight,
+                          const float *bias, const void *state,
+                          const int32_t *lengths, const void *dy,
+                          const falcon_strides *dy_strides, const void *dstate_out,
+                          void *dx, const falcon_strides *dx_strides,
+                          float *dweight, float *dbias, void *dstate,
+                          void *workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/* One token of N sequences: x [N,C] dtype with row stride x_stride, y [N,C]
+ * dtype dense, out; state [pool, width-1, C] dtype, updated in place (the oldest
+ * input leaves, x enters). */
+int falcon_short_conv_step(int64_t N, int32_t C, int32_t width, int32_t dtype,
+                           int32_t activation, const void *x, int64_t x_stride,
+                           const float *weight, const float *bias, void *state,
+                           int64_t pool, const int32_t *slots,
+                           const uint8_t *fresh, void *y, cudaStream_t stream);
+
+/* B rows of T tokens, D channels in G groups (D a multiple of G) that share
+ * their B and C vectors, N states a channel (1 .. 128); softplus nonzero:
+ * the step size is softplus(delta + delta_bias), otherwise their sum. */
+typedef struct {
+  int64_t B, T;
+  int32_t D, G, N, dtype, softplus;
+} falcon_scan_shape;
+
+/* Selective scan: for channel d of group g,
+ *   s_t = softplus(delta_t + delta_bias),
+ *   h_t = exp(s_t A) h_{t-1} + s_t u_t Bm_t      (per state n)
+ *   y_t = (<Cm_t, h_t> + Dskip u_t) silu(z_t).
+ *   u, delta, z, y  [B,T,D] dtype (z nullable: no gate; `head` stride unused)
+ *   Bm, Cm          [B,T,G,N] dtype (`head` is the group's stride)
+ *   A               [D,N] f32;  Dskip, delta_bias [D] f32, nullable (zeros)
+ *   h0              [B,D,N] f32, nullable (zeros);  h_out [B,D,N] f32, out, may
+ *                   alias h0
+ * No workspace.  Errors as for falcon_short_conv_fwd. */
+int falcon_selective_scan_fwd(const falcon_scan_shape *shape, const void *u,
+                              const falcon_strides *u_strides, const void *delta,
+                              const falcon_strides *delta_strides, const float *A,
+                              const void *Bm, const falcon_strides *B_strides,
+                              const void *Cm, const falcon_strides *C_strides,
+                              const float *Dskip, const void *z,
+                              const falcon_strides *z_strides,
+                              const float *delta_bias, const float *h0,
+                              const int32_t *lengths, void *y,
+                              const falcon_strides *y_strides, float *h_out,
+                              cudaStream_t stream);
+
+/* Gradients of <dy, y> + <dh_T, h_T> of the call above; the forward is
+ * recomputed.  With g_t the adjoint of h_t (g_t = Cm_t dy_t + exp(s_{t+1} A)
+ * g_{t+1}, dy_t after the gate): dC_t = sum_d dy_t h_t, dB_t = sum_d g_t s_t u_t,
+ * du_t = s_t <g_t, Bm_t> + Dskip dy_t, ds_t = <g_t exp(s_t A) h_{t-1}, A> +
+ * <g_t, Bm_t> u_t, dA = sum_t g_t exp(s_t A) h_{t-1} s_t.
+ *   dy [B,T,D] dtype;  dh_T [B,D,N] f32, nullable (zeros)
+ *   du, ddelta [B,T,D] dtype, dense, out;  dz [B,T,D] dtype, dense, out, given
+ *   exactly where z is;  dB, dC [B,T,G,N] dtype, dense, out;  dA [D,N] f32, out;
+ *   dDskip, ddelta_bias [D] f32, out, nullable;  dh0 [B,D,N] f32, out, nullable,
+ *   may alias dh_T
+ *   workspace: at least falcon_selective_scan_bwd_workspace_bytes(shape) bytes,
+ *   256-byte aligned.  Sums over tokens and channels run in a fixed order. */
+size_t falcon_selective_scan_bwd_workspace_bytes(const falcon_scan_shape *shape);
+int falcon_selective_scan_bwd(const falcon_scan_shape *shape, const void *u,
+                              const falcon_strides *u_strides, const void *delta,
+                              const falcon_strides *delta_strides, const float *A,
+                              const void *Bm, const falcon_strides *B_strides,
+                              const void *Cm, const falcon_strides *C_strides,
+                              const float *Dskip, const void *z,
+                              const falcon_strides *z_strides,
+                              const float *delta_bias, const float *h0,
+                              const int32_t *lengths, const void *dy,
+                              const falcon_strides *dy_strides, const float *dh_T,
+                              void *du, void *ddelta, float *dA, void *dB, void *dC,
+                              float *dDskip, void *dz, float *ddelta_bias, float *dh0,
+                              void *workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
+/* One token of N sequences: u, delta, z [N,D] dtype with row strides, Bm, Cm
+ * [N,G,S] dtype (`batch` the row's stride, `head` the group's), y [N,D] dtype
+ * dense, out; h [pool,D,S] f32, updated in place.  S states a channel (1 .. 128). */
+int falcon_selective_scan_step(int64_t N, int32_t D, int32_t G, int32_t S,
+                               int32_t dtype, int32_t softplus, const void *u,
+                               int64_t u_stride, const void *delta,
+                               int64_t delta_stride, const float *A, const void *Bm,
+                               const falcon_strides *B_strides, const void *Cm,
+                               const falcon_strides *C_strides, const float *Dskip,
+                               const void *z, int64_t z_stride,
+                               const float *delta_bias, float *h, int64_t pool,
+                               const int32_t *slots, const uint8_t *fresh, void *y,
+                               cudaStream_t stream);
+
+/* One gradient of a step: `count` elements at `grad`, scaled into `out`
+ * (out == grad: in place). */
+typedef struct {
+  const void *grad;
+  void *out;
+  int64_t count;
+  int32_t dtype; /* FALCON_BF16 or FALCON_F32 */
+} falcon_grad;
+
+/* Clips the gradients of a step by their global norm n = sqrt(sum g^2):
+ *   out = g * min(1, max_norm / (n + eps)).
+ *   grads  HOST array of `tensors` descriptions (read before the call returns);
+ *          dense tensors of any size, element-aligned
+ *   norm   [1] f32, out: n (before clipping)
+ * In place, gradients that need no scaling are not rewritten.  A norm that is
+ * NaN makes every output NaN; an infinite one scales by 0 (an infinite
+ * gradient becomes NaN).  The sum of squares is float32 within a thread and
+ * float64 across threads; values whose square overflows float32 give an infinite norm.
+ *   workspace: at least falcon_clip_workspace_bytes(grads, tensors) bytes,
+ *   16-byte aligned.
+ * Errors: FALCON_ERR_NULL_PTR, _BAD_SHAPE (negative count), _BAD_DTYPE,
+ * _MISALIGNED, _WORKSPACE, _BAD_ARG (max_norm or eps negative or NaN), _DEVICE;
+ * _CUDA. */
+size_t falcon_clip_workspace_bytes(const falcon_grad *grads, int64_t tensors);
+int falcon_clip_grad_norm(const falcon_grad *grads, int64_t tensors, float max_norm,
+                          float eps, float *norm, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
 /* Waits for `stream`, then reads and clears the library's device error word
  * (set by a kernel whose bounded wait ran out).  Returns FALCON_OK,
  * FALCON_ERR_TIMEOUT, or FALCON_ERR_CUDA if the stream itself failed.
