@@ -127,6 +127,91 @@ __device__ __forceinline__ float softplus(float x) {
   return fmaxf(x, 0.f) + w * p;
 }
 
+// Two floats in one 64-bit register pair: one instruction for two lanes' worth.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// decay() of two states.
+__device__ __forceinline__ f32x2 decay2(f32x2 s, f32x2 A2) {
+  const float2 x = unpack2(fma2(s, A2, pack2(kDecayLift, kDecayLift)));
+  return pack2(exp2_approx(x.x), exp2_approx(x.y));
+}
+
+// 1, 2 or 4 neighbouring elements as they lie in memory.
+template <typename E>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  typedef uint32_t Pair;
+  typedef uint2 Quad;
+};
+template <>
+struct Raw<float> {
+  typedef float2 Pair;
+  typedef float4 Quad;
+};
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float2 widen(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ float2 widen(float2 w) { return w; }
+__device__ __forceinline__ float4 widen(uint2 w) {
+  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+__device__ __forceinline__ float4 widen(float4 w) { return w; }
+__device__ __forceinline__ uint32_t narrow(float2 v, uint32_t) { return pack_bf16(v.x, v.y); }
+__device__ __forceinline__ float2 narrow(float2 v, float2) { return v; }
+__device__ __forceinline__ uint2 narrow(float4 v, uint2) {
+  return make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+__device__ __forceinline__ float4 narrow(float4 v, float4) { return v; }
+
+// Elements `have` of a pair or quad at p (vec: in one access); the others are zero.
+template <typename E>
+__device__ __forceinline__ typename Raw<E>::Pair load_pair(const E* p, bool vec, int have) {
+  typedef typename Raw<E>::Pair P;
+  if (vec && have > 0) return *reinterpret_cast<const P*>(p);
+  return narrow(make_float2(have > 0 ? load_vec<E, 1>(p).v[0] : 0.f,
+                            have > 1 ? load_vec<E, 1>(p + 1).v[0] : 0.f),
+                P());
+}
+template <typename E>
+__device__ __forceinline__ typename Raw<E>::Quad load_quad(const E* p, bool vec, int have) {
+  typedef typename Raw<E>::Quad Q;
+  if (vec && have > 0) return *reinterpret_cast<const Q*>(p);
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = have > i ? load_vec<E, 1>(p + i).v[0] : 0.f;
+  return narrow(make_float4(v[0], v[1], v[2], v[3]), Q());
+}
+template <typename E>
+__device__ __forceinline__ void store_pair(E* p, bool vec, int have, float2 v) {
+  typedef typename Raw<E>::Pair P;
+  if (vec && have > 0) {
+    *reinterpret_cast<P*>(p) = narrow(v, P());
+    return;
+  }
+  if (have > 0) store_vec<E, 1>(p, FloatV<1>{{v.x}});
+  if (have > 1) store_vec<E, 1>(p + 1, FloatV<1>{{v.y}});
+}
+
 struct ConvArgs {
   int64_t B, H, T;
   int m, width, dtype, act;
@@ -165,7 +250,14 @@ struct ScanArgs {
   void *y, *du, *ddelta, *dB, *dC, *dz;
   float *h_out, *dA, *dDskip, *ddelta_bias, *dh0;
   void* ws;
+  // every channel pair of u, delta, z (dy) and the outputs, and every quad of
+  // states of Bm and Cm, is one aligned access
+  bool vec_ch, vec_bc;
 };
+// Channels a warp holds, for N states a channel: four states and two channels a lane.
+__host__ __device__ constexpr int scan_lanes(int N) {
+  return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32;
+}
 cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream);
 size_t scan_bwd_workspace_bytes(const falcon_scan_shape& s);
 cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t stream);
