@@ -3,17 +3,21 @@
 //   y_t = (<C_t, h_t> + Dskip u_t) silu(z_t)
 // for every channel with its N states.
 //
-// A warp owns 2 * 32 / LN channels: LN = ceil(N / 4) lanes (a power of two) share
-// two channels, four states each, in registers as f32x2 pairs.  It walks the
-// tokens in tiles: a lane turns the u and delta of LN-th tokens of its channel
-// pair into (s, s u) in shared memory, where the LN lanes of the pair read them,
-// B and C lie there in fp32, and the next tile's loads are in flight while the
-// tile is computed.  Two channels a lane, because every lane reads B_t and C_t
-// (32 bytes for its four states): shared memory delivers 128 bytes a clock to
-// an SM, so one channel a lane would be held at 16 states a clock by these reads
-// alone, below the 32 that the exponential unit does.  <C_t, h_t> is
-// summed over the LN lanes for LN tokens at a time, halving the tokens a lane
-// keeps at each exchange, so that a lane ends with the token it stores.
+// A warp owns 2 * 32 / LN channels: LN lanes share two channels, NS states each,
+// in registers, and walk the tokens two at a time: the exponents of tokens t and
+// t + 1, s u B, and <C, h> are f32x2 operations on the pair (A is kept doubled), only
+// h_t = a_t h_{t-1} + b_t runs token by token.  Pairs of tokens need no copies of
+// a value into both halves and no sum of the halves, which pairs of states do.
+//
+// Tokens come in tiles: a lane turns u and delta of its channel pair and token pair
+// into s and s u in shared memory, where the LN lanes of the channels read them; B and
+// C lie there in fp32, by token pairs; the next tile's loads are in flight while the
+// tile is computed.  Two channels a lane, because every lane reads B_t and C_t of
+// its states: shared memory delivers 128 bytes a clock to an SM, so one channel a
+// lane would be held at 16 states a clock by these reads alone, below the 32 that the
+// exponential unit does.  <C_t, h_t> is summed over the LN lanes for LN token pairs
+// at a time, halving the tokens a lane keeps at each exchange, so that a lane ends
+// with the tokens it stores.
 //
 // With few channels the tokens are split over a cluster of K warps: each first
 // finds its segment's end state from a zero start and the sum of its steps (the
@@ -32,29 +36,35 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-template <int LN>
+template <int LN, int NS>
 struct Cfg {
   static constexpr int kGroups = 32 / LN;        // channel pairs of a warp
   static constexpr int kChannels = 2 * kGroups;  // channels of a warp
-  static constexpr int kTile = LN <= 2 ? 8 : LN <= 16 ? 16 : 32;  // tokens of a tile
-  static constexpr int kItems = kTile / LN;      // (token, pair) items of a lane
-  static constexpr int kN4 = 4 * LN;
-  static constexpr int kQuads = kTile * 2 * LN;  // quads of B and C in a tile
-  static constexpr int kLaneQuads = (kQuads + 31) / 32;
-  static constexpr bool kAhead = kLaneQuads <= 8;  // the next tile's quads wait in registers
+  static constexpr int kTile = LN <= 2 ? 8 : LN <= 8 ? 16 : 32;  // tokens of a tile
+  static constexpr int kItems = kTile / 2 / LN;  // (token pair, channel pair) items of a lane
+  static constexpr int kNP = NS * LN;            // states, padded
+  // rows of steps and gains: padded so that the eight lanes of a store phase (LN
+  // token pairs of their channel pairs) fall in different banks
+  static constexpr int kRow = kGroups + (LN == 1 ? 0 : LN == 2 ? 4 : LN == 4 ? 2 : 1);
+  static constexpr int kNQ = kNP / 4;
+  static constexpr int kUnits = kTile * kNQ;     // (token pair, B or C, quad of states)
+  static constexpr int kLaneUnits = (kUnits + 31) / 32;
+  static constexpr bool kAhead = kLaneUnits <= 4;  // the next tile's quads wait in registers
+  static_assert(kItems >= 1 && NS % 4 == 0, "tile");
 };
 
-template <typename E, int LN, bool SPLIT>
-__global__ void __launch_bounds__(32) scan_fwd_kernel(ScanArgs a) {
-  typedef Cfg<LN> C;
+template <typename E, int LN, int NS, bool SPLIT>
+__global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
+  typedef Cfg<LN, NS> C;
   typedef typename Raw<E>::Pair Pair;
   typedef typename Raw<E>::Quad Quad;
-  __shared__ __align__(16) float bc[C::kTile][2][C::kN4];
-  __shared__ float4 step[C::kTile][C::kGroups];  // s of both channels, s u of both
-  __shared__ __align__(16) float end_h[SPLIT ? C::kChannels : 1][C::kN4];
+  __shared__ __align__(16) float bc[C::kTile / 2][2][C::kNP][2];
+  __shared__ float4 steps[C::kTile / 2][C::kRow];  // s: channel 0 at t, t+1, channel 1
+  __shared__ float4 gains[C::kTile / 2][C::kRow];  // s u
+  __shared__ __align__(16) float end_h[SPLIT ? C::kChannels : 1][C::kNP];
   __shared__ float2 end_s[SPLIT ? C::kGroups : 1];
 
-  const int lane = threadIdx.x, pair = lane / LN, q = lane % LN, n0 = q * 4;
+  const int lane = threadIdx.x, pair = lane / LN, q = lane % LN, n0 = q * NS;
   const int R = a.D / a.G;
   const int blocks = (R + C::kChannels - 1) / C::kChannels;
   int K = 1, rank = 0;
@@ -72,51 +82,83 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(ScanArgs a) {
   const int64_t begin = rank * per * C::kTile < n ? rank * per * C::kTile : n;
   const int64_t end = begin + per * C::kTile < n ? begin + per * C::kTile : n;
 
-  f32x2 A2[2][2], h[2][2], first[2][2];
-  float bias[2], skip[2];
+  f32x2 A2[2][NS];
+  float h[2][NS], first[2][NS], bias[2], skip[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const bool live = c < have;
-    float v[4], w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NS; ++i) {
       const bool in = live && n0 + i < a.N;
-      v[i] = in ? a.A[(int64_t)(d + c) * a.N + n0 + i] * kLog2e : 0.f;
-      w[i] = in && a.h0 ? a.h0[(b * a.D + d + c) * a.N + n0 + i] : 0.f;
+      const float v = in ? a.A[(int64_t)(d + c) * a.N + n0 + i] * kLog2e : 0.f;
+      A2[c][i] = pack2(v, v);
+      first[c][i] = in && a.h0 ? a.h0[(b * a.D + d + c) * a.N + n0 + i] : 0.f;
     }
-    A2[c][0] = pack2(v[0], v[1]), A2[c][1] = pack2(v[2], v[3]);
-    first[c][0] = pack2(w[0], w[1]), first[c][1] = pack2(w[2], w[3]);
     bias[c] = live && a.delta_bias ? a.delta_bias[d + c] : 0.f;
     skip[c] = live && a.Dskip ? a.Dskip[d + c] : 0.f;
   }
-  const E* u = static_cast<const E*>(a.u) + b * a.us.batch + d;
-  const E* dl = static_cast<const E*>(a.delta) + b * a.ds.batch + d;
-  const E* z = a.z ? static_cast<const E*>(a.z) + b * a.zs.batch + d : nullptr;
+  // every lane's channels and states exist: no access needs a test of its own
+  const bool whole = a.fast && a.N == C::kNP &&
+                     (blk - g * blocks + 1) * C::kChannels <= R;
+  const bool has_z = a.z != nullptr;
+  const E* u = static_cast<const E*>(a.u) + b * a.us.batch;
+  const E* dl = static_cast<const E*>(a.delta) + b * a.ds.batch;
+  const E* z = static_cast<const E*>(a.z) + (has_z ? b * a.zs.batch : 0);
   const E* Bm = static_cast<const E*>(a.Bm) + b * a.bs.batch + g * a.bs.head;
   const E* Cm = static_cast<const E*>(a.Cm) + b * a.cs.batch + g * a.cs.head;
-  E* y = static_cast<E*>(a.y) + b * a.ys.batch + d;
+  E* y = static_cast<E*>(a.y) + b * a.ys.batch;
 
-  Pair ru[C::kItems], rd[C::kItems], rz[C::kItems];
-  Quad rq[C::kAhead ? C::kLaneQuads : 1];
-  auto quad_at = [&](int64_t t0, int i) {  // i-th quad of the tile
-    const int k = i / (2 * LN), w = i % (2 * LN), s = (w % LN) * 4;
-    const int64_t t = t0 + k;
-    const E* p = w < LN ? Bm + t * a.bs.time : Cm + t * a.cs.time;
-    return load_quad<E>(p + s, a.vec_bc, t < end ? a.N - s : 0);
+  Pair ru[C::kItems][2], rd[C::kItems][2], rz[C::kItems][2];
+  Quad rq[C::kAhead ? C::kLaneUnits : 1][2];
+  // quads of unit i (of the tile's) at its two tokens
+  auto load_unit = [&](int64_t t0, int i, bool full, Quad (&v)[2]) {
+    const int tp = i / (2 * C::kNQ), w = i % (2 * C::kNQ), s = w % C::kNQ * 4;
+    const bool isB = w < C::kNQ;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int k = 2 * tp + e;
+      if (full) {
+        const E* p = isB ? Bm + t0 * a.bs.time : Cm + t0 * a.cs.time;
+        const unsigned off = (unsigned)(k * (int)(isB ? a.bs.time : a.cs.time) + s);
+        v[e] = *reinterpret_cast<const Quad*>(p + off);
+      } else {
+        const int64_t t = t0 + k;
+        const E* p = isB ? Bm + t * a.bs.time : Cm + t * a.cs.time;
+        v[e] = load_quad<E>(p + s, a.vec_bc, t < end ? a.N - s : 0);
+      }
+    }
   };
   auto fetch = [&](int64_t t0, bool gate) {
+    const bool full = whole && t0 + C::kTile <= end;
+    if (full) {
+      const E *pu = u + t0 * a.us.time, *pd = dl + t0 * a.ds.time, *pz = z + t0 * a.zs.time;
 #pragma unroll
-    for (int i = 0; i < C::kItems; ++i) {
-      const int64_t t = t0 + i * LN + q;
-      const int k = t < end ? have : 0;
-      ru[i] = load_pair<E>(u + t * a.us.time, a.vec_ch, k);
-      rd[i] = load_pair<E>(dl + t * a.ds.time, a.vec_ch, k);
-      if (gate) rz[i] = load_pair<E>(z + t * a.zs.time, a.vec_ch, k);
+      for (int i = 0; i < C::kItems; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int k = 2 * (i * LN + q) + e;
+          ru[i][e] = *reinterpret_cast<const Pair*>(pu + (unsigned)(k * (int)a.us.time + d));
+          rd[i][e] = *reinterpret_cast<const Pair*>(pd + (unsigned)(k * (int)a.ds.time + d));
+          if (gate)
+            rz[i][e] = *reinterpret_cast<const Pair*>(pz + (unsigned)(k * (int)a.zs.time + d));
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C::kItems; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int64_t t = t0 + 2 * (i * LN + q) + e;
+          const int k = t < end ? have : 0;
+          ru[i][e] = load_pair<E>(u + t * a.us.time + d, a.vec_ch, k);
+          rd[i][e] = load_pair<E>(dl + t * a.ds.time + d, a.vec_ch, k);
+          if (gate) rz[i][e] = load_pair<E>(z + t * a.zs.time + d, a.vec_ch, k);
+        }
     }
     if (C::kAhead) {
 #pragma unroll
-      for (int i = 0; i < C::kLaneQuads; ++i)
-        if (i * 32 + lane < C::kQuads) rq[i] = quad_at(t0, i * 32 + lane);
+      for (int i = 0; i < C::kLaneUnits; ++i)
+        if (C::kUnits % 32 == 0 || i * 32 + lane < C::kUnits)
+          load_unit(t0, i * 32 + lane, full, rq[C::kAhead ? i : 0]);
     }
   };
 
@@ -125,73 +167,125 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(ScanArgs a) {
   float2 sum = make_float2(0.f, 0.f);
   auto walk = [&](auto out) {
     constexpr bool OUT = decltype(out)::value;
-    const bool gate = OUT && z != nullptr;
+    const bool gate = OUT && has_z;
     if (begin < end) fetch(begin, gate);
     for (int64_t t0 = begin; t0 < end; t0 += C::kTile) {
-      float2 cu[C::kItems];
-      Pair cz[C::kItems];
+      const bool full = whole && t0 + C::kTile <= end;
+      float2 cu[C::kItems][2];
+      Pair cz[C::kItems][2];
 #pragma unroll
       for (int i = 0; i < C::kItems; ++i) {
-        const int k = i * LN + q;
-        cu[i] = widen(ru[i]);
-        cz[i] = rz[i];
-        float2 s = widen(rd[i]);
-        s.x += bias[0], s.y += bias[1];
-        if (a.softplus) s.x = softplus(s.x), s.y = softplus(s.y);
-        if (t0 + k >= end) s = make_float2(0.f, 0.f);
-        if (!OUT) sum.x += s.x, sum.y += s.y;
-        step[k][pair] = make_float4(s.x, s.y, s.x * cu[i].x, s.y * cu[i].y);
+        float2 s[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          cu[i][e] = widen(ru[i][e]);
+          cz[i][e] = rz[i][e];
+          s[e] = unpack2(add2(pair2(widen(rd[i][e])), pack2(bias[0], bias[1])));
+          if (a.softplus) s[e] = softplus2(s[e]);
+          if (!full && t0 + 2 * (i * LN + q) + e >= end) s[e] = make_float2(0.f, 0.f);
+          if (!OUT) sum.x += s[e].x, sum.y += s[e].y;
+        }
+        const int tp = i * LN + q;
+        steps[tp][pair] = make_float4(s[0].x, s[1].x, s[0].y, s[1].y);
+        gains[tp][pair] = make_float4(s[0].x * cu[i][0].x, s[1].x * cu[i][1].x,
+                                      s[0].y * cu[i][0].y, s[1].y * cu[i][1].y);
       }
 #pragma unroll
-      for (int i = 0; i < C::kLaneQuads; ++i) {
+      for (int i = 0; i < C::kLaneUnits; ++i) {
         const int k = i * 32 + lane;
-        if (k < C::kQuads)
-          *reinterpret_cast<float4*>(&bc[0][0][0] + 4 * k) =
-              widen(C::kAhead ? rq[C::kAhead ? i : 0] : quad_at(t0, k));
+        if (C::kUnits % 32 == 0 || k < C::kUnits) {
+          if (!C::kAhead) load_unit(t0, k, full, rq[0]);
+          const float4 v0 = widen(rq[C::kAhead ? i : 0][0]), v1 = widen(rq[C::kAhead ? i : 0][1]);
+          float4* to = reinterpret_cast<float4*>(&bc[0][0][0][0] + 8 * k);
+          to[0] = make_float4(v0.x, v1.x, v0.y, v1.y);
+          to[1] = make_float4(v0.z, v1.z, v0.w, v1.w);
+        }
       }
       __syncwarp();
       if (t0 + C::kTile < end) fetch(t0 + C::kTile, gate);
 
 #pragma unroll
       for (int i = 0; i < C::kItems; ++i) {
-        float2 o[LN];  // <C_t, h_t> of LN tokens, this lane's states
+        float2 o[LN][2];  // <C, h> of LN token pairs, two channels, this lane's states
 #pragma unroll
         for (int j = 0; j < LN; ++j) {
-          const int k = i * LN + j;
-          const float4 s = step[k][pair];
-          const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(&bc[k][0][n0]);
-          const f32x2 s0 = pack2(s.x, s.x), s1 = pack2(s.y, s.y);
-          const f32x2 v0 = pack2(s.z, s.z), v1 = pack2(s.w, s.w);
-          h[0][0] = fma2(decay2(s0, A2[0][0]), h[0][0], mul2(v0, B.x));
-          h[0][1] = fma2(decay2(s0, A2[0][1]), h[0][1], mul2(v0, B.y));
-          h[1][0] = fma2(decay2(s1, A2[1][0]), h[1][0], mul2(v1, B.x));
-          h[1][1] = fma2(decay2(s1, A2[1][1]), h[1][1], mul2(v1, B.y));
-          if (OUT) {
-            const ulonglong2 Ct = *reinterpret_cast<const ulonglong2*>(&bc[k][1][n0]);
-            const float2 p0 = unpack2(fma2(Ct.y, h[0][1], mul2(Ct.x, h[0][0])));
-            const float2 p1 = unpack2(fma2(Ct.y, h[1][1], mul2(Ct.x, h[1][0])));
-            o[j] = make_float2(p0.x + p0.y, p1.x + p1.y);
+          const int tp = i * LN + j;
+          const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(&steps[tp][pair]);
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&gains[tp][pair]);
+          // level by level over the lane's 2 NS chains, so that neighbouring
+          // instructions do not wait for one another
+          f32x2 Bt[NS], Ct[NS], acc[2];
+#pragma unroll
+          for (int k = 0; k < NS; k += 2) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&bc[tp][0][n0 + k][0]);
+            Bt[k] = x.x, Bt[k + 1] = x.y;
+            if (OUT) {
+              const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(&bc[tp][1][n0 + k][0]);
+              Ct[k] = w.x, Ct[k + 1] = w.y;
+            }
           }
+          float2 at[2][NS], bt[2][NS];
+#pragma unroll
+          for (int k = 0; k < NS; ++k)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) at[c][k] = unpack2(decay2(c ? s.y : s.x, A2[c][k]));
+#pragma unroll
+          for (int k = 0; k < NS; ++k)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) bt[c][k] = unpack2(mul2(c ? v.y : v.x, Bt[k]));
+          float h0[2][NS];
+#pragma unroll
+          for (int k = 0; k < NS; ++k)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) h0[c][k] = fmaf(at[c][k].x, h[c][k], bt[c][k].x);
+#pragma unroll
+          for (int k = 0; k < NS; ++k)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) h[c][k] = fmaf(at[c][k].y, h0[c][k], bt[c][k].y);
+          if (OUT) {
+#pragma unroll
+            for (int k = 0; k < NS; ++k)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const f32x2 hp = pack2(h0[c][k], h[c][k]);
+                acc[c] = k == 0 ? mul2(Ct[k], hp) : fma2(Ct[k], hp, acc[c]);
+              }
+          }
+          if (OUT) o[j][0] = unpack2(acc[0]), o[j][1] = unpack2(acc[1]);
         }
         if (OUT) {
 #pragma unroll
           for (int w = LN / 2; w > 0; w >>= 1) {
             const bool up = q & w;
 #pragma unroll
-            for (int j = 0; j < w; ++j) {
-              const float2 give = up ? o[j] : o[j + w], keep = up ? o[j + w] : o[j];
-              o[j].x = keep.x + __shfl_xor_sync(0xffffffffu, give.x, w);
-              o[j].y = keep.y + __shfl_xor_sync(0xffffffffu, give.y, w);
+            for (int j = 0; j < w; ++j)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float2 give = up ? o[j][c] : o[j + w][c], keep = up ? o[j + w][c] : o[j][c];
+                o[j][c].x = keep.x + __shfl_xor_sync(0xffffffffu, give.x, w);
+                o[j][c].y = keep.y + __shfl_xor_sync(0xffffffffu, give.y, w);
+              }
+          }
+          E* py = y + t0 * a.ys.time;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 oe = e ? make_float2(o[0][0].y, o[0][1].y)
+                                : make_float2(o[0][0].x, o[0][1].x);
+            float2 v = make_float2(fmaf(skip[0], cu[i][e].x, oe.x),
+                                   fmaf(skip[1], cu[i][e].y, oe.y));
+            if (gate) {
+              const float2 zt = widen(cz[i][e]);
+              v.x *= zt.x * sigmoid(zt.x);
+              v.y *= zt.y * sigmoid(zt.y);
+            }
+            const int k = 2 * (i * LN + q) + e;
+            if (full) {
+              *reinterpret_cast<Pair*>(py + (unsigned)(k * (int)a.ys.time + d)) =
+                  narrow(v, Pair());
+            } else if (t0 + k < end) {
+              store_pair<E>(py + k * a.ys.time + d, a.vec_ch, have, v);
             }
           }
-          float2 v = make_float2(fmaf(skip[0], cu[i].x, o[0].x), fmaf(skip[1], cu[i].y, o[0].y));
-          if (gate) {
-            const float2 zt = widen(cz[i]);
-            v.x *= zt.x * sigmoid(zt.x);
-            v.y *= zt.y * sigmoid(zt.y);
-          }
-          const int64_t t = t0 + i * LN + q;
-          if (t < end) store_pair<E>(y + t * a.ys.time, a.vec_ch, have, v);
         }
       }
       __syncwarp();
@@ -200,7 +294,9 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(ScanArgs a) {
 
   if (SPLIT) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) h[c][0] = h[c][1] = pack2(0.f, 0.f);
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < NS; ++i) h[c][i] = 0.f;
     if (rank + 1 < K) walk(std::false_type());
 #pragma unroll
     for (int w = LN / 2; w > 0; w >>= 1) {
@@ -210,47 +306,56 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(ScanArgs a) {
     if (q == 0) end_s[pair] = sum;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      *reinterpret_cast<ulonglong2*>(&end_h[pair * 2 + c][n0]) = make_ulonglong2(h[c][0], h[c][1]);
+#pragma unroll
+      for (int i = 0; i < NS; i += 4)
+        *reinterpret_cast<float4*>(&end_h[pair * 2 + c][n0 + i]) =
+            make_float4(h[c][i], h[c][i + 1], h[c][i + 2], h[c][i + 3]);
     cg::this_cluster().sync();
     for (int k = 0; k < rank; ++k) {
       const float2 s = *cg::this_cluster().map_shared_rank(&end_s[pair], k);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(
-            cg::this_cluster().map_shared_rank(&end_h[pair * 2 + c][n0], k));
-        const float sc = c ? s.y : s.x;
-        first[c][0] = fma2(decay2(pack2(sc, sc), A2[c][0]), first[c][0], e.x);
-        first[c][1] = fma2(decay2(pack2(sc, sc), A2[c][1]), first[c][1], e.y);
-      }
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < NS; i += 4) {
+          const float4 e = *reinterpret_cast<const float4*>(
+              cg::this_cluster().map_shared_rank(&end_h[pair * 2 + c][n0 + i], k));
+          const float ev[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            first[c][i + x] = fmaf(decay(c ? s.y : s.x, unpack2(A2[c][i + x]).x), first[c][i + x],
+                                   ev[x]);
+        }
     }
     cg::this_cluster().barrier_arrive();  // this warp has read the others' memory
   }
 #pragma unroll
-  for (int c = 0; c < 2; ++c) h[c][0] = first[c][0], h[c][1] = first[c][1];
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) h[c][i] = first[c][i];
   walk(std::true_type());
 
   for (int64_t t = n + rank * LN + q; t < a.T; t += K * LN)
-    store_pair<E>(y + t * a.ys.time, a.vec_ch, have, make_float2(0.f, 0.f));
+    store_pair<E>(y + t * a.ys.time + d, a.vec_ch, have, make_float2(0.f, 0.f));
   if (rank == K - 1) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float2 v0 = unpack2(h[c][0]), v1 = unpack2(h[c][1]);
-      const float v[4] = {v0.x, v0.y, v1.x, v1.y};
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c < have && n0 + i < a.N) a.h_out[(b * a.D + d + c) * a.N + n0 + i] = v[i];
-    }
+      for (int i = 0; i < NS; ++i)
+        if (c < have && n0 + i < a.N) a.h_out[(b * a.D + d + c) * a.N + n0 + i] = h[c][i];
   }
   if (SPLIT) cg::this_cluster().barrier_wait();  // until the others have read this one's
 }
 
 // Warps that fill the GPU: about six an SM.  With fewer, the tokens are split
 // while a segment keeps at least two tiles.
-constexpr int64_t kFullWarps = 152 * 6;
+#ifndef FULL_WARPS
+#define FULL_WARPS (152 * 6)
+#endif
+constexpr int64_t kFullWarps = FULL_WARPS;
 
-template <typename E, int LN>
+template <typename E, int LN, int NS>
 cudaError_t fwd_lanes(const ScanArgs& a, cudaStream_t stream) {
-  typedef Cfg<LN> C;
+  typedef Cfg<LN, NS> C;
   const int R = a.D / a.G;
   const int64_t blocks = (int64_t)a.G * ((R + C::kChannels - 1) / C::kChannels);
   const int64_t tiles = (a.T + C::kTile - 1) / C::kTile;
@@ -260,9 +365,9 @@ cudaError_t fwd_lanes(const ScanArgs& a, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned)(blocks * K), (unsigned)a.B);
   cfg.blockDim = dim3(32);
   cfg.stream = stream;
-  if (K == 1) return cudaLaunchKernelEx(&cfg, scan_fwd_kernel<E, LN, false>, a);
+  if (K == 1) return cudaLaunchKernelEx(&cfg, scan_fwd_kernel<E, LN, NS, false>, a);
   if (K > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<E, LN, true>,
+    const cudaError_t e = cudaFuncSetAttribute(scan_fwd_kernel<E, LN, NS, true>,
                                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
@@ -272,38 +377,43 @@ cudaError_t fwd_lanes(const ScanArgs& a, cudaStream_t stream) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, scan_fwd_kernel<E, LN, true>, a);
+  return cudaLaunchKernelEx(&cfg, scan_fwd_kernel<E, LN, NS, true>, a);
 }
 
 template <typename E>
 cudaError_t fwd_typed(const ScanArgs& a, cudaStream_t stream) {
-  switch (scan_lanes(a.N)) {
-    case 1: return fwd_lanes<E, 1>(a, stream);
-    case 2: return fwd_lanes<E, 2>(a, stream);
-    case 4: return fwd_lanes<E, 4>(a, stream);
-    case 8: return fwd_lanes<E, 8>(a, stream);
-    case 16: return fwd_lanes<E, 16>(a, stream);
-    default: return fwd_lanes<E, 32>(a, stream);
-  }
+  if (a.N <= 4) return fwd_lanes<E, 1, 4>(a, stream);
+  if (a.N <= 8) return fwd_lanes<E, 2, 4>(a, stream);
+  if (a.N <= 16) return fwd_lanes<E, 4, 4>(a, stream);
+  if (a.N <= 32) return fwd_lanes<E, 8, 4>(a, stream);
+  if (a.N <= 64) return fwd_lanes<E, 16, 4>(a, stream);
+  return fwd_lanes<E, 16, 8>(a, stream);
 }
 
-}  // namespace
-
 // Whether pointer and strides keep every access of `elems` elements aligned.
-bool scan_rows_fit(const void* p, const falcon_strides& s, int elems, int esz) {
+bool rows_fit(const void* p, const falcon_strides& s, int elems, int esz) {
   return reinterpret_cast<uintptr_t>(p) % (uintptr_t)(elems * esz) == 0 && s.batch % elems == 0 &&
          s.time % elems == 0 && s.head % elems == 0;
 }
 
+}  // namespace
+
+void scan_access(ScanArgs* a) {
+  const int esz = a->dtype == FALCON_BF16 ? 2 : 4;
+  a->us.head = a->ds.head = a->zs.head = a->ys.head = a->dys.head = 0;  // unused
+  a->vec_ch = a->D / a->G % 2 == 0 && rows_fit(a->u, a->us, 2, esz) &&
+              rows_fit(a->delta, a->ds, 2, esz) && rows_fit(a->z, a->zs, 2, esz) &&
+              rows_fit(a->y, a->ys, 2, esz) && rows_fit(a->dy, a->dys, 2, esz);
+  a->vec_bc = a->N % 4 == 0 && rows_fit(a->Bm, a->bs, 4, esz) && rows_fit(a->Cm, a->cs, 4, esz);
+  const int64_t most = (0x7fffffffLL - a->D) / 32;
+  a->fast = a->vec_ch && a->vec_bc && a->us.time < most && a->ds.time < most &&
+            a->zs.time < most && a->ys.time < most && a->dys.time < most && a->bs.time < most &&
+            a->cs.time < most;
+}
+
 cudaError_t launch_scan_fwd(const ScanArgs& in, cudaStream_t stream) {
   ScanArgs a = in;
-  const int esz = a.dtype == FALCON_BF16 ? 2 : 4;
-  a.us.head = a.ds.head = a.zs.head = a.ys.head = 0;  // unused
-  a.vec_ch = a.D / a.G % 2 == 0 && scan_rows_fit(a.u, a.us, 2, esz) &&
-             scan_rows_fit(a.delta, a.ds, 2, esz) && scan_rows_fit(a.z, a.zs, 2, esz) &&
-             scan_rows_fit(a.y, a.ys, 2, esz);
-  a.vec_bc = a.N % 4 == 0 && scan_rows_fit(a.Bm, a.bs, 4, esz) &&
-             scan_rows_fit(a.Cm, a.cs, 4, esz);
+  scan_access(&a);
   return a.dtype == FALCON_BF16 ? fwd_typed<__nv_bfloat16>(a, stream)
                                 : fwd_typed<float>(a, stream);
 }

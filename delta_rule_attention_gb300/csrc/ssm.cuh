@@ -108,23 +108,20 @@ __device__ __forceinline__ float sigmoid(float x) {
 }
 
 // softplus(x) = max(x, 0) + log1p(e), e = e^{-|x|} in (0, 1].
-// log1p(e) = 2 atanh(w), w = e / (2 + e) in (0, 1/3], by the odd series of atanh
-// up to w^15 (the first term left out is below 2e-9 of the sum): the result
-// keeps its relative precision where it is small, which a logarithm of 1 + e
-// would not.
+// log1p(e) = 2 atanh(w), w = e / (2 + e) in (0, 1/3]: w times a polynomial of
+// degree 4 in w^2, fitted to 2 atanh(w) / w at Chebyshev nodes of [0, 1/9] (off by
+// less than 8e-9 of it there).  The result keeps its relative precision where it is
+// small, which a logarithm of 1 + e would not.
+constexpr float kAtanh0 = 2.0000000078777487f, kAtanh1 = 0.6666631593508076f,
+                kAtanh2 = 0.40024853723465403f, kAtanh3 = 0.2796141883493225f,
+                kAtanh4 = 0.28174657262265285f;
 __device__ __forceinline__ float softplus(float x) {
   const float e = exp2_approx(-fabsf(x) * kLog2e);
   const float w = e * rcp_approx(2.f + e);
   const float q = w * w;
-  float p = 2.f / 15.f;
-  p = fmaf(p, q, 2.f / 13.f);
-  p = fmaf(p, q, 2.f / 11.f);
-  p = fmaf(p, q, 2.f / 9.f);
-  p = fmaf(p, q, 2.f / 7.f);
-  p = fmaf(p, q, 2.f / 5.f);
-  p = fmaf(p, q, 2.f / 3.f);
-  p = fmaf(p, q, 2.f);
-  return fmaxf(x, 0.f) + w * p;
+  const float p =
+      fmaf(fmaf(fmaf(fmaf(kAtanh4, q, kAtanh3), q, kAtanh2), q, kAtanh1), q, kAtanh0);
+  return fmaf(w, p, fmaxf(x, 0.f));
 }
 
 // Two floats in one 64-bit register pair: one instruction for two lanes' worth.
@@ -149,10 +146,28 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-// decay() of two states.
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 pair2(float2 v) { return pack2(v.x, v.y); }
+// decay() twice: two steps of one state, or one step of two.
 __device__ __forceinline__ f32x2 decay2(f32x2 s, f32x2 A2) {
   const float2 x = unpack2(fma2(s, A2, pack2(kDecayLift, kDecayLift)));
   return pack2(exp2_approx(x.x), exp2_approx(x.y));
+}
+// softplus() twice.
+__device__ __forceinline__ float2 softplus2(float2 x) {
+  const float2 e = make_float2(exp2_approx(-fabsf(x.x) * kLog2e), exp2_approx(-fabsf(x.y) * kLog2e));
+  const float2 den = unpack2(add2(pair2(e), pack2(2.f, 2.f)));
+  const f32x2 w = mul2(pair2(e), pack2(rcp_approx(den.x), rcp_approx(den.y)));
+  const f32x2 q = mul2(w, w);
+  f32x2 p = fma2(pack2(kAtanh4, kAtanh4), q, pack2(kAtanh3, kAtanh3));
+  p = fma2(p, q, pack2(kAtanh2, kAtanh2));
+  p = fma2(p, q, pack2(kAtanh1, kAtanh1));
+  p = fma2(p, q, pack2(kAtanh0, kAtanh0));
+  return unpack2(fma2(w, p, pack2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f))));
 }
 
 // 1, 2 or 4 neighbouring elements as they lie in memory.
@@ -253,11 +268,11 @@ struct ScanArgs {
   // every channel pair of u, delta, z (dy) and the outputs, and every quad of
   // states of Bm and Cm, is one aligned access
   bool vec_ch, vec_bc;
+  // both, and the offsets inside a tile of 32 tokens fit 31 bits
+  bool fast;
 };
-// Channels a warp holds, for N states a channel: four states and two channels a lane.
-__host__ __device__ constexpr int scan_lanes(int N) {
-  return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32;
-}
+// Fills vec_ch, vec_bc and fast (outputs besides y are dense).
+void scan_access(ScanArgs* a);
 cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t stream);
 size_t scan_bwd_workspace_bytes(const falcon_scan_shape& s);
 cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t stream);
