@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
     for (int i = 0; i < NS; ++i) {
       const bool in = live && n0 + i < a.N;
       const float v = in ? a.A[(int64_t)(d + c) * a.N + n0 + i] * kLog2e : 0.f;
-      A2[c][i] = pack2(v, v);
+      A2[c][i] = opaque2(pack2(v, v));
       first[c][i] = in && a.h0 ? a.h0[(b * a.D + d + c) * a.N + n0 + i] : 0.f;
     }
     bias[c] = live && a.delta_bias ? a.delta_bias[d + c] : 0.f;
@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
     }
   };
 
+  const f32x2 lift = opaque2(pack2(kDecayLift, kDecayLift));
   // One walk over the segment.  OUT: with outputs; otherwise only h and the
   // sum of the steps.
   float2 sum = make_float2(0.f, 0.f);
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
 #pragma unroll
           for (int k = 0; k < NS; ++k)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) at[c][k] = unpack2(decay2(c ? s.y : s.x, A2[c][k]));
+            for (int c = 0; c < 2; ++c) at[c][k] = decay2(c ? s.y : s.x, A2[c][k], lift);
 #pragma unroll
           for (int k = 0; k < NS; ++k)
 #pragma unroll
@@ -348,10 +349,7 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
 
 // Warps that fill the GPU: about six an SM.  With fewer, the tokens are split
 // while a segment keeps at least two tiles.
-#ifndef FULL_WARPS
-#define FULL_WARPS (152 * 6)
-#endif
-constexpr int64_t kFullWarps = FULL_WARPS;
+constexpr int64_t kFullWarps = 152 * 6;
 
 template <typename E, int LN, int NS>
 cudaError_t fwd_lanes(const ScanArgs& a, cudaStream_t stream) {

@@ -1,223 +1,629 @@
-// Gradient of the selective scan.  With a_t = exp(s_t A), g_t the adjoint of h_t:
+// Gradient of the selective scan.  With a_t = exp(s_t A), g_t the adjoint of h_t,
+// dy_t after the gate:
 //   g_t = C_t dy_t + a_{t+1} g_{t+1},   w_t = g_t a_t h_{t-1}
 //   dC_t = sum_d dy_t h_t,  dB_t = sum_d g_t s_t u_t,  dA = sum_t w_t s_t,
 //   du_t = s_t <g_t, B_t> + Dskip dy_t,  ds_t = <w_t, A> + <g_t, B_t> u_t.
-// A forward sweep keeps the state entering every tile of kTile tokens; the
-// reverse sweep recomputes a tile's states in registers and walks it back.
-// dB and dC sum over the channels of a block in shared memory, and over blocks
-// (and rows, for dA, dDskip and ddelta_bias) in a second launch, in a fixed order.
+//
+// Tokens are cut into chunks of kChunk, which run in parallel:
+//   1. every chunk by itself: its end state from a zero start, the adjoint it hands to
+//      the chunk before it from a zero end, and the sum of its steps (the
+//      decay of the whole chunk is exp(A sum s));
+//   2. a walk over the chunks turns these into the state entering and the adjoint
+//      leaving every chunk (one thread for four states of a channel);
+//   3. every chunk again, from its true ends: a forward sweep keeps the state before
+//      each group of kSub tokens in shared memory, then the groups are walked back,
+//      each one's states and decays recomputed into registers;
+//   4. sums: dB and dC over the blocks of channels, dA, dDskip and ddelta_bias over
+//      the blocks of tokens, in a fixed order.
+// A warp owns 2 * 32 / LN channels: LN lanes share two channels, four states each, as
+// f32x2 pairs.  <g, B>, <w, A> and <C, h> are summed over the LN lanes for kSub
+// tokens at once, halving the tokens a lane keeps at each exchange; dB and dC are
+// added up over the lane's two channels in registers, over the warp's lanes through
+// shared memory, and over the block's warps when the chunk ends.
+//
+// Bound by instruction issue: about 27 instructions a lane for each (token, channel,
+// state), of them two exponentials.
 
-#include <type_traits>
+#include <initializer_list>
 
 #include "ssm.cuh"
 
 namespace falcon {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kTile = 8;
+constexpr int kChunk = 32;
+constexpr int kSub = 4;
+constexpr int kSubs = kChunk / kSub;
 
 int lanes_of(int N) {
   int ln = 1;
   while (ln * 4 < N) ln *= 2;
   return ln;
 }
+__host__ __device__ constexpr int warps_of(int LN) { return LN <= 8 ? 4 : LN == 16 ? 2 : 1; }
+
+template <int LN>
+struct Cfg {
+  static constexpr int kWarps = warps_of(LN);
+  static constexpr int kGroups = 32 / LN;        // channel pairs of a warp
+  static constexpr int kChannels = 2 * kGroups;  // channels of a warp
+  static constexpr int kNP = 4 * LN;             // states, padded
+  // rows padded so that the lanes of a store phase fall in different banks
+  static constexpr int kRow = kGroups + (LN == 1 ? 0 : LN == 2 ? 4 : LN == 4 ? 2 : 1);
+  static constexpr int kBase = kGroups * kNP + 16;  // one token's dB (or dC) terms, padded
+  // the chunk's dB and dC of a warp lie over its used steps where they fit
+  static constexpr bool kOver = kRow * 4 >= 2 * kNP;
+};
+
+template <int LN>
+struct WarpShared {
+  typedef Cfg<LN> C;
+  float4 sv[kChunk][C::kRow];   // s of both channels, s u of both
+  float2 dyg[kChunk][C::kRow];  // dy after the gate
+};
+template <int LN>
+struct GradShared {
+  typedef Cfg<LN> C;
+  float4 kept[kSubs][2][32];             // state before each group of tokens, by lane
+  float terms[kSub][2][C::kBase];        // dB and dC terms by lane group
+  float sums[C::kOver || C::kWarps == 1 ? 1 : kChunk][2 * C::kNP];
+};
 
 // Parts of the workspace, in floats.
 struct Layout {
-  int64_t tiles, parts, N4;
-  size_t ckpt, dbc, dA, dD, dbias, total;
+  int64_t chunks, parts, groups, per, NP;
+  size_t hin, gin, sums, dbc, dA, dD, dbias, total;
   Layout(int64_t B, int64_t T, int D, int G, int N) {
-    const int ln = lanes_of(N), per = 32 / ln * kWarps;
-    N4 = 4 * ln;
-    tiles = (T + kTile - 1) / kTile;
-    parts = (D / G + per - 1) / per;
-    ckpt = 0;
-    dbc = ckpt + (size_t)(B * tiles * D * N4);
-    dA = dbc + (size_t)(parts * B * T * G * 2 * N4);
-    dD = dA + (size_t)(B * D * N4);
-    dbias = dD + (size_t)(B * D);
-    total = dbias + (size_t)(B * D);
+    const int ln = lanes_of(N), ch = 64 / ln * warps_of(ln);
+    NP = 4 * ln;
+    chunks = (T + kChunk - 1) / kChunk;
+    parts = (D / G + ch - 1) / ch;
+    // chunks a block walks in step 3: as many as leave four blocks a resident slot
+    per = 1;
+    while (per < 8 && G * parts * B * (chunks / (2 * per)) >= 152 * 3 * 4) per *= 2;
+    groups = (chunks + per - 1) / per;
+    size_t at = 0;
+    auto take = [&](int64_t n) {
+      const size_t p = at;
+      at += (size_t)((n + 63) / 64 * 64);
+      return p;
+    };
+    hin = take(B * chunks * D * NP);
+    gin = take(B * chunks * D * NP);
+    sums = take(B * chunks * D);
+    dbc = take(parts * B * T * G * 2 * NP);
+    dA = take(groups * B * D * NP);
+    dD = take(groups * B * D);
+    dbias = take(groups * B * D);
+    total = at;
   }
 };
 
+// What a warp knows of its place.
 template <typename E, int LN>
-__global__ void __launch_bounds__(kWarps * 32) scan_bwd_kernel(ScanArgs a, float* ws, Layout l) {
-  constexpr int kCh = 32 / LN, N4 = 4 * LN;
-  __shared__ float bc[kWarps][kTile][2][N4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int q = lane % LN, n0 = q * 4;
-  const int R = a.D / a.G;
-  const int g = blockIdx.x / (int)l.parts, part = blockIdx.x - g * (int)l.parts;
-  const int r = (part * kWarps + warp) * kCh + lane / LN;
-  const bool live = r < R;
-  const int d = g * R + (live ? r : 0);
-  const int64_t b = blockIdx.y;
-  const int64_t n = row_length(a.lengths, b, a.T);
+struct Place {
+  typedef Cfg<LN> C;
+  int lane, warp, pair, q, n0, g, part, have, d;
+  int64_t b, n;
+  bool whole;
+  float bias[2];
+  const E *u, *dl, *z, *dy, *Bm, *Cm;
 
-  float A2[4], h[4], dA[4] = {0.f, 0.f, 0.f, 0.f}, gc[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool in = n0 + i < a.N;
-    const int64_t k = (b * a.D + d) * a.N + n0 + i;
-    A2[i] = in ? a.A[(int64_t)d * a.N + n0 + i] * kLog2e : 0.f;
-    h[i] = in && a.h0 ? a.h0[k] : 0.f;
-    gc[i] = in && a.dh_T ? a.dh_T[k] : 0.f;
+  __device__ __forceinline__ Place(const ScanArgs& a, int parts) {
+    lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pair = lane / LN, q = lane % LN, n0 = q * 4;
+    const int R = a.D / a.G;
+    const int blk = blockIdx.x % (a.G * parts);
+    g = blk / parts, part = blk - g * parts;
+    const int w0 = (part * C::kWarps + warp) * C::kChannels, r0 = w0 + pair * 2;
+    have = r0 >= R ? 0 : (r0 + 1 < R ? 2 : 1);
+    d = g * R + (have ? r0 : 0);
+    b = blockIdx.y;
+    n = row_length(a.lengths, b, a.T);
+    whole = a.vec_ch && w0 + C::kChannels <= R;
+    bias[0] = have > 0 && a.delta_bias ? a.delta_bias[d] : 0.f;
+    bias[1] = have > 1 && a.delta_bias ? a.delta_bias[d + 1] : 0.f;
+    u = static_cast<const E*>(a.u) + b * a.us.batch + d;
+    dl = static_cast<const E*>(a.delta) + b * a.ds.batch + d;
+    z = a.z ? static_cast<const E*>(a.z) + b * a.zs.batch + d : nullptr;
+    dy = static_cast<const E*>(a.dy) + b * a.dys.batch + d;
+    Bm = static_cast<const E*>(a.Bm) + b * a.bs.batch + g * a.bs.head;
+    Cm = static_cast<const E*>(a.Cm) + b * a.cs.batch + g * a.cs.head;
   }
-  const float bias = a.delta_bias ? a.delta_bias[d] : 0.f;
-  const float skip = a.Dskip ? a.Dskip[d] : 0.f;
-  const E* u = static_cast<const E*>(a.u) + b * a.us.batch + d;
-  const E* dl = static_cast<const E*>(a.delta) + b * a.ds.batch + d;
-  const E* z = a.z ? static_cast<const E*>(a.z) + b * a.zs.batch + d : nullptr;
-  const E* dy = static_cast<const E*>(a.dy) + b * a.dys.batch + d;
-  const E* Bm = static_cast<const E*>(a.Bm) + b * a.bs.batch + g * a.bs.head + n0;
-  const E* Cm = static_cast<const E*>(a.Cm) + b * a.cs.batch + g * a.cs.head + n0;
-  E* du = static_cast<E*>(a.du) + b * a.T * a.D + d;
-  E* dd = static_cast<E*>(a.ddelta) + b * a.T * a.D + d;
-  E* dz = a.z ? static_cast<E*>(a.dz) + b * a.T * a.D + d : nullptr;
-  auto bc_at = [&](const E* p, int64_t stride, int64_t t, int i) {
-    return n0 + i < a.N ? load_vec<E, 1>(p + t * stride + i).v[0] : 0.f;
-  };
-  float* ck = ws + l.ckpt + (b * l.tiles * a.D + d) * N4 + n0;
-
-  for (int64_t t = 0; t < n; ++t) {
-    if (t % kTile == 0 && live)
-      *reinterpret_cast<float4*>(ck + t / kTile * a.D * N4) = make_float4(h[0], h[1], h[2], h[3]);
-    const float ut = load_vec<E, 1>(u + t * a.us.time).v[0];
-    float s = load_vec<E, 1>(dl + t * a.ds.time).v[0] + bias;
-    if (a.softplus) s = softplus(s);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      h[i] = fmaf(decay(s, A2[i]), h[i], s * ut * bc_at(Bm, a.bs.time, t, i));
+  __device__ __forceinline__ float2 at(const ScanArgs& a, const E* p, int64_t stride,
+                                       int64_t t) const {
+    if (whole) return widen(*reinterpret_cast<const typename Raw<E>::Pair*>(p + t * stride));
+    return widen(load_pair<E>(p + t * stride, a.vec_ch, have));
   }
-
-  float dD = 0.f, dbias = 0.f;
-  for (int64_t tile = l.tiles - 1; tile >= 0; --tile) {
-    const int64_t t0 = tile * kTile;
-    const float4 c0 = live && t0 < n ? *reinterpret_cast<const float4*>(ck + tile * a.D * N4)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-    float hs[kTile + 1][4] = {{c0.x, c0.y, c0.z, c0.w}};
-    float s[kTile], raw[kTile], ut[kTile];
+  // A in units of log2(e), two states a pair
+  __device__ __forceinline__ void decays(const ScanArgs& a, f32x2 (&A2)[2][2]) const {
 #pragma unroll
-    for (int k = 0; k < kTile; ++k) {
-      const int64_t t = t0 + k;
-      s[k] = ut[k] = raw[k] = 0.f;
-      if (t < n) {
-        ut[k] = load_vec<E, 1>(u + t * a.us.time).v[0];
-        raw[k] = load_vec<E, 1>(dl + t * a.ds.time).v[0] + bias;
-        s[k] = a.softplus ? softplus(raw[k]) : raw[k];
-      }
+    for (int c = 0; c < 2; ++c) {
+      float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        hs[k + 1][i] = fmaf(decay(s[k], A2[i]), hs[k][i],
-                            t < n ? s[k] * ut[k] * bc_at(Bm, a.bs.time, t, i) : 0.f);
+        v[i] = c < have && n0 + i < a.N ? a.A[(int64_t)(d + c) * a.N + n0 + i] * kLog2e : 0.f;
+      A2[c][0] = pack2(v[0], v[1]), A2[c][1] = pack2(v[2], v[3]);
     }
-#pragma unroll
-    for (int k = kTile - 1; k >= 0; --k) {
-      const int64_t t = t0 + k;
-      float s1 = 0.f, s2 = 0.f, yo = 0.f, vB[4], vC[4];
-      float dyt = 0.f, zt = 0.f;
-      if (t < n) {
-        dyt = load_vec<E, 1>(dy + t * a.dys.time).v[0];
-        zt = z ? load_vec<E, 1>(z + t * a.zs.time).v[0] : 0.f;
-      }
-      const float sg = sigmoid(zt), dyg = z ? dyt * zt * sg : dyt;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float Bt = t < n ? bc_at(Bm, a.bs.time, t, i) : 0.f;
-        const float Ct = t < n ? bc_at(Cm, a.cs.time, t, i) : 0.f;
-        yo = fmaf(Ct, hs[k + 1][i], yo);
-        vC[i] = live ? dyg * hs[k + 1][i] : 0.f;
-        const float gt = fmaf(dyg, Ct, gc[i]);
-        s1 = fmaf(gt, Bt, s1);
-        vB[i] = live ? gt * s[k] * ut[k] : 0.f;
-        gc[i] = gt * decay(s[k], A2[i]);
-        const float w = gc[i] * hs[k][i];
-        dA[i] = fmaf(w, s[k], dA[i]);
-        s2 = fmaf(w, A2[i], s2);
-      }
-#pragma unroll
-      for (int x = LN / 2; x > 0; x >>= 1) {
-        s1 += __shfl_xor_sync(0xffffffffu, s1, x);
-        s2 += __shfl_xor_sync(0xffffffffu, s2, x);
-        yo += __shfl_xor_sync(0xffffffffu, yo, x);
-      }
-#pragma unroll
-      for (int x = 16; x >= LN; x >>= 1)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          vB[i] += __shfl_xor_sync(0xffffffffu, vB[i], x);
-          vC[i] += __shfl_xor_sync(0xffffffffu, vC[i], x);
-        }
-      if (lane < LN)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          bc[warp][k][0][n0 + i] = vB[i];
-          bc[warp][k][1][n0 + i] = vC[i];
-        }
-      if (live && q == 0 && t < a.T) {
-        const float ds = fmaf(s1, ut[k], s2 * kLn2);
-        const float dr = a.softplus ? (t < n ? ds * sigmoid(raw[k]) : 0.f) : (t < n ? ds : 0.f);
-        store_vec<E, 1>(du + t * a.D, FloatV<1>{{t < n ? fmaf(s1, s[k], skip * dyg) : 0.f}});
-        store_vec<E, 1>(dd + t * a.D, FloatV<1>{{dr}});
-        if (z)
-          store_vec<E, 1>(dz + t * a.D,
-                          FloatV<1>{{t < n ? dyt * fmaf(skip, ut[k], yo) * sg *
-                                                 fmaf(zt, 1.f - sg, 1.f)
-                                           : 0.f}});
-        dD = fmaf(dyg, ut[k], dD);
-        dbias += dr;
-      }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTile * 2 * N4; i += kWarps * 32) {
-      const int64_t t = t0 + i / (2 * N4);
-      float v = 0.f;
-      for (int x = 0; x < kWarps; ++x) v += (&bc[x][0][0][0])[i];
-      if (t < a.T)
-        ws[l.dbc + (((part * a.B + b) * a.T + t) * a.G + g) * 2 * N4 + i % (2 * N4)] = v;
-    }
-    __syncthreads();
   }
-  if (!live) return;
-  *reinterpret_cast<float4*>(ws + l.dA + (b * a.D + d) * N4 + n0) =
-      make_float4(dA[0], dA[1], dA[2], dA[3]);
+};
+
+// Brings the tokens t0 .. of a chunk into shared memory; adds up the lane's steps.
+template <typename E, int LN>
+__device__ __forceinline__ float2 stage_chunk(const ScanArgs& a, const Place<E, LN>& p, int64_t t0,
+                                              float (&bc)[kChunk][2][4 * LN],
+                                              WarpShared<LN>& ws) {
+  typedef Cfg<LN> C;
+  for (int i = threadIdx.x; i < kChunk * 2 * LN; i += C::kWarps * 32) {
+    const int k = i / (2 * LN), w = i % (2 * LN), s = w % LN * 4;
+    const int64_t t = t0 + k;
+    const E* src = w < LN ? p.Bm + t * a.bs.time : p.Cm + t * a.cs.time;
+    reinterpret_cast<float4*>(bc)[i] =
+        widen(load_quad<E>(src + s, a.vec_bc, t < p.n ? a.N - s : 0));
+  }
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < kChunk / LN; ++i) {
+    const int k = i * LN + p.q;
+    const int64_t t = t0 + k;
+    float2 s = make_float2(0.f, 0.f), v = s, o = s;
+    if (t < p.n) {
+      const float2 ut = p.at(a, p.u, a.us.time, t);
+      s = p.at(a, p.dl, a.ds.time, t);
+      o = p.at(a, p.dy, a.dys.time, t);
+      s.x += p.bias[0], s.y += p.bias[1];
+      if (a.softplus) s = softplus2(s);
+      v = make_float2(s.x * ut.x, s.y * ut.y);
+      if (p.z) {
+        const float2 zt = p.at(a, p.z, a.zs.time, t);
+        o.x *= zt.x * sigmoid(zt.x), o.y *= zt.y * sigmoid(zt.y);
+      }
+    }
+    // a pair without a second (or any) channel contributes nothing
+    if (p.have < 2) v.y = o.y = s.y = 0.f;
+    if (p.have < 1) v.x = o.x = s.x = 0.f;
+    sum.x += s.x, sum.y += s.y;
+    ws.sv[k][p.pair] = make_float4(s.x, s.y, v.x, v.y);
+    ws.dyg[k][p.pair] = o;
+  }
+  return sum;
+}
+
+__device__ __forceinline__ f32x2 dup2(float v) { return pack2(v, v); }
+__device__ __forceinline__ f32x2 decay_pair(f32x2 s, f32x2 A2) {
+  const float2 e = decay2(s, A2, dup2(kDecayLift));
+  return pack2(e.x, e.y);
+}
+
+// Step 1.
+template <typename E, int LN>
+__global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
+    scan_bwd_chunk_kernel(const __grid_constant__ ScanArgs a, float* ws,
+                          const __grid_constant__ Layout l) {
+  typedef Cfg<LN> C;
+  extern __shared__ __align__(16) unsigned char bytes[];
+  auto& bc = *reinterpret_cast<float(*)[kChunk][2][C::kNP]>(bytes);
+  const Place<E, LN> p(a, (int)l.parts);
+  WarpShared<LN>& sh = reinterpret_cast<WarpShared<LN>*>(bytes + sizeof(bc))[p.warp];
+  const int64_t chunk = blockIdx.x / (unsigned)(a.G * l.parts), t0 = chunk * kChunk;
+  if (t0 >= p.n) return;
+  f32x2 A2[2][2], h[2][2], P[2][2], r[2][2];
+  p.decays(a, A2);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) h[c][x] = r[c][x] = dup2(0.f), P[c][x] = dup2(1.f);
+  float2 sum = stage_chunk<E, LN>(a, p, t0, bc, sh);
+  __syncthreads();
+#pragma unroll 4
+  for (int k = 0; k < kChunk; ++k) {
+    const float4 sv = sh.sv[k][p.pair];
+    const float2 o = sh.dyg[k][p.pair];
+    const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(&bc[k][0][p.n0]);
+    const ulonglong2 Ct = *reinterpret_cast<const ulonglong2*>(&bc[k][1][p.n0]);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const f32x2 s2 = dup2(c ? sv.y : sv.x), v2 = dup2(c ? sv.w : sv.z), o2 = dup2(c ? o.y : o.x);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const f32x2 at = decay_pair(s2, A2[c][x]);
+        h[c][x] = fma2(at, h[c][x], mul2(v2, x ? B.y : B.x));
+        P[c][x] = mul2(at, P[c][x]);
+        r[c][x] = fma2(P[c][x], mul2(o2, x ? Ct.y : Ct.x), r[c][x]);
+      }
+    }
+  }
+#pragma unroll
+  for (int w = LN / 2; w > 0; w >>= 1) {
+    sum.x += __shfl_xor_sync(0xffffffffu, sum.x, w);
+    sum.y += __shfl_xor_sync(0xffffffffu, sum.y, w);
+  }
+  const int64_t row = (p.b * l.chunks + chunk) * a.D + p.d;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (c < p.have) {
+      *reinterpret_cast<ulonglong2*>(ws + l.hin + (row + c) * C::kNP + p.n0) =
+          make_ulonglong2(h[c][0], h[c][1]);
+      *reinterpret_cast<ulonglong2*>(ws + l.gin + (row + c) * C::kNP + p.n0) =
+          make_ulonglong2(r[c][0], r[c][1]);
+      if (p.q == 0) ws[l.sums + row + c] = c ? sum.y : sum.x;
+    }
+}
+
+// Step 2: hin[c] becomes the state entering chunk c, gin[c] the adjoint entering it
+// from behind.
+__global__ void __launch_bounds__(128)
+    scan_bwd_chain_kernel(const __grid_constant__ ScanArgs a, float* ws,
+                          const __grid_constant__ Layout l) {
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t quads = l.NP / 4;
+  if (i >= (int64_t)a.D * quads) return;
+  const int64_t d = i / quads, b = blockIdx.y;
+  const int n0 = (int)(i - d * quads) * 4;
+  const int64_t n = row_length(a.lengths, b, a.T), count = (n + kChunk - 1) / kChunk;
+  float A2[4], h[4], g[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const bool in = n0 + k < a.N;
+    const int64_t at = (b * a.D + d) * a.N + n0 + k;
+    A2[k] = in ? a.A[d * a.N + n0 + k] * kLog2e : 0.f;
+    h[k] = in && a.h0 ? a.h0[at] : 0.f;
+    g[k] = in && a.dh_T ? a.dh_T[at] : 0.f;
+  }
+  const int64_t step = (int64_t)a.D * l.NP;
+  float* hp = ws + l.hin + (b * l.chunks * a.D + d) * l.NP + n0;
+  float* gp = ws + l.gin + (b * l.chunks * a.D + d) * l.NP + n0;
+  const float* sp = ws + l.sums + b * l.chunks * a.D + d;
+  // both walks at once, eight chunks of each in flight
+  constexpr int kAhead = 8;
+  for (int64_t c0 = 0; c0 < count; c0 += kAhead) {
+    float4 hv[kAhead], gv[kAhead];
+    float hs[kAhead], gs[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t c = c0 + k, e = count - 1 - c;
+      if (c < count) {
+        hv[k] = *reinterpret_cast<const float4*>(hp + c * step);
+        gv[k] = *reinterpret_cast<const float4*>(gp + e * step);
+        hs[k] = sp[c * a.D];
+        gs[k] = sp[e * a.D];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t c = c0 + k, e = count - 1 - c;
+      if (c < count) {
+        *reinterpret_cast<float4*>(hp + c * step) = make_float4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<float4*>(gp + e * step) = make_float4(g[0], g[1], g[2], g[3]);
+        const float ha[4] = {hv[k].x, hv[k].y, hv[k].z, hv[k].w};
+        const float ga[4] = {gv[k].x, gv[k].y, gv[k].z, gv[k].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          h[x] = fmaf(decay(hs[k], A2[x]), h[x], ha[x]);
+          g[x] = fmaf(decay(gs[k], A2[x]), g[x], ga[x]);
+        }
+      }
+    }
+  }
   if (a.dh0)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n0 + i < a.N) a.dh0[(b * a.D + d) * a.N + n0 + i] = gc[i];
-  if (q == 0) {
-    ws[l.dD + b * a.D + d] = dD;
-    ws[l.dbias + b * a.D + d] = dbias;
+    for (int k = 0; k < 4; ++k)
+      if (n0 + k < a.N) a.dh0[(b * a.D + d) * a.N + n0 + k] = g[k];
+}
+
+// Step 3.
+template <typename E, int LN>
+__global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
+    scan_bwd_grad_kernel(const __grid_constant__ ScanArgs a, float* ws,
+                         const __grid_constant__ Layout l) {
+  typedef Cfg<LN> C;
+  constexpr int kMine = LN >= kSub ? 1 : kSub / LN;  // tokens of a group a lane finishes
+  extern __shared__ __align__(16) unsigned char bytes[];
+  auto& bc = *reinterpret_cast<float(*)[kChunk][2][C::kNP]>(bytes);
+  const Place<E, LN> p(a, (int)l.parts);
+  WarpShared<LN>* all = reinterpret_cast<WarpShared<LN>*>(bytes + sizeof(bc));
+  GradShared<LN>* grads = reinterpret_cast<GradShared<LN>*>(all + C::kWarps);
+  WarpShared<LN>& sh = all[p.warp];
+  GradShared<LN>& gs = grads[p.warp];
+  auto sums_row = [&](int warp, int k) -> float* {
+    return C::kOver ? reinterpret_cast<float*>(all[warp].sv[k]) : grads[warp].sums[k];
+  };
+  const float skip0 = p.have > 0 && a.Dskip ? a.Dskip[p.d] : 0.f;
+  const float skip1 = p.have > 1 && a.Dskip ? a.Dskip[p.d + 1] : 0.f;
+  f32x2 A2[2][2], dA[2][2];
+  p.decays(a, A2);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) dA[c][0] = dA[c][1] = dup2(0.f);
+  float2 dD = make_float2(0.f, 0.f), dbias = dD;
+  // first token of a group that this lane finishes, and whether it stores it
+  const int mine = LN >= 4 ? (p.q & (LN / 2) ? 2 : 0) + (p.q & (LN / 4) ? 1 : 0)
+                           : (LN == 2 ? p.q * 2 : 0);
+  const bool stores = LN <= 4 || (p.q & (LN / 4 - 1)) == 0;
+  E* du = static_cast<E*>(a.du) + p.b * a.T * a.D + p.d;
+  E* dd = static_cast<E*>(a.ddelta) + p.b * a.T * a.D + p.d;
+  E* dz = a.z ? static_cast<E*>(a.dz) + p.b * a.T * a.D + p.d : nullptr;
+
+  const int64_t group = blockIdx.x / (unsigned)(a.G * l.parts);
+  for (int64_t chunk = group * l.per; chunk < (group + 1) * l.per && chunk < l.chunks; ++chunk) {
+    const int64_t t0 = chunk * kChunk;
+    if (t0 >= p.n) {  // behind the row's end
+      for (int k = p.q; k < kChunk && t0 + k < a.T; k += LN) {
+        const float2 none = make_float2(0.f, 0.f);
+        store_pair<E>(du + (t0 + k) * a.D, a.vec_ch, p.have, none);
+        store_pair<E>(dd + (t0 + k) * a.D, a.vec_ch, p.have, none);
+        if (dz) store_pair<E>(dz + (t0 + k) * a.D, a.vec_ch, p.have, none);
+      }
+      continue;
+    }
+    stage_chunk<E, LN>(a, p, t0, bc, sh);
+    __syncthreads();
+    const int64_t row = (p.b * l.chunks + chunk) * a.D + p.d;
+    f32x2 h[2][2], g[2][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      ulonglong2 hv = make_ulonglong2(0, 0), gv = hv;
+      if (c < p.have) {
+        hv = *reinterpret_cast<const ulonglong2*>(ws + l.hin + (row + c) * C::kNP + p.n0);
+        gv = *reinterpret_cast<const ulonglong2*>(ws + l.gin + (row + c) * C::kNP + p.n0);
+      }
+      h[c][0] = hv.x, h[c][1] = hv.y, g[c][0] = gv.x, g[c][1] = gv.y;
+    }
+    auto forward = [&](int k, f32x2 (&hc)[2][2], f32x2 (&at)[2][2]) {
+      const float4 sv = sh.sv[k][p.pair];
+      const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(&bc[k][0][p.n0]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const f32x2 s2 = dup2(c ? sv.y : sv.x), v2 = dup2(c ? sv.w : sv.z);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          at[c][x] = decay_pair(s2, A2[c][x]);
+          hc[c][x] = fma2(at[c][x], hc[c][x], mul2(v2, x ? B.y : B.x));
+        }
+      }
+    };
+    auto keep = [&](int sub) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<ulonglong2*>(&gs.kept[sub][c][p.lane]) =
+            make_ulonglong2(h[c][0], h[c][1]);
+    };
+    keep(0);
+#pragma unroll 1
+    for (int sub = 0; sub + 1 < kSubs; ++sub) {
+#pragma unroll
+      for (int k = 0; k < kSub; ++k) {
+        f32x2 at[2][2];
+        forward(sub * kSub + k, h, at);
+      }
+      keep(sub + 1);
+    }
+
+#pragma unroll 1
+    for (int sub = kSubs - 1; sub >= 0; --sub) {
+      const int k0 = sub * kSub;
+      f32x2 hs[kSub + 1][2][2], at[kSub][2][2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&gs.kept[sub][c][p.lane]);
+        hs[0][c][0] = v.x, hs[0][c][1] = v.y;
+      }
+#pragma unroll
+      for (int k = 0; k < kSub; ++k) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          hs[k + 1][c][0] = hs[k][c][0], hs[k + 1][c][1] = hs[k][c][1];
+        forward(k0 + k, hs[k + 1], at[k]);
+      }
+      float2 gB[kSub], wA[kSub], yC[kSub];  // of both channels, this lane's states
+#pragma unroll
+      for (int k = kSub - 1; k >= 0; --k) {
+        const float4 sv = sh.sv[k0 + k][p.pair];
+        const float2 o = sh.dyg[k0 + k][p.pair];
+        const ulonglong2 Bq = *reinterpret_cast<const ulonglong2*>(&bc[k0 + k][0][p.n0]);
+        const ulonglong2 Cq = *reinterpret_cast<const ulonglong2*>(&bc[k0 + k][1][p.n0]);
+        f32x2 vB[2], vC[2];
+        float part[3][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const f32x2 s2 = dup2(c ? sv.y : sv.x), v2 = dup2(c ? sv.w : sv.z),
+                      o2 = dup2(c ? o.y : o.x);
+          f32x2 acc[3];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const f32x2 Bx = x ? Bq.y : Bq.x, Cx = x ? Cq.y : Cq.x, now = hs[k + 1][c][x];
+            const f32x2 gt = fma2(o2, Cx, g[c][x]);
+            const f32x2 gn = mul2(gt, at[k][c][x]);
+            const f32x2 w = mul2(gn, hs[k][c][x]);
+            g[c][x] = gn;
+            dA[c][x] = fma2(w, s2, dA[c][x]);
+            acc[0] = x ? fma2(gt, Bx, acc[0]) : mul2(gt, Bx);
+            acc[1] = x ? fma2(w, A2[c][x], acc[1]) : mul2(w, A2[c][x]);
+            acc[2] = x ? fma2(Cx, now, acc[2]) : mul2(Cx, now);
+            vB[x] = c ? fma2(gt, v2, vB[x]) : mul2(gt, v2);
+            vC[x] = c ? fma2(o2, now, vC[x]) : mul2(o2, now);
+          }
+#pragma unroll
+          for (int m = 0; m < 3; ++m) {
+            const float2 v = unpack2(acc[m]);
+            part[m][c] = v.x + v.y;
+          }
+        }
+        gB[k] = make_float2(part[0][0], part[0][1]);
+        wA[k] = make_float2(part[1][0], part[1][1]);
+        yC[k] = make_float2(part[2][0], part[2][1]);
+        *reinterpret_cast<ulonglong2*>(&gs.terms[k][0][p.pair * C::kNP + p.n0]) =
+            make_ulonglong2(vB[0], vB[1]);
+        *reinterpret_cast<ulonglong2*>(&gs.terms[k][1][p.pair * C::kNP + p.n0]) =
+            make_ulonglong2(vC[0], vC[1]);
+      }
+      // <g, B>, <w, A>, <C, h>: after the exchanges this lane has token `mine`
+      auto exchange = [&](float2(&v)[kSub]) {
+        if (LN >= 2) {
+          const bool up = p.q & (LN / 2);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 give = up ? v[k] : v[k + 2], have = up ? v[k + 2] : v[k];
+            v[k].x = have.x + __shfl_xor_sync(0xffffffffu, give.x, LN / 2);
+            v[k].y = have.y + __shfl_xor_sync(0xffffffffu, give.y, LN / 2);
+          }
+        }
+        if (LN >= 4) {
+          const bool up = p.q & (LN / 4);
+          const float2 give = up ? v[0] : v[1], have = up ? v[1] : v[0];
+          v[0].x = have.x + __shfl_xor_sync(0xffffffffu, give.x, LN / 4);
+          v[0].y = have.y + __shfl_xor_sync(0xffffffffu, give.y, LN / 4);
+        }
+#pragma unroll
+        for (int w = LN / 8; w > 0; w >>= 1) {
+          v[0].x += __shfl_xor_sync(0xffffffffu, v[0].x, w);
+          v[0].y += __shfl_xor_sync(0xffffffffu, v[0].y, w);
+        }
+      };
+      exchange(gB);
+      exchange(wA);
+      exchange(yC);
+      if (stores) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+          const int k = k0 + mine + m;
+          const int64_t t = t0 + k;
+          if (t < a.T) {
+            float2 vu = make_float2(0.f, 0.f), vd = vu, vz = vu;
+            if (t < p.n) {
+              const float4 sv = sh.sv[k][p.pair];
+              const float2 o = sh.dyg[k][p.pair];
+              const float2 ut = p.at(a, p.u, a.us.time, t);
+              vu = make_float2(fmaf(gB[m].x, sv.x, skip0 * o.x), fmaf(gB[m].y, sv.y, skip1 * o.y));
+              vd = make_float2(fmaf(gB[m].x, ut.x, wA[m].x * kLn2),
+                               fmaf(gB[m].y, ut.y, wA[m].y * kLn2));
+              if (a.softplus) {
+                const float2 raw = p.at(a, p.dl, a.ds.time, t);
+                vd.x *= sigmoid(raw.x + p.bias[0]);
+                vd.y *= sigmoid(raw.y + p.bias[1]);
+              }
+              if (dz) {
+                const float2 zt = p.at(a, p.z, a.zs.time, t), yt = p.at(a, p.dy, a.dys.time, t);
+                const float q0 = sigmoid(zt.x), q1 = sigmoid(zt.y);
+                vz.x = yt.x * fmaf(skip0, ut.x, yC[m].x) * q0 * fmaf(zt.x, 1.f - q0, 1.f);
+                vz.y = yt.y * fmaf(skip1, ut.y, yC[m].y) * q1 * fmaf(zt.y, 1.f - q1, 1.f);
+              }
+              dD.x = fmaf(o.x, ut.x, dD.x), dD.y = fmaf(o.y, ut.y, dD.y);
+              dbias.x += vd.x, dbias.y += vd.y;
+            }
+            store_pair<E>(du + t * a.D, a.vec_ch, p.have, vu);
+            store_pair<E>(dd + t * a.D, a.vec_ch, p.have, vd);
+            if (dz) store_pair<E>(dz + t * a.D, a.vec_ch, p.have, vz);
+          }
+        }
+      }
+      __syncwarp();
+      // dB and dC of the group's tokens over the warp's channel pairs, four states a lane
+#pragma unroll
+      for (int i = 0; i < (kSub * 2 * LN + 31) / 32; ++i) {
+        const int e = i * 32 + p.lane;
+        if (kSub * 2 * LN % 32 == 0 || e < kSub * 2 * LN) {
+          const int k = e / (2 * LN), w = e % (2 * LN);
+          const float* from = &gs.terms[k][w / LN][w % LN * 4];
+          ulonglong2 v = *reinterpret_cast<const ulonglong2*>(from);
+#pragma unroll
+          for (int j = 1; j < C::kGroups; ++j) {
+            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(from + j * C::kNP);
+            v.x = add2(v.x, m.x), v.y = add2(v.y, m.y);
+          }
+          if (C::kWarps > 1)
+            *reinterpret_cast<ulonglong2*>(sums_row(p.warp, k0 + k) + w * 4) = v;
+          else if (t0 + k0 + k < p.n)
+            *reinterpret_cast<ulonglong2*>(
+                ws + l.dbc +
+                (((p.part * a.B + p.b) * a.T + t0 + k0 + k) * a.G + p.g) * 2 * C::kNP + w * 4) = v;
+        }
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+    if (C::kWarps > 1) {
+      for (int i = threadIdx.x; i < kChunk * 2 * LN; i += C::kWarps * 32) {
+        const int k = i / (2 * LN), w = i % (2 * LN);
+        if (t0 + k < p.n) {
+          ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sums_row(0, k) + w * 4);
+#pragma unroll
+          for (int m = 1; m < C::kWarps; ++m) {
+            const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(sums_row(m, k) + w * 4);
+            v.x = add2(v.x, e.x), v.y = add2(v.y, e.y);
+          }
+          *reinterpret_cast<ulonglong2*>(
+              ws + l.dbc +
+              (((p.part * a.B + p.b) * a.T + t0 + k) * a.G + p.g) * 2 * C::kNP + w * 4) = v;
+        }
+      }
+      __syncthreads();
+    }
   }
+#pragma unroll
+  for (int w = LN / 2; w > 0; w >>= 1) {
+    dD.x += __shfl_xor_sync(0xffffffffu, dD.x, w);
+    dD.y += __shfl_xor_sync(0xffffffffu, dD.y, w);
+    dbias.x += __shfl_xor_sync(0xffffffffu, dbias.x, w);
+    dbias.y += __shfl_xor_sync(0xffffffffu, dbias.y, w);
+  }
+  const int64_t out = (group * a.B + p.b) * a.D + p.d;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (c < p.have) {
+      *reinterpret_cast<ulonglong2*>(ws + l.dA + (out + c) * C::kNP + p.n0) =
+          make_ulonglong2(dA[c][0], dA[c][1]);
+      if (p.q == 0) {
+        ws[l.dD + out + c] = c ? dD.y : dD.x;
+        ws[l.dbias + out + c] = c ? dbias.y : dbias.x;
+      }
+    }
 }
 
+// Step 4.
 template <typename E>
-__global__ void scan_bwd_bc_kernel(ScanArgs a, const float* ws, Layout l) {
+__global__ void __launch_bounds__(256)
+    scan_bwd_bc_kernel(const __grid_constant__ ScanArgs a, const float* ws,
+                       const __grid_constant__ Layout l) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t rows = a.B * a.T * a.G;
-  if (i >= rows * 2 * l.N4) return;
-  const int64_t row = i / (2 * l.N4), k = i - row * 2 * l.N4;
-  const int64_t n = k % l.N4;
-  if (n >= a.N) return;
-  float v = 0.f;
-  for (int64_t p = 0; p < l.parts; ++p) v += ws[l.dbc + p * rows * 2 * l.N4 + i];
-  store_vec<E, 1>(static_cast<E*>(k < l.N4 ? a.dB : a.dC) + row * a.N + n, FloatV<1>{{v}});
+  const int64_t rows = a.B * a.T * a.G, quads = 2 * l.NP / 4;
+  if (i >= rows * quads) return;
+  const int64_t row = i / quads;
+  const int w = (int)(i - row * quads), n0 = w * 4 % (int)l.NP;
+  const int64_t bt = row / a.G, b = bt / a.T;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (bt - b * a.T < row_length(a.lengths, b, a.T)) {
+    const float* from = ws + l.dbc + i * 4;
+#pragma unroll 4
+    for (int64_t p = 0; p < l.parts; ++p) {
+      const float4 e = *reinterpret_cast<const float4*>(from + p * rows * 2 * l.NP);
+      v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
+    }
+  }
+  E* to = static_cast<E*>(w * 4 < l.NP ? a.dB : a.dC) + row * a.N + n0;
+  const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (n0 + k < a.N) store_vec<E, 1>(to + k, FloatV<1>{{f[k]}});
 }
 
-__global__ void scan_bwd_param_kernel(ScanArgs a, const float* ws, Layout l) {
+__global__ void __launch_bounds__(128)
+    scan_bwd_param_kernel(const __grid_constant__ ScanArgs a, const float* ws,
+                          const __grid_constant__ Layout l) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t parts = l.groups * a.B;
   if (i < (int64_t)a.D * a.N) {
     const int64_t d = i / a.N, n = i - d * a.N;
     float v = 0.f;
-    for (int64_t b = 0; b < a.B; ++b) v += ws[l.dA + (b * a.D + d) * l.N4 + n];
+#pragma unroll 8
+    for (int64_t p = 0; p < parts; ++p) v += ws[l.dA + (p * a.D + d) * l.NP + n];
     a.dA[i] = v;
   }
   if (i < a.D) {
     float v = 0.f, w = 0.f;
-    for (int64_t b = 0; b < a.B; ++b) {
-      v += ws[l.dD + b * a.D + i];
-      w += ws[l.dbias + b * a.D + i];
+#pragma unroll 8
+    for (int64_t p = 0; p < parts; ++p) {
+      v += ws[l.dD + p * a.D + i];
+      w += ws[l.dbias + p * a.D + i];
     }
     if (a.dDskip) a.dDskip[i] = v;
     if (a.ddelta_bias) a.ddelta_bias[i] = w;
@@ -226,18 +632,41 @@ __global__ void scan_bwd_param_kernel(ScanArgs a, const float* ws, Layout l) {
 
 template <typename E, int LN>
 cudaError_t bwd_lanes(const ScanArgs& a, cudaStream_t stream) {
+  typedef Cfg<LN> C;
   const Layout l(a.B, a.T, a.D, a.G, a.N);
   float* ws = static_cast<float*>(a.ws);
-  scan_bwd_kernel<E, LN>
-      <<<dim3((unsigned)(a.G * l.parts), (unsigned)a.B), kWarps * 32, 0, stream>>>(a, ws, l);
-  cudaError_t e = cudaGetLastError();
-  const int64_t bc = a.B * a.T * a.G * 2 * l.N4, pa = (int64_t)a.D * a.N;
-  if (e == cudaSuccess && bc > 0) {
-    scan_bwd_bc_kernel<E><<<(unsigned)((bc + 255) / 256), 256, 0, stream>>>(a, ws, l);
-    e = cudaGetLastError();
-  }
+  const int bc = kChunk * 2 * C::kNP * 4;
+  const int bytes1 = bc + C::kWarps * (int)sizeof(WarpShared<LN>);
+  const int bytes3 = bytes1 + C::kWarps * (int)sizeof(GradShared<LN>);
+  cudaError_t e = cudaSuccess;
+  if (bytes1 > 48 * 1024)
+    e = cudaFuncSetAttribute(scan_bwd_chunk_kernel<E, LN>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes1);
+  if (e == cudaSuccess && bytes3 > 48 * 1024)
+    e = cudaFuncSetAttribute(scan_bwd_grad_kernel<E, LN>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes3);
   if (e != cudaSuccess) return e;
-  scan_bwd_param_kernel<<<(unsigned)((pa + 127) / 128), 128, 0, stream>>>(a, ws, l);
+  const int64_t blocks = a.G * l.parts;
+  if (blocks * l.chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const dim3 chunks((unsigned)(blocks * l.chunks), (unsigned)a.B);
+  const dim3 groups((unsigned)(blocks * l.groups), (unsigned)a.B);
+  if (l.chunks > 0) {
+    scan_bwd_chunk_kernel<E, LN><<<chunks, C::kWarps * 32, bytes1, stream>>>(a, ws, l);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int64_t quads = (int64_t)a.D * LN;
+  scan_bwd_chain_kernel<<<dim3((unsigned)((quads + 127) / 128), (unsigned)a.B), 128, 0, stream>>>(
+      a, ws, l);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (l.chunks > 0) {
+    scan_bwd_grad_kernel<E, LN><<<groups, C::kWarps * 32, bytes3, stream>>>(a, ws, l);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int64_t sums = a.B * a.T * a.G * 2 * LN;
+    scan_bwd_bc_kernel<E><<<(unsigned)((sums + 255) / 256), 256, 0, stream>>>(a, ws, l);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int64_t params = (int64_t)a.D * a.N;
+  scan_bwd_param_kernel<<<(unsigned)((params + 127) / 128), 128, 0, stream>>>(a, ws, l);
   return cudaGetLastError();
 }
 
@@ -260,7 +689,13 @@ size_t scan_bwd_workspace_bytes(const falcon_scan_shape& s) {
   return sizeof(float) * Layout(s.B, s.T, s.D, s.G, s.N).total;
 }
 
-cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t stream) {
+cudaError_t launch_scan_bwd(const ScanArgs& in, cudaStream_t stream) {
+  ScanArgs a = in;
+  scan_access(&a);
+  // the dense outputs' pairs as well
+  const int pair = a.dtype == FALCON_BF16 ? 4 : 8;
+  for (const void* p : {(const void*)a.du, (const void*)a.ddelta, (const void*)a.dz})
+    a.vec_ch = a.vec_ch && reinterpret_cast<uintptr_t>(p) % pair == 0;
   return a.dtype == FALCON_BF16 ? bwd_typed<__nv_bfloat16>(a, stream)
                                 : bwd_typed<float>(a, stream);
 }

@@ -152,10 +152,16 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   return r;
 }
 __device__ __forceinline__ f32x2 pair2(float2 v) { return pack2(v.x, v.y); }
+// The same pair, its halves unknown to the compiler: a doubled value stays in its
+// two registers instead of being copied together before every use.
+__device__ __forceinline__ f32x2 opaque2(f32x2 v) {
+  asm volatile("" : "+l"(v));
+  return v;
+}
 // decay() twice: two steps of one state, or one step of two.
-__device__ __forceinline__ f32x2 decay2(f32x2 s, f32x2 A2) {
-  const float2 x = unpack2(fma2(s, A2, pack2(kDecayLift, kDecayLift)));
-  return pack2(exp2_approx(x.x), exp2_approx(x.y));
+__device__ __forceinline__ float2 decay2(f32x2 s, f32x2 A2, f32x2 lift) {
+  const float2 x = unpack2(fma2(s, A2, lift));
+  return make_float2(exp2_approx(x.x), exp2_approx(x.y));
 }
 // softplus() twice.
 __device__ __forceinline__ float2 softplus2(float2 x) {
