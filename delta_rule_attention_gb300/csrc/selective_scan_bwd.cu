@@ -48,8 +48,13 @@ struct Cfg {
   static constexpr int kGroups = 32 / LN;        // channel pairs of a warp
   static constexpr int kChannels = 2 * kGroups;  // channels of a warp
   static constexpr int kNP = 4 * LN;             // states, padded
-  // rows padded so that the lanes of a store phase fall in different banks
-  static constexpr int kRow = kGroups + (LN == 1 ? 0 : LN == 2 ? 4 : LN == 4 ? 2 : 1);
+  static constexpr int kRow = kGroups;
+  // Where a row keeps its channel pair: rows are turned against one another so
+  // that the lanes of a store phase (LN tokens of a pair) fall in different banks.
+  __device__ static constexpr int at(int k, int pair) {
+    return pair ^ (LN == 2 ? (k & 1) << 2 : LN == 4 ? (k & 3) << 1 : LN == 8 ? (k >> 1) & 3
+                   : LN == 16 ? (k >> 2) & 1 : 0);
+  }
   static constexpr int kBase = kGroups * kNP + 16;  // one token's dB (or dC) terms, padded
   // the chunk's dB and dC of a warp lie over its used steps where they fit
   static constexpr bool kOver = kRow * 4 >= 2 * kNP;
@@ -64,7 +69,7 @@ struct WarpShared {
 template <int LN>
 struct GradShared {
   typedef Cfg<LN> C;
-  float4 kept[kSubs][2][32];             // state before each group of tokens, by lane
+  float4 kept[kSubs - 1][2][32];         // state before each group but the first, by lane
   float terms[kSub][2][C::kBase];        // dB and dC terms by lane group
   float sums[C::kOver || C::kWarps == 1 ? 1 : kChunk][2 * C::kNP];
 };
@@ -130,11 +135,6 @@ struct Place {
     Bm = static_cast<const E*>(a.Bm) + b * a.bs.batch + g * a.bs.head;
     Cm = static_cast<const E*>(a.Cm) + b * a.cs.batch + g * a.cs.head;
   }
-  __device__ __forceinline__ float2 at(const ScanArgs& a, const E* p, int64_t stride,
-                                       int64_t t) const {
-    if (whole) return widen(*reinterpret_cast<const typename Raw<E>::Pair*>(p + t * stride));
-    return widen(load_pair<E>(p + t * stride, a.vec_ch, have));
-  }
   // A in units of log2(e), two states a pair
   __device__ __forceinline__ void decays(const ScanArgs& a, f32x2 (&A2)[2][2]) const {
 #pragma unroll
@@ -149,42 +149,78 @@ struct Place {
 };
 
 // Brings the tokens t0 .. of a chunk into shared memory; adds up the lane's steps.
+// A whole chunk's loads are all under way before the first is used.
 template <typename E, int LN>
 __device__ __forceinline__ float2 stage_chunk(const ScanArgs& a, const Place<E, LN>& p, int64_t t0,
                                               float (&bc)[kChunk][2][4 * LN],
                                               WarpShared<LN>& ws) {
   typedef Cfg<LN> C;
-  for (int i = threadIdx.x; i < kChunk * 2 * LN; i += C::kWarps * 32) {
+  typedef typename Raw<E>::Pair Pair;
+  typedef typename Raw<E>::Quad Quad;
+  constexpr int kItems = kChunk / LN, kBatch = kItems < 8 ? kItems : 8;
+  constexpr int kQuads = kChunk * 2 * LN / (C::kWarps * 32) > 0
+                             ? kChunk * 2 * LN / (C::kWarps * 32) : 1;
+  constexpr int kQuadBatch = kQuads < 4 ? kQuads : 4;
+  const bool full = p.whole && t0 + kChunk <= p.n;
+  auto quad_at = [&](int i) {
     const int k = i / (2 * LN), w = i % (2 * LN), s = w % LN * 4;
     const int64_t t = t0 + k;
     const E* src = w < LN ? p.Bm + t * a.bs.time : p.Cm + t * a.cs.time;
-    reinterpret_cast<float4*>(bc)[i] =
-        widen(load_quad<E>(src + s, a.vec_bc, t < p.n ? a.N - s : 0));
-  }
+    return load_quad<E>(src + s, a.vec_bc, t < p.n ? a.N - s : 0);
+  };
   float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < kChunk / LN; ++i) {
-    const int k = i * LN + p.q;
-    const int64_t t = t0 + k;
-    float2 s = make_float2(0.f, 0.f), v = s, o = s;
-    if (t < p.n) {
-      const float2 ut = p.at(a, p.u, a.us.time, t);
-      s = p.at(a, p.dl, a.ds.time, t);
-      o = p.at(a, p.dy, a.dys.time, t);
-      s.x += p.bias[0], s.y += p.bias[1];
-      if (a.softplus) s = softplus2(s);
-      v = make_float2(s.x * ut.x, s.y * ut.y);
-      if (p.z) {
-        const float2 zt = p.at(a, p.z, a.zs.time, t);
-        o.x *= zt.x * sigmoid(zt.x), o.y *= zt.y * sigmoid(zt.y);
+  auto put = [&](int k, float2 ut, float2 s, float2 o, float2 zt) {
+    s.x += p.bias[0], s.y += p.bias[1];
+    if (a.softplus) s = softplus2(s);
+    if (p.z) o.x *= zt.x * sigmoid(zt.x), o.y *= zt.y * sigmoid(zt.y);
+    if (!full) {  // no token, or a pair without a second (or any) channel
+      const int have = t0 + k < p.n ? p.have : 0;
+      if (have < 2) s.y = o.y = 0.f;
+      if (have < 1) s.x = o.x = 0.f;
+    }
+    sum.x += s.x, sum.y += s.y;
+    ws.sv[k][C::at(k, p.pair)] = make_float4(s.x, s.y, s.x * ut.x, s.y * ut.y);
+    ws.dyg[k][C::at(k, p.pair)] = o;
+  };
+  for (int i0 = 0; i0 < kQuads; i0 += kQuadBatch) {
+    Quad rq[kQuadBatch];
+#pragma unroll
+    for (int i = 0; i < kQuadBatch; ++i) {
+      const int e = (i0 + i) * C::kWarps * 32 + threadIdx.x;
+      if (kChunk * 2 * LN % (C::kWarps * 32) == 0 || e < kChunk * 2 * LN) rq[i] = quad_at(e);
+    }
+    if (i0 == 0) {
+#pragma unroll 1
+      for (int j0 = 0; j0 < kItems; j0 += kBatch) {
+        Pair ru[kBatch], rd[kBatch], ro[kBatch], rz[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int64_t t = t0 + (j0 + i) * LN + p.q;
+          rz[i] = Pair();
+          if (full) {
+            ru[i] = *reinterpret_cast<const Pair*>(p.u + t * a.us.time);
+            rd[i] = *reinterpret_cast<const Pair*>(p.dl + t * a.ds.time);
+            ro[i] = *reinterpret_cast<const Pair*>(p.dy + t * a.dys.time);
+            if (p.z) rz[i] = *reinterpret_cast<const Pair*>(p.z + t * a.zs.time);
+          } else {
+            const int have = t < p.n ? p.have : 0;
+            ru[i] = load_pair<E>(p.u + t * a.us.time, a.vec_ch, have);
+            rd[i] = load_pair<E>(p.dl + t * a.ds.time, a.vec_ch, have);
+            ro[i] = load_pair<E>(p.dy + t * a.dys.time, a.vec_ch, have);
+            if (p.z) rz[i] = load_pair<E>(p.z + t * a.zs.time, a.vec_ch, have);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          put((j0 + i) * LN + p.q, widen(ru[i]), widen(rd[i]), widen(ro[i]), widen(rz[i]));
       }
     }
-    // a pair without a second (or any) channel contributes nothing
-    if (p.have < 2) v.y = o.y = s.y = 0.f;
-    if (p.have < 1) v.x = o.x = s.x = 0.f;
-    sum.x += s.x, sum.y += s.y;
-    ws.sv[k][p.pair] = make_float4(s.x, s.y, v.x, v.y);
-    ws.dyg[k][p.pair] = o;
+#pragma unroll
+    for (int i = 0; i < kQuadBatch; ++i) {
+      const int e = (i0 + i) * C::kWarps * 32 + threadIdx.x;
+      if (kChunk * 2 * LN % (C::kWarps * 32) == 0 || e < kChunk * 2 * LN)
+        reinterpret_cast<float4*>(bc)[e] = widen(rq[i]);
+    }
   }
   return sum;
 }
@@ -217,8 +253,8 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
   __syncthreads();
 #pragma unroll 4
   for (int k = 0; k < kChunk; ++k) {
-    const float4 sv = sh.sv[k][p.pair];
-    const float2 o = sh.dyg[k][p.pair];
+    const float4 sv = sh.sv[k][C::at(k, p.pair)];
+    const float2 o = sh.dyg[k][C::at(k, p.pair)];
     const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(&bc[k][0][p.n0]);
     const ulonglong2 Ct = *reinterpret_cast<const ulonglong2*>(&bc[k][1][p.n0]);
 #pragma unroll
@@ -313,10 +349,11 @@ __global__ void __launch_bounds__(128)
 
 // Step 3.
 template <typename E, int LN>
-__global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
+__global__ void __launch_bounds__(Cfg<LN>::kWarps * 32, LN == 4 ? 3 : 1)
     scan_bwd_grad_kernel(const __grid_constant__ ScanArgs a, float* ws,
                          const __grid_constant__ Layout l) {
   typedef Cfg<LN> C;
+  typedef typename Raw<E>::Pair Pair;
   constexpr int kMine = LN >= kSub ? 1 : kSub / LN;  // tokens of a group a lane finishes
   extern __shared__ __align__(16) unsigned char bytes[];
   auto& bc = *reinterpret_cast<float(*)[kChunk][2][C::kNP]>(bytes);
@@ -355,6 +392,7 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
       }
       continue;
     }
+    const bool full = p.whole && t0 + kChunk <= p.n;
     stage_chunk<E, LN>(a, p, t0, bc, sh);
     __syncthreads();
     const int64_t row = (p.b * l.chunks + chunk) * a.D + p.d;
@@ -369,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
       h[c][0] = hv.x, h[c][1] = hv.y, g[c][0] = gv.x, g[c][1] = gv.y;
     }
     auto forward = [&](int k, f32x2 (&hc)[2][2], f32x2 (&at)[2][2]) {
-      const float4 sv = sh.sv[k][p.pair];
+      const float4 sv = sh.sv[k][C::at(k, p.pair)];
       const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(&bc[k][0][p.n0]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -387,7 +425,7 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
         *reinterpret_cast<ulonglong2*>(&gs.kept[sub][c][p.lane]) =
             make_ulonglong2(h[c][0], h[c][1]);
     };
-    keep(0);
+    const f32x2 h0[2][2] = {{h[0][0], h[0][1]}, {h[1][0], h[1][1]}};
 #pragma unroll 1
     for (int sub = 0; sub + 1 < kSubs; ++sub) {
 #pragma unroll
@@ -395,17 +433,40 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
         f32x2 at[2][2];
         forward(sub * kSub + k, h, at);
       }
-      keep(sub + 1);
+      keep(sub);  // before group sub + 1
     }
 
 #pragma unroll 1
     for (int sub = kSubs - 1; sub >= 0; --sub) {
       const int k0 = sub * kSub;
       f32x2 hs[kSub + 1][2][2], at[kSub][2][2];
+      // what this lane needs to finish its tokens, on its way meanwhile
+      Pair ru[kMine], rd[kMine], ro[kMine], rz[kMine];
+#pragma unroll
+      for (int m = 0; m < kMine; ++m) {
+        const int64_t t = t0 + k0 + mine + m;
+        rz[m] = Pair();
+        if (full) {
+          ru[m] = *reinterpret_cast<const Pair*>(p.u + t * a.us.time);
+          rd[m] = *reinterpret_cast<const Pair*>(p.dl + t * a.ds.time);
+          ro[m] = *reinterpret_cast<const Pair*>(p.dy + t * a.dys.time);
+          if (dz) rz[m] = *reinterpret_cast<const Pair*>(p.z + t * a.zs.time);
+        } else {
+          const int have = t < p.n ? p.have : 0;
+          ru[m] = load_pair<E>(p.u + t * a.us.time, a.vec_ch, have);
+          rd[m] = load_pair<E>(p.dl + t * a.ds.time, a.vec_ch, have);
+          ro[m] = load_pair<E>(p.dy + t * a.dys.time, a.vec_ch, have);
+          if (dz) rz[m] = load_pair<E>(p.z + t * a.zs.time, a.vec_ch, have);
+        }
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&gs.kept[sub][c][p.lane]);
-        hs[0][c][0] = v.x, hs[0][c][1] = v.y;
+        if (sub > 0) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&gs.kept[sub - 1][c][p.lane]);
+          hs[0][c][0] = v.x, hs[0][c][1] = v.y;
+        } else {
+          hs[0][c][0] = h0[c][0], hs[0][c][1] = h0[c][1];
+        }
       }
 #pragma unroll
       for (int k = 0; k < kSub; ++k) {
@@ -417,8 +478,8 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
       float2 gB[kSub], wA[kSub], yC[kSub];  // of both channels, this lane's states
 #pragma unroll
       for (int k = kSub - 1; k >= 0; --k) {
-        const float4 sv = sh.sv[k0 + k][p.pair];
-        const float2 o = sh.dyg[k0 + k][p.pair];
+        const float4 sv = sh.sv[k0 + k][C::at(k0 + k, p.pair)];
+        const float2 o = sh.dyg[k0 + k][C::at(k0 + k, p.pair)];
         const ulonglong2 Bq = *reinterpret_cast<const ulonglong2*>(&bc[k0 + k][0][p.n0]);
         const ulonglong2 Cq = *reinterpret_cast<const ulonglong2*>(&bc[k0 + k][1][p.n0]);
         f32x2 vB[2], vC[2];
@@ -490,19 +551,19 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
           if (t < a.T) {
             float2 vu = make_float2(0.f, 0.f), vd = vu, vz = vu;
             if (t < p.n) {
-              const float4 sv = sh.sv[k][p.pair];
-              const float2 o = sh.dyg[k][p.pair];
-              const float2 ut = p.at(a, p.u, a.us.time, t);
+              const float4 sv = sh.sv[k][C::at(k, p.pair)];
+              const float2 o = sh.dyg[k][C::at(k, p.pair)];
+              const float2 ut = widen(ru[m]);
               vu = make_float2(fmaf(gB[m].x, sv.x, skip0 * o.x), fmaf(gB[m].y, sv.y, skip1 * o.y));
               vd = make_float2(fmaf(gB[m].x, ut.x, wA[m].x * kLn2),
                                fmaf(gB[m].y, ut.y, wA[m].y * kLn2));
               if (a.softplus) {
-                const float2 raw = p.at(a, p.dl, a.ds.time, t);
+                const float2 raw = widen(rd[m]);
                 vd.x *= sigmoid(raw.x + p.bias[0]);
                 vd.y *= sigmoid(raw.y + p.bias[1]);
               }
               if (dz) {
-                const float2 zt = p.at(a, p.z, a.zs.time, t), yt = p.at(a, p.dy, a.dys.time, t);
+                const float2 zt = widen(rz[m]), yt = widen(ro[m]);
                 const float q0 = sigmoid(zt.x), q1 = sigmoid(zt.y);
                 vz.x = yt.x * fmaf(skip0, ut.x, yC[m].x) * q0 * fmaf(zt.x, 1.f - q0, 1.f);
                 vz.y = yt.y * fmaf(skip1, ut.y, yC[m].y) * q1 * fmaf(zt.y, 1.f - q1, 1.f);
