@@ -8,7 +8,9 @@ consecutive channels are adjacent; parameters and states are dense.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import functools
 
 import torch
 
@@ -75,9 +77,15 @@ def declare(lib):
         fn.restype = _sz if name.endswith("_bytes") else ctypes.c_int
 
 
+_lib = None
+
+
 def _library():
-    from . import load_library
-    return load_library()
+    global _lib
+    if _lib is None:
+        from . import load_library
+        _lib = load_library()
+    return _lib
 
 
 def _check(rc, what):
@@ -91,33 +99,54 @@ def _at(t):
 
 
 def _current(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else \
+        stream.cuda_stream
 
 
-def _rows(t, name, dtype, shape):
-    """A CUDA tensor of this type and shape whose last dimension is adjacent."""
+# Descriptions by their values: the structures of a shape met before are not built
+# again.
+@functools.lru_cache(maxsize=4096)
+def _strides(batch, head, time):
+    return ctypes.byref(falcon_strides(batch, head, time))
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_shape(*fields):
+    return ctypes.byref(falcon_conv_shape(*fields))
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_shape(*fields):
+    return ctypes.byref(falcon_scan_shape(*fields))
+
+
+def _refuse(t, name, dtype, shape, device, what):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or (t.stride(-1) != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name} must be a CUDA tensor with adjacent channels")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, x or u on {device}")
+    raise ValueError(f"{name} must {what}")
+
+
+def _rows(t, name, dtype, shape, device):
+    """A tensor of this type, shape and GPU whose last dimension is adjacent."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or
+            t.device != device or not t.is_cuda or (t.stride(-1) != 1 and t.shape[-1] > 1)):
+        _refuse(t, name, dtype, shape, device, "have adjacent channels")
     return t
 
 
-def _dense(t, name, dtype, shape):
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+def _dense(t, name, dtype, shape, device):
+    if t is not None and (
+            not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or
+            t.device != device or not t.is_cuda or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, device, "be contiguous")
     return t
 
 
@@ -129,12 +158,6 @@ def _dtype(t, name):
     return t.dtype
 
 
-def _same_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors are on {device} and {t.device}")
-
-
 def _workspace(need, workspace, device):
     if workspace is None:
         return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
@@ -144,7 +167,7 @@ def _workspace(need, workspace, device):
 def _conv_rows(t):
     """Strides of [B,T,m] or [B,H,T,m]."""
     s = t.stride()
-    return falcon_strides(s[0], 0, s[1]) if t.dim() == 3 else falcon_strides(s[0], s[1], s[2])
+    return _strides(s[0], 0, s[1]) if len(s) == 3 else _strides(s[0], s[1], s[2])
 
 
 def _conv_setup(x, weight, bias, state, lengths, activation):
@@ -153,19 +176,19 @@ def _conv_setup(x, weight, bias, state, lengths, activation):
         raise ValueError("x must be [B,T,m] or [B,H,T,m]")
     if activation not in _ACT:
         raise ValueError(f"activation must be one of {sorted(_ACT)}")
-    _rows(x, "x", dt, x.shape)
+    dev = x.device
+    _rows(x, "x", dt, x.shape, dev)
     B, T, m = x.shape[0], x.shape[-2], x.shape[-1]
     H = 1 if x.dim() == 3 else x.shape[1]
     C = H * m
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [channels, width]")
     W = weight.shape[1]
-    _dense(weight, "weight", torch.float32, (C, W))
-    _dense(bias, "bias", torch.float32, (C,))
-    _dense(state, "state", dt, (B, W - 1, C))
-    _dense(lengths, "lengths", torch.int32, (B,))
-    _same_device(x.device, weight, bias, state, lengths)
-    return falcon_conv_shape(B, H, T, m, W, _DTYPE[dt], _ACT[activation]), dt, B, C, W
+    _dense(weight, "weight", torch.float32, (C, W), dev)
+    _dense(bias, "bias", torch.float32, (C,), dev)
+    _dense(state, "state", dt, (B, W - 1, C), dev)
+    _dense(lengths, "lengths", torch.int32, (B,), dev)
+    return _conv_shape(B, H, T, m, W, _DTYPE[dt], _ACT[activation]), dt, dev, B, C, W
 
 
 def falcon_short_conv_fwd(x, weight, bias=None, state=None, lengths=None, activation="silu",
@@ -177,14 +200,14 @@ def falcon_short_conv_fwd(x, weight, bias=None, state=None, lengths=None, activa
     "identity".  Returns (y, state_out): y of x's shape, dense unless passed in,
     and the last width-1 inputs of every row."""
     lib = _library()
-    shape, dt, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
-    y = torch.empty(x.shape, dtype=dt, device=x.device) if y is None else \
-        _rows(y, "y", dt, x.shape)
-    state_out = torch.empty((B, W - 1, C), dtype=dt, device=x.device) if state_out is None else \
-        _dense(state_out, "state_out", dt, (B, W - 1, C))
+    shape, dt, dev, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
+    y = torch.empty(x.shape, dtype=dt, device=dev) if y is None else \
+        _rows(y, "y", dt, x.shape, dev)
+    state_out = torch.empty((B, W - 1, C), dtype=dt, device=dev) if state_out is None else \
+        _dense(state_out, "state_out", dt, (B, W - 1, C), dev)
     rc = lib.falcon_short_conv_fwd(shape, _at(x), _conv_rows(x), _at(weight), _at(bias),
                                    _at(state), _at(lengths), _at(y), _conv_rows(y),
-                                   _at(state_out), _current(stream, x.device))
+                                   _at(state_out), _current(stream, dev))
     _check(rc, "falcon_short_conv_fwd")
     return y, state_out
 
@@ -195,11 +218,9 @@ def falcon_short_conv_bwd(x, weight, dy, bias=None, state=None, lengths=None, ds
     Returns a dict with dx (dense, x's shape), dweight, dbias (fp32) and dstate;
     ``grads`` may pass preallocated outputs."""
     lib = _library()
-    shape, dt, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
-    _rows(dy, "dy", dt, x.shape)
-    _dense(dstate_out, "dstate_out", dt, (B, W - 1, C))
-    dev = x.device
-    _same_device(dev, dy, dstate_out)
+    shape, dt, dev, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
+    _rows(dy, "dy", dt, x.shape, dev)
+    _dense(dstate_out, "dstate_out", dt, (B, W - 1, C), dev)
     g = {} if grads is None else grads
     if "dx" not in g:
         g["dx"] = torch.empty(x.shape, dtype=dt, device=dev)
@@ -209,10 +230,11 @@ def falcon_short_conv_bwd(x, weight, dy, bias=None, state=None, lengths=None, ds
         g["dbias"] = torch.empty((C,), dtype=torch.float32, device=dev)
     if "dstate" not in g:
         g["dstate"] = torch.empty((B, W - 1, C), dtype=dt, device=dev)
-    _rows(g["dx"], "dx", dt, x.shape)
-    _dense(g["dweight"], "dweight", torch.float32, (C, W))
-    _dense(g["dbias"], "dbias", torch.float32, (C,))
-    _dense(g["dstate"], "dstate", dt, (B, W - 1, C))
+    if grads is not None:
+        _rows(g["dx"], "dx", dt, x.shape, dev)
+        _dense(g["dweight"], "dweight", torch.float32, (C, W), dev)
+        _dense(g["dbias"], "dbias", torch.float32, (C,), dev)
+        _dense(g["dstate"], "dstate", dt, (B, W - 1, C), dev)
     workspace, have = _workspace(int(lib.falcon_short_conv_bwd_workspace_bytes(shape)),
                                  workspace, dev)
     rc = lib.falcon_short_conv_bwd(
@@ -237,19 +259,19 @@ def falcon_short_conv_step(x, weight, state, bias=None, slots=None, fresh=None,
         raise ValueError(f"activation must be one of {sorted(_ACT)}")
     N, C = x.shape
     W = weight.shape[1]
-    _rows(x, "x", dt, x.shape)
-    _dense(weight, "weight", torch.float32, (C, W))
-    _dense(bias, "bias", torch.float32, (C,))
+    dev = x.device
+    _rows(x, "x", dt, x.shape, dev)
+    _dense(weight, "weight", torch.float32, (C, W), dev)
+    _dense(bias, "bias", torch.float32, (C,), dev)
     pool = _pool(state, "state", slots, N)
-    _dense(state, "state", dt, (pool, W - 1, C))
-    _dense(slots, "slots", torch.int32, (N,))
-    _dense(fresh, "fresh", torch.uint8, (N,))
-    _same_device(x.device, weight, bias, state, slots, fresh)
-    y = torch.empty((N, C), dtype=dt, device=x.device) if y is None else \
-        _dense(y, "y", dt, (N, C))
+    _dense(state, "state", dt, (pool, W - 1, C), dev)
+    _dense(slots, "slots", torch.int32, (N,), dev)
+    _dense(fresh, "fresh", torch.uint8, (N,), dev)
+    y = torch.empty((N, C), dtype=dt, device=dev) if y is None else \
+        _dense(y, "y", dt, (N, C), dev)
     rc = lib.falcon_short_conv_step(N, C, W, _DTYPE[dt], _ACT[activation], _at(x), x.stride(0),
                                     _at(weight), _at(bias), _at(state), pool, _at(slots),
-                                    _at(fresh), _at(y), _current(stream, x.device))
+                                    _at(fresh), _at(y), _current(stream, dev))
     _check(rc, "falcon_short_conv_step")
     return y
 
@@ -264,12 +286,12 @@ def _pool(state, name, slots, N):
 
 def _time_rows(t):
     s = t.stride()
-    return falcon_strides(s[0], 0, s[1])
+    return _strides(s[0], 0, s[1])
 
 
 def _group_rows(t):
     s = t.stride()
-    return falcon_strides(s[0], s[2], s[1])
+    return _strides(s[0], s[2], s[1])
 
 
 def _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus):
@@ -282,19 +304,19 @@ def _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus):
     if not isinstance(Bm, torch.Tensor) or Bm.dim() != 4:
         raise ValueError("Bm and Cm must be [B,T,G,N]")
     N, G = A.shape[1], Bm.shape[2]
-    _rows(u, "u", dt, (B, T, C))
-    _rows(delta, "delta", dt, (B, T, C))
-    _rows(Bm, "Bm", dt, (B, T, G, N))
-    _rows(Cm, "Cm", dt, (B, T, G, N))
+    dev, row, bc, f32 = u.device, (B, T, C), (B, T, G, N), torch.float32
+    _rows(u, "u", dt, row, dev)
+    _rows(delta, "delta", dt, row, dev)
+    _rows(Bm, "Bm", dt, bc, dev)
+    _rows(Cm, "Cm", dt, bc, dev)
     if z is not None:
-        _rows(z, "z", dt, (B, T, C))
-    _dense(A, "A", torch.float32, (C, N))
-    _dense(D, "D", torch.float32, (C,))
-    _dense(delta_bias, "delta_bias", torch.float32, (C,))
-    _dense(h0, "h0", torch.float32, (B, C, N))
-    _dense(lengths, "lengths", torch.int32, (B,))
-    _same_device(u.device, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths)
-    return falcon_scan_shape(B, T, C, G, N, _DTYPE[dt], 1 if softplus else 0), dt
+        _rows(z, "z", dt, row, dev)
+    _dense(A, "A", f32, (C, N), dev)
+    _dense(D, "D", f32, (C,), dev)
+    _dense(delta_bias, "delta_bias", f32, (C,), dev)
+    _dense(h0, "h0", f32, (B, C, N), dev)
+    _dense(lengths, "lengths", torch.int32, (B,), dev)
+    return _scan_shape(B, T, C, G, N, _DTYPE[dt], 1 if softplus else 0), dt, dev, (B, C, N)
 
 
 def falcon_selective_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, h0=None,
@@ -304,12 +326,11 @@ def falcon_selective_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=No
     and Bm, Cm [B,T,G,N] (bf16 or fp32, any row strides); A [D,N], D, delta_bias
     [D] and h0 [B,D,N] fp32; lengths [B] int32.  Returns (y, h_T)."""
     lib = _library()
-    shape, dt = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
-    dev = u.device
-    y = torch.empty(u.shape, dtype=dt, device=dev) if y is None else _rows(y, "y", dt, u.shape)
-    hs = (shape.B, shape.D, shape.N)
+    shape, dt, dev, hs = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
+    y = torch.empty(u.shape, dtype=dt, device=dev) if y is None else \
+        _rows(y, "y", dt, u.shape, dev)
     h_out = torch.empty(hs, dtype=torch.float32, device=dev) if h_out is None else \
-        _dense(h_out, "h_out", torch.float32, hs)
+        _dense(h_out, "h_out", torch.float32, hs, dev)
     rc = lib.falcon_selective_scan_fwd(
         shape, _at(u), _time_rows(u), _at(delta), _time_rows(delta), _at(A), _at(Bm),
         _group_rows(Bm), _at(Cm), _group_rows(Cm), _at(D), _at(z),
@@ -327,12 +348,9 @@ def falcon_selective_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bia
     dh0 (fp32); dz, dD and ddelta_bias are None where z, D or delta_bias is.
     ``grads`` may pass preallocated outputs."""
     lib = _library()
-    shape, dt = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
-    dev = u.device
-    _rows(dy, "dy", dt, u.shape)
-    hs = (shape.B, shape.D, shape.N)
-    _dense(dh_T, "dh_T", torch.float32, hs)
-    _same_device(dev, dy, dh_T)
+    shape, dt, dev, hs = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
+    _rows(dy, "dy", dt, u.shape, dev)
+    _dense(dh_T, "dh_T", torch.float32, hs, dev)
     f32 = torch.float32
     bc = tuple(Bm.shape)
     want = {"du": (dt, tuple(u.shape)), "ddelta": (dt, tuple(u.shape)),
@@ -346,7 +364,7 @@ def falcon_selective_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bia
         if spec is None:
             g[name] = None
         elif name in g:
-            _dense(g[name], name, *spec)
+            _dense(g[name], name, *spec, dev)
         else:
             g[name] = torch.empty(spec[1], dtype=spec[0], device=dev)
     workspace, have = _workspace(int(lib.falcon_selective_scan_bwd_workspace_bytes(shape)),
@@ -374,29 +392,28 @@ def falcon_selective_scan_step(u, delta, A, Bm, Cm, h, D=None, z=None, delta_bia
         raise ValueError("u must be [N,D], A [D,S] and Bm, Cm [N,G,S]")
     N, C = u.shape
     S, G = A.shape[1], Bm.shape[1]
-    _rows(u, "u", dt, (N, C))
-    _rows(delta, "delta", dt, (N, C))
-    _rows(Bm, "Bm", dt, (N, G, S))
-    _rows(Cm, "Cm", dt, (N, G, S))
+    dev, row, bc, f32 = u.device, (N, C), (N, G, S), torch.float32
+    _rows(u, "u", dt, row, dev)
+    _rows(delta, "delta", dt, row, dev)
+    _rows(Bm, "Bm", dt, bc, dev)
+    _rows(Cm, "Cm", dt, bc, dev)
     if z is not None:
-        _rows(z, "z", dt, (N, C))
-    _dense(A, "A", torch.float32, (C, S))
-    _dense(D, "D", torch.float32, (C,))
-    _dense(delta_bias, "delta_bias", torch.float32, (C,))
+        _rows(z, "z", dt, row, dev)
+    _dense(A, "A", f32, (C, S), dev)
+    _dense(D, "D", f32, (C,), dev)
+    _dense(delta_bias, "delta_bias", f32, (C,), dev)
     pool = _pool(h, "h", slots, N)
-    _dense(h, "h", torch.float32, (pool, C, S))
-    _dense(slots, "slots", torch.int32, (N,))
-    _dense(fresh, "fresh", torch.uint8, (N,))
-    _same_device(u.device, delta, A, Bm, Cm, h, D, z, delta_bias, slots, fresh)
-    y = torch.empty((N, C), dtype=dt, device=u.device) if y is None else \
-        _dense(y, "y", dt, (N, C))
+    _dense(h, "h", f32, (pool, C, S), dev)
+    _dense(slots, "slots", torch.int32, (N,), dev)
+    _dense(fresh, "fresh", torch.uint8, (N,), dev)
+    y = torch.empty(row, dtype=dt, device=dev) if y is None else _dense(y, "y", dt, row, dev)
     b, c = Bm.stride(), Cm.stride()
     rc = lib.falcon_selective_scan_step(
         N, C, G, S, _DTYPE[dt], 1 if softplus else 0, _at(u), u.stride(0), _at(delta),
-        delta.stride(0), _at(A), _at(Bm), falcon_strides(b[0], b[1], 0), _at(Cm),
-        falcon_strides(c[0], c[1], 0), _at(D), _at(z), 0 if z is None else z.stride(0),
+        delta.stride(0), _at(A), _at(Bm), _strides(b[0], b[1], 0), _at(Cm),
+        _strides(c[0], c[1], 0), _at(D), _at(z), 0 if z is None else z.stride(0),
         _at(delta_bias), _at(h), pool, _at(slots), _at(fresh), _at(y),
-        _current(stream, u.device))
+        _current(stream, dev))
     _check(rc, "falcon_selective_scan_step")
     return y
 
@@ -405,7 +422,7 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
                           stream=None):
     """Scales a list of dense gradients (bf16 or fp32, mixed, any shapes) by
     min(1, max_norm / (n + eps)), n their global 2-norm: in place, or into the
-    tensors of ``out`` (same shapes and dtypes).  Returns n, a 0-d fp32 tensor on
+    tensors of ``out`` (same sizes and dtypes).  Returns n, a 0-d fp32 tensor on
     the gradients' device; the host does not wait for it."""
     lib = _library()
     grads = list(grads)
@@ -414,22 +431,39 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
     into = grads if out is None else list(out)
     if len(into) != len(grads):
         raise ValueError("out must hold one tensor a gradient")
+    T = torch.Tensor
+    if not all(isinstance(t, T) for t in grads) or not all(isinstance(t, T) for t in into):
+        raise TypeError("gradients and outputs must be torch.Tensor")
+    kinds = [t.dtype for t in grads]
+    if not _DTYPE.keys() >= set(kinds):
+        raise TypeError("gradients must be bfloat16 or float32")
+    counts = list(map(T.numel, grads))
+    index = grads[0].get_device()
+    both = grads if into is grads else grads + into
+    if index < 0 or list(map(T.get_device, both)).count(index) != len(both):
+        raise ValueError("gradients and outputs must be CUDA tensors of one device")
+    if not all(map(T.is_contiguous, both)):
+        raise ValueError("gradients and outputs must be contiguous")
+    at = array.array("q", map(T.data_ptr, grads))
+    if into is grads:
+        to = at
+    else:
+        if [t.dtype for t in into] != kinds:
+            raise TypeError("outputs must have their gradients' dtypes")
+        if list(map(T.numel, into)) != counts:
+            raise ValueError("outputs must have their gradients' sizes")
+        to = array.array("q", map(T.data_ptr, into))
+    # the rows of falcon_grad: four 64-bit words each
+    table = array.array("q", bytes(32 * len(grads)))
+    table[0::4], table[1::4], table[2::4] = at, to, array.array("q", counts)
+    table[3::4] = array.array("q", map(_DTYPE.__getitem__, kinds))
+    rows = ctypes.cast(table.buffer_info()[0], ctypes.POINTER(falcon_grad))
     dev = grads[0].device
-    table = (falcon_grad * len(grads))()
-    for i, (g, o) in enumerate(zip(grads, into)):
-        if g.dtype not in _DTYPE or o.dtype != g.dtype:
-            raise TypeError("gradients must be bfloat16 or float32, outputs of the same dtype")
-        if g.device != dev or o.device != dev or not g.is_cuda:
-            raise ValueError("gradients and outputs must be CUDA tensors of one device")
-        if o.shape != g.shape or not g.is_contiguous() or not o.is_contiguous():
-            raise ValueError("gradients and outputs must be contiguous and of the same shapes")
-        e = table[i]
-        e.grad, e.out, e.count, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), _DTYPE[g.dtype]
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=dev)
-    workspace, have = _workspace(int(lib.falcon_clip_workspace_bytes(table, len(grads))),
+    workspace, have = _workspace(int(lib.falcon_clip_workspace_bytes(rows, len(grads))),
                                  workspace, dev)
-    rc = lib.falcon_clip_grad_norm(table, len(grads), float(max_norm), float(eps), _at(norm),
+    rc = lib.falcon_clip_grad_norm(rows, len(grads), float(max_norm), float(eps), _at(norm),
                                    _at(workspace), have, _current(stream, dev))
     _check(rc, "falcon_clip_grad_norm")
     return norm

@@ -4,6 +4,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -28,15 +29,22 @@ bool misaligned(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 1
 
 bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
-// The kernels are built for sm_103a only.
+// The kernels are built for sm_103a only.  A device's answer is kept: it does
+// not change, and the queries cost a small call a microsecond.
 int check_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FALCON_ERR_CUDA;
+  constexpr int kKept = 64;
+  static std::atomic<int> known[kKept];  // 0: not asked, 1: sm_103, 2: another
+  const int was = dev >= 0 && dev < kKept ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (was) return was == 1 ? FALCON_OK : FALCON_ERR_DEVICE;
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
     return FALCON_ERR_CUDA;
-  return (major == 10 && minor == 3) ? FALCON_OK : FALCON_ERR_DEVICE;
+  const bool ok = major == 10 && minor == 3;
+  if (dev >= 0 && dev < kKept) known[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
+  return ok ? FALCON_OK : FALCON_ERR_DEVICE;
 }
 
 int check_common(int dtype, int phi, int ridge, float eps, float eps_gamma) {
