@@ -432,12 +432,10 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
     if len(into) != len(grads):
         raise ValueError("out must hold one tensor a gradient")
     T = torch.Tensor
-    if not all(isinstance(t, T) for t in grads) or not all(isinstance(t, T) for t in into):
-        raise TypeError("gradients and outputs must be torch.Tensor")
+    counts = list(map(T.numel, grads))  # refuses what is no tensor
     kinds = [t.dtype for t in grads]
     if not _DTYPE.keys() >= set(kinds):
         raise TypeError("gradients must be bfloat16 or float32")
-    counts = list(map(T.numel, grads))
     index = grads[0].get_device()
     both = grads if into is grads else grads + into
     if index < 0 or list(map(T.get_device, both)).count(index) != len(both):

@@ -3,7 +3,8 @@
 //
 // Two launches over the same chunks of all tensors: squares into one partial
 // sum a block, then every block adds the partial sums in the same order (so
-// that all agree on n without an atomic or a third launch) and scales.  The
+// that all agree on n without an atomic or a third launch) and scales, from the
+// back, where L2 still holds what the first launch read last.  The
 // tensors' addresses travel as kernel arguments; more than kMost tensors take
 // further launches of each kind.
 
@@ -13,21 +14,24 @@ namespace falcon {
 namespace {
 
 constexpr int kMost = 512;        // tensors of one launch
+constexpr int kFew = 64;          // of a launch with short arguments
 constexpr int kThreads = 256;
-constexpr int kChunk = 16384;     // elements a block takes at a time
-constexpr int kBlocks = 152 * 4;  // of one launch
+constexpr int kChunk = 8192;      // elements a block takes at a time
+constexpr int kBlocks = 152 * 8;  // of one launch
 
+template <int MOST>
 struct Batch {
-  const void* grad[kMost];
-  void* out[kMost];
-  int64_t count[kMost];
-  int64_t first[kMost];  // chunks before this tensor's
-  unsigned char dtype[kMost];
+  const void* grad[MOST];
+  void* out[MOST];
+  int64_t count[MOST];
+  int64_t first[MOST];  // chunks before this tensor's
+  unsigned char dtype[MOST];
   int tensors;
   int64_t chunks;
 };
 
-__device__ __forceinline__ int tensor_of(const Batch& p, int64_t chunk) {
+template <int MOST>
+__device__ __forceinline__ int tensor_of(const Batch<MOST>& p, int64_t chunk) {
   int lo = 0, hi = p.tensors - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -49,42 +53,61 @@ __device__ __forceinline__ float block_sum_f64(double v, double* sh, double* tot
   return (float)s;
 }
 
+// A block's part of a tensor as 16-byte vectors between the elements before the
+// first 16-byte boundary and those after the last.
+struct Span {
+  int head, vecs, tail;  // elements, vectors, first element of the rest
+  __device__ __forceinline__ Span(const void* p, int n, int esz, bool vectors) {
+    head = (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / esz;
+    if (!vectors || head > n) head = n;
+    vecs = (n - head) / (16 / esz);
+    tail = head + vecs * (16 / esz);
+  }
+};
+constexpr int kBatch = 4;  // vectors of a thread under way at a time
+
 template <typename E>
-__device__ __forceinline__ float chunk_squares(const E* g, int64_t n) {
+__device__ __forceinline__ float chunk_squares(const E* g, int n) {
   constexpr int V = 16 / (int)sizeof(E);
-  // elements before the first 16-byte boundary, whole vectors, the rest
-  int64_t head = (int64_t)((16 - (reinterpret_cast<uintptr_t>(g) & 15)) & 15) / (int)sizeof(E);
-  if (head > n) head = n;
-  const int64_t vecs = (n - head) / V, tail = head + vecs * V;
+  const Span s(g, n, (int)sizeof(E), true);
   float s0 = 0.f, s1 = 0.f;
-  if (threadIdx.x < head) {
+  if ((int)threadIdx.x < s.head) {
     const float x = load_vec<E, 1>(g + threadIdx.x).v[0];
     s0 = fmaf(x, x, s0);
   }
-  if (threadIdx.x < n - tail) {
-    const float x = load_vec<E, 1>(g + tail + threadIdx.x).v[0];
+  if ((int)threadIdx.x < n - s.tail) {
+    const float x = load_vec<E, 1>(g + s.tail + threadIdx.x).v[0];
     s0 = fmaf(x, x, s0);
   }
-#pragma unroll 4
-  for (int64_t i = threadIdx.x; i < vecs; i += kThreads) {
-    const FloatV<V> x = load_vec<E, V>(g + head + i * V);
+  for (int i0 = threadIdx.x; i0 < s.vecs; i0 += kThreads * kBatch) {
+    uint4 q[kBatch];
 #pragma unroll
-    for (int k = 0; k < V; k += 2) {
-      s0 = fmaf(x.v[k], x.v[k], s0);
-      s1 = fmaf(x.v[k + 1], x.v[k + 1], s1);
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads;
+      q[j] = i < s.vecs ? reinterpret_cast<const uint4*>(g + s.head)[i] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const FloatV<V> x = load_vec<E, V>(reinterpret_cast<const E*>(&q[j]));
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        s0 = fmaf(x.v[k], x.v[k], s0);
+        s1 = fmaf(x.v[k + 1], x.v[k + 1], s1);
+      }
     }
   }
   return s0 + s1;
 }
 
-__global__ void __launch_bounds__(kThreads) clip_squares_kernel(const __grid_constant__ Batch p,
-                                                                double* partial) {
+template <int MOST>
+__global__ void __launch_bounds__(kThreads)
+    clip_squares_kernel(const __grid_constant__ Batch<MOST> p, double* partial) {
   __shared__ double sh[kThreads / 32];
   double acc = 0.0;
   for (int64_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
     const int k = tensor_of(p, c);
     const int64_t at = (c - p.first[k]) * kChunk;
-    const int64_t n = p.count[k] - at < kChunk ? p.count[k] - at : kChunk;
+    const int n = (int)(p.count[k] - at < kChunk ? p.count[k] - at : kChunk);
     acc += p.dtype[k] == FALCON_BF16
                ? chunk_squares(static_cast<const __nv_bfloat16*>(p.grad[k]) + at, n)
                : chunk_squares(static_cast<const float*>(p.grad[k]) + at, n);
@@ -95,29 +118,41 @@ __global__ void __launch_bounds__(kThreads) clip_squares_kernel(const __grid_con
 }
 
 template <typename E>
-__device__ __forceinline__ void chunk_scale(const E* g, E* o, int64_t n, float c) {
+__device__ __forceinline__ void chunk_scale(const E* g, E* o, int n, float c) {
   constexpr int V = 16 / (int)sizeof(E);
+  // alignments that differ: one element at a time
   const bool same = (reinterpret_cast<uintptr_t>(g) & 15) == (reinterpret_cast<uintptr_t>(o) & 15);
-  int64_t head = (int64_t)((16 - (reinterpret_cast<uintptr_t>(g) & 15)) & 15) / (int)sizeof(E);
-  if (head > n || !same) head = n;  // alignments that differ: one element at a time
-  const int64_t vecs = (n - head) / V, tail = head + vecs * V;
-  for (int64_t i = threadIdx.x; i < head; i += kThreads)
+  const Span s(g, n, (int)sizeof(E), same);
+  for (int i = threadIdx.x; i < s.head; i += kThreads)
     store_vec<E, 1>(o + i, FloatV<1>{{load_vec<E, 1>(g + i).v[0] * c}});
-  for (int64_t i = tail + threadIdx.x; i < n; i += kThreads)
+  for (int i = s.tail + threadIdx.x; i < n; i += kThreads)
     store_vec<E, 1>(o + i, FloatV<1>{{load_vec<E, 1>(g + i).v[0] * c}});
-#pragma unroll 4
-  for (int64_t i = threadIdx.x; i < vecs; i += kThreads) {
-    FloatV<V> x = load_vec<E, V>(g + head + i * V);
+  for (int i0 = threadIdx.x; i0 < s.vecs; i0 += kThreads * kBatch) {
+    uint4 q[kBatch];
 #pragma unroll
-    for (int k = 0; k < V; ++k) x.v[k] *= c;
-    store_vec<E, V>(o + head + i * V, x);
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i < s.vecs) q[j] = __ldcs(reinterpret_cast<const uint4*>(g + s.head) + i);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i < s.vecs) {
+        FloatV<V> x = load_vec<E, V>(reinterpret_cast<const E*>(&q[j]));
+#pragma unroll
+        for (int k = 0; k < V; ++k) x.v[k] *= c;
+        uint4 r;
+        store_vec<E, V>(reinterpret_cast<E*>(&r), x);
+        __stcs(reinterpret_cast<uint4*>(o + s.head) + i, r);  // not read again here
+      }
+    }
   }
 }
 
-__global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ Batch p,
-                                                              const double* partial, int parts,
-                                                              float max_norm, float eps,
-                                                              float* norm) {
+template <int MOST>
+__global__ void __launch_bounds__(kThreads)
+    clip_scale_kernel(const __grid_constant__ Batch<MOST> p, const double* partial, int parts,
+                      float max_norm, float eps, float* norm) {
   __shared__ double sh[kThreads / 32];
   double acc = 0.0;
   for (int i = threadIdx.x; i < parts; i += kThreads) acc += partial[i];
@@ -127,11 +162,12 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
   const float ratio = max_norm / (n + eps);
   const float c = ratio > 1.f ? 1.f : ratio;  // a NaN stays
-  for (int64_t i = blockIdx.x; i < p.chunks; i += gridDim.x) {
+  // from the back: the first pass has left the last chunks in L2
+  for (int64_t i = p.chunks - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
     const int k = tensor_of(p, i);
     if (c == 1.f && p.grad[k] == p.out[k]) continue;
     const int64_t at = (i - p.first[k]) * kChunk;
-    const int64_t m = p.count[k] - at < kChunk ? p.count[k] - at : kChunk;
+    const int m = (int)(p.count[k] - at < kChunk ? p.count[k] - at : kChunk);
     if (p.dtype[k] == FALCON_BF16)
       chunk_scale(static_cast<const __nv_bfloat16*>(p.grad[k]) + at,
                   static_cast<__nv_bfloat16*>(p.out[k]) + at, m, c);
@@ -142,10 +178,11 @@ __global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_const
 }
 
 // Fills p with the next tensors from `at` on; returns the index after them.
-int64_t fill(Batch* p, const falcon_grad* grads, int64_t tensors, int64_t at) {
+template <int MOST>
+int64_t fill(Batch<MOST>* p, const falcon_grad* grads, int64_t tensors, int64_t at) {
   p->tensors = 0;
   p->chunks = 0;
-  for (; at < tensors && p->tensors < kMost; ++at) {
+  for (; at < tensors && p->tensors < MOST; ++at) {
     if (grads[at].count == 0) continue;
     const int k = p->tensors++;
     p->grad[k] = grads[at].grad;
@@ -158,8 +195,31 @@ int64_t fill(Batch* p, const falcon_grad* grads, int64_t tensors, int64_t at) {
   return at;
 }
 
-unsigned blocks_of(const Batch& p) {
-  return (unsigned)(p.chunks < kBlocks ? (p.chunks > 0 ? p.chunks : 1) : kBlocks);
+template <int MOST>
+cudaError_t clip(const falcon_grad* grads, int64_t tensors, float max_norm, float eps, float* norm,
+                 double* partial, cudaStream_t stream) {
+  static thread_local Batch<MOST> p;
+  auto blocks_of = [] { return (unsigned)(p.chunks < 1 ? 1 : p.chunks < kBlocks ? p.chunks : kBlocks); };
+  int parts = 0;
+  int64_t at = 0;
+  do {
+    at = fill(&p, grads, tensors, at);
+    clip_squares_kernel<MOST><<<blocks_of(), kThreads, 0, stream>>>(p, partial + parts);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    parts += (int)blocks_of();
+  } while (at < tensors);
+  const bool again = tensors > MOST;  // otherwise p still holds all of them
+  at = again ? 0 : tensors;
+  do {
+    if (again) at = fill(&p, grads, tensors, at);
+    clip_scale_kernel<MOST><<<blocks_of(), kThreads, 0, stream>>>(p, partial, parts, max_norm, eps,
+                                                                norm);
+    norm = nullptr;
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  } while (at < tensors);
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -170,29 +230,10 @@ size_t clip_workspace_bytes(const falcon_grad*, int64_t tensors) {
 
 cudaError_t launch_clip(const falcon_grad* grads, int64_t tensors, float max_norm, float eps,
                         float* norm, void* ws, cudaStream_t stream) {
-  static thread_local Batch p;
   double* partial = static_cast<double*>(ws);
-  int parts = 0;
-  int64_t at = 0;
-  do {
-    at = fill(&p, grads, tensors, at);
-    const unsigned blocks = blocks_of(p);
-    clip_squares_kernel<<<blocks, kThreads, 0, stream>>>(p, partial + parts);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    parts += (int)blocks;
-  } while (at < tensors);
-  at = 0;
-  bool first = true;
-  do {
-    at = fill(&p, grads, tensors, at);
-    clip_scale_kernel<<<blocks_of(p), kThreads, 0, stream>>>(p, partial, parts, max_norm, eps,
-                                                            first ? norm : nullptr);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    first = false;
-  } while (at < tensors);
-  return cudaSuccess;
+  if (tensors <= kFew)
+    return clip<kFew>(grads, tensors, max_norm, eps, norm, partial, stream);
+  return clip<kMost>(grads, tensors, max_norm, eps, norm, partial, stream);
 }
 
 }  // namespace falcon

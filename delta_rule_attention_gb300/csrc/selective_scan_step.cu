@@ -1,6 +1,5 @@
 // One token of the selective scan for N sequences: the scan's formulas with the
-// state read from and written to a pool.  A group of lanes owns a channel's
-// state, four states (16 bytes) a lane: the step is bound by the state's traffic.
+// state read from and written to a pool.  Bound by the state's traffic.
 
 #include "ssm.cuh"
 
@@ -9,78 +8,93 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// LN lanes of a channel (a power of two); VEC: S is a multiple of four and the
-// state rows are 16-byte aligned.
-template <typename E, int LN, bool VEC>
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanStepArgs a) {
-  const int64_t at = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / LN;
+// LN lanes share two neighbouring channels.  vec_h: S is a multiple of four and
+// the states lie on 16-byte boundaries; vec_ch, vec_bc: channel pairs and quads of B
+// and C are one access.  A lane's loads do not depend on one another (but for the
+// slot), so that its 32 bytes of state and 32 of A are under way together.
+template <typename E, int LN>
+__global__ void __launch_bounds__(kThreads)
+    scan_step_kernel(const __grid_constant__ ScanStepArgs a) {
+  const int pairs = (a.D + 1) / 2;  // of a row
+  const unsigned at = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / LN;
   const int q = threadIdx.x % LN, n0 = q * 4;
-  const bool live = at < a.N * a.D;
-  const int64_t row = live ? at / a.D : 0;
-  const int d = live ? (int)(at - row * a.D) : 0;
+  const bool live = at < (unsigned)(a.N * pairs);
+  const int row = live ? (int)(at / (unsigned)pairs) : 0;
+  const int d = live ? (int)(at - (unsigned)row * (unsigned)pairs) * 2 : 0;
+  const int have = !live ? 0 : d + 1 < a.D ? 2 : 1;
   const int64_t slot = a.slots ? a.slots[row] : row;
   const bool has = live && slot >= 0 && slot < a.pool;
   const bool fresh = a.fresh && a.fresh[row];
-  const int g = d / (a.D / a.G);
+  const int R = a.D / a.G, g0 = d / R, g1 = have == 2 ? (d + 1) / R : g0;
   float* hp = a.h + ((has ? slot : 0) * a.D + d) * a.S + n0;
-  float h[4] = {0.f, 0.f, 0.f, 0.f};
-  if (has && !fresh) {
-    if (VEC) {
-      if (n0 < a.S) {
-        const float4 v = *reinterpret_cast<const float4*>(hp);
-        h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
+  const int own = n0 < a.S ? (a.S - n0 < 4 ? a.S - n0 : 4) : 0;  // states of this lane
+  float4 h[2], A[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int k = c < have ? own : 0;
+    h[c] = load_quad<float>(hp + c * a.S, a.vec_h, has && !fresh ? k : 0);
+    A[c] = load_quad<float>(a.A + (int64_t)(d + c) * a.S + n0, a.vec_A, k);
+  }
+  const E* Bm = static_cast<const E*>(a.Bm) + row * a.bs.batch + n0;
+  const E* Cm = static_cast<const E*>(a.Cm) + row * a.cs.batch + n0;
+  const int kb = live ? own : 0;
+  const float4 B0 = widen(load_quad<E>(Bm + g0 * a.bs.head, a.vec_bc, kb));
+  const float4 C0 = widen(load_quad<E>(Cm + g0 * a.cs.head, a.vec_bc, kb));
+  const float4 B1 = g1 == g0 ? B0 : widen(load_quad<E>(Bm + g1 * a.bs.head, a.vec_bc, kb));
+  const float4 C1 = g1 == g0 ? C0 : widen(load_quad<E>(Cm + g1 * a.cs.head, a.vec_bc, kb));
+  const float2 u = widen(load_pair<E>(static_cast<const E*>(a.u) + row * a.u_stride + d, a.vec_ch, have));
+  float2 s =
+      widen(load_pair<E>(static_cast<const E*>(a.delta) + row * a.delta_stride + d, a.vec_ch, have));
+  float2 z = make_float2(0.f, 0.f);
+  if (a.z) z = widen(load_pair<E>(static_cast<const E*>(a.z) + row * a.z_stride + d, a.vec_ch, have));
+  if (a.delta_bias) {
+    if (have > 0) s.x += a.delta_bias[d];
+    if (have > 1) s.y += a.delta_bias[d + 1];
+  }
+  if (a.softplus) s = softplus2(s);
+  float o[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const float sc = c ? s.y : s.x, v = sc * (c ? u.y : u.x), s2 = sc * kLog2e;
+    const float4 B = c ? B1 : B0, Ct = c ? C1 : C0;
+    h[c].x = fmaf(decay(s2, A[c].x), h[c].x, v * B.x);
+    h[c].y = fmaf(decay(s2, A[c].y), h[c].y, v * B.y);
+    h[c].z = fmaf(decay(s2, A[c].z), h[c].z, v * B.z);
+    h[c].w = fmaf(decay(s2, A[c].w), h[c].w, v * B.w);
+    o[c] = fmaf(Ct.w, h[c].w, fmaf(Ct.z, h[c].z, fmaf(Ct.y, h[c].y, Ct.x * h[c].x)));
+    if (has && c < have) {
+      float* to = hp + c * a.S;
+      if (a.vec_h) {
+        if (own > 0) *reinterpret_cast<float4*>(to) = h[c];
+      } else {
+        const float f[4] = {h[c].x, h[c].y, h[c].z, h[c].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < own) to[i] = f[i];
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n0 + i < a.S) h[i] = hp[i];
-    }
-  }
-  const float ut = load_vec<E, 1>(static_cast<const E*>(a.u) + row * a.u_stride + d).v[0];
-  float s = load_vec<E, 1>(static_cast<const E*>(a.delta) + row * a.delta_stride + d).v[0];
-  if (a.delta_bias) s += a.delta_bias[d];
-  if (a.softplus) s = softplus(s);
-  const E* Bm = static_cast<const E*>(a.Bm) + row * a.bs.batch + g * a.bs.head + n0;
-  const E* Cm = static_cast<const E*>(a.Cm) + row * a.cs.batch + g * a.cs.head + n0;
-  float o = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n0 + i < a.S) {
-      const float A2 = a.A[(int64_t)d * a.S + n0 + i] * kLog2e;
-      h[i] = fmaf(decay(s, A2), h[i], s * ut * load_vec<E, 1>(Bm + i).v[0]);
-      o = fmaf(load_vec<E, 1>(Cm + i).v[0], h[i], o);
-    }
-  }
-  if (has) {
-    if (VEC) {
-      if (n0 < a.S) *reinterpret_cast<float4*>(hp) = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n0 + i < a.S) hp[i] = h[i];
     }
   }
 #pragma unroll
-  for (int k = LN / 2; k > 0; k >>= 1) o += __shfl_xor_sync(0xffffffffu, o, k);
-  if (live && q == 0) {
-    if (a.Dskip) o = fmaf(a.Dskip[d], ut, o);
-    if (a.z) {
-      const float zt = load_vec<E, 1>(static_cast<const E*>(a.z) + row * a.z_stride + d).v[0];
-      o *= zt * sigmoid(zt);
+  for (int k = LN / 2; k > 0; k >>= 1) {
+    o[0] += __shfl_xor_sync(0xffffffffu, o[0], k);
+    o[1] += __shfl_xor_sync(0xffffffffu, o[1], k);
+  }
+  if (q == 0) {
+    if (a.Dskip) {
+      if (have > 0) o[0] = fmaf(a.Dskip[d], u.x, o[0]);
+      if (have > 1) o[1] = fmaf(a.Dskip[d + 1], u.y, o[1]);
     }
-    store_vec<E, 1>(static_cast<E*>(a.y) + row * a.D + d, FloatV<1>{{has ? o : 0.f}});
+    if (a.z) o[0] *= z.x * sigmoid(z.x), o[1] *= z.y * sigmoid(z.y);
+    store_pair<E>(static_cast<E*>(a.y) + (int64_t)row * a.D + d, a.vec_ch, have,
+                  has ? make_float2(o[0], o[1]) : make_float2(0.f, 0.f));
   }
 }
 
 template <typename E, int LN>
 cudaError_t step_lanes(const ScanStepArgs& a, cudaStream_t stream) {
-  const int64_t blocks = (a.N * a.D * LN + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const bool vec = a.S % 4 == 0 && reinterpret_cast<uintptr_t>(a.h) % 16 == 0;
-  if (vec)
-    scan_step_kernel<E, LN, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-  else
-    scan_step_kernel<E, LN, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  const int64_t blocks = (a.N * ((a.D + 1) / 2) * LN + kThreads - 1) / kThreads;
+  if (blocks > 0xffffffffLL / kThreads) return cudaErrorInvalidValue;
+  scan_step_kernel<E, LN><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -96,7 +110,17 @@ cudaError_t step_typed(const ScanStepArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream) {
+cudaError_t launch_scan_step(const ScanStepArgs& in, cudaStream_t stream) {
+  ScanStepArgs a = in;
+  const int esz = a.dtype == FALCON_BF16 ? 2 : 4;
+  auto on = [](const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+  a.vec_h = a.S % 4 == 0 && on(a.h, 16);
+  a.vec_A = a.S % 4 == 0 && on(a.A, 16);
+  a.vec_ch = a.D % 2 == 0 && a.u_stride % 2 == 0 && a.delta_stride % 2 == 0 &&
+             (!a.z || a.z_stride % 2 == 0) && on(a.u, 2 * esz) && on(a.delta, 2 * esz) &&
+             on(a.z, 2 * esz) && on(a.y, 2 * esz);
+  a.vec_bc = a.S % 4 == 0 && on(a.Bm, 4 * esz) && on(a.Cm, 4 * esz) && a.bs.batch % 4 == 0 &&
+             a.cs.batch % 4 == 0 && a.bs.head % 4 == 0 && a.cs.head % 4 == 0;
   return a.dtype == FALCON_BF16 ? step_typed<__nv_bfloat16>(a, stream)
                                 : step_typed<float>(a, stream);
 }

@@ -4,9 +4,11 @@
 //   dp_t = dy_t act'(p_t),  dx_t = sum_j w_j dp_{t+W-1-j},
 //   dw_j = sum_t dp_t x_{t-W+1+j},  dbias = sum_t dp_t
 //
-// A thread owns V neighbouring channels (one access of up to 16 bytes) and
-// walks a run of tokens with the last W inputs in registers, so each input is
-// read from memory once and W - 1 times more at a run's edge, from cache.
+// Bound by memory traffic.  A thread owns V neighbouring channels (one access of
+// up to 16 bytes) and a run of tokens; all rows of the run, with the W - 1 before
+// it (and after it, for the gradient), are loaded before the first is used, so
+// that the traffic does not wait for the arithmetic.  A run's edge rows are read
+// twice, the second time from cache.
 
 #include <type_traits>
 
@@ -17,10 +19,16 @@ namespace {
 
 constexpr int kThreads = 128;
 
+// a / b; a 64-bit division costs many times a 32-bit one.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((uint64_t)(a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // Offset of channel c of row (b, t): channels are grouped in heads of m.
 __device__ __forceinline__ int64_t row_offset(const falcon_strides& s, int64_t b, int64_t c,
                                               int m) {
-  const int64_t h = c / m;
+  const int64_t h = quotient(c, m);
   return b * s.batch + h * s.head + (c - h * m);
 }
 
@@ -47,133 +55,193 @@ struct Filter {
   float bias[V];
 };
 
+// vec: the filters of V channels lie on a 16-byte boundary.
 template <int V, int W>
 __device__ __forceinline__ Filter<V, W> load_filter(const float* weight, const float* bias,
-                                                    int64_t c) {
+                                                    int64_t c, bool vec) {
   Filter<V, W> f;
+  if (vec && V % 4 == 0) {
+    float4 v[V * W / 4 > 0 ? V * W / 4 : 1];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V * W / 4; ++i) v[i] = reinterpret_cast<const float4*>(weight + c * W)[i];
 #pragma unroll
-    for (int j = 0; j < W; ++j) f.w[j][i] = weight[(c + i) * W + j];
-    f.bias[i] = bias ? bias[c + i] : 0.f;
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const float4 q = v[(i * W + j) / 4];
+        const int k = (i * W + j) % 4;
+        f.w[j][i] = k == 0 ? q.x : k == 1 ? q.y : k == 2 ? q.z : q.w;
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) f.w[j][i] = weight[(c + i) * W + j];
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) f.bias[i] = bias ? bias[c + i] : 0.f;
   return f;
 }
 
+// V elements as they lie in memory.
+template <typename E, int V>
+struct alignas(V * sizeof(E)) Row {
+  E e[V];
+};
+template <typename E, int V>
+__device__ __forceinline__ FloatV<V> open_row(const Row<E, V>& r) {
+  return load_vec<E, V>(r.e);
+}
+
+constexpr int kFwdRun = 8;
+
+// One thread for V channels and a run; a row's last run + 1 writes state_out.
 template <typename E, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int run, int64_t nruns) {
-  const int64_t c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * V;
-  if (c >= a.C) return;
-  for (int64_t job = blockIdx.y; job < a.B * (nruns + 1); job += gridDim.y) {
-    const int64_t b = job / (nruns + 1), r = job - b * (nruns + 1);
-    const int64_t n = row_length(a.lengths, b, a.T);
-    const E* x = static_cast<const E*>(a.x) + row_offset(a.xs, b, c, a.m);
-    const E* state = static_cast<const E*>(a.state);
-    if (r == nruns) {  // the row's last W - 1 inputs
-      if (!a.state_out) continue;
+__global__ void __launch_bounds__(kThreads)
+    conv_fwd_kernel(const __grid_constant__ ConvArgs a, int64_t nruns) {
+  typedef Row<E, V> R;
+  const int64_t nvec = a.C / V, id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (id >= nvec * a.B * (nruns + 1)) return;
+  const int64_t job = quotient(id, nvec), c = (id - job * nvec) * V;
+  const int64_t b = quotient(job, nruns + 1), r = job - b * (nruns + 1);
+  const int64_t n = row_length(a.lengths, b, a.T);
+  const E* x = static_cast<const E*>(a.x) + row_offset(a.xs, b, c, a.m);
+  const E* state = static_cast<const E*>(a.state);
+  if (r == nruns) {  // the row's last W - 1 inputs
+    if (!a.state_out) return;
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-        store_vec<E, V>(static_cast<E*>(a.state_out) + (b * (W - 1) + j) * a.C + c,
-                        input_at<E, V, W>(x, a.xs.time, state, b, a.C, c, n - (W - 1) + j));
-      continue;
+    for (int j = 0; j < W - 1; ++j)
+      store_vec<E, V>(static_cast<E*>(a.state_out) + (b * (W - 1) + j) * a.C + c,
+                      input_at<E, V, W>(x, a.xs.time, state, b, a.C, c, n - (W - 1) + j));
+    return;
+  }
+  const int64_t t0 = r * kFwdRun;
+  E* y = static_cast<E*>(a.y) + row_offset(a.ys, b, c, a.m);
+  if (t0 >= n) {
+    for (int64_t t = t0; t < t0 + kFwdRun && t < a.T; ++t)
+      store_vec<E, V>(y + t * a.ys.time, zeros<V>());
+    return;
+  }
+  R rows[kFwdRun + W - 1];
+#pragma unroll
+  for (int k = 0; k < kFwdRun + W - 1; ++k) {
+    const int64_t t = t0 + k - (W - 1);
+    rows[k] = R();
+    if (t >= 0) {
+      if (t < n) rows[k] = *reinterpret_cast<const R*>(x + t * a.xs.time);
+    } else if (state) {
+      rows[k] = *reinterpret_cast<const R*>(state + (b * (W - 1) + (t + W - 1)) * a.C + c);
     }
-    const int64_t t0 = r * run, t1 = t0 + run < a.T ? t0 + run : a.T;
-    const int64_t te = t1 < n ? t1 : n;
-    E* y = static_cast<E*>(a.y) + row_offset(a.ys, b, c, a.m);
-    if (t0 < te) {
-      const Filter<V, W> f = load_filter<V, W>(a.weight, a.bias, c);
-      FloatV<V> win[W];
+  }
+  const Filter<V, W> f = load_filter<V, W>(a.weight, a.bias, c, a.vec_w);
+  FloatV<V> win[W];
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-        win[j] = input_at<E, V, W>(x, a.xs.time, state, b, a.C, c, t0 - (W - 1) + j);
-#pragma unroll 4
-      for (int64_t t = t0; t < te; ++t) {
-        win[W - 1] = load_vec<E, V>(x + t * a.xs.time);
-        FloatV<V> o;
+  for (int j = 0; j < W - 1; ++j) win[j] = open_row<E, V>(rows[j]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float p = f.bias[i];
+  for (int k = 0; k < kFwdRun; ++k) {
+    const int64_t t = t0 + k;
+    win[W - 1] = open_row<E, V>(rows[k + W - 1]);
+    FloatV<V> o;
 #pragma unroll
-          for (int j = 0; j < W; ++j) p = fmaf(f.w[j][i], win[j].v[i], p);
-          o.v[i] = SILU ? p * sigmoid(p) : p;
-        }
-        store_vec<E, V>(y + t * a.ys.time, o);
+    for (int i = 0; i < V; ++i) {
+      float p = f.bias[i];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
-      }
+      for (int j = 0; j < W; ++j) p = fmaf(f.w[j][i], win[j].v[i], p);
+      o.v[i] = SILU ? p * sigmoid(p) : p;
     }
-    for (int64_t t = te > t0 ? te : t0; t < t1; ++t) store_vec<E, V>(y + t * a.ys.time, zeros<V>());
+    if (t < a.T) store_vec<E, V>(y + t * a.ys.time, t < n ? o : zeros<V>());
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
   }
 }
 
+constexpr int kBwdRun = 8;
+
 // Gradient: dp of the run's tokens and of the W - 1 after it (recomputed from
-// x), each dp_t adding w_j dp_t to dx_{t-W+1+j}.  A block walks every
-// gridDim.y-th run with its sums of dw and dbias in registers and writes them
-// once; conv_sum_kernel adds the blocks' sums in their order.
+// x), each dp_t adding w_j dp_t to dx_{t-W+1+j}.  A thread walks every `parts`-th
+// run of its channels with its sums of dw and dbias in registers and writes them
+// once; conv_sum_kernel adds the parts in their order.
 template <typename E, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a, int run, int64_t nruns) {
-  const int64_t c = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * V;
-  if (c >= a.C) return;
-  const Filter<V, W> f = load_filter<V, W>(a.weight, a.bias, c);
+__global__ void __launch_bounds__(kThreads, V == 1 ? 4 : sizeof(E) == 2 ? 3 : 2)
+    conv_bwd_kernel(const __grid_constant__ ConvArgs a, int64_t nruns, int parts) {
+  typedef Row<E, V> R;
+  const int64_t nvec = a.C / V, id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (id >= nvec * parts) return;
+  const int64_t part = quotient(id, nvec), c = (id - part * nvec) * V;
+  const Filter<V, W> f = load_filter<V, W>(a.weight, a.bias, c, a.vec_w);
   float dw[W][V] = {}, db[V] = {};
-  for (int64_t job = blockIdx.y; job < a.B * nruns; job += gridDim.y) {
-    const int64_t b = job / nruns, r = job - b * nruns;
+  for (int64_t job = part; job < a.B * nruns; job += parts) {
+    const int64_t b = quotient(job, nruns), r = job - b * nruns;
     const int64_t n = row_length(a.lengths, b, a.T);
     const E* x = static_cast<const E*>(a.x) + row_offset(a.xs, b, c, a.m);
     const E* dy = static_cast<const E*>(a.dy) + row_offset(a.dys, b, c, a.m);
     E* dx = static_cast<E*>(a.dx) + row_offset(a.dxs, b, c, a.m);
     const E* state = static_cast<const E*>(a.state);
     const E* dso = static_cast<const E*>(a.dstate_out);
-    const int64_t t0 = r * run, t1 = t0 + run < a.T ? t0 + run : a.T;
+    const int64_t t0 = r * kBwdRun, t1 = t0 + kBwdRun < a.T ? t0 + kBwdRun : a.T;
+    R xr[kBwdRun + 2 * (W - 1)], gr[kBwdRun + W - 1];
+#pragma unroll
+    for (int k = 0; k < kBwdRun + 2 * (W - 1); ++k) {
+      const int64_t t = t0 + k - (W - 1);
+      xr[k] = R();
+      if (t >= 0) {
+        if (t < n) xr[k] = *reinterpret_cast<const R*>(x + t * a.xs.time);
+      } else if (state) {
+        xr[k] = *reinterpret_cast<const R*>(state + (b * (W - 1) + (t + W - 1)) * a.C + c);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBwdRun + W - 1; ++k) {
+      gr[k] = R();
+      if (t0 + k < n) gr[k] = *reinterpret_cast<const R*>(dy + (t0 + k) * a.dys.time);
+    }
     // acc[j] gathers the gradient of input t - W + 1 + j
     FloatV<V> win[W], acc[W];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-      win[j] = input_at<E, V, W>(x, a.xs.time, state, b, a.C, c, t0 - (W - 1) + j);
+      win[j] = open_row<E, V>(xr[j]);
       acc[j] = zeros<V>();
     }
-    // gradient of an input: stored where the input is this run's own; the
-    // first run also stores those of the carried inputs
-    auto finish = [&](int64_t s, FloatV<V> g) {
-      if (s >= t1 || (s < t0 && s >= 0) || (s < 0 && t0 > 0)) return;
-      const int64_t k = s - (n - (W - 1));  // its place in state_out
-      if (dso && k >= 0 && s < n) {
-        const FloatV<V> d = load_vec<E, V>(dso + (b * (W - 1) + k) * a.C + c);
 #pragma unroll
-        for (int i = 0; i < V; ++i) g.v[i] += d.v[i];
-      }
-      if (s >= 0)
-        store_vec<E, V>(dx + s * a.dxs.time, g);
-      else if (a.dstate)
-        store_vec<E, V>(static_cast<E*>(a.dstate) + (b * (W - 1) + s + W - 1) * a.C + c, g);
-    };
-    const int64_t last = t1 + W - 1;
-#pragma unroll 2
-    for (int64_t t = t0; t < last; ++t) {
+    for (int k = 0; k < kBwdRun + W - 1; ++k) {
+      const int64_t t = t0 + k;
       acc[W - 1] = zeros<V>();
-      win[W - 1] = zeros<V>();
-      if (t < n) {
-        win[W - 1] = load_vec<E, V>(x + t * a.xs.time);
-        FloatV<V> d = load_vec<E, V>(dy + t * a.dys.time);
+      win[W - 1] = open_row<E, V>(xr[k + W - 1]);
+      const FloatV<V> g = open_row<E, V>(gr[k]);  // zero where there is no token
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (SILU) {
-            float p = f.bias[i];
+      for (int i = 0; i < V; ++i) {
+        float d = g.v[i];
+        if (SILU && t < n) {
+          float p = f.bias[i];
 #pragma unroll
-            for (int j = 0; j < W; ++j) p = fmaf(f.w[j][i], win[j].v[i], p);
-            const float s = sigmoid(p);
-            d.v[i] *= s * fmaf(p, 1.f - s, 1.f);
-          }
+          for (int j = 0; j < W; ++j) p = fmaf(f.w[j][i], win[j].v[i], p);
+          const float s = sigmoid(p);
+          d *= s * fmaf(p, 1.f - s, 1.f);
+        }
 #pragma unroll
-          for (int j = 0; j < W; ++j) acc[j].v[i] = fmaf(f.w[j][i], d.v[i], acc[j].v[i]);
-          if (t < t1) {
-            db[i] += d.v[i];
+        for (int j = 0; j < W; ++j) acc[j].v[i] = fmaf(f.w[j][i], d, acc[j].v[i]);
+        if (k < kBwdRun) {
+          db[i] += d;
 #pragma unroll
-            for (int j = 0; j < W; ++j) dw[j][i] = fmaf(d.v[i], win[j].v[i], dw[j][i]);
-          }
+          for (int j = 0; j < W; ++j) dw[j][i] = fmaf(d, win[j].v[i], dw[j][i]);
         }
       }
-      finish(t - (W - 1), acc[0]);
+      // input s has met its last token: stored where it is this run's own; the
+      // first run also stores the carried inputs' gradients
+      const int64_t s = t - (W - 1);
+      if (k >= W - 1 ? s < t1 : t0 == 0) {
+        FloatV<V> o = acc[0];
+        const int64_t at = s - (n - (W - 1));  // its place in state_out
+        if (dso && at >= 0 && s < n) {
+          const FloatV<V> e = load_vec<E, V>(dso + (b * (W - 1) + at) * a.C + c);
+#pragma unroll
+          for (int i = 0; i < V; ++i) o.v[i] += e.v[i];
+        }
+        if (s >= 0)
+          store_vec<E, V>(dx + s * a.dxs.time, o);
+        else if (a.dstate)
+          store_vec<E, V>(static_cast<E*>(a.dstate) + (b * (W - 1) + s + W - 1) * a.C + c, o);
+      }
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) {
         win[j] = win[j + 1];
@@ -181,22 +249,31 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvArgs a, int run,
       }
     }
   }
-  float* ws = a.ws + (int64_t)blockIdx.y * (W + 1) * a.C;
+  float* ws = a.ws + part * (W + 1) * a.C;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
+  for (int j = 0; j <= W; ++j)
 #pragma unroll
-    for (int j = 0; j < W; ++j) ws[j * a.C + c + i] = dw[j][i];
-    ws[W * a.C + c + i] = db[i];
-  }
+    for (int i = 0; i < V; ++i) ws[j * a.C + c + i] = j < W ? dw[j < W ? j : 0][i] : db[i];
 }
 
-__global__ void conv_sum_kernel(const float* ws, int parts, int64_t C, int W, float* dweight,
-                                float* dbias) {
-  const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int j = blockIdx.y;
-  if (c >= C) return;
+// Sums of the parts: a warp's lanes hold neighbouring channels, a block's eight
+// warps an eighth of the parts each.
+__global__ void __launch_bounds__(256)
+    conv_sum_kernel(const float* ws, int parts, int64_t C, int W, float* dweight, float* dbias) {
+  __shared__ float sh[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.y;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.f;
-  for (int p = 0; p < parts; ++p) s += ws[((int64_t)p * (W + 1) + j) * C + c];
+  if (c < C) {
+#pragma unroll 8
+    for (int p = warp; p < parts; p += 8) s += ws[((int64_t)p * (W + 1) + j) * C + c];
+  }
+  sh[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || c >= C) return;
+  s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) s += sh[w][lane];
   if (j < W)
     dweight[c * W + j] = s;
   else if (dbias)
@@ -204,11 +281,12 @@ __global__ void conv_sum_kernel(const float* ws, int parts, int64_t C, int W, fl
 }
 
 template <typename E, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a) {
+__global__ void __launch_bounds__(kThreads)
+    conv_step_kernel(const __grid_constant__ ConvStepArgs a) {
   const int64_t per_row = (a.C + V - 1) / V;
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= a.N * per_row) return;
-  const int64_t row = i / per_row, c = (i - row * per_row) * V;
+  const int64_t row = quotient(i, per_row), c = (i - row * per_row) * V;
   const int64_t slot = a.slots ? a.slots[row] : row;
   E* y = static_cast<E*>(a.y) + row * a.C + c;
   if (slot < 0 || slot >= a.pool) {
@@ -217,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a) {
   }
   const bool fresh = a.fresh && a.fresh[row];
   E* st = static_cast<E*>(a.state) + slot * (W - 1) * a.C + c;
-  const Filter<V, W> f = load_filter<V, W>(a.weight, a.bias, c);
+  const Filter<V, W> f = load_filter<V, W>(a.weight, a.bias, c, a.vec_w);
   FloatV<V> win[W], o;
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) win[j] = fresh ? zeros<V>() : load_vec<E, V>(st + j * a.C);
@@ -256,38 +334,37 @@ cudaError_t with_width(int width, int act, F&& f) {
 
 template <typename E, int V>
 cudaError_t fwd_typed(const ConvArgs& a, cudaStream_t stream) {
-  const int run = 16;
-  const int64_t nruns = (a.T + run - 1) / run;
-  const int64_t cblocks = (a.C + (int64_t)kThreads * V - 1) / ((int64_t)kThreads * V);
-  const int64_t jobs = a.B * (nruns + 1);
-  const dim3 grid((unsigned)cblocks, (unsigned)(jobs < 65535 ? jobs : 65535));
+  const int64_t nruns = (a.T + kFwdRun - 1) / kFwdRun;
+  const int64_t blocks = (a.C / V * a.B * (nruns + 1) + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   return with_width(a.width, a.act, [&](auto w, auto silu) {
     conv_fwd_kernel<E, V, decltype(w)::value, decltype(silu)::value>
-        <<<grid, kThreads, 0, stream>>>(a, run, nruns);
+        <<<(unsigned)blocks, kThreads, 0, stream>>>(a, nruns);
     return cudaGetLastError();
   });
 }
 
-constexpr int kBwdRun = 32;
-// Blocks along (row, run): each leaves one set of sums.
-int bwd_parts(int64_t B, int64_t T) {
+// Parts of the sums: enough threads (of four channels) to fill the GPU, each
+// with as many runs as that leaves.
+int bwd_parts(int64_t B, int64_t T, int64_t C) {
   const int64_t jobs = B * ((T + kBwdRun - 1) / kBwdRun);
-  return (int)(jobs < 256 ? jobs : 256);
+  const int64_t fill = (152 * 1024 + (C + 3) / 4 - 1) / ((C + 3) / 4);
+  return (int)(jobs < fill ? jobs : fill);
 }
 
 template <typename E, int V>
 cudaError_t bwd_typed(const ConvArgs& a, cudaStream_t stream) {
   const int64_t nruns = (a.T + kBwdRun - 1) / kBwdRun;
-  const int64_t cblocks = (a.C + (int64_t)kThreads * V - 1) / ((int64_t)kThreads * V);
-  const int parts = bwd_parts(a.B, a.T);
-  const dim3 grid((unsigned)cblocks, (unsigned)parts);
+  const int parts = bwd_parts(a.B, a.T, a.C);
+  const int64_t blocks = (a.C / V * parts + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   return with_width(a.width, a.act, [&](auto w, auto silu) {
     constexpr int W = decltype(w)::value;
-    conv_bwd_kernel<E, V, W, decltype(silu)::value><<<grid, kThreads, 0, stream>>>(a, kBwdRun,
-                                                                                nruns);
+    conv_bwd_kernel<E, V, W, decltype(silu)::value>
+        <<<(unsigned)blocks, kThreads, 0, stream>>>(a, nruns, parts);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    conv_sum_kernel<<<dim3((unsigned)((a.C + 127) / 128), W + 1), 128, 0, stream>>>(
+    conv_sum_kernel<<<dim3((unsigned)((a.C + 31) / 32), W + 1), 256, 0, stream>>>(
         a.ws, parts, a.C, W, a.dweight, a.dbias);
     return cudaGetLastError();
   });
@@ -307,10 +384,12 @@ cudaError_t step_typed(const ConvStepArgs& a, cudaStream_t stream) {
 
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C, int width) {
   if (B == 0 || T == 0 || C == 0) return 0;
-  return sizeof(float) * (size_t)bwd_parts(B, T) * (size_t)(width + 1) * (size_t)C;
+  return sizeof(float) * (size_t)bwd_parts(B, T, C) * (size_t)(width + 1) * (size_t)C;
 }
 
-cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t stream) {
+cudaError_t launch_conv_fwd(const ConvArgs& in, cudaStream_t stream) {
+  ConvArgs a = in;
+  a.vec_w = fits(a.weight, 16);
   const int esz = a.dtype == FALCON_BF16 ? 2 : 4;
   const int v = 16 / esz;
   const bool vec = a.m % v == 0 && fits(a.x, 16) && fits(a.y, 16) && fits(a.state, 16) &&
@@ -320,7 +399,9 @@ cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t stream) {
   return vec ? fwd_typed<float, 4>(a, stream) : fwd_typed<float, 1>(a, stream);
 }
 
-cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t stream) {
+cudaError_t launch_conv_bwd(const ConvArgs& in, cudaStream_t stream) {
+  ConvArgs a = in;
+  a.vec_w = fits(a.weight, 16);
   const int esz = a.dtype == FALCON_BF16 ? 2 : 4;
   const int64_t tail = a.B * (a.width - 1) * a.C;
   if (a.T == 0) {  // no token: dweight = dbias = 0, dstate = dstate_out
@@ -341,12 +422,16 @@ cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t stream) {
   return vec ? bwd_typed<float, 4>(a, stream) : bwd_typed<float, 1>(a, stream);
 }
 
-cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t stream) {
-  const int v = a.dtype == FALCON_BF16 ? 8 : 4;
-  const bool vec = a.C % v == 0 && a.x_stride % v == 0 && fits(a.x, 16) && fits(a.state, 16) &&
-                   fits(a.y, 16);
+cudaError_t launch_conv_step(const ConvStepArgs& in, cudaStream_t stream) {
+  // four channels a thread for either type: the call is short, and more threads
+  // with fewer loads each end sooner
+  ConvStepArgs a = in;
+  a.vec_w = fits(a.weight, 16);
+  const int bytes = a.dtype == FALCON_BF16 ? 8 : 16;
+  const bool vec = a.C % 4 == 0 && a.x_stride % 4 == 0 && fits(a.x, bytes) &&
+                   fits(a.state, bytes) && fits(a.y, bytes);
   if (a.dtype == FALCON_BF16)
-    return vec ? step_typed<__nv_bfloat16, 8>(a, stream) : step_typed<__nv_bfloat16, 1>(a, stream);
+    return vec ? step_typed<__nv_bfloat16, 4>(a, stream) : step_typed<__nv_bfloat16, 1>(a, stream);
   return vec ? step_typed<float, 4>(a, stream) : step_typed<float, 1>(a, stream);
 }
 

@@ -244,6 +244,7 @@ struct ConvArgs {
   void *y, *state_out, *dx, *dstate;
   float *dweight, *dbias;
   float* ws;
+  bool vec_w;  // weight is 16-byte aligned
 };
 cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t stream);
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C, int width);
@@ -258,6 +259,7 @@ struct ConvStepArgs {
   const int32_t* slots;
   const uint8_t* fresh;
   void* y;
+  bool vec_w;
 };
 cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t stream);
 
@@ -293,6 +295,7 @@ struct ScanStepArgs {
   const int32_t* slots;
   const uint8_t* fresh;
   void* y;
+  bool vec_h, vec_A, vec_ch, vec_bc;  // aligned quads and pairs
 };
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream);
 
