@@ -16,7 +16,14 @@ namespace {
 constexpr int kMost = 512;        // tensors of one launch
 constexpr int kFew = 64;          // of a launch with short arguments
 constexpr int kThreads = 256;
-constexpr int kChunk = 8192;      // elements a block takes at a time
+// Elements a block takes at a time: many of a large set, where finding a chunk's
+// tensor should cost little beside it, few of a small one, where all blocks
+// should have some.
+constexpr int kChunkMost = 32768, kChunkLeast = 4096;
+constexpr int64_t kLarge = 152LL * 4 * kChunkMost;
+// Bytes read last in the first pass that the second finds in L2 (of 126 MB, each
+// half of which may hold its own copy); what comes before is marked as passing.
+constexpr int64_t kStays = 40LL << 20;
 constexpr int kBlocks = 152 * 8;  // of one launch
 
 template <int MOST>
@@ -26,8 +33,8 @@ struct Batch {
   int64_t count[MOST];
   int64_t first[MOST];  // chunks before this tensor's
   unsigned char dtype[MOST];
-  int tensors;
-  int64_t chunks;
+  int tensors, chunk;
+  int64_t chunks, passing;  // chunks of the batch, those not to be kept in L2
 };
 
 template <int MOST>
@@ -64,10 +71,10 @@ struct Span {
     tail = head + vecs * (16 / esz);
   }
 };
-constexpr int kBatch = 4;  // vectors of a thread under way at a time
+constexpr int kBatch = 8;  // vectors of a thread under way at a time
 
 template <typename E>
-__device__ __forceinline__ float chunk_squares(const E* g, int n) {
+__device__ __forceinline__ float chunk_squares(const E* g, int n, bool passing) {
   constexpr int V = 16 / (int)sizeof(E);
   const Span s(g, n, (int)sizeof(E), true);
   float s0 = 0.f, s1 = 0.f;
@@ -84,7 +91,9 @@ __device__ __forceinline__ float chunk_squares(const E* g, int n) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int i = i0 + j * kThreads;
-      q[j] = i < s.vecs ? reinterpret_cast<const uint4*>(g + s.head)[i] : make_uint4(0, 0, 0, 0);
+      const uint4* from = reinterpret_cast<const uint4*>(g + s.head) + i;
+      q[j] = make_uint4(0, 0, 0, 0);
+      if (i < s.vecs) q[j] = passing ? __ldcs(from) : *from;
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -106,11 +115,11 @@ __global__ void __launch_bounds__(kThreads)
   double acc = 0.0;
   for (int64_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
     const int k = tensor_of(p, c);
-    const int64_t at = (c - p.first[k]) * kChunk;
-    const int n = (int)(p.count[k] - at < kChunk ? p.count[k] - at : kChunk);
+    const int64_t at = (c - p.first[k]) * p.chunk;
+    const int n = (int)(p.count[k] - at < p.chunk ? p.count[k] - at : p.chunk);
     acc += p.dtype[k] == FALCON_BF16
-               ? chunk_squares(static_cast<const __nv_bfloat16*>(p.grad[k]) + at, n)
-               : chunk_squares(static_cast<const float*>(p.grad[k]) + at, n);
+               ? chunk_squares(static_cast<const __nv_bfloat16*>(p.grad[k]) + at, n, c < p.passing)
+               : chunk_squares(static_cast<const float*>(p.grad[k]) + at, n, c < p.passing);
   }
   double total;
   block_sum_f64(acc, sh, &total);
@@ -166,8 +175,8 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t i = p.chunks - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
     const int k = tensor_of(p, i);
     if (c == 1.f && p.grad[k] == p.out[k]) continue;
-    const int64_t at = (i - p.first[k]) * kChunk;
-    const int m = (int)(p.count[k] - at < kChunk ? p.count[k] - at : kChunk);
+    const int64_t at = (i - p.first[k]) * p.chunk;
+    const int m = (int)(p.count[k] - at < p.chunk ? p.count[k] - at : p.chunk);
     if (p.dtype[k] == FALCON_BF16)
       chunk_scale(static_cast<const __nv_bfloat16*>(p.grad[k]) + at,
                   static_cast<__nv_bfloat16*>(p.out[k]) + at, m, c);
@@ -179,9 +188,11 @@ __global__ void __launch_bounds__(kThreads)
 
 // Fills p with the next tensors from `at` on; returns the index after them.
 template <int MOST>
-int64_t fill(Batch<MOST>* p, const falcon_grad* grads, int64_t tensors, int64_t at) {
+int64_t fill(Batch<MOST>* p, const falcon_grad* grads, int64_t tensors, int64_t at, int chunk) {
   p->tensors = 0;
+  p->chunk = chunk;
   p->chunks = 0;
+  int64_t bytes = 0;
   for (; at < tensors && p->tensors < MOST; ++at) {
     if (grads[at].count == 0) continue;
     const int k = p->tensors++;
@@ -190,8 +201,10 @@ int64_t fill(Batch<MOST>* p, const falcon_grad* grads, int64_t tensors, int64_t 
     p->count[k] = grads[at].count;
     p->dtype[k] = (unsigned char)grads[at].dtype;
     p->first[k] = p->chunks;
-    p->chunks += (grads[at].count + kChunk - 1) / kChunk;
+    p->chunks += (grads[at].count + chunk - 1) / chunk;
+    bytes += grads[at].count * (grads[at].dtype == FALCON_BF16 ? 2 : 4);
   }
+  p->passing = bytes > kStays ? (int64_t)((double)(bytes - kStays) / bytes * p->chunks) : 0;
   return at;
 }
 
@@ -200,10 +213,13 @@ cudaError_t clip(const falcon_grad* grads, int64_t tensors, float max_norm, floa
                  double* partial, cudaStream_t stream) {
   static thread_local Batch<MOST> p;
   auto blocks_of = [] { return (unsigned)(p.chunks < 1 ? 1 : p.chunks < kBlocks ? p.chunks : kBlocks); };
+  int64_t all = 0;
+  for (int64_t i = 0; i < tensors; ++i) all += grads[i].count;
+  const int chunk = all >= kLarge ? kChunkMost : kChunkLeast;
   int parts = 0;
   int64_t at = 0;
   do {
-    at = fill(&p, grads, tensors, at);
+    at = fill(&p, grads, tensors, at, chunk);
     clip_squares_kernel<MOST><<<blocks_of(), kThreads, 0, stream>>>(p, partial + parts);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -212,7 +228,7 @@ cudaError_t clip(const falcon_grad* grads, int64_t tensors, float max_norm, floa
   const bool again = tensors > MOST;  // otherwise p still holds all of them
   at = again ? 0 : tensors;
   do {
-    if (again) at = fill(&p, grads, tensors, at);
+    if (again) at = fill(&p, grads, tensors, at, chunk);
     clip_scale_kernel<MOST><<<blocks_of(), kThreads, 0, stream>>>(p, partial, parts, max_norm, eps,
                                                                 norm);
     norm = nullptr;

@@ -12,41 +12,45 @@ constexpr int kThreads = 256;
 // the states lie on 16-byte boundaries; vec_ch, vec_bc: channel pairs and quads of B
 // and C are one access.  A lane's loads do not depend on one another (but for the
 // slot), so that its 32 bytes of state and 32 of A are under way together.
-template <typename E, int LN>
+// WHOLE: all of these hold, S = 4 LN and no pair spans two groups.
+template <typename E, int LN, bool WHOLE>
 __global__ void __launch_bounds__(kThreads)
     scan_step_kernel(const __grid_constant__ ScanStepArgs a) {
+  const bool vec_h = WHOLE || a.vec_h, vec_A = WHOLE || a.vec_A, vec_ch = WHOLE || a.vec_ch,
+             vec_bc = WHOLE || a.vec_bc;
   const int pairs = (a.D + 1) / 2;  // of a row
   const unsigned at = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / LN;
   const int q = threadIdx.x % LN, n0 = q * 4;
   const bool live = at < (unsigned)(a.N * pairs);
   const int row = live ? (int)(at / (unsigned)pairs) : 0;
   const int d = live ? (int)(at - (unsigned)row * (unsigned)pairs) * 2 : 0;
-  const int have = !live ? 0 : d + 1 < a.D ? 2 : 1;
+  const int have = WHOLE ? 2 : !live ? 0 : d + 1 < a.D ? 2 : 1;  // WHOLE: surplus lanes read row 0
   const int64_t slot = a.slots ? a.slots[row] : row;
   const bool has = live && slot >= 0 && slot < a.pool;
   const bool fresh = a.fresh && a.fresh[row];
-  const int R = a.D / a.G, g0 = d / R, g1 = have == 2 ? (d + 1) / R : g0;
+  const int R = a.D / a.G, g0 = d / R, g1 = !WHOLE && have == 2 ? (d + 1) / R : g0;
   float* hp = a.h + ((has ? slot : 0) * a.D + d) * a.S + n0;
-  const int own = n0 < a.S ? (a.S - n0 < 4 ? a.S - n0 : 4) : 0;  // states of this lane
+  // states of this lane
+  const int own = WHOLE ? 4 : n0 < a.S ? (a.S - n0 < 4 ? a.S - n0 : 4) : 0;
   float4 h[2], A[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int k = c < have ? own : 0;
-    h[c] = load_quad<float>(hp + c * a.S, a.vec_h, has && !fresh ? k : 0);
-    A[c] = load_quad<float>(a.A + (int64_t)(d + c) * a.S + n0, a.vec_A, k);
+    h[c] = load_quad<float>(hp + c * a.S, vec_h, has && !fresh ? k : 0);
+    A[c] = load_quad<float>(a.A + (int64_t)(d + c) * a.S + n0, vec_A, k);
   }
   const E* Bm = static_cast<const E*>(a.Bm) + row * a.bs.batch + n0;
   const E* Cm = static_cast<const E*>(a.Cm) + row * a.cs.batch + n0;
-  const int kb = live ? own : 0;
-  const float4 B0 = widen(load_quad<E>(Bm + g0 * a.bs.head, a.vec_bc, kb));
-  const float4 C0 = widen(load_quad<E>(Cm + g0 * a.cs.head, a.vec_bc, kb));
-  const float4 B1 = g1 == g0 ? B0 : widen(load_quad<E>(Bm + g1 * a.bs.head, a.vec_bc, kb));
-  const float4 C1 = g1 == g0 ? C0 : widen(load_quad<E>(Cm + g1 * a.cs.head, a.vec_bc, kb));
-  const float2 u = widen(load_pair<E>(static_cast<const E*>(a.u) + row * a.u_stride + d, a.vec_ch, have));
+  const int kb = WHOLE || live ? own : 0;
+  const float4 B0 = widen(load_quad<E>(Bm + g0 * a.bs.head, vec_bc, kb));
+  const float4 C0 = widen(load_quad<E>(Cm + g0 * a.cs.head, vec_bc, kb));
+  const float4 B1 = g1 == g0 ? B0 : widen(load_quad<E>(Bm + g1 * a.bs.head, vec_bc, kb));
+  const float4 C1 = g1 == g0 ? C0 : widen(load_quad<E>(Cm + g1 * a.cs.head, vec_bc, kb));
+  const float2 u = widen(load_pair<E>(static_cast<const E*>(a.u) + row * a.u_stride + d, vec_ch, have));
   float2 s =
-      widen(load_pair<E>(static_cast<const E*>(a.delta) + row * a.delta_stride + d, a.vec_ch, have));
+      widen(load_pair<E>(static_cast<const E*>(a.delta) + row * a.delta_stride + d, vec_ch, have));
   float2 z = make_float2(0.f, 0.f);
-  if (a.z) z = widen(load_pair<E>(static_cast<const E*>(a.z) + row * a.z_stride + d, a.vec_ch, have));
+  if (a.z) z = widen(load_pair<E>(static_cast<const E*>(a.z) + row * a.z_stride + d, vec_ch, have));
   if (a.delta_bias) {
     if (have > 0) s.x += a.delta_bias[d];
     if (have > 1) s.y += a.delta_bias[d + 1];
@@ -64,7 +68,7 @@ __global__ void __launch_bounds__(kThreads)
     o[c] = fmaf(Ct.w, h[c].w, fmaf(Ct.z, h[c].z, fmaf(Ct.y, h[c].y, Ct.x * h[c].x)));
     if (has && c < have) {
       float* to = hp + c * a.S;
-      if (a.vec_h) {
+      if (vec_h) {
         if (own > 0) *reinterpret_cast<float4*>(to) = h[c];
       } else {
         const float f[4] = {h[c].x, h[c].y, h[c].z, h[c].w};
@@ -79,13 +83,13 @@ __global__ void __launch_bounds__(kThreads)
     o[0] += __shfl_xor_sync(0xffffffffu, o[0], k);
     o[1] += __shfl_xor_sync(0xffffffffu, o[1], k);
   }
-  if (q == 0) {
+  if (q == 0 && live) {
     if (a.Dskip) {
       if (have > 0) o[0] = fmaf(a.Dskip[d], u.x, o[0]);
       if (have > 1) o[1] = fmaf(a.Dskip[d + 1], u.y, o[1]);
     }
     if (a.z) o[0] *= z.x * sigmoid(z.x), o[1] *= z.y * sigmoid(z.y);
-    store_pair<E>(static_cast<E*>(a.y) + (int64_t)row * a.D + d, a.vec_ch, have,
+    store_pair<E>(static_cast<E*>(a.y) + (int64_t)row * a.D + d, vec_ch, have,
                   has ? make_float2(o[0], o[1]) : make_float2(0.f, 0.f));
   }
 }
@@ -94,7 +98,12 @@ template <typename E, int LN>
 cudaError_t step_lanes(const ScanStepArgs& a, cudaStream_t stream) {
   const int64_t blocks = (a.N * ((a.D + 1) / 2) * LN + kThreads - 1) / kThreads;
   if (blocks > 0xffffffffLL / kThreads) return cudaErrorInvalidValue;
-  scan_step_kernel<E, LN><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  const bool whole = a.vec_h && a.vec_A && a.vec_ch && a.vec_bc && a.S == 4 * LN &&
+                     a.D / a.G % 2 == 0;
+  if (whole)
+    scan_step_kernel<E, LN, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  else
+    scan_step_kernel<E, LN, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -40,6 +40,21 @@ __device__ __forceinline__ FloatV<V> zeros() {
   return r;
 }
 
+template <int V>
+__device__ __forceinline__ FloatV<V> ones() {
+  FloatV<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = 1.f;
+  return r;
+}
+template <int V>
+__device__ __forceinline__ FloatV<V> sigmoid_vec(const FloatV<V>& x) {
+  FloatV<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = sigmoid(x.v[i]);
+  return r;
+}
+
 // Input at time t of row b, which may be a carried one (t < 0).
 template <typename E, int V, int W>
 __device__ __forceinline__ FloatV<V> input_at(const E* xrow, int64_t tstride, const E* state,
@@ -51,8 +66,8 @@ __device__ __forceinline__ FloatV<V> input_at(const E* xrow, int64_t tstride, co
 
 template <int V, int W>
 struct Filter {
-  float w[W][V];
-  float bias[V];
+  FloatV<V> w[W];
+  FloatV<V> bias;
 };
 
 // vec: the filters of V channels lie on a 16-byte boundary.
@@ -70,16 +85,16 @@ __device__ __forceinline__ Filter<V, W> load_filter(const float* weight, const f
       for (int j = 0; j < W; ++j) {
         const float4 q = v[(i * W + j) / 4];
         const int k = (i * W + j) % 4;
-        f.w[j][i] = k == 0 ? q.x : k == 1 ? q.y : k == 2 ? q.z : q.w;
+        f.w[j].v[i] = k == 0 ? q.x : k == 1 ? q.y : k == 2 ? q.z : q.w;
       }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < W; ++j) f.w[j][i] = weight[(c + i) * W + j];
+      for (int j = 0; j < W; ++j) f.w[j].v[i] = weight[(c + i) * W + j];
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) f.bias[i] = bias ? bias[c + i] : 0.f;
+  for (int i = 0; i < V; ++i) f.bias.v[i] = bias ? bias[c + i] : 0.f;
   return f;
 }
 
@@ -141,14 +156,10 @@ __global__ void __launch_bounds__(kThreads)
   for (int k = 0; k < kFwdRun; ++k) {
     const int64_t t = t0 + k;
     win[W - 1] = open_row<E, V>(rows[k + W - 1]);
-    FloatV<V> o;
+    FloatV<V> o = f.bias;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float p = f.bias[i];
-#pragma unroll
-      for (int j = 0; j < W; ++j) p = fmaf(f.w[j][i], win[j].v[i], p);
-      o.v[i] = SILU ? p * sigmoid(p) : p;
-    }
+    for (int j = 0; j < W; ++j) o = fma_vec(f.w[j], win[j], o);
+    if (SILU) o = mul_vec(o, sigmoid_vec(o));
     if (t < a.T) store_vec<E, V>(y + t * a.ys.time, t < n ? o : zeros<V>());
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
@@ -169,7 +180,9 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 4 : sizeof(E) == 2 ? 3 : 2)
   if (id >= nvec * parts) return;
   const int64_t part = quotient(id, nvec), c = (id - part * nvec) * V;
   const Filter<V, W> f = load_filter<V, W>(a.weight, a.bias, c, a.vec_w);
-  float dw[W][V] = {}, db[V] = {};
+  FloatV<V> dw[W], db = zeros<V>();
+#pragma unroll
+  for (int j = 0; j < W; ++j) dw[j] = zeros<V>();
   for (int64_t job = part; job < a.B * nruns; job += parts) {
     const int64_t b = quotient(job, nruns), r = job - b * nruns;
     const int64_t n = row_length(a.lengths, b, a.T);
@@ -207,24 +220,24 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 4 : sizeof(E) == 2 ? 3 : 2)
       const int64_t t = t0 + k;
       acc[W - 1] = zeros<V>();
       win[W - 1] = open_row<E, V>(xr[k + W - 1]);
-      const FloatV<V> g = open_row<E, V>(gr[k]);  // zero where there is no token
+      FloatV<V> d = open_row<E, V>(gr[k]);  // zero where there is no token
+      if (SILU && t < n) {
+        // silu'(p) = s (1 + p (1 - s)), s = sigmoid(p)
+        FloatV<V> p = f.bias;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float d = g.v[i];
-        if (SILU && t < n) {
-          float p = f.bias[i];
+        for (int j = 0; j < W; ++j) p = fma_vec(f.w[j], win[j], p);
+        const FloatV<V> s = sigmoid_vec(p), one = ones<V>();
+        FloatV<V> m;
 #pragma unroll
-          for (int j = 0; j < W; ++j) p = fmaf(f.w[j][i], win[j].v[i], p);
-          const float s = sigmoid(p);
-          d *= s * fmaf(p, 1.f - s, 1.f);
-        }
+        for (int i = 0; i < V; ++i) m.v[i] = -s.v[i];
+        d = mul_vec(d, mul_vec(s, fma_vec(p, add_vec(one, m), one)));
+      }
 #pragma unroll
-        for (int j = 0; j < W; ++j) acc[j].v[i] = fmaf(f.w[j][i], d, acc[j].v[i]);
-        if (k < kBwdRun) {
-          db[i] += d;
+      for (int j = 0; j < W; ++j) acc[j] = fma_vec(f.w[j], d, acc[j]);
+      if (k < kBwdRun) {
+        db = add_vec(db, d);
 #pragma unroll
-          for (int j = 0; j < W; ++j) dw[j][i] = fmaf(d, win[j].v[i], dw[j][i]);
-        }
+        for (int j = 0; j < W; ++j) dw[j] = fma_vec(d, win[j], dw[j]);
       }
       // input s has met its last token: stored where it is this run's own; the
       // first run also stores the carried inputs' gradients
@@ -253,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 4 : sizeof(E) == 2 ? 3 : 2)
 #pragma unroll
   for (int j = 0; j <= W; ++j)
 #pragma unroll
-    for (int i = 0; i < V; ++i) ws[j * a.C + c + i] = j < W ? dw[j < W ? j : 0][i] : db[i];
+    for (int i = 0; i < V; ++i) ws[j * a.C + c + i] = j < W ? dw[j < W ? j : 0].v[i] : db.v[i];
 }
 
 // Sums of the parts: a warp's lanes hold neighbouring channels, a block's eight
@@ -296,17 +309,13 @@ __global__ void __launch_bounds__(kThreads)
   const bool fresh = a.fresh && a.fresh[row];
   E* st = static_cast<E*>(a.state) + slot * (W - 1) * a.C + c;
   const Filter<V, W> f = load_filter<V, W>(a.weight, a.bias, c, a.vec_w);
-  FloatV<V> win[W], o;
+  FloatV<V> win[W], o = f.bias;
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) win[j] = fresh ? zeros<V>() : load_vec<E, V>(st + j * a.C);
   win[W - 1] = load_vec<E, V>(static_cast<const E*>(a.x) + row * a.x_stride + c);
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    float p = f.bias[k];
-#pragma unroll
-    for (int j = 0; j < W; ++j) p = fmaf(f.w[j][k], win[j].v[k], p);
-    o.v[k] = SILU ? p * sigmoid(p) : p;
-  }
+  for (int j = 0; j < W; ++j) o = fma_vec(f.w[j], win[j], o);
+  if (SILU) o = mul_vec(o, sigmoid_vec(o));
   store_vec<E, V>(y, o);
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) store_vec<E, V>(st + j * a.C, win[j + 1]);
@@ -390,12 +399,11 @@ size_t conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C, int width) {
 cudaError_t launch_conv_fwd(const ConvArgs& in, cudaStream_t stream) {
   ConvArgs a = in;
   a.vec_w = fits(a.weight, 16);
-  const int esz = a.dtype == FALCON_BF16 ? 2 : 4;
-  const int v = 16 / esz;
-  const bool vec = a.m % v == 0 && fits(a.x, 16) && fits(a.y, 16) && fits(a.state, 16) &&
-                   fits(a.state_out, 16) && fits(a.xs, a.H, v) && fits(a.ys, a.H, v);
+  const int bytes = a.dtype == FALCON_BF16 ? 8 : 16;
+  const bool vec = a.m % 4 == 0 && fits(a.x, bytes) && fits(a.y, bytes) && fits(a.state, bytes) &&
+                   fits(a.state_out, bytes) && fits(a.xs, a.H, 4) && fits(a.ys, a.H, 4);
   if (a.dtype == FALCON_BF16)
-    return vec ? fwd_typed<__nv_bfloat16, 8>(a, stream) : fwd_typed<__nv_bfloat16, 1>(a, stream);
+    return vec ? fwd_typed<__nv_bfloat16, 4>(a, stream) : fwd_typed<__nv_bfloat16, 1>(a, stream);
   return vec ? fwd_typed<float, 4>(a, stream) : fwd_typed<float, 1>(a, stream);
 }
 

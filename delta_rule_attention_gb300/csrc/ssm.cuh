@@ -233,6 +233,55 @@ __device__ __forceinline__ void store_pair(E* p, bool vec, int have, float2 v) {
   if (have > 1) store_vec<E, 1>(p + 1, FloatV<1>{{v.y}});
 }
 
+// acc + a * b and a * b of V values, two to an instruction.
+template <int V>
+__device__ __forceinline__ FloatV<V> fma_vec(const FloatV<V>& a, const FloatV<V>& b,
+                                             const FloatV<V>& acc) {
+  FloatV<V> r;
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 v = unpack2(fma2(pack2(a.v[i], a.v[i + 1]), pack2(b.v[i], b.v[i + 1]),
+                                    pack2(acc.v[i], acc.v[i + 1])));
+      r.v[i] = v.x, r.v[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = fmaf(a.v[i], b.v[i], acc.v[i]);
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ FloatV<V> mul_vec(const FloatV<V>& a, const FloatV<V>& b) {
+  FloatV<V> r;
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 v = unpack2(mul2(pack2(a.v[i], a.v[i + 1]), pack2(b.v[i], b.v[i + 1])));
+      r.v[i] = v.x, r.v[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = a.v[i] * b.v[i];
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ FloatV<V> add_vec(const FloatV<V>& a, const FloatV<V>& b) {
+  FloatV<V> r;
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 v = unpack2(add2(pack2(a.v[i], a.v[i + 1]), pack2(b.v[i], b.v[i + 1])));
+      r.v[i] = v.x, r.v[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = a.v[i] + b.v[i];
+  }
+  return r;
+}
+
 struct ConvArgs {
   int64_t B, H, T;
   int m, width, dtype, act;
