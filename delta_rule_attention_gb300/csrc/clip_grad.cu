@@ -19,12 +19,13 @@ constexpr int kThreads = 256;
 // Elements a block takes at a time: many of a large set, where finding a chunk's
 // tensor should cost little beside it, few of a small one, where all blocks
 // should have some.
-constexpr int kChunkMost = 32768, kChunkLeast = 4096;
+constexpr int kChunkMost = 16384, kChunkLeast = 4096;
 constexpr int64_t kLarge = 152LL * 4 * kChunkMost;
 // Bytes read last in the first pass that the second finds in L2 (of 126 MB, each
 // half of which may hold its own copy); what comes before is marked as passing.
 constexpr int64_t kStays = 40LL << 20;
-constexpr int kBlocks = 152 * 8;  // of one launch
+// Blocks of a launch: what the SMs hold at once.
+constexpr int kSquareBlocks = 152 * 4, kScaleBlocks = 152 * 3;
 
 template <int MOST>
 struct Batch {
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(kThreads)
     clip_scale_kernel(const __grid_constant__ Batch<MOST> p, const double* partial, int parts,
                       float max_norm, float eps, float* norm) {
   __shared__ double sh[kThreads / 32];
+  cudaGridDependencySynchronize();
   double acc = 0.0;
   for (int i = threadIdx.x; i < parts; i += kThreads) acc += partial[i];
   double total;
@@ -212,7 +214,9 @@ template <int MOST>
 cudaError_t clip(const falcon_grad* grads, int64_t tensors, float max_norm, float eps, float* norm,
                  double* partial, cudaStream_t stream) {
   static thread_local Batch<MOST> p;
-  auto blocks_of = [] { return (unsigned)(p.chunks < 1 ? 1 : p.chunks < kBlocks ? p.chunks : kBlocks); };
+  auto blocks_of = [](int most) {
+    return (unsigned)(p.chunks < 1 ? 1 : p.chunks < most ? p.chunks : most);
+  };
   int64_t all = 0;
   for (int64_t i = 0; i < tensors; ++i) all += grads[i].count;
   const int chunk = all >= kLarge ? kChunkMost : kChunkLeast;
@@ -220,19 +224,29 @@ cudaError_t clip(const falcon_grad* grads, int64_t tensors, float max_norm, floa
   int64_t at = 0;
   do {
     at = fill(&p, grads, tensors, at, chunk);
-    clip_squares_kernel<MOST><<<blocks_of(), kThreads, 0, stream>>>(p, partial + parts);
+    const unsigned blocks = blocks_of(kSquareBlocks);
+    clip_squares_kernel<MOST><<<blocks, kThreads, 0, stream>>>(p, partial + parts);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    parts += (int)blocks_of();
+    parts += (int)blocks;
   } while (at < tensors);
   const bool again = tensors > MOST;  // otherwise p still holds all of them
   at = again ? 0 : tensors;
   do {
     if (again) at = fill(&p, grads, tensors, at, chunk);
-    clip_scale_kernel<MOST><<<blocks_of(), kThreads, 0, stream>>>(p, partial, parts, max_norm, eps,
-                                                                norm);
+    // set up while the launch before it ends; it waits for that launch's results
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks_of(kScaleBlocks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = early;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, clip_scale_kernel<MOST>, p,
+                                             (const double*)partial, parts, max_norm, eps, norm);
     norm = nullptr;
-    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   } while (at < tensors);
   return cudaSuccess;
@@ -241,7 +255,7 @@ cudaError_t clip(const falcon_grad* grads, int64_t tensors, float max_norm, floa
 }  // namespace
 
 size_t clip_workspace_bytes(const falcon_grad*, int64_t tensors) {
-  return sizeof(double) * kBlocks * (size_t)((tensors + kMost - 1) / kMost + 1);
+  return sizeof(double) * kSquareBlocks * (size_t)((tensors + kMost - 1) / kMost + 1);
 }
 
 cudaError_t launch_clip(const falcon_grad* grads, int64_t tensors, float max_norm, float eps,

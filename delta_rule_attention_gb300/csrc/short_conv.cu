@@ -55,10 +55,12 @@ __device__ __forceinline__ FloatV<V> sigmoid_vec(const FloatV<V>& x) {
   return r;
 }
 
-// Input at time t of row b, which may be a carried one (t < 0).
+// Input at time t of row b, which may be a carried one (t < 0) or none (t >= n).
 template <typename E, int V, int W>
 __device__ __forceinline__ FloatV<V> input_at(const E* xrow, int64_t tstride, const E* state,
-                                              int64_t b, int64_t C, int64_t c, int64_t t) {
+                                              int64_t b, int64_t C, int64_t c, int64_t t,
+                                              int64_t n) {
+  if (t >= n) return zeros<V>();
   if (t >= 0) return load_vec<E, V>(xrow + t * tstride);
   if (state) return load_vec<E, V>(state + (b * (W - 1) + (t + W - 1)) * C + c);
   return zeros<V>();
@@ -70,12 +72,13 @@ struct Filter {
   FloatV<V> bias;
 };
 
-// vec: the filters of V channels lie on a 16-byte boundary.
+// vec: the weights lie on a 16-byte boundary, and so does every V-th filter where
+// V * W is a multiple of four.
 template <int V, int W>
 __device__ __forceinline__ Filter<V, W> load_filter(const float* weight, const float* bias,
                                                     int64_t c, bool vec) {
   Filter<V, W> f;
-  if (vec && V % 4 == 0) {
+  if (vec && V * W % 4 == 0) {
     float4 v[V * W / 4 > 0 ? V * W / 4 : 1];
 #pragma unroll
     for (int i = 0; i < V * W / 4; ++i) v[i] = reinterpret_cast<const float4*>(weight + c * W)[i];
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
       store_vec<E, V>(static_cast<E*>(a.state_out) + (b * (W - 1) + j) * a.C + c,
-                      input_at<E, V, W>(x, a.xs.time, state, b, a.C, c, n - (W - 1) + j));
+                      input_at<E, V, W>(x, a.xs.time, state, b, a.C, c, n - (W - 1) + j, n));
     return;
   }
   const int64_t t0 = r * kFwdRun;
@@ -138,43 +141,58 @@ __global__ void __launch_bounds__(kThreads)
     return;
   }
   R rows[kFwdRun + W - 1];
+  const bool whole = t0 > 0 && t0 + kFwdRun <= n;  // no carried input, no missing token
+  const E* px = x + (t0 - (W - 1)) * a.xs.time;
+  if (whole) {
 #pragma unroll
-  for (int k = 0; k < kFwdRun + W - 1; ++k) {
-    const int64_t t = t0 + k - (W - 1);
-    rows[k] = R();
-    if (t >= 0) {
-      if (t < n) rows[k] = *reinterpret_cast<const R*>(x + t * a.xs.time);
-    } else if (state) {
-      rows[k] = *reinterpret_cast<const R*>(state + (b * (W - 1) + (t + W - 1)) * a.C + c);
+    for (int k = 0; k < kFwdRun + W - 1; ++k) {
+      rows[k] = *reinterpret_cast<const R*>(px);
+      px += a.xs.time;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kFwdRun + W - 1; ++k) {
+      const int64_t t = t0 + k - (W - 1);
+      rows[k] = R();
+      if (t >= 0) {
+        if (t < n) rows[k] = *reinterpret_cast<const R*>(px);
+      } else if (state) {
+        rows[k] = *reinterpret_cast<const R*>(state + (b * (W - 1) + (t + W - 1)) * a.C + c);
+      }
+      px += a.xs.time;
     }
   }
   const Filter<V, W> f = load_filter<V, W>(a.weight, a.bias, c, a.vec_w);
   FloatV<V> win[W];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) win[j] = open_row<E, V>(rows[j]);
+  E* py = y + t0 * a.ys.time;
 #pragma unroll
   for (int k = 0; k < kFwdRun; ++k) {
-    const int64_t t = t0 + k;
     win[W - 1] = open_row<E, V>(rows[k + W - 1]);
     FloatV<V> o = f.bias;
 #pragma unroll
     for (int j = 0; j < W; ++j) o = fma_vec(f.w[j], win[j], o);
     if (SILU) o = mul_vec(o, sigmoid_vec(o));
-    if (t < a.T) store_vec<E, V>(y + t * a.ys.time, t < n ? o : zeros<V>());
+    if (whole)
+      store_vec<E, V>(py, o);
+    else if (t0 + k < a.T)
+      store_vec<E, V>(py, t0 + k < n ? o : zeros<V>());
+    py += a.ys.time;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
   }
 }
 
-constexpr int kBwdRun = 8;
+constexpr int kBwdBlock = 8;  // tokens whose rows are under way together
 
-// Gradient: dp of the run's tokens and of the W - 1 after it (recomputed from
-// x), each dp_t adding w_j dp_t to dx_{t-W+1+j}.  A thread walks every `parts`-th
-// run of its channels with its sums of dw and dbias in registers and writes them
-// once; conv_sum_kernel adds the parts in their order.
+// Gradient: a thread walks a run of `run` tokens and the W - 1 after it, whose dp
+// it recomputes from x; each dp_t adds w_j dp_t to dx_{t-W+1+j}.  A thread takes
+// every `parts`-th run of its channels with its sums of dw and dbias in registers and
+// writes them once; conv_sum_kernel adds the parts in their order.
 template <typename E, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads, V == 1 ? 4 : sizeof(E) == 2 ? 3 : 2)
-    conv_bwd_kernel(const __grid_constant__ ConvArgs a, int64_t nruns, int parts) {
+__global__ void __launch_bounds__(kThreads)
+    conv_bwd_kernel(const __grid_constant__ ConvArgs a, int run, int64_t nruns, int parts) {
   typedef Row<E, V> R;
   const int64_t nvec = a.C / V, id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (id >= nvec * parts) return;
@@ -191,75 +209,104 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 4 : sizeof(E) == 2 ? 3 : 2)
     E* dx = static_cast<E*>(a.dx) + row_offset(a.dxs, b, c, a.m);
     const E* state = static_cast<const E*>(a.state);
     const E* dso = static_cast<const E*>(a.dstate_out);
-    const int64_t t0 = r * kBwdRun, t1 = t0 + kBwdRun < a.T ? t0 + kBwdRun : a.T;
-    R xr[kBwdRun + 2 * (W - 1)], gr[kBwdRun + W - 1];
+    const int64_t t0 = r * run, t1 = t0 + run < a.T ? t0 + run : a.T, te = t1 + W - 1;
+    R xr[kBwdBlock], gr[kBwdBlock];
+    // pointers walk with the tokens: a product for every row would fill the registers
+    const E *px = x + t0 * a.xs.time, *pg = dy + t0 * a.dys.time;
+    E* po = dx + (t0 - (W - 1)) * a.dxs.time;
+    const int readable = (int)((n < te ? n : te) - t0), total = (int)(te - t0),
+              own = (int)(t1 - t0);
+    auto fetch = [&](int k0) {
+      if (k0 + kBwdBlock <= readable) {
 #pragma unroll
-    for (int k = 0; k < kBwdRun + 2 * (W - 1); ++k) {
-      const int64_t t = t0 + k - (W - 1);
-      xr[k] = R();
-      if (t >= 0) {
-        if (t < n) xr[k] = *reinterpret_cast<const R*>(x + t * a.xs.time);
-      } else if (state) {
-        xr[k] = *reinterpret_cast<const R*>(state + (b * (W - 1) + (t + W - 1)) * a.C + c);
+        for (int k = 0; k < kBwdBlock; ++k) {
+          xr[k] = *reinterpret_cast<const R*>(px);
+          gr[k] = *reinterpret_cast<const R*>(pg);
+          px += a.xs.time;
+          pg += a.dys.time;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kBwdBlock; ++k) {
+          xr[k] = gr[k] = R();
+          if (k0 + k < readable) {
+            xr[k] = *reinterpret_cast<const R*>(px);
+            gr[k] = *reinterpret_cast<const R*>(pg);
+          }
+          px += a.xs.time;
+          pg += a.dys.time;
+        }
       }
-    }
-#pragma unroll
-    for (int k = 0; k < kBwdRun + W - 1; ++k) {
-      gr[k] = R();
-      if (t0 + k < n) gr[k] = *reinterpret_cast<const R*>(dy + (t0 + k) * a.dys.time);
-    }
+    };
+    fetch(0);
     // acc[j] gathers the gradient of input t - W + 1 + j
     FloatV<V> win[W], acc[W];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-      win[j] = open_row<E, V>(xr[j]);
+      win[j] = input_at<E, V, W>(x, a.xs.time, state, b, a.C, c, t0 - (W - 1) + j, n);
       acc[j] = zeros<V>();
     }
+    // places in state_out begin at token n - (W - 1); the row's last inputs only
+    const int tail = dso && n - (W - 1) < te ? (int)(n - t0) - (W - 1) : total;
+    // one block of tokens; WHOLE: all are the run's own tokens, and all inputs that
+    // they complete are the run's own and not among the row's last
+    auto block = [&](int k0, auto whole) {
+      constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
-    for (int k = 0; k < kBwdRun + W - 1; ++k) {
-      const int64_t t = t0 + k;
-      acc[W - 1] = zeros<V>();
-      win[W - 1] = open_row<E, V>(xr[k + W - 1]);
-      FloatV<V> d = open_row<E, V>(gr[k]);  // zero where there is no token
-      if (SILU && t < n) {
-        // silu'(p) = s (1 + p (1 - s)), s = sigmoid(p)
-        FloatV<V> p = f.bias;
+      for (int k = 0; k < kBwdBlock; ++k) {
+        const int kt = k0 + k;  // token, counted from the run's first
+        acc[W - 1] = zeros<V>();
+        win[W - 1] = open_row<E, V>(xr[k]);
+        FloatV<V> d = open_row<E, V>(gr[k]);  // zero where there is no token
+        if (SILU && (WHOLE || kt < readable)) {
+          // silu'(p) = s (1 + p (1 - s)), s = sigmoid(p)
+          FloatV<V> p = f.bias;
 #pragma unroll
-        for (int j = 0; j < W; ++j) p = fma_vec(f.w[j], win[j], p);
-        const FloatV<V> s = sigmoid_vec(p), one = ones<V>();
-        FloatV<V> m;
+          for (int j = 0; j < W; ++j) p = fma_vec(f.w[j], win[j], p);
+          const FloatV<V> s = sigmoid_vec(p), one = ones<V>();
+          FloatV<V> m;
 #pragma unroll
-        for (int i = 0; i < V; ++i) m.v[i] = -s.v[i];
-        d = mul_vec(d, mul_vec(s, fma_vec(p, add_vec(one, m), one)));
-      }
-#pragma unroll
-      for (int j = 0; j < W; ++j) acc[j] = fma_vec(f.w[j], d, acc[j]);
-      if (k < kBwdRun) {
-        db = add_vec(db, d);
-#pragma unroll
-        for (int j = 0; j < W; ++j) dw[j] = fma_vec(d, win[j], dw[j]);
-      }
-      // input s has met its last token: stored where it is this run's own; the
-      // first run also stores the carried inputs' gradients
-      const int64_t s = t - (W - 1);
-      if (k >= W - 1 ? s < t1 : t0 == 0) {
-        FloatV<V> o = acc[0];
-        const int64_t at = s - (n - (W - 1));  // its place in state_out
-        if (dso && at >= 0 && s < n) {
-          const FloatV<V> e = load_vec<E, V>(dso + (b * (W - 1) + at) * a.C + c);
-#pragma unroll
-          for (int i = 0; i < V; ++i) o.v[i] += e.v[i];
+          for (int i = 0; i < V; ++i) m.v[i] = -s.v[i];
+          d = mul_vec(d, mul_vec(s, fma_vec(p, add_vec(one, m), one)));
         }
-        if (s >= 0)
-          store_vec<E, V>(dx + s * a.dxs.time, o);
-        else if (a.dstate)
-          store_vec<E, V>(static_cast<E*>(a.dstate) + (b * (W - 1) + s + W - 1) * a.C + c, o);
-      }
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) {
-        win[j] = win[j + 1];
-        acc[j] = acc[j + 1];
+        for (int j = 0; j < W; ++j) acc[j] = fma_vec(f.w[j], d, acc[j]);
+        if (WHOLE || kt < own) {
+          db = add_vec(db, d);
+#pragma unroll
+          for (int j = 0; j < W; ++j) dw[j] = fma_vec(d, win[j], dw[j]);
+        }
+        // input ks has met its last token: stored where it is this run's own; the
+        // first run also stores the carried inputs' gradients
+        const int ks = kt - (W - 1);
+        if (WHOLE) {
+          store_vec<E, V>(po, acc[0]);
+        } else if (kt < total && (ks >= 0 || t0 == 0)) {
+          FloatV<V> o = acc[0];
+          if (ks >= tail && t0 + ks < n)
+            o = add_vec(o, load_vec<E, V>(dso + (b * (W - 1) + (ks - tail)) * a.C + c));
+          if (ks >= 0)
+            store_vec<E, V>(po, o);
+          else if (a.dstate)
+            store_vec<E, V>(static_cast<E*>(a.dstate) + (b * (W - 1) + kt) * a.C + c, o);
+        }
+        po += a.dxs.time;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+          win[j] = win[j + 1];
+          acc[j] = acc[j + 1];
+        }
       }
+    };
+    const int plain = (own < readable ? own : readable) < tail + W - 1
+                          ? (own < readable ? own : readable) : tail + W - 1;
+#pragma unroll 1
+    for (int k0 = 0; k0 < total; k0 += kBwdBlock) {
+      if (k0 >= kBwdBlock && k0 + kBwdBlock <= plain)
+        block(k0, std::true_type());
+      else
+        block(k0, std::false_type());
+      if (k0 + kBwdBlock < total) fetch(k0 + kBwdBlock);
     }
   }
   float* ws = a.ws + part * (W + 1) * a.C;
@@ -353,24 +400,32 @@ cudaError_t fwd_typed(const ConvArgs& a, cudaStream_t stream) {
   });
 }
 
-// Parts of the sums: enough threads (of four channels) to fill the GPU, each
-// with as many runs as that leaves.
+// The longest run (a run's W - 1 recomputed tokens cost less beside more) that
+// leaves a thousand threads of two channels an SM.
+int bwd_run(int64_t B, int64_t T, int64_t C) {
+  int run = 64;
+  while (run > 8 && (C + 1) / 2 * B * ((T + run - 1) / run) < 152 * 1024) run /= 2;
+  return run;
+}
+// Parts of the sums: one for every run while they are few.
 int bwd_parts(int64_t B, int64_t T, int64_t C) {
-  const int64_t jobs = B * ((T + kBwdRun - 1) / kBwdRun);
-  const int64_t fill = (152 * 1024 + (C + 3) / 4 - 1) / ((C + 3) / 4);
+  const int run = bwd_run(B, T, C);
+  const int64_t jobs = B * ((T + run - 1) / run);
+  const int64_t pairs = (C + 1) / 2, fill = (152 * 2048 + pairs - 1) / pairs;
   return (int)(jobs < fill ? jobs : fill);
 }
 
 template <typename E, int V>
 cudaError_t bwd_typed(const ConvArgs& a, cudaStream_t stream) {
-  const int64_t nruns = (a.T + kBwdRun - 1) / kBwdRun;
+  const int run = bwd_run(a.B, a.T, a.C);
+  const int64_t nruns = (a.T + run - 1) / run;
   const int parts = bwd_parts(a.B, a.T, a.C);
   const int64_t blocks = (a.C / V * parts + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   return with_width(a.width, a.act, [&](auto w, auto silu) {
     constexpr int W = decltype(w)::value;
     conv_bwd_kernel<E, V, W, decltype(silu)::value>
-        <<<(unsigned)blocks, kThreads, 0, stream>>>(a, nruns, parts);
+        <<<(unsigned)blocks, kThreads, 0, stream>>>(a, run, nruns, parts);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     conv_sum_kernel<<<dim3((unsigned)((a.C + 31) / 32), W + 1), 256, 0, stream>>>(
@@ -421,13 +476,15 @@ cudaError_t launch_conv_bwd(const ConvArgs& in, cudaStream_t stream) {
     return cudaMemcpyAsync(a.dstate, a.dstate_out, (size_t)tail * esz, cudaMemcpyDeviceToDevice,
                            stream);
   }
-  const int bytes = 4 * esz;
-  const bool vec = a.m % 4 == 0 && fits(a.x, bytes) && fits(a.dy, bytes) && fits(a.dx, bytes) &&
+  // two channels a thread: four need 170 registers (97 us for 8 x 2048 x 2048
+  // bf16 elements, against 68 us with two)
+  const int bytes = 2 * esz;
+  const bool vec = a.m % 2 == 0 && fits(a.x, bytes) && fits(a.dy, bytes) && fits(a.dx, bytes) &&
                    fits(a.state, bytes) && fits(a.dstate_out, bytes) && fits(a.dstate, bytes) &&
-                   fits(a.xs, a.H, 4) && fits(a.dys, a.H, 4) && fits(a.dxs, a.H, 4);
+                   fits(a.xs, a.H, 2) && fits(a.dys, a.H, 2) && fits(a.dxs, a.H, 2);
   if (a.dtype == FALCON_BF16)
-    return vec ? bwd_typed<__nv_bfloat16, 4>(a, stream) : bwd_typed<__nv_bfloat16, 1>(a, stream);
-  return vec ? bwd_typed<float, 4>(a, stream) : bwd_typed<float, 1>(a, stream);
+    return vec ? bwd_typed<__nv_bfloat16, 2>(a, stream) : bwd_typed<__nv_bfloat16, 1>(a, stream);
+  return vec ? bwd_typed<float, 2>(a, stream) : bwd_typed<float, 1>(a, stream);
 }
 
 cudaError_t launch_conv_step(const ConvStepArgs& in, cudaStream_t stream) {

@@ -20,8 +20,11 @@ __device__ __forceinline__ FloatV<V> load_vec(const E* p) {
   if constexpr (sizeof(E) == 4) {
     if constexpr (V == 1) {
       r.v[0] = *p;
+    } else if constexpr (V == 2) {
+      const float2 q = *reinterpret_cast<const float2*>(p);
+      r.v[0] = q.x, r.v[1] = q.y;
     } else {
-      static_assert(V == 4, "fp32 rows move four channels or one");
+      static_assert(V == 4, "fp32 rows move 1, 2 or 4 channels");
       const float4 q = *reinterpret_cast<const float4*>(p);
       r.v[0] = q.x, r.v[1] = q.y, r.v[2] = q.z, r.v[3] = q.w;
     }
@@ -60,6 +63,8 @@ __device__ __forceinline__ void store_vec(E* p, const FloatV<V>& x) {
   if constexpr (sizeof(E) == 4) {
     if constexpr (V == 1)
       *p = x.v[0];
+    else if constexpr (V == 2)
+      *reinterpret_cast<float2*>(p) = make_float2(x.v[0], x.v[1]);
     else
       *reinterpret_cast<float4*>(p) = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
   } else {
