@@ -286,65 +286,58 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
     }
 }
 
-// Step 2: hin[c] becomes the state entering chunk c, gin[c] the adjoint entering it
-// from behind.
+// Step 2: hin[c] becomes the state entering chunk c (blockIdx.z = 0), gin[c] the
+// adjoint entering it from behind (blockIdx.z = 1).  Bound by latency: a thread's walk
+// is serial, so it keeps sixteen chunks' loads under way.
 __global__ void __launch_bounds__(128)
     scan_bwd_chain_kernel(const __grid_constant__ ScanArgs a, float* ws,
                           const __grid_constant__ Layout l) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t quads = l.NP / 4;
   if (i >= (int64_t)a.D * quads) return;
+  const bool back = blockIdx.z == 1;
   const int64_t d = i / quads, b = blockIdx.y;
   const int n0 = (int)(i - d * quads) * 4;
-  const int64_t n = row_length(a.lengths, b, a.T), count = (n + kChunk - 1) / kChunk;
-  float A2[4], h[4], g[4];
+  const int64_t n = row_length(a.lengths, b, a.T);
+  const int count = (int)((n + kChunk - 1) / kChunk);
+  const float* from = back ? a.dh_T : a.h0;
+  float A2[4], h[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const bool in = n0 + k < a.N;
-    const int64_t at = (b * a.D + d) * a.N + n0 + k;
     A2[k] = in ? a.A[d * a.N + n0 + k] * kLog2e : 0.f;
-    h[k] = in && a.h0 ? a.h0[at] : 0.f;
-    g[k] = in && a.dh_T ? a.dh_T[at] : 0.f;
+    h[k] = in && from ? from[(b * a.D + d) * a.N + n0 + k] : 0.f;
   }
-  const int64_t step = (int64_t)a.D * l.NP;
-  float* hp = ws + l.hin + (b * l.chunks * a.D + d) * l.NP + n0;
-  float* gp = ws + l.gin + (b * l.chunks * a.D + d) * l.NP + n0;
-  const float* sp = ws + l.sums + b * l.chunks * a.D + d;
-  // both walks at once, eight chunks of each in flight
-  constexpr int kAhead = 8;
-  for (int64_t c0 = 0; c0 < count; c0 += kAhead) {
-    float4 hv[kAhead], gv[kAhead];
-    float hs[kAhead], gs[kAhead];
+  // the walk's first chunk and its direction
+  const int64_t start = back ? count - 1 : 0, dir = back ? -1 : 1;
+  const int64_t step = dir * a.D * l.NP, sstep = dir * a.D;
+  float* hp = ws + (back ? l.gin : l.hin) + ((b * l.chunks + start) * a.D + d) * l.NP + n0;
+  const float* sp = ws + l.sums + (b * l.chunks + start) * a.D + d;
+  constexpr int kAhead = 16;
+  for (int c0 = 0; c0 < count; c0 += kAhead) {
+    float4 hv[kAhead];
+    float hs[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int64_t c = c0 + k, e = count - 1 - c;
-      if (c < count) {
-        hv[k] = *reinterpret_cast<const float4*>(hp + c * step);
-        gv[k] = *reinterpret_cast<const float4*>(gp + e * step);
-        hs[k] = sp[c * a.D];
-        gs[k] = sp[e * a.D];
+    for (int k = 0; k < kAhead; ++k)
+      if (c0 + k < count) {
+        hv[k] = *reinterpret_cast<const float4*>(hp + k * step);
+        hs[k] = sp[k * sstep];
       }
-    }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int64_t c = c0 + k, e = count - 1 - c;
-      if (c < count) {
-        *reinterpret_cast<float4*>(hp + c * step) = make_float4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<float4*>(gp + e * step) = make_float4(g[0], g[1], g[2], g[3]);
+    for (int k = 0; k < kAhead; ++k)
+      if (c0 + k < count) {
+        *reinterpret_cast<float4*>(hp + k * step) = make_float4(h[0], h[1], h[2], h[3]);
         const float ha[4] = {hv[k].x, hv[k].y, hv[k].z, hv[k].w};
-        const float ga[4] = {gv[k].x, gv[k].y, gv[k].z, gv[k].w};
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          h[x] = fmaf(decay(hs[k], A2[x]), h[x], ha[x]);
-          g[x] = fmaf(decay(gs[k], A2[x]), g[x], ga[x]);
-        }
+        for (int x = 0; x < 4; ++x) h[x] = fmaf(decay(hs[k], A2[x]), h[x], ha[x]);
       }
-    }
+    hp += kAhead * step;
+    sp += kAhead * sstep;
   }
-  if (a.dh0)
+  if (back && a.dh0)
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (n0 + k < a.N) a.dh0[(b * a.D + d) * a.N + n0 + k] = g[k];
+      if (n0 + k < a.N) a.dh0[(b * a.D + d) * a.N + n0 + k] = h[k];
 }
 
 // Step 3.
@@ -667,27 +660,45 @@ __global__ void __launch_bounds__(256)
     if (n0 + k < a.N) store_vec<E, 1>(to + k, FloatV<1>{{f[k]}});
 }
 
-__global__ void __launch_bounds__(128)
+// Rows of `width` values summed over `parts`: a warp's lanes hold neighbouring
+// values, a block's eight warps an eighth of the parts each.
+__device__ __forceinline__ float sum_parts(const float* from, int64_t width, int64_t at,
+                                           int64_t parts, float (&sh)[8][32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float v = 0.f;
+  if (at < width) {
+#pragma unroll 8
+    for (int64_t p = warp; p < parts; p += 8) v += from[p * width + at];
+  }
+  __syncthreads();
+  sh[warp][lane] = v;
+  __syncthreads();
+  v = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) v += sh[w][lane];
+  return v;
+}
+
+// Blocks over the padded [D,NP] values of dA, then over the D of dDskip and ddelta_bias.
+__global__ void __launch_bounds__(256)
     scan_bwd_param_kernel(const __grid_constant__ ScanArgs a, const float* ws,
                           const __grid_constant__ Layout l) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t parts = l.groups * a.B;
-  if (i < (int64_t)a.D * a.N) {
-    const int64_t d = i / a.N, n = i - d * a.N;
-    float v = 0.f;
-#pragma unroll 8
-    for (int64_t p = 0; p < parts; ++p) v += ws[l.dA + (p * a.D + d) * l.NP + n];
-    a.dA[i] = v;
+  __shared__ float sh[8][32];
+  const int64_t parts = l.groups * a.B, width = (int64_t)a.D * l.NP;
+  const int64_t first = (width + 31) / 32;
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x < first) {
+    const int64_t at = (int64_t)blockIdx.x * 32 + lane, d = at / l.NP, n = at - d * l.NP;
+    const float v = sum_parts(ws + l.dA, width, at, parts, sh);
+    if (threadIdx.x < 32 && at < width && n < a.N) a.dA[d * a.N + n] = v;
+    return;
   }
-  if (i < a.D) {
-    float v = 0.f, w = 0.f;
-#pragma unroll 8
-    for (int64_t p = 0; p < parts; ++p) {
-      v += ws[l.dD + p * a.D + i];
-      w += ws[l.dbias + p * a.D + i];
-    }
-    if (a.dDskip) a.dDskip[i] = v;
-    if (a.ddelta_bias) a.ddelta_bias[i] = w;
+  const int64_t d = (blockIdx.x - first) * 32 + lane;
+  const float v = sum_parts(ws + l.dD, a.D, d, parts, sh);
+  const float w = sum_parts(ws + l.dbias, a.D, d, parts, sh);
+  if (threadIdx.x < 32 && d < a.D) {
+    if (a.dDskip) a.dDskip[d] = v;
+    if (a.ddelta_bias) a.ddelta_bias[d] = w;
   }
 }
 
@@ -716,8 +727,8 @@ cudaError_t bwd_lanes(const ScanArgs& a, cudaStream_t stream) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const int64_t quads = (int64_t)a.D * LN;
-  scan_bwd_chain_kernel<<<dim3((unsigned)((quads + 127) / 128), (unsigned)a.B), 128, 0, stream>>>(
-      a, ws, l);
+  scan_bwd_chain_kernel<<<dim3((unsigned)((quads + 127) / 128), (unsigned)a.B, 2), 128, 0,
+                          stream>>>(a, ws, l);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (l.chunks > 0) {
     scan_bwd_grad_kernel<E, LN><<<groups, C::kWarps * 32, bytes3, stream>>>(a, ws, l);
@@ -726,8 +737,8 @@ cudaError_t bwd_lanes(const ScanArgs& a, cudaStream_t stream) {
     scan_bwd_bc_kernel<E><<<(unsigned)((sums + 255) / 256), 256, 0, stream>>>(a, ws, l);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const int64_t params = (int64_t)a.D * a.N;
-  scan_bwd_param_kernel<<<(unsigned)((params + 127) / 128), 128, 0, stream>>>(a, ws, l);
+  const int64_t params = ((int64_t)a.D * l.NP + 31) / 32 + (a.D + 31) / 32;
+  scan_bwd_param_kernel<<<(unsigned)params, 256, 0, stream>>>(a, ws, l);
   return cudaGetLastError();
 }
 
