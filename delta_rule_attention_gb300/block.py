@@ -137,7 +137,7 @@ def _refuse(t, name, dtype, shape, device, what):
 def _rows(t, name, dtype, shape, device):
     """A tensor of this type, shape and GPU whose last dimension is adjacent."""
     if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or
-            t.device != device or not t.is_cuda or (t.stride(-1) != 1 and t.shape[-1] > 1)):
+            t.device != device or (t.stride(-1) != 1 and t.shape[-1] > 1)):
         _refuse(t, name, dtype, shape, device, "have adjacent channels")
     return t
 
@@ -145,16 +145,19 @@ def _rows(t, name, dtype, shape, device):
 def _dense(t, name, dtype, shape, device):
     if t is not None and (
             not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or
-            t.device != device or not t.is_cuda or not t.is_contiguous()):
+            t.device != device or not t.is_contiguous()):
         _refuse(t, name, dtype, shape, device, "be contiguous")
     return t
 
 
 def _dtype(t, name):
+    """The dtype of a call's first tensor, whose GPU the others are held to."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _DTYPE:
         raise TypeError(f"{name} must be bfloat16 or float32")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     return t.dtype
 
 
@@ -205,9 +208,9 @@ def falcon_short_conv_fwd(x, weight, bias=None, state=None, lengths=None, activa
         _rows(y, "y", dt, x.shape, dev)
     state_out = torch.empty((B, W - 1, C), dtype=dt, device=dev) if state_out is None else \
         _dense(state_out, "state_out", dt, (B, W - 1, C), dev)
-    rc = lib.falcon_short_conv_fwd(shape, _at(x), _conv_rows(x), _at(weight), _at(bias),
-                                   _at(state), _at(lengths), _at(y), _conv_rows(y),
-                                   _at(state_out), _current(stream, dev))
+    rc = lib.falcon_short_conv_fwd(shape, x.data_ptr(), _conv_rows(x), weight.data_ptr(), _at(bias),
+                                   _at(state), _at(lengths), y.data_ptr(), _conv_rows(y),
+                                   state_out.data_ptr(), _current(stream, dev))
     _check(rc, "falcon_short_conv_fwd")
     return y, state_out
 
@@ -238,7 +241,8 @@ def falcon_short_conv_bwd(x, weight, dy, bias=None, state=None, lengths=None, ds
     workspace, have = _workspace(int(lib.falcon_short_conv_bwd_workspace_bytes(shape)),
                                  workspace, dev)
     rc = lib.falcon_short_conv_bwd(
-        shape, _at(x), _conv_rows(x), _at(weight), _at(bias), _at(state), _at(lengths), _at(dy),
+        shape, x.data_ptr(), _conv_rows(x), weight.data_ptr(), _at(bias), _at(state),
+        _at(lengths), dy.data_ptr(),
         _conv_rows(dy), _at(dstate_out), _at(g["dx"]), _conv_rows(g["dx"]), _at(g["dweight"]),
         _at(g["dbias"]), _at(g["dstate"]), _at(workspace), have, _current(stream, dev))
     _check(rc, "falcon_short_conv_bwd")
@@ -269,9 +273,9 @@ def falcon_short_conv_step(x, weight, state, bias=None, slots=None, fresh=None,
     _dense(fresh, "fresh", torch.uint8, (N,), dev)
     y = torch.empty((N, C), dtype=dt, device=dev) if y is None else \
         _dense(y, "y", dt, (N, C), dev)
-    rc = lib.falcon_short_conv_step(N, C, W, _DTYPE[dt], _ACT[activation], _at(x), x.stride(0),
-                                    _at(weight), _at(bias), _at(state), pool, _at(slots),
-                                    _at(fresh), _at(y), _current(stream, dev))
+    rc = lib.falcon_short_conv_step(N, C, W, _DTYPE[dt], _ACT[activation], x.data_ptr(),
+                                    x.stride(0), weight.data_ptr(), _at(bias), _at(state), pool,
+                                    _at(slots), _at(fresh), y.data_ptr(), _current(stream, dev))
     _check(rc, "falcon_short_conv_step")
     return y
 
@@ -332,10 +336,11 @@ def falcon_selective_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=No
     h_out = torch.empty(hs, dtype=torch.float32, device=dev) if h_out is None else \
         _dense(h_out, "h_out", torch.float32, hs, dev)
     rc = lib.falcon_selective_scan_fwd(
-        shape, _at(u), _time_rows(u), _at(delta), _time_rows(delta), _at(A), _at(Bm),
-        _group_rows(Bm), _at(Cm), _group_rows(Cm), _at(D), _at(z),
-        None if z is None else _time_rows(z), _at(delta_bias), _at(h0), _at(lengths), _at(y),
-        _time_rows(y), _at(h_out), _current(stream, dev))
+        shape, u.data_ptr(), _time_rows(u), delta.data_ptr(), _time_rows(delta), A.data_ptr(),
+        Bm.data_ptr(),
+        _group_rows(Bm), Cm.data_ptr(), _group_rows(Cm), _at(D), _at(z),
+        None if z is None else _time_rows(z), _at(delta_bias), _at(h0), _at(lengths), y.data_ptr(),
+        _time_rows(y), h_out.data_ptr(), _current(stream, dev))
     _check(rc, "falcon_selective_scan_fwd")
     return y, h_out
 
@@ -370,9 +375,10 @@ def falcon_selective_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bia
     workspace, have = _workspace(int(lib.falcon_selective_scan_bwd_workspace_bytes(shape)),
                                  workspace, dev)
     rc = lib.falcon_selective_scan_bwd(
-        shape, _at(u), _time_rows(u), _at(delta), _time_rows(delta), _at(A), _at(Bm),
-        _group_rows(Bm), _at(Cm), _group_rows(Cm), _at(D), _at(z),
-        None if z is None else _time_rows(z), _at(delta_bias), _at(h0), _at(lengths), _at(dy),
+        shape, u.data_ptr(), _time_rows(u), delta.data_ptr(), _time_rows(delta), A.data_ptr(),
+        Bm.data_ptr(),
+        _group_rows(Bm), Cm.data_ptr(), _group_rows(Cm), _at(D), _at(z),
+        None if z is None else _time_rows(z), _at(delta_bias), _at(h0), _at(lengths), dy.data_ptr(),
         _time_rows(dy), _at(dh_T), _at(g["du"]), _at(g["ddelta"]), _at(g["dA"]), _at(g["dB"]),
         _at(g["dC"]), _at(g["dD"]), _at(g["dz"]), _at(g["ddelta_bias"]), _at(g["dh0"]),
         _at(workspace), have, _current(stream, dev))
@@ -409,10 +415,10 @@ def falcon_selective_scan_step(u, delta, A, Bm, Cm, h, D=None, z=None, delta_bia
     y = torch.empty(row, dtype=dt, device=dev) if y is None else _dense(y, "y", dt, row, dev)
     b, c = Bm.stride(), Cm.stride()
     rc = lib.falcon_selective_scan_step(
-        N, C, G, S, _DTYPE[dt], 1 if softplus else 0, _at(u), u.stride(0), _at(delta),
-        delta.stride(0), _at(A), _at(Bm), _strides(b[0], b[1], 0), _at(Cm),
+        N, C, G, S, _DTYPE[dt], 1 if softplus else 0, u.data_ptr(), u.stride(0), delta.data_ptr(),
+        delta.stride(0), A.data_ptr(), Bm.data_ptr(), _strides(b[0], b[1], 0), Cm.data_ptr(),
         _strides(c[0], c[1], 0), _at(D), _at(z), 0 if z is None else z.stride(0),
-        _at(delta_bias), _at(h), pool, _at(slots), _at(fresh), _at(y),
+        _at(delta_bias), h.data_ptr(), pool, _at(slots), _at(fresh), y.data_ptr(),
         _current(stream, dev))
     _check(rc, "falcon_selective_scan_step")
     return y
@@ -461,7 +467,7 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
         norm = torch.empty((), dtype=torch.float32, device=dev)
     workspace, have = _workspace(int(lib.falcon_clip_workspace_bytes(rows, len(grads))),
                                  workspace, dev)
-    rc = lib.falcon_clip_grad_norm(rows, len(grads), float(max_norm), float(eps), _at(norm),
+    rc = lib.falcon_clip_grad_norm(rows, len(grads), float(max_norm), float(eps), norm.data_ptr(),
                                    _at(workspace), have, _current(stream, dev))
     _check(rc, "falcon_clip_grad_norm")
     return norm

@@ -24,7 +24,8 @@ __global__ void __launch_bounds__(kThreads)
   const bool live = at < (unsigned)(a.N * pairs);
   const int row = live ? (int)(at / (unsigned)pairs) : 0;
   const int d = live ? (int)(at - (unsigned)row * (unsigned)pairs) * 2 : 0;
-  const int have = WHOLE ? 2 : !live ? 0 : d + 1 < a.D ? 2 : 1;  // WHOLE: surplus lanes read row 0
+  // surplus lanes of a whole launch read row 0 and store nothing
+  const int have = WHOLE ? 2 : !live ? 0 : d + 1 < a.D ? 2 : 1;
   const int64_t slot = a.slots ? a.slots[row] : row;
   const bool has = live && slot >= 0 && slot < a.pool;
   const bool fresh = a.fresh && a.fresh[row];
@@ -46,11 +47,12 @@ __global__ void __launch_bounds__(kThreads)
   const float4 C0 = widen(load_quad<E>(Cm + g0 * a.cs.head, vec_bc, kb));
   const float4 B1 = g1 == g0 ? B0 : widen(load_quad<E>(Bm + g1 * a.bs.head, vec_bc, kb));
   const float4 C1 = g1 == g0 ? C0 : widen(load_quad<E>(Cm + g1 * a.cs.head, vec_bc, kb));
-  const float2 u = widen(load_pair<E>(static_cast<const E*>(a.u) + row * a.u_stride + d, vec_ch, have));
-  float2 s =
-      widen(load_pair<E>(static_cast<const E*>(a.delta) + row * a.delta_stride + d, vec_ch, have));
-  float2 z = make_float2(0.f, 0.f);
-  if (a.z) z = widen(load_pair<E>(static_cast<const E*>(a.z) + row * a.z_stride + d, vec_ch, have));
+  auto pair_of = [&](const void* p, int64_t stride) {
+    return widen(load_pair<E>(static_cast<const E*>(p) + row * stride + d, vec_ch, have));
+  };
+  const float2 u = pair_of(a.u, a.u_stride);
+  float2 s = pair_of(a.delta, a.delta_stride), z = make_float2(0.f, 0.f);
+  if (a.z) z = pair_of(a.z, a.z_stride);
   if (a.delta_bias) {
     if (have > 0) s.x += a.delta_bias[d];
     if (have > 1) s.y += a.delta_bias[d + 1];

@@ -170,7 +170,8 @@ __device__ __forceinline__ float2 decay2(f32x2 s, f32x2 A2, f32x2 lift) {
 }
 // softplus() twice.
 __device__ __forceinline__ float2 softplus2(float2 x) {
-  const float2 e = make_float2(exp2_approx(-fabsf(x.x) * kLog2e), exp2_approx(-fabsf(x.y) * kLog2e));
+  const float2 e =
+      make_float2(exp2_approx(-fabsf(x.x) * kLog2e), exp2_approx(-fabsf(x.y) * kLog2e));
   const float2 den = unpack2(add2(pair2(e), pack2(2.f, 2.f)));
   const f32x2 w = mul2(pair2(e), pack2(rcp_approx(den.x), rcp_approx(den.y)));
   const f32x2 q = mul2(w, w);

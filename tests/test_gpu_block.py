@@ -251,6 +251,15 @@ def test_scan_lengths(dtype, T):
     _scan_check(_scan_case(g, dtype, 2, T, 16, 1, 16, state=T % 2 == 1), dtype)
 
 
+@pytest.mark.parametrize("T,D,N,ragged", [(1301, 16, 16, True), (1100, 40, 8, False),
+                                          (600, 8, 33, True), (1030, 6, 1, True)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scan_split_over_many_segments(dtype, T, D, N, ragged):
+    g = _gen(T)
+    _scan_check(_scan_case(g, dtype, 2, T, D, 1, N, state=True, ragged=ragged), dtype,
+                poison=ragged)
+
+
 @pytest.mark.parametrize("T,N,G", [(1, 16, 1), (9, 16, 2), (40, 16, 1), (130, 8, 4), (67, 40, 1),
                                    (257, 16, 1)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
