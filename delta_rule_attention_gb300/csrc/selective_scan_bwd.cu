@@ -633,33 +633,6 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32, LN == 4 ? 3 : 1)
     }
 }
 
-// Step 4.
-template <typename E>
-__global__ void __launch_bounds__(256)
-    scan_bwd_bc_kernel(const __grid_constant__ ScanArgs a, const float* ws,
-                       const __grid_constant__ Layout l) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t rows = a.B * a.T * a.G, quads = 2 * l.NP / 4;
-  if (i >= rows * quads) return;
-  const int64_t row = i / quads;
-  const int w = (int)(i - row * quads), n0 = w * 4 % (int)l.NP;
-  const int64_t bt = row / a.G, b = bt / a.T;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (bt - b * a.T < row_length(a.lengths, b, a.T)) {
-    const float* from = ws + l.dbc + i * 4;
-#pragma unroll 4
-    for (int64_t p = 0; p < l.parts; ++p) {
-      const float4 e = *reinterpret_cast<const float4*>(from + p * rows * 2 * l.NP);
-      v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
-    }
-  }
-  E* to = static_cast<E*>(w * 4 < l.NP ? a.dB : a.dC) + row * a.N + n0;
-  const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (n0 + k < a.N) store_vec<E, 1>(to + k, FloatV<1>{{f[k]}});
-}
-
 // Rows of `width` values summed over `parts`: a warp's lanes hold neighbouring
 // values, a block's eight warps an eighth of the parts each.
 __device__ __forceinline__ float sum_parts(const float* from, int64_t width, int64_t at,
@@ -679,13 +652,14 @@ __device__ __forceinline__ float sum_parts(const float* from, int64_t width, int
   return v;
 }
 
-// Blocks over the padded [D,NP] values of dA, then over the D of dDskip and ddelta_bias.
+// Step 4: the first `first` blocks sum the padded [D,NP] values of dA, the next ones up
+// to `second` the D of dDskip and ddelta_bias, the others dB and dC.
+template <typename E>
 __global__ void __launch_bounds__(256)
-    scan_bwd_param_kernel(const __grid_constant__ ScanArgs a, const float* ws,
-                          const __grid_constant__ Layout l) {
+    scan_bwd_sum_kernel(const __grid_constant__ ScanArgs a, const float* ws,
+                        const __grid_constant__ Layout l, int64_t first, int64_t second) {
   __shared__ float sh[8][32];
   const int64_t parts = l.groups * a.B, width = (int64_t)a.D * l.NP;
-  const int64_t first = (width + 31) / 32;
   const int lane = threadIdx.x & 31;
   if (blockIdx.x < first) {
     const int64_t at = (int64_t)blockIdx.x * 32 + lane, d = at / l.NP, n = at - d * l.NP;
@@ -693,13 +667,36 @@ __global__ void __launch_bounds__(256)
     if (threadIdx.x < 32 && at < width && n < a.N) a.dA[d * a.N + n] = v;
     return;
   }
-  const int64_t d = (blockIdx.x - first) * 32 + lane;
-  const float v = sum_parts(ws + l.dD, a.D, d, parts, sh);
-  const float w = sum_parts(ws + l.dbias, a.D, d, parts, sh);
-  if (threadIdx.x < 32 && d < a.D) {
-    if (a.dDskip) a.dDskip[d] = v;
-    if (a.ddelta_bias) a.ddelta_bias[d] = w;
+  if (blockIdx.x < second) {
+    const int64_t d = (blockIdx.x - first) * 32 + lane;
+    const float v = sum_parts(ws + l.dD, a.D, d, parts, sh);
+    const float w = sum_parts(ws + l.dbias, a.D, d, parts, sh);
+    if (threadIdx.x < 32 && d < a.D) {
+      if (a.dDskip) a.dDskip[d] = v;
+      if (a.ddelta_bias) a.ddelta_bias[d] = w;
+    }
+    return;
   }
+  const int64_t i = (blockIdx.x - second) * 256 + threadIdx.x;
+  const int64_t rows = a.B * a.T * a.G, quads = 2 * l.NP / 4;
+  if (i >= rows * quads) return;
+  const int64_t row = i / quads;
+  const int w = (int)(i - row * quads), n0 = w * 4 % (int)l.NP;
+  const int64_t bt = row / a.G, b = bt / a.T;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (bt - b * a.T < row_length(a.lengths, b, a.T)) {
+    const float* from = ws + l.dbc + i * 4;
+#pragma unroll 8
+    for (int64_t p = 0; p < l.parts; ++p) {
+      const float4 e = *reinterpret_cast<const float4*>(from + p * rows * 2 * l.NP);
+      v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
+    }
+  }
+  E* to = static_cast<E*>(w * 4 < l.NP ? a.dB : a.dC) + row * a.N + n0;
+  const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (n0 + k < a.N) store_vec<E, 1>(to + k, FloatV<1>{{f[k]}});
 }
 
 template <typename E, int LN>
@@ -710,13 +707,9 @@ cudaError_t bwd_lanes(const ScanArgs& a, cudaStream_t stream) {
   const int bc = kChunk * 2 * C::kNP * 4;
   const int bytes1 = bc + C::kWarps * (int)sizeof(WarpShared<LN>);
   const int bytes3 = bytes1 + C::kWarps * (int)sizeof(GradShared<LN>);
-  cudaError_t e = cudaSuccess;
-  if (bytes1 > 48 * 1024)
-    e = cudaFuncSetAttribute(scan_bwd_chunk_kernel<E, LN>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes1);
-  if (e == cudaSuccess && bytes3 > 48 * 1024)
-    e = cudaFuncSetAttribute(scan_bwd_grad_kernel<E, LN>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes3);
+  static std::atomic<uint64_t> done1, done3;
+  cudaError_t e = allow_shared(scan_bwd_chunk_kernel<E, LN>, bytes1, &done1);
+  if (e == cudaSuccess) e = allow_shared(scan_bwd_grad_kernel<E, LN>, bytes3, &done3);
   if (e != cudaSuccess) return e;
   const int64_t blocks = a.G * l.parts;
   if (blocks * l.chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -733,12 +726,10 @@ cudaError_t bwd_lanes(const ScanArgs& a, cudaStream_t stream) {
   if (l.chunks > 0) {
     scan_bwd_grad_kernel<E, LN><<<groups, C::kWarps * 32, bytes3, stream>>>(a, ws, l);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int64_t sums = a.B * a.T * a.G * 2 * LN;
-    scan_bwd_bc_kernel<E><<<(unsigned)((sums + 255) / 256), 256, 0, stream>>>(a, ws, l);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const int64_t params = ((int64_t)a.D * l.NP + 31) / 32 + (a.D + 31) / 32;
-  scan_bwd_param_kernel<<<(unsigned)params, 256, 0, stream>>>(a, ws, l);
+  const int64_t first = ((int64_t)a.D * l.NP + 31) / 32, second = first + (a.D + 31) / 32;
+  const int64_t sums = second + (a.B * a.T * a.G * 2 * LN + 255) / 256;
+  scan_bwd_sum_kernel<E><<<(unsigned)sums, 256, 0, stream>>>(a, ws, l, first, second);
   return cudaGetLastError();
 }
 

@@ -6,7 +6,7 @@
 namespace falcon {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // LN lanes share two neighbouring channels.  vec_h: S is a multiple of four and
 // the states lie on 16-byte boundaries; vec_ch, vec_bc: channel pairs and quads of B
@@ -18,18 +18,19 @@ __global__ void __launch_bounds__(kThreads)
     scan_step_kernel(const __grid_constant__ ScanStepArgs a) {
   const bool vec_h = WHOLE || a.vec_h, vec_A = WHOLE || a.vec_A, vec_ch = WHOLE || a.vec_ch,
              vec_bc = WHOLE || a.vec_bc;
-  const int pairs = (a.D + 1) / 2;  // of a row
-  const unsigned at = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / LN;
+  // a block stays within one row, whose addresses are then the same for all its lanes
+  const int row = blockIdx.x, pairs = (a.D + 1) / 2;
+  const int at = ((int)blockIdx.y * kThreads + (int)threadIdx.x) / LN;
   const int q = threadIdx.x % LN, n0 = q * 4;
-  const bool live = at < (unsigned)(a.N * pairs);
-  const int row = live ? (int)(at / (unsigned)pairs) : 0;
-  const int d = live ? (int)(at - (unsigned)row * (unsigned)pairs) * 2 : 0;
-  // surplus lanes of a whole launch read row 0 and store nothing
+  const bool live = at < pairs;
+  const int d = live ? at * 2 : 0;
+  // surplus lanes of a whole launch read channel 0 and store nothing
   const int have = WHOLE ? 2 : !live ? 0 : d + 1 < a.D ? 2 : 1;
   const int64_t slot = a.slots ? a.slots[row] : row;
   const bool has = live && slot >= 0 && slot < a.pool;
   const bool fresh = a.fresh && a.fresh[row];
-  const int R = a.D / a.G, g0 = d / R, g1 = !WHOLE && have == 2 ? (d + 1) / R : g0;
+  const int R = a.G == 1 ? a.D : a.D / a.G, g0 = a.G == 1 ? 0 : d / R;
+  const int g1 = !WHOLE && have == 2 && a.G > 1 ? (d + 1) / R : g0;
   float* hp = a.h + ((has ? slot : 0) * a.D + d) * a.S + n0;
   // states of this lane
   const int own = WHOLE ? 4 : n0 < a.S ? (a.S - n0 < 4 ? a.S - n0 : 4) : 0;
@@ -59,14 +60,17 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (a.softplus) s = softplus2(s);
   float o[2];
+  const f32x2 lift = pack2(kDecayLift, kDecayLift);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const float sc = c ? s.y : s.x, v = sc * (c ? u.y : u.x), s2 = sc * kLog2e;
     const float4 B = c ? B1 : B0, Ct = c ? C1 : C0;
-    h[c].x = fmaf(decay(s2, A[c].x), h[c].x, v * B.x);
-    h[c].y = fmaf(decay(s2, A[c].y), h[c].y, v * B.y);
-    h[c].z = fmaf(decay(s2, A[c].z), h[c].z, v * B.z);
-    h[c].w = fmaf(decay(s2, A[c].w), h[c].w, v * B.w);
+    const float2 d0 = decay2(pack2(s2, s2), pack2(A[c].x, A[c].y), lift);
+    const float2 d1 = decay2(pack2(s2, s2), pack2(A[c].z, A[c].w), lift);
+    h[c].x = fmaf(d0.x, h[c].x, v * B.x);
+    h[c].y = fmaf(d0.y, h[c].y, v * B.y);
+    h[c].z = fmaf(d1.x, h[c].z, v * B.z);
+    h[c].w = fmaf(d1.y, h[c].w, v * B.w);
     o[c] = fmaf(Ct.w, h[c].w, fmaf(Ct.z, h[c].z, fmaf(Ct.y, h[c].y, Ct.x * h[c].x)));
     if (has && c < have) {
       float* to = hp + c * a.S;
@@ -98,14 +102,15 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename E, int LN>
 cudaError_t step_lanes(const ScanStepArgs& a, cudaStream_t stream) {
-  const int64_t blocks = (a.N * ((a.D + 1) / 2) * LN + kThreads - 1) / kThreads;
-  if (blocks > 0xffffffffLL / kThreads) return cudaErrorInvalidValue;
+  const int64_t blocks = ((int64_t)((a.D + 1) / 2) * LN + kThreads - 1) / kThreads;
+  if (blocks > 65535) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)a.N, (unsigned)blocks);
   const bool whole = a.vec_h && a.vec_A && a.vec_ch && a.vec_bc && a.S == 4 * LN &&
                      a.D / a.G % 2 == 0;
   if (whole)
-    scan_step_kernel<E, LN, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    scan_step_kernel<E, LN, true><<<grid, kThreads, 0, stream>>>(a);
   else
-    scan_step_kernel<E, LN, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    scan_step_kernel<E, LN, false><<<grid, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -2,6 +2,8 @@
 // vector loads of bf16 or fp32 rows, softplus and silu in fp32.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace falcon {
@@ -357,6 +359,21 @@ cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream);
 size_t clip_workspace_bytes(const falcon_grad* grads, int64_t tensors);
 cudaError_t launch_clip(const falcon_grad* grads, int64_t tensors, float max_norm, float eps,
                         float* norm, void* ws, cudaStream_t stream);
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device; asked
+// once for each kernel (one `done` each) and device.
+template <typename K>
+inline cudaError_t allow_shared(K kernel, int bytes, std::atomic<uint64_t>* done) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (bit && (done->load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Row length of batch entry b.
 __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b, int64_t T) {

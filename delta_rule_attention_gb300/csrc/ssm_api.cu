@@ -316,7 +316,8 @@ int falcon_selective_scan_step(int64_t N, int32_t D, int32_t G, int32_t S, int32
   if (rc) return rc;
   if (N < 0 || pool < 0) return FALCON_ERR_BAD_SHAPE;
   if (N == 0 || D == 0) return FALCON_OK;
-  if (N > kMostGrid / D) return FALCON_ERR_BAD_SHAPE;
+  // rows along x, 128 lanes of channel pairs along y of the grid
+  if (N > kMostGrid / D || D > (1 << 18)) return FALCON_ERR_BAD_SHAPE;
   if (!u || !delta || !A || !Bm || !Cm || !bs || !cs || !y || (pool > 0 && !h))
     return FALCON_ERR_NULL_PTR;
   if (u_stride < 0 || delta_stride < 0 || (z && z_stride < 0) || negative(bs) || negative(cs))

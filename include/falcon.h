@@ -554,7 +554,8 @@ int falcon_selective_scan_bwd(const falcon_scan_shape *shape, const void *u,
 
 /* One token of N sequences: u, delta, z [N,D] dtype with row strides, Bm, Cm
  * [N,G,S] dtype (`batch` the row's stride, `head` the group's), y [N,D] dtype
- * dense, out; h [pool,D,S] f32, updated in place.  S states a channel (1 .. 128). */
+ * dense, out; h [pool,D,S] f32, updated in place.  S states a channel (1 .. 128),
+ * D up to 262144. */
 int falcon_selective_scan_step(int64_t N, int32_t D, int32_t G, int32_t S,
                                int32_t dtype, int32_t softplus, const void *u,
                                int64_t u_stride, const void *delta,
