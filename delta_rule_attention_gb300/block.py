@@ -161,9 +161,18 @@ def _dtype(t, name):
     return t.dtype
 
 
-def _workspace(need, workspace, device):
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on ``stream``: memory given back on the current stream must
+    not be reused before a call on another one is done with it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _workspace(need, workspace, device, stream):
     if workspace is None:
-        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
+        return (_empty(need, torch.uint8, device, stream), need) if need else (None, 0)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -204,9 +213,9 @@ def falcon_short_conv_fwd(x, weight, bias=None, state=None, lengths=None, activa
     and the last width-1 inputs of every row."""
     lib = _library()
     shape, dt, dev, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
-    y = torch.empty(x.shape, dtype=dt, device=dev) if y is None else \
+    y = _empty(x.shape, dt, dev, stream) if y is None else \
         _rows(y, "y", dt, x.shape, dev)
-    state_out = torch.empty((B, W - 1, C), dtype=dt, device=dev) if state_out is None else \
+    state_out = _empty((B, W - 1, C), dt, dev, stream) if state_out is None else \
         _dense(state_out, "state_out", dt, (B, W - 1, C), dev)
     rc = lib.falcon_short_conv_fwd(shape, x.data_ptr(), _conv_rows(x), weight.data_ptr(), _at(bias),
                                    _at(state), _at(lengths), y.data_ptr(), _conv_rows(y),
@@ -226,20 +235,20 @@ def falcon_short_conv_bwd(x, weight, dy, bias=None, state=None, lengths=None, ds
     _dense(dstate_out, "dstate_out", dt, (B, W - 1, C), dev)
     g = {} if grads is None else grads
     if "dx" not in g:
-        g["dx"] = torch.empty(x.shape, dtype=dt, device=dev)
+        g["dx"] = _empty(x.shape, dt, dev, stream)
     if "dweight" not in g:
-        g["dweight"] = torch.empty((C, W), dtype=torch.float32, device=dev)
+        g["dweight"] = _empty((C, W), torch.float32, dev, stream)
     if "dbias" not in g:
-        g["dbias"] = torch.empty((C,), dtype=torch.float32, device=dev)
+        g["dbias"] = _empty((C,), torch.float32, dev, stream)
     if "dstate" not in g:
-        g["dstate"] = torch.empty((B, W - 1, C), dtype=dt, device=dev)
+        g["dstate"] = _empty((B, W - 1, C), dt, dev, stream)
     if grads is not None:
         _rows(g["dx"], "dx", dt, x.shape, dev)
         _dense(g["dweight"], "dweight", torch.float32, (C, W), dev)
         _dense(g["dbias"], "dbias", torch.float32, (C,), dev)
         _dense(g["dstate"], "dstate", dt, (B, W - 1, C), dev)
     workspace, have = _workspace(int(lib.falcon_short_conv_bwd_workspace_bytes(shape)),
-                                 workspace, dev)
+                                 workspace, dev, stream)
     rc = lib.falcon_short_conv_bwd(
         shape, x.data_ptr(), _conv_rows(x), weight.data_ptr(), _at(bias), _at(state),
         _at(lengths), dy.data_ptr(),
@@ -271,7 +280,7 @@ def falcon_short_conv_step(x, weight, state, bias=None, slots=None, fresh=None,
     _dense(state, "state", dt, (pool, W - 1, C), dev)
     _dense(slots, "slots", torch.int32, (N,), dev)
     _dense(fresh, "fresh", torch.uint8, (N,), dev)
-    y = torch.empty((N, C), dtype=dt, device=dev) if y is None else \
+    y = _empty((N, C), dt, dev, stream) if y is None else \
         _dense(y, "y", dt, (N, C), dev)
     rc = lib.falcon_short_conv_step(N, C, W, _DTYPE[dt], _ACT[activation], x.data_ptr(),
                                     x.stride(0), weight.data_ptr(), _at(bias), _at(state), pool,
@@ -331,9 +340,9 @@ def falcon_selective_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=No
     [D] and h0 [B,D,N] fp32; lengths [B] int32.  Returns (y, h_T)."""
     lib = _library()
     shape, dt, dev, hs = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
-    y = torch.empty(u.shape, dtype=dt, device=dev) if y is None else \
+    y = _empty(u.shape, dt, dev, stream) if y is None else \
         _rows(y, "y", dt, u.shape, dev)
-    h_out = torch.empty(hs, dtype=torch.float32, device=dev) if h_out is None else \
+    h_out = _empty(hs, torch.float32, dev, stream) if h_out is None else \
         _dense(h_out, "h_out", torch.float32, hs, dev)
     rc = lib.falcon_selective_scan_fwd(
         shape, u.data_ptr(), _time_rows(u), delta.data_ptr(), _time_rows(delta), A.data_ptr(),
@@ -371,9 +380,9 @@ def falcon_selective_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bia
         elif name in g:
             _dense(g[name], name, *spec, dev)
         else:
-            g[name] = torch.empty(spec[1], dtype=spec[0], device=dev)
+            g[name] = _empty(spec[1], spec[0], dev, stream)
     workspace, have = _workspace(int(lib.falcon_selective_scan_bwd_workspace_bytes(shape)),
-                                 workspace, dev)
+                                 workspace, dev, stream)
     rc = lib.falcon_selective_scan_bwd(
         shape, u.data_ptr(), _time_rows(u), delta.data_ptr(), _time_rows(delta), A.data_ptr(),
         Bm.data_ptr(),
@@ -412,7 +421,7 @@ def falcon_selective_scan_step(u, delta, A, Bm, Cm, h, D=None, z=None, delta_bia
     _dense(h, "h", f32, (pool, C, S), dev)
     _dense(slots, "slots", torch.int32, (N,), dev)
     _dense(fresh, "fresh", torch.uint8, (N,), dev)
-    y = torch.empty(row, dtype=dt, device=dev) if y is None else _dense(y, "y", dt, row, dev)
+    y = _empty(row, dt, dev, stream) if y is None else _dense(y, "y", dt, row, dev)
     b, c = Bm.stride(), Cm.stride()
     rc = lib.falcon_selective_scan_step(
         N, C, G, S, _DTYPE[dt], 1 if softplus else 0, u.data_ptr(), u.stride(0), delta.data_ptr(),
@@ -464,9 +473,9 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
     rows = ctypes.cast(table.buffer_info()[0], ctypes.POINTER(falcon_grad))
     dev = grads[0].device
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
+        norm = _empty((), torch.float32, dev, stream)
     workspace, have = _workspace(int(lib.falcon_clip_workspace_bytes(rows, len(grads))),
-                                 workspace, dev)
+                                 workspace, dev, stream)
     rc = lib.falcon_clip_grad_norm(rows, len(grads), float(max_norm), float(eps), norm.data_ptr(),
                                    _at(workspace), have, _current(stream, dev))
     _check(rc, "falcon_clip_grad_norm")

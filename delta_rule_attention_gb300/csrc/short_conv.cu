@@ -467,11 +467,11 @@ cudaError_t launch_conv_bwd(const ConvArgs& in, cudaStream_t stream) {
   a.vec_w = fits(a.weight, 16);
   const int esz = a.dtype == FALCON_BF16 ? 2 : 4;
   const int64_t tail = a.B * (a.width - 1) * a.C;
-  if (a.T == 0) {  // no token: dweight = dbias = 0, dstate = dstate_out
+  if (a.T == 0 || a.B == 0) {  // no token: dweight = dbias = 0, dstate = dstate_out
     cudaError_t e = cudaMemsetAsync(a.dweight, 0, sizeof(float) * a.C * a.width, stream);
     if (e == cudaSuccess && a.dbias)
       e = cudaMemsetAsync(a.dbias, 0, sizeof(float) * a.C, stream);
-    if (e != cudaSuccess || !a.dstate) return e;
+    if (e != cudaSuccess || !a.dstate || tail == 0) return e;
     if (!a.dstate_out) return cudaMemsetAsync(a.dstate, 0, (size_t)tail * esz, stream);
     return cudaMemcpyAsync(a.dstate, a.dstate_out, (size_t)tail * esz, cudaMemcpyDeviceToDevice,
                            stream);

@@ -448,6 +448,49 @@ def test_calls_run_on_the_callers_stream_and_in_graphs():
     del outs
 
 
+def test_calls_on_a_given_stream_keep_their_memory():
+    """A call on another stream than the current one: what it allocates is not handed
+    out again before the call is done with it."""
+    g = _gen(17)
+    m = falcon()
+    d = _cuda(_scan_case(g, BF16, 2, 600, 256, 1, 16))
+    dy = _draw(g, 2, 600, 256, dtype=BF16).cuda()
+    w = _draw(g, 256, 4).cuda()
+    want = m.falcon_selective_scan_bwd(**d, dy=dy)
+    cw = m.falcon_short_conv_bwd(d["u"], w, dy)
+    n0 = m.falcon_clip_grad_norm([want["dA"]], 1e9)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        got = m.falcon_selective_scan_bwd(**d, dy=dy, stream=side)
+        cg = m.falcon_short_conv_bwd(d["u"], w, dy, stream=side)
+        n1 = m.falcon_clip_grad_norm([want["dA"]], 1e9, stream=side)
+        # the current stream writes over whatever the allocator holds free
+        for _ in range(8):
+            torch.full((1 << 22,), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], want[k]) for k in want)
+        assert all(torch.equal(cg[k], cw[k]) for k in cw)
+        assert float(n0) == float(n1)
+
+
+def test_no_row_at_all():
+    m = falcon()
+    x = torch.empty(0, 5, 16, device="cuda")
+    w = torch.ones(16, 4, device="cuda")
+    y, tail = m.falcon_short_conv_fwd(x, w)
+    assert y.shape == x.shape and tail.shape == (0, 3, 16)
+    got = m.falcon_short_conv_bwd(x, w, x)
+    assert not got["dweight"].any() and not got["dbias"].any()
+    A, bc = -torch.ones(16, 8, device="cuda"), torch.empty(0, 5, 1, 8, device="cuda")
+    y, h = m.falcon_selective_scan_fwd(x, x, A, bc, bc)
+    assert h.shape == (0, 16, 8)
+    got = m.falcon_selective_scan_bwd(x, x, A, bc, bc, x, D=torch.ones(16, device="cuda"))
+    assert not got["dA"].any() and not got["dD"].any()
+    one = torch.empty(0, 16, device="cuda")
+    assert m.falcon_short_conv_step(one, w, torch.empty(0, 3, 16, device="cuda")).shape == (0, 16)
+
+
 # ------------------------------------------------------------------------- clip
 
 def _clip_ref(grads, max_norm, eps=1e-6):
