@@ -7,6 +7,9 @@
 // back, where L2 still holds what the first launch read last.  The
 // tensors' addresses travel as kernel arguments; more than kMost tensors take
 // further launches of each kind.
+//
+// Bound by memory: 88 M bf16 gradients (177 MB) 31 and 56 us alone, 88 to 92 us a call;
+// reading them twice and writing them once at a copy's rate takes 78.
 
 #include "ssm.cuh"
 

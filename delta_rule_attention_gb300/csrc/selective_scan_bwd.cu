@@ -21,8 +21,14 @@
 // added up over the lane's two channels in registers, over the warp's lanes through
 // shared memory, and over the block's warps when the chunk ends.
 //
-// Bound by instruction issue: about 27 instructions a lane for each (token, channel,
-// state), of them two exponentials.
+// B8 T2048 D2048 N16 bf16: 0.91 ms, of which step 1 takes 197 us, step 2 about 40, step 3 650,
+// step 4 17; its bytes would take 70 us.  Steps 1 and 3 are bound by instruction issue and
+// shared memory together (70% and 71% busy in step 1, 59% and 66% in step 3, whose
+// 167 registers and 77 KB leave three blocks an SM): about ten and 27 instructions a
+// lane for each (token, channel, state), three exponentials among them.  A chunk of 32
+// costs step 2 a state and an adjoint for every 32 tokens (0.2 GB there and back); a group
+// of four tokens is what fits the registers with its states and decays.  Measured and not
+// kept: scalar arithmetic instead of doubled scalars in pairs (954 us).
 
 #include <initializer_list>
 
@@ -287,8 +293,7 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
 }
 
 // Step 2: hin[c] becomes the state entering chunk c (blockIdx.z = 0), gin[c] the
-// adjoint entering it from behind (blockIdx.z = 1).  Bound by latency: a thread's walk
-// is serial, so it keeps sixteen chunks' loads under way.
+// adjoint entering it from behind (blockIdx.z = 1), four chunks' loads ahead.
 __global__ void __launch_bounds__(128)
     scan_bwd_chain_kernel(const __grid_constant__ ScanArgs a, float* ws,
                           const __grid_constant__ Layout l) {
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(128)
   const int64_t step = dir * a.D * l.NP, sstep = dir * a.D;
   float* hp = ws + (back ? l.gin : l.hin) + ((b * l.chunks + start) * a.D + d) * l.NP + n0;
   const float* sp = ws + l.sums + (b * l.chunks + start) * a.D + d;
-  constexpr int kAhead = 16;
+  constexpr int kAhead = 4;
   for (int c0 = 0; c0 < count; c0 += kAhead) {
     float4 hv[kAhead];
     float hs[kAhead];

@@ -9,6 +9,12 @@
 // it (and after it, for the gradient), are loaded before the first is used, so
 // that the traffic does not wait for the arithmetic.  A run's edge rows are read
 // twice, the second time from cache.
+//
+// B8 H12 T2048 m64 W4 bf16, silu, from strided heads: 15.4 us (3.3 TB/s of the 50 MB it
+// must move; issue slots 63% busy).  Its gradient for B8 T2048 C2048: 57 us and 6 for
+// the sums (3.5 TB/s of 202 MB): bound by the latency of its loads at 17 warps an SM.
+// Eight tokens a forward run and four channels a thread: 16.8 us with eight
+// channels, 15.0 with runs of 16, 19.3 with runs of 4.
 
 #include <type_traits>
 
@@ -489,7 +495,8 @@ cudaError_t launch_conv_bwd(const ConvArgs& in, cudaStream_t stream) {
 
 cudaError_t launch_conv_step(const ConvStepArgs& in, cudaStream_t stream) {
   // four channels a thread for either type: the call is short, and more threads
-  // with fewer loads each end sooner
+  // with fewer loads each end sooner (256 sequences of 2048 channels, bf16: 5.3 us,
+  // 12.6 with eight channels and filters read one weight at a time)
   ConvStepArgs a = in;
   a.vec_w = fits(a.weight, 16);
   const int bytes = a.dtype == FALCON_BF16 ? 8 : 16;

@@ -3,7 +3,9 @@
  * library: chunk-parallel forward of Falcon-1 and Falcon-1A and its backward
  * pass, the forward of Falcon-2 and Falcon-2A (per-column step sizes) and of
  * Falcon-3A (sliding window) in token-recurrent and chunk form, and the
- * single-token recurrent decode step.
+ * single-token recurrent decode step.  Beside these, the operators of a
+ * selective state space block (short causal convolution, selective scan,
+ * clipping of a step's gradients), in a part of their own below.
  *
  * The operations are defined on the page hyper.ai/fr/papers/2608.27763
  * ("Fast Weight Attention for Continual Learning"):
