@@ -55,11 +55,11 @@ struct Cfg {
   static constexpr int kChannels = 2 * kGroups;  // channels of a warp
   static constexpr int kNP = 4 * LN;             // states, padded
   static constexpr int kRow = kGroups;
-  // Where a row keeps its channel pair: rows are turned against one another so
-  // that the lanes of a store phase (LN tokens of a pair) fall in different banks.
-  __device__ static constexpr int at(int k, int pair) {
-    return pair ^ (LN == 2 ? (k & 1) << 2 : LN == 4 ? (k & 3) << 1 : LN == 8 ? (k >> 1) & 3
-                   : LN == 16 ? (k >> 2) & 1 : 0);
+  // A lane brings the tokens i * LN + q of channel pair `pair ^ turn(q)`, so that the
+  // eight lanes of a store phase, whose rows begin in the same bank, store to
+  // different places of them.
+  __host__ __device__ static constexpr int turn(int q) {
+    return LN == 2 ? q << 2 : LN == 4 ? q << 1 : LN == 8 ? q >> 1 : LN == 16 ? (q >> 2) & 1 : 0;
   }
   static constexpr int kBase = kGroups * kNP + 16;  // one token's dB (or dC) terms, padded
   // the chunk's dB and dC of a warp lie over its used steps where they fit
@@ -91,7 +91,7 @@ struct Layout {
     parts = (D / G + ch - 1) / ch;
     // chunks a block walks in step 3: as many as leave four blocks a resident slot
     per = 1;
-    while (per < 8 && G * parts * B * (chunks / (2 * per)) >= 152 * 3 * 4) per *= 2;
+    while (per < 8 && G * parts * B * (chunks / (2 * per)) >= 152 * 3 * 8) per *= 2;
     groups = (chunks + per - 1) / per;
     size_t at = 0;
     auto take = [&](int64_t n) {
@@ -118,6 +118,10 @@ struct Place {
   int64_t b, n;
   bool whole;
   float bias[2];
+  // the channel pair whose tokens this lane brings, its live channels, how far its
+  // channels are from d, and their biases
+  int brings, its_have, off;
+  float its_bias[2];
   const E *u, *dl, *z, *dy, *Bm, *Cm;
 
   __device__ __forceinline__ Place(const ScanArgs& a, int parts) {
@@ -134,6 +138,12 @@ struct Place {
     whole = a.vec_ch && w0 + C::kChannels <= R;
     bias[0] = have > 0 && a.delta_bias ? a.delta_bias[d] : 0.f;
     bias[1] = have > 1 && a.delta_bias ? a.delta_bias[d + 1] : 0.f;
+    brings = pair ^ C::turn(q);
+    const int r1 = w0 + brings * 2;
+    its_have = r1 >= R ? 0 : (r1 + 1 < R ? 2 : 1);
+    off = g * R + (its_have ? r1 : 0) - d;
+    its_bias[0] = its_have > 0 && a.delta_bias ? a.delta_bias[d + off] : 0.f;
+    its_bias[1] = its_have > 1 && a.delta_bias ? a.delta_bias[d + off + 1] : 0.f;
     u = static_cast<const E*>(a.u) + b * a.us.batch + d;
     dl = static_cast<const E*>(a.delta) + b * a.ds.batch + d;
     z = a.z ? static_cast<const E*>(a.z) + b * a.zs.batch + d : nullptr;
@@ -176,17 +186,17 @@ __device__ __forceinline__ float2 stage_chunk(const ScanArgs& a, const Place<E, 
   };
   float2 sum = make_float2(0.f, 0.f);
   auto put = [&](int k, float2 ut, float2 s, float2 o, float2 zt) {
-    s.x += p.bias[0], s.y += p.bias[1];
+    s.x += p.its_bias[0], s.y += p.its_bias[1];
     if (a.softplus) s = softplus2(s);
     if (p.z) o.x *= zt.x * sigmoid(zt.x), o.y *= zt.y * sigmoid(zt.y);
     if (!full) {  // no token, or a pair without a second (or any) channel
-      const int have = t0 + k < p.n ? p.have : 0;
+      const int have = t0 + k < p.n ? p.its_have : 0;
       if (have < 2) s.y = o.y = 0.f;
       if (have < 1) s.x = o.x = 0.f;
     }
     sum.x += s.x, sum.y += s.y;
-    ws.sv[k][C::at(k, p.pair)] = make_float4(s.x, s.y, s.x * ut.x, s.y * ut.y);
-    ws.dyg[k][C::at(k, p.pair)] = o;
+    ws.sv[k][p.brings] = make_float4(s.x, s.y, s.x * ut.x, s.y * ut.y);
+    ws.dyg[k][p.brings] = o;
   };
   for (int i0 = 0; i0 < kQuads; i0 += kQuadBatch) {
     Quad rq[kQuadBatch];
@@ -204,16 +214,16 @@ __device__ __forceinline__ float2 stage_chunk(const ScanArgs& a, const Place<E, 
           const int64_t t = t0 + (j0 + i) * LN + p.q;
           rz[i] = Pair();
           if (full) {
-            ru[i] = *reinterpret_cast<const Pair*>(p.u + t * a.us.time);
-            rd[i] = *reinterpret_cast<const Pair*>(p.dl + t * a.ds.time);
-            ro[i] = *reinterpret_cast<const Pair*>(p.dy + t * a.dys.time);
-            if (p.z) rz[i] = *reinterpret_cast<const Pair*>(p.z + t * a.zs.time);
+            ru[i] = *reinterpret_cast<const Pair*>(p.u + p.off + t * a.us.time);
+            rd[i] = *reinterpret_cast<const Pair*>(p.dl + p.off + t * a.ds.time);
+            ro[i] = *reinterpret_cast<const Pair*>(p.dy + p.off + t * a.dys.time);
+            if (p.z) rz[i] = *reinterpret_cast<const Pair*>(p.z + p.off + t * a.zs.time);
           } else {
-            const int have = t < p.n ? p.have : 0;
-            ru[i] = load_pair<E>(p.u + t * a.us.time, a.vec_ch, have);
-            rd[i] = load_pair<E>(p.dl + t * a.ds.time, a.vec_ch, have);
-            ro[i] = load_pair<E>(p.dy + t * a.dys.time, a.vec_ch, have);
-            if (p.z) rz[i] = load_pair<E>(p.z + t * a.zs.time, a.vec_ch, have);
+            const int have = t < p.n ? p.its_have : 0;
+            ru[i] = load_pair<E>(p.u + p.off + t * a.us.time, a.vec_ch, have);
+            rd[i] = load_pair<E>(p.dl + p.off + t * a.ds.time, a.vec_ch, have);
+            ro[i] = load_pair<E>(p.dy + p.off + t * a.dys.time, a.vec_ch, have);
+            if (p.z) rz[i] = load_pair<E>(p.z + p.off + t * a.zs.time, a.vec_ch, have);
           }
         }
 #pragma unroll
@@ -259,8 +269,8 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
   __syncthreads();
 #pragma unroll 4
   for (int k = 0; k < kChunk; ++k) {
-    const float4 sv = sh.sv[k][C::at(k, p.pair)];
-    const float2 o = sh.dyg[k][C::at(k, p.pair)];
+    const float4 sv = sh.sv[k][p.pair];
+    const float2 o = sh.dyg[k][p.pair];
     const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(&bc[k][0][p.n0]);
     const ulonglong2 Ct = *reinterpret_cast<const ulonglong2*>(&bc[k][1][p.n0]);
 #pragma unroll
@@ -275,10 +285,11 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
       }
     }
   }
+  // over the LN lanes that brought a pair's tokens; the lane with q = 0 brought its own's
 #pragma unroll
   for (int w = LN / 2; w > 0; w >>= 1) {
-    sum.x += __shfl_xor_sync(0xffffffffu, sum.x, w);
-    sum.y += __shfl_xor_sync(0xffffffffu, sum.y, w);
+    sum.x += __shfl_xor_sync(0xffffffffu, sum.x, C::turn(w) * LN + w);
+    sum.y += __shfl_xor_sync(0xffffffffu, sum.y, C::turn(w) * LN + w);
   }
   const int64_t row = (p.b * l.chunks + chunk) * a.D + p.d;
 #pragma unroll
@@ -405,7 +416,7 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32, LN == 4 ? 3 : 1)
       h[c][0] = hv.x, h[c][1] = hv.y, g[c][0] = gv.x, g[c][1] = gv.y;
     }
     auto forward = [&](int k, f32x2 (&hc)[2][2], f32x2 (&at)[2][2]) {
-      const float4 sv = sh.sv[k][C::at(k, p.pair)];
+      const float4 sv = sh.sv[k][p.pair];
       const ulonglong2 B = *reinterpret_cast<const ulonglong2*>(&bc[k][0][p.n0]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -476,8 +487,8 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32, LN == 4 ? 3 : 1)
       float2 gB[kSub], wA[kSub], yC[kSub];  // of both channels, this lane's states
 #pragma unroll
       for (int k = kSub - 1; k >= 0; --k) {
-        const float4 sv = sh.sv[k0 + k][C::at(k0 + k, p.pair)];
-        const float2 o = sh.dyg[k0 + k][C::at(k0 + k, p.pair)];
+        const float4 sv = sh.sv[k0 + k][p.pair];
+        const float2 o = sh.dyg[k0 + k][p.pair];
         const ulonglong2 Bq = *reinterpret_cast<const ulonglong2*>(&bc[k0 + k][0][p.n0]);
         const ulonglong2 Cq = *reinterpret_cast<const ulonglong2*>(&bc[k0 + k][1][p.n0]);
         f32x2 vB[2], vC[2];
@@ -549,8 +560,8 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32, LN == 4 ? 3 : 1)
           if (t < a.T) {
             float2 vu = make_float2(0.f, 0.f), vd = vu, vz = vu;
             if (t < p.n) {
-              const float4 sv = sh.sv[k][C::at(k, p.pair)];
-              const float2 o = sh.dyg[k][C::at(k, p.pair)];
+              const float4 sv = sh.sv[k][p.pair];
+              const float2 o = sh.dyg[k][p.pair];
               const float2 ut = widen(ru[m]);
               vu = make_float2(fmaf(gB[m].x, sv.x, skip0 * o.x), fmaf(gB[m].y, sv.y, skip1 * o.y));
               vd = make_float2(fmaf(gB[m].x, ut.x, wA[m].x * kLn2),
