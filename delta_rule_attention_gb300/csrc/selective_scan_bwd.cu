@@ -21,8 +21,8 @@
 // added up over the lane's two channels in registers, over the warp's lanes through
 // shared memory, and over the block's warps when the chunk ends.
 //
-// B8 T2048 D2048 N16 bf16: 0.91 ms, of which step 1 takes 197 us, step 2 about 40, step 3 650,
-// step 4 17; its bytes would take 70 us.  Steps 1 and 3 are bound by instruction issue and
+// B8 T2048 D2048 N16 bf16: 0.88 ms, of which step 1 takes 195 us, step 2 38, step 3 620,
+// step 4 18; its bytes would take 70 us.  Steps 1 and 3 are bound by instruction issue and
 // shared memory together (70% and 71% busy in step 1, 59% and 66% in step 3, whose
 // 167 registers and 77 KB leave three blocks an SM): about ten and 27 instructions a
 // lane for each (token, channel, state), three exponentials among them.  A chunk of 32

@@ -11,8 +11,8 @@
 // twice, the second time from cache.
 //
 // B8 H12 T2048 m64 W4 bf16, silu, from strided heads: 15.4 us (3.3 TB/s of the 50 MB it
-// must move; issue slots 63% busy).  Its gradient for B8 T2048 C2048: 57 us and 6 for
-// the sums (3.5 TB/s of 202 MB): bound by the latency of its loads at 17 warps an SM.
+// must move; issue slots 63% busy).  Its gradient for B8 T2048 C2048: 50 us and 6 for
+// the sums (3.6 TB/s of 202 MB): bound by the latency of its loads at 14 warps an SM.
 // Eight tokens a forward run and four channels a thread: 16.8 us with eight
 // channels, 15.0 with runs of 16, 19.3 with runs of 4.
 
@@ -256,14 +256,14 @@ __global__ void __launch_bounds__(kThreads)
     const int tail = dso && n - (W - 1) < te ? (int)(n - t0) - (W - 1) : total;
     // one block of tokens; WHOLE: all are the run's own tokens, and all inputs that
     // they complete are the run's own and not among the row's last
-    auto block = [&](int k0, auto whole) {
+    auto block = [&](int k0, const R(&xc)[kBwdBlock], const R(&gc)[kBwdBlock], auto whole) {
       constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
       for (int k = 0; k < kBwdBlock; ++k) {
         const int kt = k0 + k;  // token, counted from the run's first
         acc[W - 1] = zeros<V>();
-        win[W - 1] = open_row<E, V>(xr[k]);
-        FloatV<V> d = open_row<E, V>(gr[k]);  // zero where there is no token
+        win[W - 1] = open_row<E, V>(xc[k]);
+        FloatV<V> d = open_row<E, V>(gc[k]);  // zero where there is no token
         if (SILU && (WHOLE || kt < readable)) {
           // silu'(p) = s (1 + p (1 - s)), s = sigmoid(p)
           FloatV<V> p = f.bias;
@@ -308,11 +308,14 @@ __global__ void __launch_bounds__(kThreads)
                           ? (own < readable ? own : readable) : tail + W - 1;
 #pragma unroll 1
     for (int k0 = 0; k0 < total; k0 += kBwdBlock) {
-      if (k0 >= kBwdBlock && k0 + kBwdBlock <= plain)
-        block(k0, std::true_type());
-      else
-        block(k0, std::false_type());
+      R xc[kBwdBlock], gc[kBwdBlock];
+#pragma unroll
+      for (int k = 0; k < kBwdBlock; ++k) xc[k] = xr[k], gc[k] = gr[k];
       if (k0 + kBwdBlock < total) fetch(k0 + kBwdBlock);
+      if (k0 >= kBwdBlock && k0 + kBwdBlock <= plain)
+        block(k0, xc, gc, std::true_type());
+      else
+        block(k0, xc, gc, std::false_type());
     }
   }
   float* ws = a.ws + part * (W + 1) * a.C;
@@ -406,26 +409,35 @@ cudaError_t fwd_typed(const ConvArgs& a, cudaStream_t stream) {
   });
 }
 
-// The longest run (a run's W - 1 recomputed tokens cost less beside more) that
-// leaves a thousand threads of two channels an SM.
-int bwd_run(int64_t B, int64_t T, int64_t C) {
-  int run = 64;
-  while (run > 8 && (C + 1) / 2 * B * ((T + run - 1) / run) < 152 * 1024) run /= 2;
-  return run;
-}
-// Parts of the sums: one for every run while they are few.
-int bwd_parts(int64_t B, int64_t T, int64_t C) {
-  const int run = bwd_run(B, T, C);
-  const int64_t jobs = B * ((T + run - 1) / run);
-  const int64_t pairs = (C + 1) / 2, fill = (152 * 2048 + pairs - 1) / pairs;
-  return (int)(jobs < fill ? jobs : fill);
+// How the gradient's tokens are cut: runs (whole blocks of tokens) and parts of the
+// sums, one a run while they are few.  Of the runs up to 128 tokens, the one with the
+// least estimated time, in tokens of a thread: waves of resident blocks (four an SM)
+// times a run with its edge, and 0.06 for each part that the sums add up (measured: a
+// token 0.19 us, 64 parts 0.7 us).
+struct Cut {
+  int run, parts;
+};
+constexpr int kMostParts = 1024;
+Cut bwd_cut(int64_t B, int64_t T, int64_t C) {
+  Cut best = {kBwdBlock, 1};
+  double least = -1.0;
+  for (int run = kBwdBlock; run <= 128; run += kBwdBlock) {
+    const int64_t jobs = B * ((T + run - 1) / run);
+    const int64_t parts = jobs < kMostParts ? jobs : kMostParts;
+    const int64_t blocks = ((C + 1) / 2 * parts + kThreads - 1) / kThreads;
+    const int64_t waves = (blocks + 152 * 4 - 1) / (152 * 4), turns = (jobs + parts - 1) / parts;
+    const double cost = (double)(waves * turns) * (run + 8) + 0.06 * (double)parts;
+    if (least < 0.0 || cost <= least) least = cost, best = {run, (int)parts};
+    if (run >= T) break;
+  }
+  return best;
 }
 
 template <typename E, int V>
 cudaError_t bwd_typed(const ConvArgs& a, cudaStream_t stream) {
-  const int run = bwd_run(a.B, a.T, a.C);
+  const Cut cut = bwd_cut(a.B, a.T, a.C);
+  const int run = cut.run, parts = cut.parts;
   const int64_t nruns = (a.T + run - 1) / run;
-  const int parts = bwd_parts(a.B, a.T, a.C);
   const int64_t blocks = (a.C / V * parts + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   return with_width(a.width, a.act, [&](auto w, auto silu) {
@@ -454,7 +466,7 @@ cudaError_t step_typed(const ConvStepArgs& a, cudaStream_t stream) {
 
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C, int width) {
   if (B == 0 || T == 0 || C == 0) return 0;
-  return sizeof(float) * (size_t)bwd_parts(B, T, C) * (size_t)(width + 1) * (size_t)C;
+  return sizeof(float) * (size_t)bwd_cut(B, T, C).parts * (size_t)(width + 1) * (size_t)C;
 }
 
 cudaError_t launch_conv_fwd(const ConvArgs& in, cudaStream_t stream) {
@@ -482,8 +494,8 @@ cudaError_t launch_conv_bwd(const ConvArgs& in, cudaStream_t stream) {
     return cudaMemcpyAsync(a.dstate, a.dstate_out, (size_t)tail * esz, cudaMemcpyDeviceToDevice,
                            stream);
   }
-  // two channels a thread: four need 170 registers (97 us for 8 x 2048 x 2048
-  // bf16 elements, against 68 us with two)
+  // two channels a thread: four need over 150 registers (97 us for 8 x 2048 x 2048
+  // bf16 elements when runs were 8 tokens long, against 68 with two)
   const int bytes = 2 * esz;
   const bool vec = a.m % 2 == 0 && fits(a.x, bytes) && fits(a.dy, bytes) && fits(a.dx, bytes) &&
                    fits(a.state, bytes) && fits(a.dstate_out, bytes) && fits(a.dstate, bytes) &&
