@@ -497,7 +497,7 @@ int falcon_short_conv_step(int64_t N, int32_t C, int32_t width, int32_t dtype,
                            const uint8_t *fresh, void *y, cudaStream_t stream);
 
 /* B rows of T tokens, D channels in G groups (D a multiple of G) that share
- * their B and C vectors, N states a channel (1 .. 128); softplus nonzero:
+ * their B and C vectors, N states a channel (1 .. 128), B at most 65535; softplus nonzero:
  * the step size is softplus(delta + delta_bias), otherwise their sum. */
 typedef struct {
   int64_t B, T;
