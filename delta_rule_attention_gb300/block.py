@@ -98,9 +98,11 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _current(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else \
-        stream.cuda_stream
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 # Descriptions by their values: the structures of a shape met before are not built
@@ -134,20 +136,30 @@ def _refuse(t, name, dtype, shape, device, what):
     raise ValueError(f"{name} must {what}")
 
 
+# The checks run for every tensor of every call, small calls among them: what passes
+# costs four attributes, and what fails is asked again for the words of the error.
+
 def _rows(t, name, dtype, shape, device):
     """A tensor of this type, shape and GPU whose last dimension is adjacent."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or
-            t.device != device or (t.stride(-1) != 1 and t.shape[-1] > 1)):
-        _refuse(t, name, dtype, shape, device, "have adjacent channels")
-    return t
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.device == device and
+                (t.stride(-1) == 1 or t.shape[-1] <= 1)):
+            return t
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, device, "have adjacent channels")
 
 
 def _dense(t, name, dtype, shape, device):
-    if t is not None and (
-            not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or
-            t.device != device or not t.is_contiguous()):
-        _refuse(t, name, dtype, shape, device, "be contiguous")
-    return t
+    if t is None:
+        return None
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.device == device and
+                t.is_contiguous()):
+            return t
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, device, "be contiguous")
 
 
 def _dtype(t, name):
@@ -161,13 +173,26 @@ def _dtype(t, name):
     return t.dtype
 
 
+_new = torch.empty
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor for a call on ``stream``: memory given back on the current stream must
     not be reused before a call on another one is done with it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = _new(shape, dtype=dtype, device=device)
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+def _like(t, stream):
+    """A new dense tensor of t's shape, type and device."""
+    if not t.is_contiguous():
+        return _empty(t.shape, t.dtype, t.device, stream)
+    n = torch.empty_like(t)
+    if stream is not None:
+        n.record_stream(stream)
+    return n
 
 
 def _workspace(need, workspace, device, stream):
@@ -189,17 +214,21 @@ def _conv_setup(x, weight, bias, state, lengths, activation):
     if activation not in _ACT:
         raise ValueError(f"activation must be one of {sorted(_ACT)}")
     dev = x.device
-    _rows(x, "x", dt, x.shape, dev)
-    B, T, m = x.shape[0], x.shape[-2], x.shape[-1]
-    H = 1 if x.dim() == 3 else x.shape[1]
+    shape = x.shape
+    _rows(x, "x", dt, shape, dev)
+    B, T, m = shape[0], shape[-2], shape[-1]
+    H = 1 if len(shape) == 3 else shape[1]
     C = H * m
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [channels, width]")
     W = weight.shape[1]
     _dense(weight, "weight", torch.float32, (C, W), dev)
-    _dense(bias, "bias", torch.float32, (C,), dev)
-    _dense(state, "state", dt, (B, W - 1, C), dev)
-    _dense(lengths, "lengths", torch.int32, (B,), dev)
+    if bias is not None:
+        _dense(bias, "bias", torch.float32, (C,), dev)
+    if state is not None:
+        _dense(state, "state", dt, (B, W - 1, C), dev)
+    if lengths is not None:
+        _dense(lengths, "lengths", torch.int32, (B,), dev)
     return _conv_shape(B, H, T, m, W, _DTYPE[dt], _ACT[activation]), dt, dev, B, C, W
 
 
@@ -211,10 +240,9 @@ def falcon_short_conv_fwd(x, weight, bias=None, state=None, lengths=None, activa
     dtype (the inputs before token 0); lengths [B] int32; activation "silu" or
     "identity".  Returns (y, state_out): y of x's shape, dense unless passed in,
     and the last width-1 inputs of every row."""
-    lib = _library()
+    lib = _lib or _library()
     shape, dt, dev, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
-    y = _empty(x.shape, dt, dev, stream) if y is None else \
-        _rows(y, "y", dt, x.shape, dev)
+    y = _like(x, stream) if y is None else _rows(y, "y", dt, x.shape, dev)
     state_out = _empty((B, W - 1, C), dt, dev, stream) if state_out is None else \
         _dense(state_out, "state_out", dt, (B, W - 1, C), dev)
     rc = lib.falcon_short_conv_fwd(shape, x.data_ptr(), _conv_rows(x), weight.data_ptr(), _at(bias),
@@ -229,15 +257,15 @@ def falcon_short_conv_bwd(x, weight, dy, bias=None, state=None, lengths=None, ds
     """Gradients of <dy, y> + <dstate_out, state_out> of falcon_short_conv_fwd.
     Returns a dict with dx (dense, x's shape), dweight, dbias (fp32) and dstate;
     ``grads`` may pass preallocated outputs."""
-    lib = _library()
+    lib = _lib or _library()
     shape, dt, dev, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
     _rows(dy, "dy", dt, x.shape, dev)
     _dense(dstate_out, "dstate_out", dt, (B, W - 1, C), dev)
     g = {} if grads is None else grads
     if "dx" not in g:
-        g["dx"] = _empty(x.shape, dt, dev, stream)
+        g["dx"] = _like(x, stream)
     if "dweight" not in g:
-        g["dweight"] = _empty((C, W), torch.float32, dev, stream)
+        g["dweight"] = _like(weight, stream)
     if "dbias" not in g:
         g["dbias"] = _empty((C,), torch.float32, dev, stream)
     if "dstate" not in g:
@@ -264,7 +292,7 @@ def falcon_short_conv_step(x, weight, state, bias=None, slots=None, fresh=None,
     (x's dtype) is updated in place; slots [N] int32 names each row's state (row i
     uses state i when absent), fresh [N] uint8 marks sequences that start here.
     Returns y [N,channels]."""
-    lib = _library()
+    lib = _lib or _library()
     dt = _dtype(x, "x")
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be [N, channels] and weight [channels, width]")
@@ -280,8 +308,7 @@ def falcon_short_conv_step(x, weight, state, bias=None, slots=None, fresh=None,
     _dense(state, "state", dt, (pool, W - 1, C), dev)
     _dense(slots, "slots", torch.int32, (N,), dev)
     _dense(fresh, "fresh", torch.uint8, (N,), dev)
-    y = _empty((N, C), dt, dev, stream) if y is None else \
-        _dense(y, "y", dt, (N, C), dev)
+    y = _like(x, stream) if y is None else _dense(y, "y", dt, (N, C), dev)
     rc = lib.falcon_short_conv_step(N, C, W, _DTYPE[dt], _ACT[activation], x.data_ptr(),
                                     x.stride(0), weight.data_ptr(), _at(bias), _at(state), pool,
                                     _at(slots), _at(fresh), y.data_ptr(), _current(stream, dev))
@@ -327,8 +354,10 @@ def _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus):
     _dense(A, "A", f32, (C, N), dev)
     _dense(D, "D", f32, (C,), dev)
     _dense(delta_bias, "delta_bias", f32, (C,), dev)
-    _dense(h0, "h0", f32, (B, C, N), dev)
-    _dense(lengths, "lengths", torch.int32, (B,), dev)
+    if h0 is not None:
+        _dense(h0, "h0", f32, (B, C, N), dev)
+    if lengths is not None:
+        _dense(lengths, "lengths", torch.int32, (B,), dev)
     return _scan_shape(B, T, C, G, N, _DTYPE[dt], 1 if softplus else 0), dt, dev, (B, C, N)
 
 
@@ -338,10 +367,9 @@ def falcon_selective_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=No
     D u_t) silu(z_t), s_t = softplus(delta_t + delta_bias).  u, delta, z [B,T,D]
     and Bm, Cm [B,T,G,N] (bf16 or fp32, any row strides); A [D,N], D, delta_bias
     [D] and h0 [B,D,N] fp32; lengths [B] int32.  Returns (y, h_T)."""
-    lib = _library()
+    lib = _lib or _library()
     shape, dt, dev, hs = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
-    y = _empty(u.shape, dt, dev, stream) if y is None else \
-        _rows(y, "y", dt, u.shape, dev)
+    y = _like(delta, stream) if y is None else _rows(y, "y", dt, u.shape, dev)
     h_out = _empty(hs, torch.float32, dev, stream) if h_out is None else \
         _dense(h_out, "h_out", torch.float32, hs, dev)
     rc = lib.falcon_selective_scan_fwd(
@@ -361,26 +389,25 @@ def falcon_selective_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bia
     dict with du, ddelta, dz, dB, dC (u's dtype, dense) and dA, dD, ddelta_bias,
     dh0 (fp32); dz, dD and ddelta_bias are None where z, D or delta_bias is.
     ``grads`` may pass preallocated outputs."""
-    lib = _library()
+    lib = _lib or _library()
     shape, dt, dev, hs = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
     _rows(dy, "dy", dt, u.shape, dev)
     _dense(dh_T, "dh_T", torch.float32, hs, dev)
-    f32 = torch.float32
-    bc = tuple(Bm.shape)
-    want = {"du": (dt, tuple(u.shape)), "ddelta": (dt, tuple(u.shape)),
-            "dA": (f32, tuple(A.shape)), "dB": (dt, bc), "dC": (dt, bc),
-            "dD": None if D is None else (f32, tuple(D.shape)),
-            "dz": None if z is None else (dt, tuple(u.shape)),
-            "ddelta_bias": None if delta_bias is None else (f32, tuple(delta_bias.shape)),
-            "dh0": (f32, hs)}
+    # each gradient is shaped and typed as its input
+    like = {"du": delta, "ddelta": delta, "dA": A, "dB": Bm, "dC": Bm, "dD": D, "dz": z,
+            "ddelta_bias": delta_bias}
     g = {} if grads is None else grads
-    for name, spec in want.items():
-        if spec is None:
+    for name, t in like.items():
+        if t is None:
             g[name] = None
         elif name in g:
-            _dense(g[name], name, *spec, dev)
+            _dense(g[name], name, t.dtype, t.shape, dev)
         else:
-            g[name] = _empty(spec[1], spec[0], dev, stream)
+            g[name] = _like(t, stream)
+    if "dh0" in g:
+        _dense(g["dh0"], "dh0", torch.float32, hs, dev)
+    else:
+        g["dh0"] = _empty(hs, torch.float32, dev, stream)
     workspace, have = _workspace(int(lib.falcon_selective_scan_bwd_workspace_bytes(shape)),
                                  workspace, dev, stream)
     rc = lib.falcon_selective_scan_bwd(
@@ -400,7 +427,7 @@ def falcon_selective_scan_step(u, delta, A, Bm, Cm, h, D=None, z=None, delta_bia
     """One token of N sequences: u, delta, z [N,D], Bm, Cm [N,G,S]; h [pool,D,S]
     fp32 is updated in place; slots and fresh as in falcon_short_conv_step.
     Returns y [N,D]."""
-    lib = _library()
+    lib = _lib or _library()
     dt = _dtype(u, "u")
     if u.dim() != 2 or not isinstance(A, torch.Tensor) or A.dim() != 2 or \
             not isinstance(Bm, torch.Tensor) or Bm.dim() != 3:
@@ -421,7 +448,7 @@ def falcon_selective_scan_step(u, delta, A, Bm, Cm, h, D=None, z=None, delta_bia
     _dense(h, "h", f32, (pool, C, S), dev)
     _dense(slots, "slots", torch.int32, (N,), dev)
     _dense(fresh, "fresh", torch.uint8, (N,), dev)
-    y = _empty(row, dt, dev, stream) if y is None else _dense(y, "y", dt, row, dev)
+    y = _like(delta, stream) if y is None else _dense(y, "y", dt, row, dev)
     b, c = Bm.stride(), Cm.stride()
     rc = lib.falcon_selective_scan_step(
         N, C, G, S, _DTYPE[dt], 1 if softplus else 0, u.data_ptr(), u.stride(0), delta.data_ptr(),
@@ -439,7 +466,7 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
     min(1, max_norm / (n + eps)), n their global 2-norm: in place, or into the
     tensors of ``out`` (same sizes and dtypes).  Returns n, a 0-d fp32 tensor on
     the gradients' device; the host does not wait for it."""
-    lib = _library()
+    lib = _lib or _library()
     grads = list(grads)
     if not grads:
         raise ValueError("grads must hold at least one tensor")
