@@ -9,7 +9,10 @@
 // further launches of each kind.
 //
 // Bound by memory: 88 M bf16 gradients (177 MB) 31 and 56 us alone, 88 to 92 us a call;
-// reading them twice and writing them once at a copy's rate takes 78.
+// reading them twice and writing them once at a copy's rate takes 78.  Measured and not
+// kept: finding the next chunk's tensor while a chunk's loads are under way (98 us: the
+// registers cost more blocks than the search costs time), four vectors a batch with
+// more blocks (94).
 
 #include "ssm.cuh"
 

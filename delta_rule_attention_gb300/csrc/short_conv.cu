@@ -13,8 +13,9 @@
 // B8 H12 T2048 m64 W4 bf16, silu, from strided heads: 15.4 us (3.3 TB/s of the 50 MB it
 // must move; issue slots 63% busy).  Its gradient for B8 T2048 C2048: 50 us and 6 for
 // the sums (3.6 TB/s of 202 MB): bound by the latency of its loads at 14 warps an SM.
-// Eight tokens a forward run and four channels a thread: 16.8 us with eight
-// channels, 15.0 with runs of 16, 19.3 with runs of 4.
+// Eight tokens a forward run and four channels a thread: 15.0 us with runs of 16, 19.3
+// with runs of 4; before whole runs went without tests, 16.8 us, and 19.2 with eight
+// channels a thread.
 
 #include <type_traits>
 
