@@ -108,10 +108,11 @@ __device__ __forceinline__ float decay(float s, float A2) {
   return exp2_approx(fmaf(s, A2, kDecayLift));
 }
 
-// 1 / (1 + e^{-x}).  The exponent is held below 2^126, so that the reciprocal
-// of a large denominator stays a normal number.
+// 1 / (1 + e^{-x}).  Where the denominator is above 2^126, or infinite, the reciprocal
+// is flushed to zero: x sigmoid(x) is then zero for every finite x, where a value held
+// above zero would grow with x (-4 for the lowest float32).
 __device__ __forceinline__ float sigmoid(float x) {
-  return rcp_approx(1.f + exp2_approx(fminf(-x * kLog2e, 126.f)));
+  return rcp_approx(1.f + exp2_approx(-x * kLog2e));
 }
 
 // softplus(x) = max(x, 0) + log1p(e), e = e^{-|x|} in (0, 1].
