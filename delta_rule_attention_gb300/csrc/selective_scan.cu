@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const bool in = live && n0 + i < a.N;
-      const float v = in ? a.A[(int64_t)(d + c) * a.N + n0 + i] * kLog2e : 0.f;
+      const float v = in ? rate_log2(a.A[(int64_t)(d + c) * a.N + n0 + i]) : 0.f;
       A2[c][i] = opaque2(pack2(v, v));
       first[c][i] = in && a.h0 ? a.h0[(b * a.D + d + c) * a.N + n0 + i] : 0.f;
     }

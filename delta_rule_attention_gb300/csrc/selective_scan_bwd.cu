@@ -158,7 +158,7 @@ struct Place {
       float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        v[i] = c < have && n0 + i < a.N ? a.A[(int64_t)(d + c) * a.N + n0 + i] * kLog2e : 0.f;
+        v[i] = c < have && n0 + i < a.N ? rate_log2(a.A[(int64_t)(d + c) * a.N + n0 + i]) : 0.f;
       A2[c][0] = pack2(v[0], v[1]), A2[c][1] = pack2(v[2], v[3]);
     }
   }
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const bool in = n0 + k < a.N;
-    A2[k] = in ? a.A[d * a.N + n0 + k] * kLog2e : 0.f;
+    A2[k] = in ? rate_log2(a.A[d * a.N + n0 + k]) : 0.f;
     h[k] = in && from ? from[(b * a.D + d) * a.N + n0 + k] : 0.f;
   }
   // the walk's first chunk and its direction

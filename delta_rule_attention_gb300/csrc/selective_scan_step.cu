@@ -66,6 +66,11 @@ __global__ void __launch_bounds__(kThreads)
   for (int c = 0; c < 2; ++c) {
     const float sc = c ? s.y : s.x, v = sc * (c ? u.y : u.x), s2 = sc * kLog2e;
     const float4 B = c ? B1 : B0, Ct = c ? C1 : C0;
+    // one test for four rates, behind the loads (a call at the size above: 54 us, 60 with
+    // each rate held finite by itself, 58 with no test at all)
+    if (fmaxf(fmaxf(fabsf(A[c].x), fabsf(A[c].y)), fmaxf(fabsf(A[c].z), fabsf(A[c].w))) > kLargest)
+      A[c] = make_float4(finite_rate(A[c].x), finite_rate(A[c].y), finite_rate(A[c].z),
+                         finite_rate(A[c].w));
     const float2 d0 = decay2(pack2(s2, s2), pack2(A[c].x, A[c].y), lift);
     const float2 d1 = decay2(pack2(s2, s2), pack2(A[c].z, A[c].w), lift);
     h[c].x = fmaf(d0.x, h[c].x, v * B.x);

@@ -98,7 +98,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// exp(s A), A2 = A log2(e).  ex2.approx comes out low by 2e-8 to 5e-8 of its
+// A held finite (an infinite one as the largest number, a NaN as it is), so that a step
+// of zero leaves the state: exp(0 A) = 1.
+constexpr float kLargest = 3.402823466e38f;
+__device__ __forceinline__ float finite_rate(float A) {
+  return fabsf(A) > kLargest ? copysignf(kLargest, A) : A;
+}
+// In units of log2(e), where a rate above 2.36e38 would overflow.
+__device__ __forceinline__ float rate_log2(float A) { return finite_rate(A * kLog2e); }
+
+// exp(s A), A2 = rate_log2(A).  ex2.approx comes out low by 2e-8 to 5e-8 of its
 // value on average, which a state with a long memory adds up; the constant in
 // the exponent's fma cancels the mean at no cost (relative error of a state
 // after 2048 tokens with steps of 0.001 .. 0.1 and A of -1 .. -16: 2.3e-7, against

@@ -510,7 +510,9 @@ typedef struct {
  *   y_t = (<Cm_t, h_t> + Dskip u_t) silu(z_t).
  *   u, delta, z, y  [B,T,D] dtype (z nullable: no gate; `head` stride unused)
  *   Bm, Cm          [B,T,G,N] dtype (`head` is the group's stride)
- *   A               [D,N] f32;  Dskip, delta_bias [D] f32, nullable (zeros)
+ *   A               [D,N] f32 (an infinite rate counts as the largest number, so that
+ *                   a step of zero leaves the state);  Dskip, delta_bias [D] f32,
+ *                   nullable (zeros)
  *   h0              [B,D,N] f32, nullable (zeros);  h_out [B,D,N] f32, out, may
  *                   alias h0
  * No workspace.  Errors as for falcon_short_conv_fwd. */
