@@ -57,14 +57,15 @@ __device__ __forceinline__ int tensor_of(const Batch<MOST>& p, int64_t chunk) {
   return lo;
 }
 
-__device__ __forceinline__ float block_sum_f64(double v, double* sh, double* total) {
+// Sum over the block, for thread 0.
+__device__ __forceinline__ double block_sum_f64(double v, double* sh) {
   for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
   __syncthreads();
   double s = 0.0;
-  for (int w = 0; w < kThreads / 32; ++w) s += sh[w];
-  *total = s;
-  return (float)s;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < kThreads / 32; ++w) s += sh[w];
+  return s;
 }
 
 // A block's part of a tensor as 16-byte vectors between the elements before the
@@ -80,19 +81,40 @@ struct Span {
 };
 constexpr int kBatch = 8;  // vectors of a thread under way at a time
 
+// A thread's squares of a chunk are summed in float32, which holds them to 2^-19 while
+// the sum is neither infinite nor so small that squares may have vanished below
+// float32's range; where it is, or where a value is no number, the thread takes its
+// elements again in float64.
+constexpr float kLeastSum = 7.9e-31f;  // about 2^-100: what vanishes is below 2^-40 of it
+
 template <typename E>
-__device__ __forceinline__ float chunk_squares(const E* g, int n, bool passing) {
+__device__ __noinline__ double chunk_squares_f64(const E* g, int n, Span s) {
+  constexpr int V = 16 / (int)sizeof(E);
+  double sum = 0.0;
+  auto add = [&](int i) {
+    const double x = load_vec<E, 1>(g + i).v[0];
+    sum = fma(x, x, sum);
+  };
+  if ((int)threadIdx.x < s.head) add(threadIdx.x);
+  if ((int)threadIdx.x < n - s.tail) add(s.tail + threadIdx.x);
+  for (int i = threadIdx.x; i < s.vecs; i += kThreads)
+    for (int k = 0; k < V; ++k) add(s.head + i * V + k);
+  return sum;
+}
+
+template <typename E>
+__device__ __forceinline__ double chunk_squares(const E* g, int n, bool passing) {
   constexpr int V = 16 / (int)sizeof(E);
   const Span s(g, n, (int)sizeof(E), true);
   float s0 = 0.f, s1 = 0.f;
-  if ((int)threadIdx.x < s.head) {
-    const float x = load_vec<E, 1>(g + threadIdx.x).v[0];
+  uint32_t bits = 0;  // of all elements: zero where every one is zero
+  auto edge = [&](int i) {
+    const float x = load_vec<E, 1>(g + i).v[0];
     s0 = fmaf(x, x, s0);
-  }
-  if ((int)threadIdx.x < n - s.tail) {
-    const float x = load_vec<E, 1>(g + s.tail + threadIdx.x).v[0];
-    s0 = fmaf(x, x, s0);
-  }
+    bits |= __float_as_uint(x);
+  };
+  if ((int)threadIdx.x < s.head) edge(threadIdx.x);
+  if ((int)threadIdx.x < n - s.tail) edge(s.tail + threadIdx.x);
   for (int i0 = threadIdx.x; i0 < s.vecs; i0 += kThreads * kBatch) {
     uint4 q[kBatch];
 #pragma unroll
@@ -110,9 +132,12 @@ __device__ __forceinline__ float chunk_squares(const E* g, int n, bool passing) 
         s0 = fmaf(x.v[k], x.v[k], s0);
         s1 = fmaf(x.v[k + 1], x.v[k + 1], s1);
       }
+      bits |= q[j].x | q[j].y | q[j].z | q[j].w;
     }
   }
-  return s0 + s1;
+  const float sum = s0 + s1;
+  if (!(sum <= kLargest) || (sum < kLeastSum && bits != 0)) return chunk_squares_f64(g, n, s);
+  return sum;
 }
 
 template <int MOST>
@@ -128,8 +153,7 @@ __global__ void __launch_bounds__(kThreads)
                ? chunk_squares(static_cast<const __nv_bfloat16*>(p.grad[k]) + at, n, c < p.passing)
                : chunk_squares(static_cast<const float*>(p.grad[k]) + at, n, c < p.passing);
   }
-  double total;
-  block_sum_f64(acc, sh, &total);
+  const double total = block_sum_f64(acc, sh);
   if (threadIdx.x == 0) partial[blockIdx.x] = total;
 }
 
@@ -170,15 +194,20 @@ __global__ void __launch_bounds__(kThreads)
     clip_scale_kernel(const __grid_constant__ Batch<MOST> p, const double* partial, int parts,
                       float max_norm, float eps, float* norm) {
   __shared__ double sh[kThreads / 32];
+  __shared__ float factor;
   cudaGridDependencySynchronize();
   double acc = 0.0;
   for (int i = threadIdx.x; i < parts; i += kThreads) acc += partial[i];
-  double total;
-  block_sum_f64(acc, sh, &total);
-  const float n = (float)sqrt(total);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
-  const float ratio = max_norm / (n + eps);
-  const float c = ratio > 1.f ? 1.f : ratio;  // a NaN stays
+  acc = block_sum_f64(acc, sh);
+  if (threadIdx.x == 0) {
+    // in float64: gradients that float32 holds can have a norm that it does not
+    const double n = sqrt(acc);
+    if (norm && blockIdx.x == 0) *norm = (float)n;
+    const double ratio = (double)max_norm / (n + (double)eps);
+    factor = ratio > 1.0 ? 1.f : (float)ratio;  // a NaN stays
+  }
+  __syncthreads();
+  const float c = factor;
   // from the back: the first pass has left the last chunks in L2
   for (int64_t i = p.chunks - 1 - blockIdx.x; i >= 0; i -= gridDim.x) {
     const int k = tensor_of(p, i);

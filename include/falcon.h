@@ -586,9 +586,11 @@ typedef struct {
  *          dense tensors of any size, element-aligned
  *   norm   [1] f32, out: n (before clipping)
  * In place, gradients that need no scaling are not rewritten.  A norm that is
- * NaN makes every output NaN; an infinite one scales by 0 (an infinite
- * gradient becomes NaN).  The sum of squares is float32 within a thread and
- * float64 across threads; values whose square overflows float32 give an infinite norm.
+ * NaN makes every output NaN; an infinite gradient makes the norm infinite, becomes
+ * NaN, and scales the others by 0.  Squares are summed in float32 within a thread
+ * where that holds them, in float64 otherwise and across threads, so that sizes
+ * whose squares leave float32 count as well; a finite norm beyond float32 comes out
+ * infinite, the gradients being scaled by its value.
  *   workspace: at least falcon_clip_workspace_bytes(grads, tensors) bytes,
  *   16-byte aligned.
  * Errors: FALCON_ERR_NULL_PTR, _BAD_SHAPE (negative count), _BAD_DTYPE,
