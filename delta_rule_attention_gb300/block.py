@@ -5,6 +5,9 @@ Argument marshalling only, as in the package's other functions: the names are
 the C names, the work is in the CUDA kernels, a nonzero return code raises
 ``FalconError``.  Activations may be views with any row strides as long as
 consecutive channels are adjacent; parameters and states are dense.
+
+A call runs on the current stream, or on ``stream``: the caller then orders the inputs
+before it and the use of its results after it, as with any work on another stream.
 """
 from __future__ import annotations
 
@@ -101,8 +104,25 @@ def _at(t):
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _current(stream, device):
-    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+def _elsewhere(stream, fn, *args):
+    """fn(*args) on a stream that need not be the current one.  Its new tensors come from
+    that stream's memory: what the current stream's pool hands out may be in use by work
+    still queued there, which nothing orders before this call.  The tensors that it
+    returns are marked as used by the current stream as well, so that they may be dropped
+    there as soon as what reads them is queued."""
+    here = torch.cuda.current_stream(stream.device)
+    given = set()
+    for a in args:
+        given.update(map(id, a.values() if isinstance(a, dict) else (a,)))
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    if here.cuda_stream != stream.cuda_stream:
+        new = (out,) if isinstance(out, torch.Tensor) else \
+            out.values() if isinstance(out, dict) else out
+        for t in new:
+            if t is not None and id(t) not in given:
+                t.record_stream(here)
+    return out
 
 
 # Descriptions by their values: the structures of a shape met before are not built
@@ -176,28 +196,18 @@ def _dtype(t, name):
 _new = torch.empty
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor for a call on ``stream``: memory given back on the current stream must
-    not be reused before a call on another one is done with it."""
-    t = _new(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+def _empty(shape, dtype, device):
+    return _new(shape, dtype=dtype, device=device)
 
 
-def _like(t, stream):
+def _like(t):
     """A new dense tensor of t's shape, type and device."""
-    if not t.is_contiguous():
-        return _empty(t.shape, t.dtype, t.device, stream)
-    n = torch.empty_like(t)
-    if stream is not None:
-        n.record_stream(stream)
-    return n
+    return torch.empty_like(t) if t.is_contiguous() else _empty(t.shape, t.dtype, t.device)
 
 
-def _workspace(need, workspace, device, stream):
+def _workspace(need, workspace, device):
     if workspace is None:
-        return (_empty(need, torch.uint8, device, stream), need) if need else (None, 0)
+        return (_empty(need, torch.uint8, device), need) if need else (None, 0)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -240,14 +250,17 @@ def falcon_short_conv_fwd(x, weight, bias=None, state=None, lengths=None, activa
     dtype (the inputs before token 0); lengths [B] int32; activation "silu" or
     "identity".  Returns (y, state_out): y of x's shape, dense unless passed in,
     and the last width-1 inputs of every row."""
+    if stream is not None:
+        return _elsewhere(stream, falcon_short_conv_fwd, x, weight, bias, state, lengths,
+                          activation, y, state_out)
     lib = _lib or _library()
     shape, dt, dev, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
-    y = _like(x, stream) if y is None else _rows(y, "y", dt, x.shape, dev)
-    state_out = _empty((B, W - 1, C), dt, dev, stream) if state_out is None else \
+    y = _like(x) if y is None else _rows(y, "y", dt, x.shape, dev)
+    state_out = _empty((B, W - 1, C), dt, dev) if state_out is None else \
         _dense(state_out, "state_out", dt, (B, W - 1, C), dev)
     rc = lib.falcon_short_conv_fwd(shape, x.data_ptr(), _conv_rows(x), weight.data_ptr(), _at(bias),
                                    _at(state), _at(lengths), y.data_ptr(), _conv_rows(y),
-                                   state_out.data_ptr(), _current(stream, dev))
+                                   state_out.data_ptr(), _raw_stream(dev.index))
     _check(rc, "falcon_short_conv_fwd")
     return y, state_out
 
@@ -257,31 +270,34 @@ def falcon_short_conv_bwd(x, weight, dy, bias=None, state=None, lengths=None, ds
     """Gradients of <dy, y> + <dstate_out, state_out> of falcon_short_conv_fwd.
     Returns a dict with dx (dense, x's shape), dweight, dbias (fp32) and dstate;
     ``grads`` may pass preallocated outputs."""
+    if stream is not None:
+        return _elsewhere(stream, falcon_short_conv_bwd, x, weight, dy, bias, state, lengths,
+                          dstate_out, activation, grads, workspace)
     lib = _lib or _library()
     shape, dt, dev, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
     _rows(dy, "dy", dt, x.shape, dev)
     _dense(dstate_out, "dstate_out", dt, (B, W - 1, C), dev)
     g = {} if grads is None else grads
     if "dx" not in g:
-        g["dx"] = _like(x, stream)
+        g["dx"] = _like(x)
     if "dweight" not in g:
-        g["dweight"] = _like(weight, stream)
+        g["dweight"] = _like(weight)
     if "dbias" not in g:
-        g["dbias"] = _empty((C,), torch.float32, dev, stream)
+        g["dbias"] = _empty((C,), torch.float32, dev)
     if "dstate" not in g:
-        g["dstate"] = _empty((B, W - 1, C), dt, dev, stream)
+        g["dstate"] = _empty((B, W - 1, C), dt, dev)
     if grads is not None:
         _rows(g["dx"], "dx", dt, x.shape, dev)
         _dense(g["dweight"], "dweight", torch.float32, (C, W), dev)
         _dense(g["dbias"], "dbias", torch.float32, (C,), dev)
         _dense(g["dstate"], "dstate", dt, (B, W - 1, C), dev)
     workspace, have = _workspace(int(lib.falcon_short_conv_bwd_workspace_bytes(shape)),
-                                 workspace, dev, stream)
+                                 workspace, dev)
     rc = lib.falcon_short_conv_bwd(
         shape, x.data_ptr(), _conv_rows(x), weight.data_ptr(), _at(bias), _at(state),
         _at(lengths), dy.data_ptr(),
         _conv_rows(dy), _at(dstate_out), _at(g["dx"]), _conv_rows(g["dx"]), _at(g["dweight"]),
-        _at(g["dbias"]), _at(g["dstate"]), _at(workspace), have, _current(stream, dev))
+        _at(g["dbias"]), _at(g["dstate"]), _at(workspace), have, _raw_stream(dev.index))
     _check(rc, "falcon_short_conv_bwd")
     return g
 
@@ -292,6 +308,9 @@ def falcon_short_conv_step(x, weight, state, bias=None, slots=None, fresh=None,
     (x's dtype) is updated in place; slots [N] int32 names each row's state (row i
     uses state i when absent), fresh [N] uint8 marks sequences that start here.
     Returns y [N,channels]."""
+    if stream is not None:
+        return _elsewhere(stream, falcon_short_conv_step, x, weight, state, bias, slots, fresh,
+                          activation, y)
     lib = _lib or _library()
     dt = _dtype(x, "x")
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
@@ -308,10 +327,10 @@ def falcon_short_conv_step(x, weight, state, bias=None, slots=None, fresh=None,
     _dense(state, "state", dt, (pool, W - 1, C), dev)
     _dense(slots, "slots", torch.int32, (N,), dev)
     _dense(fresh, "fresh", torch.uint8, (N,), dev)
-    y = _like(x, stream) if y is None else _dense(y, "y", dt, (N, C), dev)
+    y = _like(x) if y is None else _dense(y, "y", dt, (N, C), dev)
     rc = lib.falcon_short_conv_step(N, C, W, _DTYPE[dt], _ACT[activation], x.data_ptr(),
                                     x.stride(0), weight.data_ptr(), _at(bias), _at(state), pool,
-                                    _at(slots), _at(fresh), y.data_ptr(), _current(stream, dev))
+                                    _at(slots), _at(fresh), y.data_ptr(), _raw_stream(dev.index))
     _check(rc, "falcon_short_conv_step")
     return y
 
@@ -367,17 +386,20 @@ def falcon_selective_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=No
     D u_t) silu(z_t), s_t = softplus(delta_t + delta_bias).  u, delta, z [B,T,D]
     and Bm, Cm [B,T,G,N] (bf16 or fp32, any row strides); A [D,N], D, delta_bias
     [D] and h0 [B,D,N] fp32; lengths [B] int32.  Returns (y, h_T)."""
+    if stream is not None:
+        return _elsewhere(stream, falcon_selective_scan_fwd, u, delta, A, Bm, Cm, D, z, delta_bias,
+                          h0, lengths, softplus, y, h_out)
     lib = _lib or _library()
     shape, dt, dev, hs = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
-    y = _like(delta, stream) if y is None else _rows(y, "y", dt, u.shape, dev)
-    h_out = _empty(hs, torch.float32, dev, stream) if h_out is None else \
+    y = _like(delta) if y is None else _rows(y, "y", dt, u.shape, dev)
+    h_out = _empty(hs, torch.float32, dev) if h_out is None else \
         _dense(h_out, "h_out", torch.float32, hs, dev)
     rc = lib.falcon_selective_scan_fwd(
         shape, u.data_ptr(), _time_rows(u), delta.data_ptr(), _time_rows(delta), A.data_ptr(),
         Bm.data_ptr(),
         _group_rows(Bm), Cm.data_ptr(), _group_rows(Cm), _at(D), _at(z),
         None if z is None else _time_rows(z), _at(delta_bias), _at(h0), _at(lengths), y.data_ptr(),
-        _time_rows(y), h_out.data_ptr(), _current(stream, dev))
+        _time_rows(y), h_out.data_ptr(), _raw_stream(dev.index))
     _check(rc, "falcon_selective_scan_fwd")
     return y, h_out
 
@@ -389,6 +411,9 @@ def falcon_selective_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bia
     dict with du, ddelta, dz, dB, dC (u's dtype, dense) and dA, dD, ddelta_bias,
     dh0 (fp32); dz, dD and ddelta_bias are None where z, D or delta_bias is.
     ``grads`` may pass preallocated outputs."""
+    if stream is not None:
+        return _elsewhere(stream, falcon_selective_scan_bwd, u, delta, A, Bm, Cm, dy, D, z,
+                          delta_bias, h0, lengths, dh_T, softplus, grads, workspace)
     lib = _lib or _library()
     shape, dt, dev, hs = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
     _rows(dy, "dy", dt, u.shape, dev)
@@ -403,13 +428,13 @@ def falcon_selective_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bia
         elif name in g:
             _dense(g[name], name, t.dtype, t.shape, dev)
         else:
-            g[name] = _like(t, stream)
+            g[name] = _like(t)
     if "dh0" in g:
         _dense(g["dh0"], "dh0", torch.float32, hs, dev)
     else:
-        g["dh0"] = _empty(hs, torch.float32, dev, stream)
+        g["dh0"] = _empty(hs, torch.float32, dev)
     workspace, have = _workspace(int(lib.falcon_selective_scan_bwd_workspace_bytes(shape)),
-                                 workspace, dev, stream)
+                                 workspace, dev)
     rc = lib.falcon_selective_scan_bwd(
         shape, u.data_ptr(), _time_rows(u), delta.data_ptr(), _time_rows(delta), A.data_ptr(),
         Bm.data_ptr(),
@@ -417,7 +442,7 @@ def falcon_selective_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bia
         None if z is None else _time_rows(z), _at(delta_bias), _at(h0), _at(lengths), dy.data_ptr(),
         _time_rows(dy), _at(dh_T), _at(g["du"]), _at(g["ddelta"]), _at(g["dA"]), _at(g["dB"]),
         _at(g["dC"]), _at(g["dD"]), _at(g["dz"]), _at(g["ddelta_bias"]), _at(g["dh0"]),
-        _at(workspace), have, _current(stream, dev))
+        _at(workspace), have, _raw_stream(dev.index))
     _check(rc, "falcon_selective_scan_bwd")
     return g
 
@@ -427,6 +452,9 @@ def falcon_selective_scan_step(u, delta, A, Bm, Cm, h, D=None, z=None, delta_bia
     """One token of N sequences: u, delta, z [N,D], Bm, Cm [N,G,S]; h [pool,D,S]
     fp32 is updated in place; slots and fresh as in falcon_short_conv_step.
     Returns y [N,D]."""
+    if stream is not None:
+        return _elsewhere(stream, falcon_selective_scan_step, u, delta, A, Bm, Cm, h, D, z,
+                          delta_bias, slots, fresh, softplus, y)
     lib = _lib or _library()
     dt = _dtype(u, "u")
     if u.dim() != 2 or not isinstance(A, torch.Tensor) or A.dim() != 2 or \
@@ -448,14 +476,14 @@ def falcon_selective_scan_step(u, delta, A, Bm, Cm, h, D=None, z=None, delta_bia
     _dense(h, "h", f32, (pool, C, S), dev)
     _dense(slots, "slots", torch.int32, (N,), dev)
     _dense(fresh, "fresh", torch.uint8, (N,), dev)
-    y = _like(delta, stream) if y is None else _dense(y, "y", dt, row, dev)
+    y = _like(delta) if y is None else _dense(y, "y", dt, row, dev)
     b, c = Bm.stride(), Cm.stride()
     rc = lib.falcon_selective_scan_step(
         N, C, G, S, _DTYPE[dt], 1 if softplus else 0, u.data_ptr(), u.stride(0), delta.data_ptr(),
         delta.stride(0), A.data_ptr(), Bm.data_ptr(), _strides(b[0], b[1], 0), Cm.data_ptr(),
         _strides(c[0], c[1], 0), _at(D), _at(z), 0 if z is None else z.stride(0),
         _at(delta_bias), h.data_ptr(), pool, _at(slots), _at(fresh), y.data_ptr(),
-        _current(stream, dev))
+        _raw_stream(dev.index))
     _check(rc, "falcon_selective_scan_step")
     return y
 
@@ -466,6 +494,8 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
     min(1, max_norm / (n + eps)), n their global 2-norm: in place, or into the
     tensors of ``out`` (same sizes and dtypes).  Returns n, a 0-d fp32 tensor on
     the gradients' device; the host does not wait for it."""
+    if stream is not None:
+        return _elsewhere(stream, falcon_clip_grad_norm, grads, max_norm, out, eps, norm, workspace)
     lib = _lib or _library()
     grads = list(grads)
     if not grads:
@@ -500,10 +530,10 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
     rows = ctypes.cast(table.buffer_info()[0], ctypes.POINTER(falcon_grad))
     dev = grads[0].device
     if norm is None:
-        norm = _empty((), torch.float32, dev, stream)
+        norm = _empty((), torch.float32, dev)
     workspace, have = _workspace(int(lib.falcon_clip_workspace_bytes(rows, len(grads))),
-                                 workspace, dev, stream)
+                                 workspace, dev)
     rc = lib.falcon_clip_grad_norm(rows, len(grads), float(max_norm), float(eps), norm.data_ptr(),
-                                   _at(workspace), have, _current(stream, dev))
+                                   _at(workspace), have, _raw_stream(dev.index))
     _check(rc, "falcon_clip_grad_norm")
     return norm

@@ -1,0 +1,154 @@
+"""The block's binding on the host: where its memory comes from and what it refuses, with
+the library, the allocator and the streams replaced by recorders (no GPU needed)."""
+import contextlib
+
+import pytest
+import torch
+
+from delta_rule_attention_gb300 import block
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it lies on a GPU."""
+    __torch_function__ = torch._C._disabled_torch_function_impl
+    index = 0
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.index)
+
+    @property
+    def is_cuda(self):
+        return True
+
+    def get_device(self):
+        return self.index
+
+    def record_stream(self, stream):
+        self.__dict__.setdefault("recorded", []).append(stream)
+
+
+def _gpu(*shape, dtype=F32, index=0):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
+    t.index = index
+    return t
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream, self.device = handle, torch.device("cuda", 0)
+
+
+class World:
+    """The current stream and device, what was allocated under which stream, and the
+    library's calls."""
+
+    def __init__(self, monkeypatch):
+        self.here, self.device = Stream(0), 0
+        self.now, self.allocated, self.calls = self.here, [], []
+
+        @contextlib.contextmanager
+        def on(stream):
+            before, self.now = self.now, stream
+            yield
+            self.now = before
+
+        def empty(shape, dtype=None, device=None):
+            self.allocated.append(self.now)
+            shape = (shape,) if isinstance(shape, int) else tuple(shape)
+            return _gpu(*shape, dtype=dtype)
+
+        def empty_like(t):
+            return empty(t.shape, t.dtype)
+
+        monkeypatch.setattr(torch.cuda, "stream", on)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.now)
+        monkeypatch.setattr(torch, "empty", empty)
+        monkeypatch.setattr(torch, "empty_like", empty_like)
+        monkeypatch.setattr(block, "_new", empty)
+        monkeypatch.setattr(block, "_raw_stream", lambda index: self.now.cuda_stream)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: self.device, raising=False)
+        monkeypatch.setattr(block, "_device_now", lambda: self.device, raising=False)
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda t: t.index)
+        monkeypatch.setattr(block, "_lib", self)
+
+    def __getattr__(self, name):
+        if not name.startswith("falcon_"):
+            raise AttributeError(name)
+
+        def call(*args):
+            if name.endswith("_bytes"):
+                return 512
+            self.calls.append((name, args))
+            return 0
+
+        return call
+
+
+@pytest.fixture
+def world(monkeypatch):
+    return World(monkeypatch)
+
+
+def _calls():
+    """Every entry point with arguments that it takes."""
+    x, w, dy = _gpu(2, 5, 8), _gpu(8, 4), _gpu(2, 5, 8)
+    A, bc, skip = _gpu(8, 16), _gpu(2, 5, 1, 16), _gpu(8)
+    return {
+        "short_conv_fwd": (block.falcon_short_conv_fwd, dict(x=x, weight=w)),
+        "short_conv_bwd": (block.falcon_short_conv_bwd, dict(x=x, weight=w, dy=dy)),
+        "short_conv_step": (block.falcon_short_conv_step,
+                            dict(x=_gpu(2, 8), weight=w, state=_gpu(2, 3, 8))),
+        "selective_scan_fwd": (block.falcon_selective_scan_fwd,
+                               dict(u=x, delta=dy, A=A, Bm=bc, Cm=bc, D=skip, z=x)),
+        "selective_scan_bwd": (block.falcon_selective_scan_bwd,
+                               dict(u=x, delta=x, A=A, Bm=bc, Cm=bc, dy=dy, D=skip, z=x,
+                                    delta_bias=skip)),
+        "selective_scan_step": (block.falcon_selective_scan_step,
+                                dict(u=_gpu(2, 8), delta=_gpu(2, 8), A=A, Bm=_gpu(2, 1, 16),
+                                     Cm=_gpu(2, 1, 16), h=_gpu(2, 8, 16))),
+        "clip_grad_norm": (block.falcon_clip_grad_norm,
+                           dict(grads=[_gpu(8), _gpu(3, dtype=BF16)], max_norm=1.0)),
+    }
+
+
+def _tensors(out):
+    if isinstance(out, torch.Tensor):
+        return [out]
+    return [t for t in (out.values() if isinstance(out, dict) else out) if t is not None]
+
+
+@pytest.mark.parametrize("name", sorted(_calls()))
+def test_memory_of_a_call_on_a_given_stream_comes_from_that_stream(world, name):
+    """Memory that the current stream's pool hands out may still be in use by work queued
+    on it, which nothing orders before a call on another stream."""
+    fn, args = _calls()[name]
+    side = Stream(77)
+    out = fn(**args, stream=side)
+    assert world.allocated and all(s is side for s in world.allocated)
+    (_, passed), = world.calls
+    assert passed[-1] == 77
+    assert world.now is world.here
+    # the results are used, and may be dropped, on the current stream
+    assert all(t.recorded == [world.here] for t in _tensors(out))
+
+
+@pytest.mark.parametrize("name", sorted(_calls()))
+def test_calls_on_the_current_stream_record_nothing(world, name):
+    fn, args = _calls()[name]
+    for out in (fn(**args), fn(**args, stream=world.here)):
+        assert not any(hasattr(t, "recorded") for t in _tensors(out))
+    assert all(s is world.here for s in world.allocated)
+    assert [a[-1] for _, a in world.calls] == [0, 0]
+
+
+def test_tensors_that_were_passed_in_are_not_recorded(world):
+    x, w, y, tail = _gpu(2, 5, 8), _gpu(8, 4), _gpu(2, 5, 8), _gpu(2, 3, 8)
+    out = block.falcon_short_conv_fwd(x, w, y=y, state_out=tail, stream=Stream(5))
+    assert out[0] is y and out[1] is tail
+    dx = _gpu(2, 5, 8)
+    g = block.falcon_short_conv_bwd(x, w, x, grads={"dx": dx}, stream=Stream(5))
+    assert g["dx"] is dx and g["dweight"].recorded == [world.here]
+    assert not any(hasattr(t, "recorded") for t in (x, w, y, tail, dx))
