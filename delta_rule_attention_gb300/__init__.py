@@ -166,6 +166,8 @@ def _need(t, name, dtype=None, shape=None):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.get_device() != block._device_now():
+        block.refuse_other_device(t, name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):

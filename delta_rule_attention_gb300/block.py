@@ -102,6 +102,13 @@ def _at(t):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_device_now = torch._C._cuda_getDevice
+
+
+def refuse_other_device(t, name):
+    """A launch goes to the current device, whatever its pointers belong to."""
+    if t.get_device() != _device_now():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_device_now()}")
 
 
 def _elsewhere(stream, fn, *args):
@@ -190,6 +197,7 @@ def _dtype(t, name):
         raise TypeError(f"{name} must be bfloat16 or float32")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    refuse_other_device(t, name)
     return t.dtype
 
 
@@ -512,6 +520,7 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
     both = grads if into is grads else grads + into
     if index < 0 or list(map(T.get_device, both)).count(index) != len(both):
         raise ValueError("gradients and outputs must be CUDA tensors of one device")
+    refuse_other_device(grads[0], "gradients")
     if not all(map(T.is_contiguous, both)):
         raise ValueError("gradients and outputs must be contiguous")
     at = array.array("q", map(T.data_ptr, grads))

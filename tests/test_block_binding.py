@@ -152,3 +152,34 @@ def test_tensors_that_were_passed_in_are_not_recorded(world):
     g = block.falcon_short_conv_bwd(x, w, x, grads={"dx": dx}, stream=Stream(5))
     assert g["dx"] is dx and g["dweight"].recorded == [world.here]
     assert not any(hasattr(t, "recorded") for t in (x, w, y, tail, dx))
+
+
+@pytest.mark.parametrize("name", sorted(_calls()))
+def test_tensors_on_a_gpu_that_is_not_the_current_one_are_refused(world, name):
+    """A launch goes to the current device, whatever its pointers belong to."""
+    fn, args = _calls()[name]
+    world.device = 1
+    with pytest.raises(ValueError, match="current"):
+        fn(**args)
+    assert world.calls == []
+    world.device = 0
+    fn(**args)
+    assert len(world.calls) == 1
+
+
+def test_the_fast_weight_calls_refuse_them_too(world, monkeypatch):
+    import delta_rule_attention_gb300 as falcon
+    monkeypatch.setattr(falcon, "_lib", world)
+    world.device = 1
+    q, beta = _gpu(2, 16), _gpu(2)
+    with pytest.raises(ValueError, match="current"):
+        falcon.falcon1_decode_step(q, q, q, beta, beta, _gpu(2, 16, 16), q)
+    q, beta = _gpu(1, 1, 4, 16), _gpu(1, 1, 4)
+    for call in (falcon.falcon1_fwd_chunked, falcon.falcon1a_fwd_chunked,
+                 falcon.falcon2_fwd_recurrent, falcon.falcon1_fwd_chunked_fixed_scratch,
+                 falcon.falcon1a_fwd_chunked_normalized):
+        with pytest.raises(ValueError, match="current"):
+            call(q, q, q, beta, beta)
+    with pytest.raises(ValueError, match="current"):
+        falcon.falcon1_bwd_chunked(q, q, q, beta, beta, q)
+    assert world.calls == []
