@@ -216,6 +216,10 @@ def _like(t):
 def _workspace(need, workspace, device):
     if workspace is None:
         return (_empty(need, torch.uint8, device), need) if need else (None, 0)
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -540,6 +544,10 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
     dev = grads[0].device
     if norm is None:
         norm = _empty((), torch.float32, dev)
+    elif not isinstance(norm, torch.Tensor) or norm.dtype != torch.float32:
+        raise TypeError("norm must be a float32 torch.Tensor")
+    elif norm.numel() != 1 or norm.device != dev:
+        raise ValueError(f"norm must be one element on {dev}")
     workspace, have = _workspace(int(lib.falcon_clip_workspace_bytes(rows, len(grads))),
                                  workspace, dev)
     rc = lib.falcon_clip_grad_norm(rows, len(grads), float(max_norm), float(eps), norm.data_ptr(),

@@ -71,7 +71,7 @@ class World:
         monkeypatch.setattr(block, "_raw_stream", lambda index: self.now.cuda_stream)
         monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: self.device, raising=False)
         monkeypatch.setattr(block, "_device_now", lambda: self.device, raising=False)
-        monkeypatch.setattr(torch.Tensor, "get_device", lambda t: t.index)
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda t: getattr(t, "index", -1))
         monkeypatch.setattr(block, "_lib", self)
 
     def __getattr__(self, name):
@@ -183,3 +183,33 @@ def test_the_fast_weight_calls_refuse_them_too(world, monkeypatch):
     with pytest.raises(ValueError, match="current"):
         falcon.falcon1_bwd_chunked(q, q, q, beta, beta, q)
     assert world.calls == []
+
+
+BAD_WORKSPACES = [(lambda: torch.zeros(4096, dtype=torch.uint8), ValueError),
+                  (lambda: _gpu(4096, dtype=torch.uint8, index=1), ValueError),
+                  (lambda: torch.zeros(64, 64)[:, ::2].as_subclass(OnGpu), ValueError),
+                  (lambda: 4096, TypeError)]
+
+
+@pytest.mark.parametrize("name", ["short_conv_bwd", "selective_scan_bwd", "clip_grad_norm"])
+@pytest.mark.parametrize("make,error", BAD_WORKSPACES)
+def test_workspaces_that_a_kernel_cannot_write_are_refused(world, name, make, error):
+    fn, args = _calls()[name]
+    with pytest.raises(error, match="workspace"):
+        fn(**args, workspace=make())
+    assert world.calls == []
+    fn(**args, workspace=_gpu(1024))
+    assert len(world.calls) == 1
+
+
+@pytest.mark.parametrize("make,error", [
+    (lambda: torch.zeros(()), ValueError), (lambda: _gpu(index=1), ValueError),
+    (lambda: _gpu(dtype=torch.float64), TypeError), (lambda: _gpu(dtype=BF16), TypeError),
+    (lambda: _gpu(0), ValueError), (lambda: _gpu(2), ValueError), (lambda: 0.0, TypeError)])
+def test_a_norm_that_a_kernel_cannot_write_is_refused(world, make, error):
+    fn, args = _calls()["clip_grad_norm"]
+    with pytest.raises(error, match="norm"):
+        fn(**args, norm=make())
+    assert world.calls == []
+    for norm in (_gpu(), _gpu(1)):
+        assert fn(**args, norm=norm) is norm
