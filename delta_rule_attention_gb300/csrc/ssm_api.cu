@@ -4,6 +4,10 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "ssm.cuh"
 
 namespace {
@@ -45,6 +49,55 @@ int check_scan(int64_t B, int64_t T, int32_t D, int32_t G, int32_t N, int32_t dt
 }
 
 int esize(int dtype) { return dtype == FALCON_BF16 ? 2 : 4; }
+
+// A clipped gradient's place.
+struct Place {
+  uintptr_t first, end;
+  int64_t index;
+};
+Place place_of(const falcon_grad& g, const void* p, int64_t index) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return {at, at + (uintptr_t)g.count * (uintptr_t)esize(g.dtype), index};
+}
+
+// Every result must have its place to itself, and share it with no gradient but its own:
+// blocks scale their parts in no order.
+int check_clip_places(const falcon_grad* grads, int64_t tensors) {
+  // results in rising order, in place or all apart from the gradients: no need to sort
+  bool rising = true, in_place = true;
+  uintptr_t last = 0, lo[2] = {UINTPTR_MAX, UINTPTR_MAX}, hi[2] = {0, 0};
+  for (int64_t i = 0; i < tensors; ++i) {
+    const falcon_grad& g = grads[i];
+    if (g.count == 0) continue;
+    const Place from = place_of(g, g.grad, i), to = place_of(g, g.out, i);
+    rising = rising && to.first >= last;
+    last = to.end;
+    in_place = in_place && from.first == to.first;
+    lo[0] = std::min(lo[0], from.first), hi[0] = std::max(hi[0], from.end);
+    lo[1] = std::min(lo[1], to.first), hi[1] = std::max(hi[1], to.end);
+  }
+  const bool apart = hi[0] <= lo[1] || hi[1] <= lo[0];
+  if (rising && (in_place || apart)) return FALCON_OK;
+  const std::unique_ptr<Place[]> out(new (std::nothrow) Place[(size_t)tensors]);
+  if (!out) return FALCON_ERR_WORKSPACE;
+  int64_t n = 0;
+  for (int64_t i = 0; i < tensors; ++i)
+    if (grads[i].count > 0) out[n++] = place_of(grads[i], grads[i].out, i);
+  std::sort(out.get(), out.get() + n,
+            [](const Place& a, const Place& b) { return a.first < b.first; });
+  for (int64_t i = 1; i < n; ++i)
+    if (out[i].first < out[i - 1].end) return FALCON_ERR_BAD_ARG;
+  if (in_place || apart) return FALCON_OK;
+  for (int64_t i = 0; i < tensors; ++i) {
+    if (grads[i].count == 0) continue;
+    const Place g = place_of(grads[i], grads[i].grad, i);
+    const Place* p = std::upper_bound(out.get(), out.get() + n, g.first,
+                                      [](uintptr_t at, const Place& q) { return at < q.end; });
+    if (p != out.get() + n && p->first < g.end && (p->index != i || p->first != g.first))
+      return FALCON_ERR_BAD_ARG;
+  }
+  return FALCON_OK;
+}
 
 falcon::ConvArgs conv_args(const falcon_conv_shape* s) {
   falcon::ConvArgs a = {};
@@ -375,10 +428,12 @@ int falcon_clip_grad_norm(const falcon_grad* grads, int64_t tensors, float max_n
     if (!element_aligned(g.grad, esize(g.dtype)) || !element_aligned(g.out, esize(g.dtype)))
       return FALCON_ERR_MISALIGNED;
   }
+  int rc = check_clip_places(grads, tensors);
+  if (rc) return rc;
   const size_t need = falcon_clip_workspace_bytes(grads, tensors);
   if (!workspace || workspace_bytes < need) return FALCON_ERR_WORKSPACE;
   if (!element_aligned(workspace, 16)) return FALCON_ERR_MISALIGNED;
-  const int rc = falcon::check_sm103_device();
+  rc = falcon::check_sm103_device();
   if (rc) return rc;
   return to_status(falcon::launch_clip(grads, tensors, max_norm, eps, norm, workspace, stream));
 }

@@ -583,7 +583,9 @@ typedef struct {
 /* Clips the gradients of a step by their global norm n = sqrt(sum g^2):
  *   out = g * min(1, max_norm / (n + eps)).
  *   grads  HOST array of `tensors` descriptions (read before the call returns);
- *          dense tensors of any size, element-aligned
+ *          dense tensors of any size, element-aligned.  A result shares its place
+ *          with no other result and no gradient but its own (so no gradient is
+ *          named twice in place)
  *   norm   [1] f32, out: n (before clipping)
  * In place, gradients that need no scaling are not rewritten.  A norm that is
  * NaN makes every output NaN; an infinite gradient makes the norm infinite, becomes
@@ -594,8 +596,8 @@ typedef struct {
  *   workspace: at least falcon_clip_workspace_bytes(grads, tensors) bytes,
  *   16-byte aligned.
  * Errors: FALCON_ERR_NULL_PTR, _BAD_SHAPE (negative count), _BAD_DTYPE,
- * _MISALIGNED, _WORKSPACE, _BAD_ARG (max_norm or eps negative or NaN), _DEVICE;
- * _CUDA. */
+ * _MISALIGNED, _WORKSPACE, _BAD_ARG (max_norm or eps negative or NaN, results that
+ * overlap), _DEVICE; _CUDA. */
 size_t falcon_clip_workspace_bytes(const falcon_grad *grads, int64_t tensors);
 int falcon_clip_grad_norm(const falcon_grad *grads, int64_t tensors, float max_norm,
                           float eps, float *norm, void *workspace,
