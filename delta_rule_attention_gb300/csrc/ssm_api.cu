@@ -20,6 +20,10 @@ bool element_aligned(const void* p, int bytes) {
 bool negative(const falcon_strides* s) {
   return s && (s->batch < 0 || s->head < 0 || s->time < 0);
 }
+// An output's rows must not lie on one another.
+bool on_itself(const falcon_strides* s, int64_t B, int64_t H, int64_t T) {
+  return (B > 1 && s->batch == 0) || (H > 1 && s->head == 0) || (T > 1 && s->time == 0);
+}
 int to_status(cudaError_t e) { return e == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA; }
 
 template <int N>
@@ -129,6 +133,8 @@ int falcon_short_conv_fwd(const falcon_conv_shape* s, const void* x, const falco
   const void* words[] = {weight, bias, lengths};
   if (any_misaligned(acts, esize(s->dtype)) || any_misaligned(words, 4))
     return FALCON_ERR_MISALIGNED;
+  // a run reads rows that the run before it would have written
+  if (s->T > 0 && (x == y || on_itself(ys, s->B, s->H, s->T))) return FALCON_ERR_BAD_ARG;
   rc = falcon::check_sm103_device();
   if (rc) return rc;
   falcon::ConvArgs a = conv_args(s);
@@ -169,6 +175,8 @@ int falcon_short_conv_bwd(const falcon_conv_shape* s, const void* x, const falco
   const size_t need = falcon_short_conv_bwd_workspace_bytes(s);
   if (need > 0 && (!workspace || workspace_bytes < need)) return FALCON_ERR_WORKSPACE;
   if (!element_aligned(workspace, 16)) return FALCON_ERR_MISALIGNED;
+  if (s->B > 0 && s->T > 0 && (dx == x || dx == dy || on_itself(dxs, s->B, s->H, s->T)))
+    return FALCON_ERR_BAD_ARG;
   rc = falcon::check_sm103_device();
   if (rc) return rc;
   falcon::ConvArgs a = conv_args(s);
@@ -245,6 +253,7 @@ int falcon_selective_scan_fwd(const falcon_scan_shape* s, const void* u, const f
   const void* words[] = {A, Dskip, delta_bias, h0, h_out, lengths};
   if (any_misaligned(acts, esize(s->dtype)) || any_misaligned(words, 4))
     return FALCON_ERR_MISALIGNED;
+  if (s->T > 0 && on_itself(ys, s->B, 1, s->T)) return FALCON_ERR_BAD_ARG;
   rc = falcon::check_sm103_device();
   if (rc) return rc;
   falcon::ScanArgs a = {};

@@ -432,7 +432,9 @@ int falcon1a_decode_step(int64_t N, int32_t m, int32_t dv, int32_t dtype,
  *     of a call must not name the same slot.
  *   - `fresh` [N] bytes, nullable: nonzero marks a sequence that starts at this
  *     token: its old state counts as zero.
- *   - Outputs must not overlap inputs unless a call says so. */
+ *   - Outputs must not overlap inputs unless a call says so, nor themselves.  An
+ *     output of the convolution that starts where an input does, or an output with
+ *     a zero stride over more than one row, is FALCON_ERR_BAD_ARG. */
 
 /* Element strides of a tensor [B,H,T,m] (or [B,T,D], [B,T,G,N]: `head` is then
  * unused, or the group's stride). */
