@@ -15,6 +15,8 @@
 //      each one's states and decays recomputed into registers;
 //   4. sums: dB and dC over the blocks of channels, dA, dDskip and ddelta_bias over
 //      the blocks of tokens, in a fixed order.
+// Where the terms of dB and dC of all blocks of channels would take more than kTermBytes,
+// steps 3 and 4 run once for each set of blocks whose terms fit.
 // A warp owns 2 * 32 / LN channels: LN lanes share two channels, four states each, as
 // f32x2 pairs.  <g, B>, <w, A> and <C, h> are summed over the LN lanes for kSub
 // tokens at once, halving the tokens a lane keeps at each exchange; dB and dC are
@@ -80,18 +82,32 @@ struct GradShared {
   float sums[C::kOver || C::kWarps == 1 ? 1 : kChunk][2 * C::kNP];
 };
 
+// Bytes of dB and dC terms that are kept at a time.  A block covers 64 channels with 16
+// states and 2 with 128, so that the terms of all blocks would grow past any tensor of
+// the call (17 GB for B8 T2048 D2048 N128).  Each pass has a last wave of its own: that
+// call takes 26.6 ms in eight passes, 27.4 with 512 MB at a time and 25.8 with all terms
+// kept; one with 64 states, whose terms are 2 GB, 5.19 ms, and 5.47 with 512 MB.
+constexpr int64_t kTermBytes = 2LL << 30;
+
 // Parts of the workspace, in floats.
 struct Layout {
   int64_t chunks, parts, groups, per, NP;
+  // parts of a pass of step 3, and the place of its first one's terms: 1 where there are
+  // several passes, whose sum so far lies in place 0
+  int64_t at_once, place0;
   size_t hin, gin, sums, dbc, dA, dD, dbias, total;
   Layout(int64_t B, int64_t T, int D, int G, int N) {
     const int ln = lanes_of(N), ch = 64 / ln * warps_of(ln);
     NP = 4 * ln;
     chunks = (T + kChunk - 1) / kChunk;
     parts = (D / G + ch - 1) / ch;
+    const int64_t rows = B * T * G * 2 * NP, most = kTermBytes / 4 / (rows > 0 ? rows : 1);
+    const int64_t passes = most >= parts ? 1 : most < 1 ? parts : (parts + most - 1) / most;
+    at_once = (parts + passes - 1) / passes;
+    place0 = passes > 1;
     // chunks a block walks in step 3: as many as leave four blocks a resident slot
     per = 1;
-    while (per < 8 && G * parts * B * (chunks / (2 * per)) >= 152 * 3 * 8) per *= 2;
+    while (per < 8 && G * at_once * B * (chunks / (2 * per)) >= 152 * 3 * 8) per *= 2;
     groups = (chunks + per - 1) / per;
     size_t at = 0;
     auto take = [&](int64_t n) {
@@ -102,7 +118,7 @@ struct Layout {
     hin = take(B * chunks * D * NP);
     gin = take(B * chunks * D * NP);
     sums = take(B * chunks * D);
-    dbc = take(parts * B * T * G * 2 * NP);
+    dbc = take((place0 + at_once) * rows);
     dA = take(groups * B * D * NP);
     dD = take(groups * B * D);
     dbias = take(groups * B * D);
@@ -124,12 +140,13 @@ struct Place {
   float its_bias[2];
   const E *u, *dl, *z, *dy, *Bm, *Cm;
 
-  __device__ __forceinline__ Place(const ScanArgs& a, int parts) {
+  // blocks of `parts` parts from part0 on
+  __device__ __forceinline__ Place(const ScanArgs& a, int parts, int part0) {
     lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pair = lane / LN, q = lane % LN, n0 = q * 4;
     const int R = a.D / a.G;
     const int blk = blockIdx.x % (a.G * parts);
-    g = blk / parts, part = blk - g * parts;
+    g = blk / parts, part = part0 + blk - g * parts;
     const int w0 = (part * C::kWarps + warp) * C::kChannels, r0 = w0 + pair * 2;
     have = r0 >= R ? 0 : (r0 + 1 < R ? 2 : 1);
     d = g * R + (have ? r0 : 0);
@@ -255,7 +272,7 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32)
   typedef Cfg<LN> C;
   extern __shared__ __align__(16) unsigned char bytes[];
   auto& bc = *reinterpret_cast<float(*)[kChunk][2][C::kNP]>(bytes);
-  const Place<E, LN> p(a, (int)l.parts);
+  const Place<E, LN> p(a, (int)l.parts, 0);
   WarpShared<LN>& sh = reinterpret_cast<WarpShared<LN>*>(bytes + sizeof(bc))[p.warp];
   const int64_t chunk = blockIdx.x / (unsigned)(a.G * l.parts), t0 = chunk * kChunk;
   if (t0 >= p.n) return;
@@ -360,13 +377,13 @@ __global__ void __launch_bounds__(128)
 template <typename E, int LN>
 __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32, LN == 4 ? 3 : 1)
     scan_bwd_grad_kernel(const __grid_constant__ ScanArgs a, float* ws,
-                         const __grid_constant__ Layout l) {
+                         const __grid_constant__ Layout l, int part0, int parts) {
   typedef Cfg<LN> C;
   typedef typename Raw<E>::Pair Pair;
   constexpr int kMine = LN >= kSub ? 1 : kSub / LN;  // tokens of a group a lane finishes
   extern __shared__ __align__(16) unsigned char bytes[];
   auto& bc = *reinterpret_cast<float(*)[kChunk][2][C::kNP]>(bytes);
-  const Place<E, LN> p(a, (int)l.parts);
+  const Place<E, LN> p(a, parts, part0);
   WarpShared<LN>* all = reinterpret_cast<WarpShared<LN>*>(bytes + sizeof(bc));
   GradShared<LN>* grads = reinterpret_cast<GradShared<LN>*>(all + C::kWarps);
   WarpShared<LN>& sh = all[p.warp];
@@ -389,7 +406,8 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32, LN == 4 ? 3 : 1)
   E* dd = static_cast<E*>(a.ddelta) + p.b * a.T * a.D + p.d;
   E* dz = a.z ? static_cast<E*>(a.dz) + p.b * a.T * a.D + p.d : nullptr;
 
-  const int64_t group = blockIdx.x / (unsigned)(a.G * l.parts);
+  const int64_t group = blockIdx.x / (unsigned)(a.G * parts);
+  const int64_t place = l.place0 + p.part - part0;  // of this part's dB and dC terms
   for (int64_t chunk = group * l.per; chunk < (group + 1) * l.per && chunk < l.chunks; ++chunk) {
     const int64_t t0 = chunk * kChunk;
     if (t0 >= p.n) {  // behind the row's end
@@ -605,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32, LN == 4 ? 3 : 1)
           else if (t0 + k0 + k < p.n)
             *reinterpret_cast<ulonglong2*>(
                 ws + l.dbc +
-                (((p.part * a.B + p.b) * a.T + t0 + k0 + k) * a.G + p.g) * 2 * C::kNP + w * 4) = v;
+                (((place * a.B + p.b) * a.T + t0 + k0 + k) * a.G + p.g) * 2 * C::kNP + w * 4) = v;
         }
       }
       __syncwarp();
@@ -623,7 +641,7 @@ __global__ void __launch_bounds__(Cfg<LN>::kWarps * 32, LN == 4 ? 3 : 1)
           }
           *reinterpret_cast<ulonglong2*>(
               ws + l.dbc +
-              (((p.part * a.B + p.b) * a.T + t0 + k) * a.G + p.g) * 2 * C::kNP + w * 4) = v;
+              (((place * a.B + p.b) * a.T + t0 + k) * a.G + p.g) * 2 * C::kNP + w * 4) = v;
         }
       }
       __syncthreads();
@@ -669,11 +687,13 @@ __device__ __forceinline__ float sum_parts(const float* from, int64_t width, int
 }
 
 // Step 4: the first `first` blocks sum the padded [D,NP] values of dA, the next ones up
-// to `second` the D of dDskip and ddelta_bias, the others dB and dC.
+// to `second` the D of dDskip and ddelta_bias, the others the terms of dB and dC in the
+// places from..to - 1: into place 0, or when `last` into dB and dC.
 template <typename E>
 __global__ void __launch_bounds__(256)
-    scan_bwd_sum_kernel(const __grid_constant__ ScanArgs a, const float* ws,
-                        const __grid_constant__ Layout l, int64_t first, int64_t second) {
+    scan_bwd_sum_kernel(const __grid_constant__ ScanArgs a, float* ws,
+                        const __grid_constant__ Layout l, int64_t first, int64_t second,
+                        int from, int to, bool last) {
   __shared__ float sh[8][32];
   const int64_t parts = l.groups * a.B, width = (int64_t)a.D * l.NP;
   const int lane = threadIdx.x & 31;
@@ -701,18 +721,20 @@ __global__ void __launch_bounds__(256)
   const int64_t bt = row / a.G, b = bt / a.T;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (bt - b * a.T < row_length(a.lengths, b, a.T)) {
-    const float* from = ws + l.dbc + i * 4;
+    const float* terms = ws + l.dbc + i * 4;
 #pragma unroll 8
-    for (int64_t p = 0; p < l.parts; ++p) {
-      const float4 e = *reinterpret_cast<const float4*>(from + p * rows * 2 * l.NP);
+    for (int64_t p = from; p < to; ++p) {
+      const float4 e = *reinterpret_cast<const float4*>(terms + p * rows * 2 * l.NP);
       v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
     }
+    if (!last) *reinterpret_cast<float4*>(ws + l.dbc + i * 4) = v;
   }
-  E* to = static_cast<E*>(w * 4 < l.NP ? a.dB : a.dC) + row * a.N + n0;
+  if (!last) return;
+  E* out = static_cast<E*>(w * 4 < l.NP ? a.dB : a.dC) + row * a.N + n0;
   const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (n0 + k < a.N) store_vec<E, 1>(to + k, FloatV<1>{{f[k]}});
+    if (n0 + k < a.N) store_vec<E, 1>(out + k, FloatV<1>{{f[k]}});
 }
 
 template <typename E, int LN>
@@ -730,7 +752,6 @@ cudaError_t bwd_lanes(const ScanArgs& a, cudaStream_t stream) {
   const int64_t blocks = a.G * l.parts;
   if (blocks * l.chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const dim3 chunks((unsigned)(blocks * l.chunks), (unsigned)a.B);
-  const dim3 groups((unsigned)(blocks * l.groups), (unsigned)a.B);
   if (l.chunks > 0) {
     scan_bwd_chunk_kernel<E, LN><<<chunks, C::kWarps * 32, bytes1, stream>>>(a, ws, l);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -739,14 +760,25 @@ cudaError_t bwd_lanes(const ScanArgs& a, cudaStream_t stream) {
   scan_bwd_chain_kernel<<<dim3((unsigned)((quads + 127) / 128), (unsigned)a.B, 2), 128, 0,
                           stream>>>(a, ws, l);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (l.chunks > 0) {
-    scan_bwd_grad_kernel<E, LN><<<groups, C::kWarps * 32, bytes3, stream>>>(a, ws, l);
+  const int64_t terms = (a.B * a.T * a.G * 2 * LN + 255) / 256;
+  for (int64_t part0 = 0; part0 < l.parts; part0 += l.at_once) {
+    const int parts = (int)(l.parts - part0 < l.at_once ? l.parts - part0 : l.at_once);
+    if (l.chunks > 0) {
+      const dim3 groups((unsigned)(a.G * parts * l.groups), (unsigned)a.B);
+      scan_bwd_grad_kernel<E, LN>
+          <<<groups, C::kWarps * 32, bytes3, stream>>>(a, ws, l, (int)part0, parts);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    const bool last = part0 + parts == l.parts;
+    const int64_t first = last ? ((int64_t)a.D * l.NP + 31) / 32 : 0;
+    const int64_t second = last ? first + (a.D + 31) / 32 : 0;
+    const int from = part0 > 0 ? 0 : (int)l.place0, to = (int)l.place0 + parts;
+    if (second + terms > 0)
+      scan_bwd_sum_kernel<E><<<(unsigned)(second + terms), 256, 0, stream>>>(a, ws, l, first,
+                                                                            second, from, to, last);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const int64_t first = ((int64_t)a.D * l.NP + 31) / 32, second = first + (a.D + 31) / 32;
-  const int64_t sums = second + (a.B * a.T * a.G * 2 * LN + 255) / 256;
-  scan_bwd_sum_kernel<E><<<(unsigned)sums, 256, 0, stream>>>(a, ws, l, first, second);
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 template <typename E>

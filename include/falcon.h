@@ -541,7 +541,9 @@ int falcon_selective_scan_fwd(const falcon_scan_shape *shape, const void *u,
  *   dDskip, ddelta_bias [D] f32, out, nullable;  dh0 [B,D,N] f32, out, nullable,
  *   may alias dh_T
  *   workspace: at least falcon_selective_scan_bwd_workspace_bytes(shape) bytes,
- *   256-byte aligned.  Sums over tokens and channels run in a fixed order. */
+ *   256-byte aligned: a state and an adjoint for every 32 tokens, and sums, of which
+ *   those of dB and dC take 2 GB at most, or two fp32 copies of dB and dC where that
+ *   is more.  Sums over tokens and channels run in a fixed order. */
 size_t falcon_selective_scan_bwd_workspace_bytes(const falcon_scan_shape *shape);
 int falcon_selective_scan_bwd(const falcon_scan_shape *shape, const void *u,
                               const falcon_strides *u_strides, const void *delta,
