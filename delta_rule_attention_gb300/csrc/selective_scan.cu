@@ -45,6 +45,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+// sigmoid() with its exponent held at 128, which changes no gate (2^128 is infinite) but
+// the kernel's registers with bf16 and N = 16: 127, and 130 without, with which 32 x 512
+// tokens of 2048 channels take 199 us instead of 188.
+__device__ __forceinline__ float gate_sigmoid(float x) {
+  return rcp_approx(1.f + exp2_approx(fminf(-x * kLog2e, 128.f)));
+}
+
 template <int LN, int NS, bool SPLIT>
 struct Cfg {
   static constexpr int kGroups = 32 / LN;        // channel pairs of a warp
@@ -195,7 +202,7 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
         s[e].x = in ? (a.softplus ? sp.x : x.x) : 0.f;
         s[e].y = in ? (a.softplus ? sp.y : x.y) : 0.f;
         v[e] = unpack2(mul2(pair2(s[e]), pair2(ut)));
-        const float2 sg = make_float2(sigmoid(zt.x), sigmoid(zt.y));
+        const float2 sg = make_float2(gate_sigmoid(zt.x), gate_sigmoid(zt.y));
         const float2 silu = unpack2(mul2(pair2(zt), pair2(sg)));
         g[e] = make_float2(gate ? silu.x : 1.f, gate ? silu.y : 1.f);
         k[e] = unpack2(mul2(mul2(pack2(skip[0], skip[1]), pair2(ut)), pair2(g[e])));
