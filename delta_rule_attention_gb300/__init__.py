@@ -192,6 +192,9 @@ def falcon_workspace_bytes(shape: falcon_shape) -> int:
 def _fwd(name, q, k, v, beta, lam, S0=None, x_prev=None, chunk=64, phi="l2", eps=1e-6,
          eps_gamma=1e-6, o=None, S_out=None, x_last=None, workspace=None, stream=None,
          want_x_last=True, ridge="given"):
+    if stream is not None:
+        return block.elsewhere(stream, _fwd, name, q, k, v, beta, lam, S0, x_prev, chunk, phi, eps,
+                               eps_gamma, o, S_out, x_last, workspace, None, want_x_last, ridge)
     lib = load_library()
     _need(q, "q")
     B, H, T, m = q.shape
@@ -246,6 +249,9 @@ def falcon1_fwd_chunked_fixed_scratch(q, k, v, beta, lam, S0=None, x_prev=None, 
     GPU work overlaps share that array and race; the first call on a device
     resolves its address and should precede any stream capture.  Returns
     (o, S_T, x_last)."""
+    if stream is not None:
+        return block.elsewhere(stream, falcon1_fwd_chunked_fixed_scratch, q, k, v, beta, lam, S0,
+                               x_prev, chunk, phi, eps, eps_gamma, o, S_out, x_last, None, ridge)
     lib = load_library()
     _need(q, "q")
     B, H, T, m = q.shape
@@ -291,6 +297,10 @@ def falcon1a_fwd_chunked_normalized(q, k, v, beta, lam, S0=None, z0=None, x_prev
     (z_t^T phi(q_t) + eps_attn), z_t = gamma_t z_{t-1} + eta_t x_t.  Arguments
     as falcon1a_fwd_chunked, plus z0 [B,H,m] fp32 or None.  Returns
     (o, S_T, z_T, x_last)."""
+    if stream is not None:
+        return block.elsewhere(stream, falcon1a_fwd_chunked_normalized, q, k, v, beta, lam, S0, z0,
+                               x_prev, eps_attn, chunk, phi, eps, eps_gamma, o, S_out, z_out,
+                               x_last, workspace, None, ridge)
     lib = load_library()
     _need(q, "q")
     B, H, T, m = q.shape
@@ -335,6 +345,9 @@ def falcon_bwd_workspace_bytes(shape: falcon_shape) -> int:
 def _bwd(name, q, k, v, beta, lam, dO, S0=None, x_prev=None, dS_T=None, dx_last=None, chunk=64,
          phi="l2", eps=1e-6, eps_gamma=1e-6, ridge="given", workspace=None, stream=None,
          grads=None):
+    if stream is not None:
+        return block.elsewhere(stream, _bwd, name, q, k, v, beta, lam, dO, S0, x_prev, dS_T,
+                               dx_last, chunk, phi, eps, eps_gamma, ridge, workspace, None, grads)
     lib = load_library()
     _need(q, "q")
     B, H, T, m = q.shape
@@ -394,6 +407,10 @@ def falcon1a_bwd_chunked(q, k, v, beta, lam, dO, S0=None, x_prev=None, dS_T=None
 def _fwd2(name, q, k, v, beta, lam, S0=None, x_prev=None, phi="l2", eps=1e-6,
           eps_gamma=1e-6, o=None, S_out=None, x_last=None, stream=None, want_x_last=True,
           ridge="given", workspace=None, chunked=False):
+    if stream is not None:
+        return block.elsewhere(stream, _fwd2, name, q, k, v, beta, lam, S0, x_prev, phi, eps,
+                               eps_gamma, o, S_out, x_last, None, want_x_last, ridge, workspace,
+                               chunked)
     lib = load_library()
     _need(q, "q")
     B, H, T, m = q.shape
@@ -474,6 +491,9 @@ def falcon3a_fwd_recurrent(q, k, v, beta, lam, window, S0=None, phi="l2", eps=1e
     """Falcon-3A forward (sliding window of ``window`` write pairs, 1..32) over
     fresh sequences.  q, k [B,H,T,m], v [B,H,T,dv] (bf16 or fp32), beta, lam
     [B,H,T] fp32; S0 [B,H,m,dv] fp32 or None.  Returns (o, S_T, x_last)."""
+    if stream is not None:
+        return block.elsewhere(stream, falcon3a_fwd_recurrent, q, k, v, beta, lam, window, S0, phi,
+                               eps, eps_gamma, o, S_out, x_last, None, want_x_last, ridge)
     lib = load_library()
     _need(q, "q")
     B, H, T, m = q.shape
@@ -509,6 +529,10 @@ def falcon3a_fwd_chunked(q, k, v, beta, lam, window, S0=None, phi="l2", eps=1e-6
     for bf16 with m = dv = 64, the token-recurrent kernel otherwise).
     Arguments as falcon3a_fwd_recurrent, plus an optional workspace of
     falcon_workspace_bytes(shape) bytes.  Returns (o, S_T, x_last)."""
+    if stream is not None:
+        return block.elsewhere(stream, falcon3a_fwd_chunked, q, k, v, beta, lam, window, S0, phi,
+                               eps, eps_gamma, o, S_out, x_last, workspace, None, want_x_last,
+                               ridge)
     lib = load_library()
     _need(q, "q")
     B, H, T, m = q.shape
@@ -543,6 +567,9 @@ def falcon3a_fwd_chunked(q, k, v, beta, lam, window, S0=None, phi="l2", eps=1e-6
 
 def _decode(name, q, k, v, beta, lam, S, x_prev, fresh=None, phi="l2", eps=1e-6,
             eps_gamma=1e-6, o=None, stream=None, ridge="given"):
+    if stream is not None:
+        return block.elsewhere(stream, _decode, name, q, k, v, beta, lam, S, x_prev, fresh, phi,
+                               eps, eps_gamma, o, None, ridge)
     lib = load_library()
     _need(q, "q")
     N, m = q.shape

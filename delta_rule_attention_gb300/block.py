@@ -111,24 +111,25 @@ def refuse_other_device(t, name):
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_device_now()}")
 
 
-def _elsewhere(stream, fn, *args):
+def elsewhere(stream, fn, *args):
     """fn(*args) on a stream that need not be the current one.  Its new tensors come from
     that stream's memory: what the current stream's pool hands out may be in use by work
     still queued there, which nothing orders before this call.  The tensors that it
     returns are marked as used by the current stream as well, so that they may be dropped
     there as soon as what reads them is queued."""
     here = torch.cuda.current_stream(stream.device)
+    if here.cuda_stream == stream.cuda_stream and stream.device.index == _device_now():
+        return fn(*args)
     given = set()
     for a in args:
         given.update(map(id, a.values() if isinstance(a, dict) else (a,)))
     with torch.cuda.stream(stream):
         out = fn(*args)
-    if here.cuda_stream != stream.cuda_stream:
-        new = (out,) if isinstance(out, torch.Tensor) else \
-            out.values() if isinstance(out, dict) else out
-        for t in new:
-            if t is not None and id(t) not in given:
-                t.record_stream(here)
+    new = (out,) if isinstance(out, torch.Tensor) else \
+        out.values() if isinstance(out, dict) else out
+    for t in new:
+        if t is not None and id(t) not in given:
+            t.record_stream(here)
     return out
 
 
@@ -263,7 +264,7 @@ def falcon_short_conv_fwd(x, weight, bias=None, state=None, lengths=None, activa
     "identity".  Returns (y, state_out): y of x's shape, dense unless passed in,
     and the last width-1 inputs of every row."""
     if stream is not None:
-        return _elsewhere(stream, falcon_short_conv_fwd, x, weight, bias, state, lengths,
+        return elsewhere(stream, falcon_short_conv_fwd, x, weight, bias, state, lengths,
                           activation, y, state_out)
     lib = _lib or _library()
     shape, dt, dev, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
@@ -283,7 +284,7 @@ def falcon_short_conv_bwd(x, weight, dy, bias=None, state=None, lengths=None, ds
     Returns a dict with dx (dense, x's shape), dweight, dbias (fp32) and dstate;
     ``grads`` may pass preallocated outputs."""
     if stream is not None:
-        return _elsewhere(stream, falcon_short_conv_bwd, x, weight, dy, bias, state, lengths,
+        return elsewhere(stream, falcon_short_conv_bwd, x, weight, dy, bias, state, lengths,
                           dstate_out, activation, grads, workspace)
     lib = _lib or _library()
     shape, dt, dev, B, C, W = _conv_setup(x, weight, bias, state, lengths, activation)
@@ -321,7 +322,7 @@ def falcon_short_conv_step(x, weight, state, bias=None, slots=None, fresh=None,
     uses state i when absent), fresh [N] uint8 marks sequences that start here.
     Returns y [N,channels]."""
     if stream is not None:
-        return _elsewhere(stream, falcon_short_conv_step, x, weight, state, bias, slots, fresh,
+        return elsewhere(stream, falcon_short_conv_step, x, weight, state, bias, slots, fresh,
                           activation, y)
     lib = _lib or _library()
     dt = _dtype(x, "x")
@@ -399,7 +400,7 @@ def falcon_selective_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=No
     and Bm, Cm [B,T,G,N] (bf16 or fp32, any row strides); A [D,N], D, delta_bias
     [D] and h0 [B,D,N] fp32; lengths [B] int32.  Returns (y, h_T)."""
     if stream is not None:
-        return _elsewhere(stream, falcon_selective_scan_fwd, u, delta, A, Bm, Cm, D, z, delta_bias,
+        return elsewhere(stream, falcon_selective_scan_fwd, u, delta, A, Bm, Cm, D, z, delta_bias,
                           h0, lengths, softplus, y, h_out)
     lib = _lib or _library()
     shape, dt, dev, hs = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
@@ -424,7 +425,7 @@ def falcon_selective_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bia
     dh0 (fp32); dz, dD and ddelta_bias are None where z, D or delta_bias is.
     ``grads`` may pass preallocated outputs."""
     if stream is not None:
-        return _elsewhere(stream, falcon_selective_scan_bwd, u, delta, A, Bm, Cm, dy, D, z,
+        return elsewhere(stream, falcon_selective_scan_bwd, u, delta, A, Bm, Cm, dy, D, z,
                           delta_bias, h0, lengths, dh_T, softplus, grads, workspace)
     lib = _lib or _library()
     shape, dt, dev, hs = _scan_setup(u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, softplus)
@@ -465,7 +466,7 @@ def falcon_selective_scan_step(u, delta, A, Bm, Cm, h, D=None, z=None, delta_bia
     fp32 is updated in place; slots and fresh as in falcon_short_conv_step.
     Returns y [N,D]."""
     if stream is not None:
-        return _elsewhere(stream, falcon_selective_scan_step, u, delta, A, Bm, Cm, h, D, z,
+        return elsewhere(stream, falcon_selective_scan_step, u, delta, A, Bm, Cm, h, D, z,
                           delta_bias, slots, fresh, softplus, y)
     lib = _lib or _library()
     dt = _dtype(u, "u")
@@ -507,7 +508,7 @@ def falcon_clip_grad_norm(grads, max_norm, out=None, eps=1e-6, norm=None, worksp
     tensors of ``out`` (same sizes and dtypes).  Returns n, a 0-d fp32 tensor on
     the gradients' device; the host does not wait for it."""
     if stream is not None:
-        return _elsewhere(stream, falcon_clip_grad_norm, grads, max_norm, out, eps, norm, workspace)
+        return elsewhere(stream, falcon_clip_grad_norm, grads, max_norm, out, eps, norm, workspace)
     lib = _lib or _library()
     grads = list(grads)
     if not grads:

@@ -75,7 +75,7 @@ class World:
         monkeypatch.setattr(block, "_lib", self)
 
     def __getattr__(self, name):
-        if not name.startswith("falcon_"):
+        if not name.startswith("falcon"):
             raise AttributeError(name)
 
         def call(*args):
@@ -213,3 +213,84 @@ def test_a_norm_that_a_kernel_cannot_write_is_refused(world, make, error):
     assert world.calls == []
     for norm in (_gpu(), _gpu(1)):
         assert fn(**args, norm=norm) is norm
+
+
+def _fast_weight_calls():
+    import delta_rule_attention_gb300 as f
+    q, b, b2 = _gpu(1, 2, 4, 16), _gpu(1, 2, 4), _gpu(1, 2, 4, 16)
+    n, nb = _gpu(2, 16), _gpu(2)
+    return {
+        "falcon1_fwd_chunked": (f.falcon1_fwd_chunked, (q, q, q, b, b), {}),
+        "falcon1a_fwd_chunked": (f.falcon1a_fwd_chunked, (q, q, q, b, b), {}),
+        "fixed_scratch": (f.falcon1_fwd_chunked_fixed_scratch, (q, q, q, b, b), {}),
+        "normalized": (f.falcon1a_fwd_chunked_normalized, (q, q, q, b, b), {}),
+        "falcon1_bwd_chunked": (f.falcon1_bwd_chunked, (q, q, q, b, b, q), {}),
+        "falcon2_fwd_recurrent": (f.falcon2_fwd_recurrent, (q, q, q, b2, b), {}),
+        "falcon2_fwd_chunked": (f.falcon2_fwd_chunked, (q, q, q, b2, b), {}),
+        "falcon2a_fwd_chunked": (f.falcon2a_fwd_chunked, (q, q, q, b2, b), {}),
+        "falcon3a_fwd_recurrent": (f.falcon3a_fwd_recurrent, (q, q, q, b, b), dict(window=4)),
+        "falcon3a_fwd_chunked": (f.falcon3a_fwd_chunked, (q, q, q, b, b), dict(window=4)),
+        "falcon1_decode_step": (f.falcon1_decode_step, (n, n, n, nb, nb, _gpu(2, 16, 16), n), {}),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(_fast_weight_calls()))
+def test_memory_of_a_fast_weight_call_on_a_given_stream_comes_from_it(world, monkeypatch, name):
+    import delta_rule_attention_gb300 as falcon
+    monkeypatch.setattr(falcon, "_lib", world)
+    fn, args, kw = _fast_weight_calls()[name]
+    side = Stream(77)
+    out = fn(*args, **kw, stream=side)
+    assert world.allocated and all(s is side for s in world.allocated)
+    (_, passed), = world.calls
+    assert passed[-1].value == 77
+    assert all(t.recorded == [world.here] for t in _tensors(out))
+    # on the current stream, nothing is recorded
+    for out in (fn(*args, **kw), fn(*args, **kw, stream=world.here)):
+        assert not any(hasattr(t, "recorded") for t in _tensors(out))
+
+
+def test_a_fast_weight_call_keeps_its_options_on_a_given_stream(world, monkeypatch):
+    """The library gets the same arguments whichever way the stream is named."""
+    import delta_rule_attention_gb300 as falcon
+    monkeypatch.setattr(falcon, "_lib", world)
+    q, b = _gpu(1, 2, 4, 16), _gpu(1, 2, 4)
+    o, S, xl, ws = _gpu(1, 2, 4, 16), _gpu(1, 2, 16, 16), _gpu(1, 2, 16), _gpu(4096)
+    S0, xp, z0 = _gpu(1, 2, 16, 16), _gpu(1, 2, 16), _gpu(1, 2, 16)
+    opts = dict(phi="rms", eps=1e-3, eps_gamma=1e-4, ridge="scaled")
+    n, nb = _gpu(2, 16), _gpu(2)
+    fresh = _gpu(2, dtype=torch.uint8)
+    dS, dx = _gpu(1, 2, 16, 16), _gpu(1, 2, 16)
+    g = {k: _gpu(1, 2, 4, 16) for k in ("dq", "dk", "dv")}
+    g.update(dbeta=_gpu(1, 2, 4), dlambda=_gpu(1, 2, 4), dS0=_gpu(1, 2, 16, 16),
+             dx_prev=_gpu(1, 2, 16))
+    outs = dict(o=o, S_out=S, x_last=xl)
+    calls = [
+        (falcon.falcon1_fwd_chunked, (q, q, q, b, b, S0, xp, 32),
+         dict(outs, workspace=ws, **opts)),
+        (falcon.falcon1_fwd_chunked_fixed_scratch, (q, q, q, b, b, S0, xp, 32), dict(outs, **opts)),
+        (falcon.falcon1a_fwd_chunked_normalized, (q, q, q, b, b, S0, z0, xp, 1e-2, 32),
+         dict(outs, z_out=_gpu(1, 2, 16), workspace=ws, **opts)),
+        (falcon.falcon1a_bwd_chunked, (q, q, q, b, b, q, S0, xp, dS, dx, 32),
+         dict(workspace=ws, grads=g, **opts)),
+        (falcon.falcon2a_fwd_chunked, (q, q, q, _gpu(1, 2, 4, 16), b, S0, xp),
+         dict(outs, workspace=ws, **opts)),
+        (falcon.falcon2_fwd_recurrent, (q, q, q, _gpu(1, 2, 4, 16), b, S0, xp), dict(outs, **opts)),
+        (falcon.falcon3a_fwd_recurrent, (q, q, q, b, b, 5, S0), dict(outs, **opts)),
+        (falcon.falcon3a_fwd_chunked, (q, q, q, b, b, 5, S0), dict(outs, workspace=ws, **opts)),
+        (falcon.falcon1a_decode_step, (n, n, n, nb, nb, _gpu(2, 16, 16), n, fresh),
+         dict(o=_gpu(2, 16), **opts)),
+    ]
+
+    def plain(a):
+        if hasattr(a, "_obj"):  # a reference to a structure
+            return bytes(a._obj)
+        return getattr(a, "value", a)
+
+    for fn, args, kw in calls:
+        world.calls.clear()
+        fn(*args, **kw)
+        fn(*args, **kw, stream=Stream(9))
+        (n0, a), (n1, c) = world.calls
+        assert n0 == n1 and plain(c[-1]) == 9
+        assert [plain(v) for v in a[:-1]] == [plain(v) for v in c[:-1]], fn
