@@ -6,10 +6,13 @@
 // that all agree on n without an atomic or a third launch) and scales, from the
 // back, where L2 still holds what the first launch read last.  The
 // tensors' addresses travel as kernel arguments; more than kMost tensors take
-// further launches of each kind.
+// further launches of each kind (arguments for 64 instead of 512 tensors save nothing:
+// 1 to 61 small tensors take 4.8 to 5.7 us in a graph, and 12 to 36 us a call, with either).
 //
-// Bound by memory: 88 M bf16 gradients (177 MB) 31 and 56 us alone, 88 to 92 us a call;
-// reading them twice and writing them once at a copy's rate takes 78.  Measured and not
+// Bound by memory: 88 M bf16 gradients (177 MB) 84 us a call in a graph, 32 and 54 us each
+// launch alone; reading them twice and writing them once at a copy's rate takes 78.  The
+// order and the marks save 1.5 to 2.5 us of a call's 90: scaling from the front takes 91.2,
+// all loads of the first pass marked as passing 92.2, none 91.1.  Measured and not
 // kept: finding the next chunk's tensor while a chunk's loads are under way (98 us: the
 // registers cost more blocks than the search costs time), four vectors a batch with
 // more blocks (94).
@@ -20,7 +23,6 @@ namespace falcon {
 namespace {
 
 constexpr int kMost = 512;        // tensors of one launch
-constexpr int kFew = 64;          // of a launch with short arguments
 constexpr int kThreads = 256;
 // Elements a block takes at a time: many of a large set, where finding a chunk's
 // tensor should cost little beside it, few of a small one, where all blocks
@@ -33,19 +35,17 @@ constexpr int64_t kStays = 40LL << 20;
 // Blocks of a launch: what the SMs hold at once.
 constexpr int kSquareBlocks = 152 * 4, kScaleBlocks = 152 * 3;
 
-template <int MOST>
 struct Batch {
-  const void* grad[MOST];
-  void* out[MOST];
-  int64_t count[MOST];
-  int64_t first[MOST];  // chunks before this tensor's
-  unsigned char dtype[MOST];
+  const void* grad[kMost];
+  void* out[kMost];
+  int64_t count[kMost];
+  int64_t first[kMost];  // chunks before this tensor's
+  unsigned char dtype[kMost];
   int tensors, chunk;
   int64_t chunks, passing;  // chunks of the batch, those not to be kept in L2
 };
 
-template <int MOST>
-__device__ __forceinline__ int tensor_of(const Batch<MOST>& p, int64_t chunk) {
+__device__ __forceinline__ int tensor_of(const Batch& p, int64_t chunk) {
   int lo = 0, hi = p.tensors - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -140,9 +140,8 @@ __device__ __forceinline__ double chunk_squares(const E* g, int n, bool passing)
   return sum;
 }
 
-template <int MOST>
 __global__ void __launch_bounds__(kThreads)
-    clip_squares_kernel(const __grid_constant__ Batch<MOST> p, double* partial) {
+    clip_squares_kernel(const __grid_constant__ Batch p, double* partial) {
   __shared__ double sh[kThreads / 32];
   double acc = 0.0;
   for (int64_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
@@ -189,9 +188,8 @@ __device__ __forceinline__ void chunk_scale(const E* g, E* o, int n, float c) {
   }
 }
 
-template <int MOST>
 __global__ void __launch_bounds__(kThreads)
-    clip_scale_kernel(const __grid_constant__ Batch<MOST> p, const double* partial, int parts,
+    clip_scale_kernel(const __grid_constant__ Batch p, const double* partial, int parts,
                       float max_norm, float eps, float* norm) {
   __shared__ double sh[kThreads / 32];
   __shared__ float factor;
@@ -224,13 +222,12 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Fills p with the next tensors from `at` on; returns the index after them.
-template <int MOST>
-int64_t fill(Batch<MOST>* p, const falcon_grad* grads, int64_t tensors, int64_t at, int chunk) {
+int64_t fill(Batch* p, const falcon_grad* grads, int64_t tensors, int64_t at, int chunk) {
   p->tensors = 0;
   p->chunk = chunk;
   p->chunks = 0;
   int64_t bytes = 0;
-  for (; at < tensors && p->tensors < MOST; ++at) {
+  for (; at < tensors && p->tensors < kMost; ++at) {
     if (grads[at].count == 0) continue;
     const int k = p->tensors++;
     p->grad[k] = grads[at].grad;
@@ -245,10 +242,16 @@ int64_t fill(Batch<MOST>* p, const falcon_grad* grads, int64_t tensors, int64_t 
   return at;
 }
 
-template <int MOST>
-cudaError_t clip(const falcon_grad* grads, int64_t tensors, float max_norm, float eps, float* norm,
-                 double* partial, cudaStream_t stream) {
-  static thread_local Batch<MOST> p;
+}  // namespace
+
+size_t clip_workspace_bytes(const falcon_grad*, int64_t tensors) {
+  return sizeof(double) * kSquareBlocks * (size_t)((tensors + kMost - 1) / kMost + 1);
+}
+
+cudaError_t launch_clip(const falcon_grad* grads, int64_t tensors, float max_norm, float eps,
+                        float* norm, void* ws, cudaStream_t stream) {
+  double* partial = static_cast<double*>(ws);
+  static thread_local Batch p;
   auto blocks_of = [](int most) {
     return (unsigned)(p.chunks < 1 ? 1 : p.chunks < most ? p.chunks : most);
   };
@@ -260,12 +263,12 @@ cudaError_t clip(const falcon_grad* grads, int64_t tensors, float max_norm, floa
   do {
     at = fill(&p, grads, tensors, at, chunk);
     const unsigned blocks = blocks_of(kSquareBlocks);
-    clip_squares_kernel<MOST><<<blocks, kThreads, 0, stream>>>(p, partial + parts);
+    clip_squares_kernel<<<blocks, kThreads, 0, stream>>>(p, partial + parts);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     parts += (int)blocks;
   } while (at < tensors);
-  const bool again = tensors > MOST;  // otherwise p still holds all of them
+  const bool again = tensors > kMost;  // otherwise p still holds all of them
   at = again ? 0 : tensors;
   do {
     if (again) at = fill(&p, grads, tensors, at, chunk);
@@ -279,26 +282,12 @@ cudaError_t clip(const falcon_grad* grads, int64_t tensors, float max_norm, floa
     early[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = early;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, clip_scale_kernel<MOST>, p,
-                                             (const double*)partial, parts, max_norm, eps, norm);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, clip_scale_kernel, p, (const double*)partial,
+                                             parts, max_norm, eps, norm);
     norm = nullptr;
     if (e != cudaSuccess) return e;
   } while (at < tensors);
   return cudaSuccess;
-}
-
-}  // namespace
-
-size_t clip_workspace_bytes(const falcon_grad*, int64_t tensors) {
-  return sizeof(double) * kSquareBlocks * (size_t)((tensors + kMost - 1) / kMost + 1);
-}
-
-cudaError_t launch_clip(const falcon_grad* grads, int64_t tensors, float max_norm, float eps,
-                        float* norm, void* ws, cudaStream_t stream) {
-  double* partial = static_cast<double*>(ws);
-  if (tensors <= kFew)
-    return clip<kFew>(grads, tensors, max_norm, eps, norm, partial, stream);
-  return clip<kMost>(grads, tensors, max_norm, eps, norm, partial, stream);
 }
 
 }  // namespace falcon

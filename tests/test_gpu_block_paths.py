@@ -146,7 +146,7 @@ def test_clip_large_sets(dtype, max_norm, in_place):
 
 
 @pytest.mark.parametrize("count", [64, 65])
-def test_clip_around_the_short_argument_list(count):
+def test_clip_of_dozens_of_tensors(count):
     m, g = falcon(), _gen(4)
     grads = [_draw(g, 1 + 37 * i % 501) for i in range(count)]
     n2 = float(sum(t.double().square().sum() for t in grads).sqrt())
