@@ -20,10 +20,10 @@
 // pairs at a time, halving the tokens a lane keeps at each exchange, so that a lane ends
 // with the tokens it stores.
 //
-// B8 T2048 D2048 N16 bf16: 231 us (1.17 TB/s); 40 us would move its bytes and 57 us run its
-// exponentials.  With 1.7 warps a scheduler the issue slots are half busy, shared
-// memory 57%, the exponential unit 29%: bound by the latency of a warp's own chain;
-// with four times the rows the same work takes 187 us.  Measured and not kept: a second
+// B8 T2048 D2048 N16 bf16: 229 us (1.18 TB/s); 40 us would move its bytes and 57 us run its
+// exponentials.  With 1.6 warps a scheduler the issue slots are 57% busy, shared
+// memory 59%, the exponential unit 30%: bound by the latency of a warp's own chain;
+// with four times the rows the same work takes 188 us.  Measured and not kept: a second
 // warp a block for loads and gates (275 us), scalar instead of paired arithmetic (250),
 // the loop unrolled by two tiles (252, instruction cache), eight tokens a tile ahead of a
 // split walk (1.50 ms for T 65536 instead of 1.35).
@@ -421,10 +421,15 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
 
 // Segments of a row's tokens.  A warp alone takes about 80 ns a token, whatever else
 // runs, up to about seven warps an SM; beyond that, a split only adds its first walk.
-// Measured at 8192 tokens, N = 16, bf16, with the walk before this one (89 ns): 128 warps
-// (2048 channels) 199 us with 8 segments, 302 with 4, 278 with 16; 32 warps 81 us with
-// 16, 146 with 8; 512 warps of 4096 tokens 387 us with 2 and 380 unsplit.  So: the most segments that stay within
-// twelve warps an SM, each of two tiles at least, but never just two.
+// The rule: the most segments that stay within twelve warps an SM (eight of the split
+// kernel's fit at a time), each of two tiles at least, but never just two.  Measured at
+// 8192 tokens, N = 16, bf16: 32 warps (512 channels) 68 us with 16 segments, 120 with 8,
+// 619 with 1; 128 warps 181 us with 8, 239 with 4, 244 with 16, 732 with 1; 256 warps
+// 350 us with 4, 360 with 8, 739 with 1.  Not the best everywhere: 512 warps of 4096
+// tokens take 382 us unsplit and 350 with 2; and over 224 shapes (80 to 600 warps, 256 to
+// 4096 tokens, 4 to 128 states, both types) the rule is 12% above the best of 1, 2, 4,
+// 8 and 16 segments on average and 73% at worst (80 warps of 256 tokens, 42 us with 16
+// segments and 24 with 8), where no split at all is 34% and 290% above.
 int segments(int64_t warps, int64_t tiles) {
   int K = 1;
   while (K < 16 && warps * K * 2 <= 152 * 12 && tiles >= 4 * K) K *= 2;

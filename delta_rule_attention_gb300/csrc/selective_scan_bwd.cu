@@ -23,10 +23,10 @@
 // added up over the lane's two channels in registers, over the warp's lanes through
 // shared memory, and over the block's warps when the chunk ends.
 //
-// B8 T2048 D2048 N16 bf16: 0.88 ms, of which step 1 takes 195 us, step 2 38, step 3 620,
-// step 4 18; its bytes would take 70 us.  Steps 1 and 3 are bound by instruction issue and
-// shared memory together (70% and 71% busy in step 1, 59% and 66% in step 3, whose
-// 167 registers and 77 KB leave three blocks an SM): about ten and 27 instructions a
+// B8 T2048 D2048 N16 bf16: 0.87 ms, of which step 1 takes 198 us, step 2 39, step 3 614,
+// step 4 21; its bytes would take 70 us.  Steps 1 and 3 are bound by instruction issue and
+// shared memory together (67% and 70% busy in step 1, 60% and 73% in step 3, whose
+// 168 registers and 77 KB leave three blocks an SM): about ten and 27 instructions a
 // lane for each (token, channel, state), three exponentials among them.  A chunk of 32
 // costs step 2 a state and an adjoint for every 32 tokens (0.2 GB there and back); a group
 // of four tokens is what fits the registers with its states and decays.  Measured and not

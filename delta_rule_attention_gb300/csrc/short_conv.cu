@@ -10,12 +10,14 @@
 // that the traffic does not wait for the arithmetic.  A run's edge rows are read
 // twice, the second time from cache.
 //
-// B8 H12 T2048 m64 W4 bf16, silu, from strided heads: 15.4 us (3.3 TB/s of the 50 MB it
-// must move; issue slots 63% busy).  Its gradient for B8 T2048 C2048: 50 us and 6 for
-// the sums (3.6 TB/s of 202 MB): bound by the latency of its loads at 14 warps an SM.
-// Eight tokens a forward run and four channels a thread: 15.0 us with runs of 16, 19.3
-// with runs of 4; before whole runs went without tests, 16.8 us, and 19.2 with eight
-// channels a thread.
+// B8 H12 T2048 m64 W4 bf16, silu, from strided heads: 13.3 us in a graph of calls (3.8 TB/s
+// of the 50 MB it must move; 16.2 us from cold caches, issue slots 60% busy).  The
+// gradient for B8 T2048 C2048: 53 us with its sums (3.8 TB/s of 202 MB; 50 and 6.6 from
+// cold caches): bound by the latency of its loads at 14 warps an SM.
+// Eight tokens a forward run and four channels a thread.  Runs of 16 take 3% less where
+// there are rows enough (B32: 48.9 us a call, 50.8 with 8) but halve the threads of a
+// small call (B1: 19 to 22 us, 17 to 18 with 8); runs of 4 took 25% more, and eight
+// channels a thread 14% more.
 
 #include <type_traits>
 
@@ -414,7 +416,11 @@ cudaError_t fwd_typed(const ConvArgs& a, cudaStream_t stream) {
 // sums, one a run while they are few.  Of the runs up to 128 tokens, the one with the
 // least estimated time, in tokens of a thread: waves of resident blocks (four an SM)
 // times a run with its edge, and 0.06 for each part that the sums add up (measured: a
-// token 0.19 us, 64 parts 0.7 us).
+// token 0.19 us, 64 parts 0.7 us).  It counts the bf16 kernel of two channels a thread
+// (112 tokens for B8 T2048 C2048); the others take the same cut, so that the workspace
+// goes by the sizes alone, and their last wave may be partly full: one channel a thread
+// makes twice the blocks, and in fp32 with silu and four taps three fit an SM
+// (155 registers).
 struct Cut {
   int run, parts;
 };
