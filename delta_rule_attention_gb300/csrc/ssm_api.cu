@@ -311,6 +311,7 @@ int falcon_selective_scan_bwd(const falcon_scan_shape* s, const void* u, const f
   if (negative(us) || negative(ds) || negative(bs) || negative(cs) || negative(dys) ||
       (z && negative(zs)) || (!z && dz))
     return FALCON_ERR_BAD_ARG;
+  if (dh0 && dh0 == h0) return FALCON_ERR_BAD_ARG;  // written while other blocks read h0
   const void* acts[] = {u, delta, Bm, Cm, z, dy, du, ddelta, dB, dC, dz};
   const void* words[] = {A, Dskip, delta_bias, h0, lengths, dh_T, dA, dDskip, ddelta_bias, dh0};
   if (any_misaligned(acts, esize(s->dtype)) || any_misaligned(words, 4))

@@ -539,7 +539,7 @@ int falcon_selective_scan_fwd(const falcon_scan_shape *shape, const void *u,
  *   du, ddelta [B,T,D] dtype, dense, out;  dz [B,T,D] dtype, dense, out, given
  *   exactly where z is;  dB, dC [B,T,G,N] dtype, dense, out;  dA [D,N] f32, out;
  *   dDskip, ddelta_bias [D] f32, out, nullable;  dh0 [B,D,N] f32, out, nullable,
- *   may alias dh_T
+ *   may alias dh_T (not h0)
  *   workspace: at least falcon_selective_scan_bwd_workspace_bytes(shape) bytes,
  *   256-byte aligned: a state and an adjoint for every 32 tokens, and sums, of which
  *   those of dB and dC take 2 GB at most, or two fp32 copies of dB and dC where that

@@ -59,3 +59,20 @@ def test_scan_refuses_results_that_lie_on_one_another(lib, ys):
     assert lib.falcon_selective_scan_fwd(
         s, _p(0x10000), st, _p(0x20000), st, _p(0x30000), _p(0x40000), st, _p(0x50000), st, None,
         None, None, None, None, None, _p(0x60000), falcon_strides(*ys), _p(0x70000), None) == BAD_ARG
+
+
+def test_scan_gradient_refuses_to_write_the_states_it_reads(lib):
+    """dh0 over h0: the walk over the chunks reads one in one block and writes the other in
+    another.  Over dh_T it may lie (the workspace is too small here, so that nothing runs)."""
+    from delta_rule_attention_gb300.block import falcon_scan_shape, falcon_strides
+    s, st = falcon_scan_shape(2, 8, 16, 1, 16, F32, 1), falcon_strides(1024, 0, 16)
+
+    def call(h0, dh_T, dh0):
+        p = [_p(0x100000 + 0x10000 * i) for i in range(12)]
+        return lib.falcon_selective_scan_bwd(
+            s, p[0], st, p[1], st, p[2], p[3], st, p[4], st, None, None, None, None, h0, None, p[5],
+            st, dh_T, p[6], p[7], p[8], p[9], p[10], None, None, None, dh0, p[11], 256, None)
+
+    a, b = _p(0x800000), _p(0x900000)
+    assert call(a, b, a) == BAD_ARG
+    assert call(a, b, b) == -5
