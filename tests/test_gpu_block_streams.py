@@ -53,3 +53,34 @@ def test_results_may_be_dropped_while_the_current_stream_reads_them():
         m.falcon_short_conv_fwd(x, other, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(kept, want)
+
+
+def test_calls_on_a_given_stream_inside_a_graph():
+    import delta_rule_attention_gb300 as m
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    B, T, D, N = 2, 90, 64, 16
+    d = dict(u=r(B, T, D), delta=r(B, T, D), A=-torch.exp(r(D, N)), Bm=r(B, T, 1, N),
+             Cm=r(B, T, 1, N), D=r(D), z=r(B, T, D))
+    dy, w = r(B, T, D), r(D, 4)
+
+    def both(**on):
+        x, _ = m.falcon_short_conv_fwd(d["u"], w, **on)
+        y, h = m.falcon_selective_scan_fwd(**{**d, "u": x}, **on)
+        grads = m.falcon_selective_scan_bwd(**{**d, "u": x}, dy=dy, **on)
+        norm = m.falcon_clip_grad_norm([grads["dA"], grads["dB"]], 1.0, **on)
+        return y, h, grads["du"], grads["dA"], grads["dB"], norm
+
+    want = [t.clone() for t in both()]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = both(stream=side)
+        here.wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
