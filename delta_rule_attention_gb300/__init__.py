@@ -17,11 +17,14 @@ import threading
 
 import torch
 
-from . import block
+from . import block, linear
 from .block import (  # noqa: F401
     falcon_clip_grad_norm, falcon_selective_scan_bwd, falcon_selective_scan_fwd,
     falcon_selective_scan_step, falcon_short_conv_bwd, falcon_short_conv_fwd,
     falcon_short_conv_step)
+from .linear import (  # noqa: F401
+    falcon_decay_attn_bwd, falcon_decay_attn_fwd, falcon_decay_attn_step,
+    falcon_gated_norm_bwd, falcon_gated_norm_fwd)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfalcon_gb300.so")
@@ -47,7 +50,7 @@ EXPORTS = (
     "falcon1a_bwd_chunked", "falcon3a_fwd_chunked", "falcon2a_fwd_chunked",
     "falcon_normalized_workspace_bytes", "falcon1a_fwd_chunked_normalized",
     "falcon2_fwd_chunked",
-) + block.EXPORTS
+) + block.EXPORTS + linear.EXPORTS
 FALCON_ERR_SCRATCH_LIMIT = -10
 FALCON_FIXED_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -133,6 +136,7 @@ def load_library(path: str | None = None):
         lib.falcon_version.restype = ctypes.c_int
         lib.falcon_version.argtypes = []
         block.declare(lib)
+        linear.declare(lib)
         _lib = lib
         return lib
 

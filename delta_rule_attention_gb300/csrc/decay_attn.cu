@@ -1,0 +1,357 @@
+// Attention with a fixed decay a head, in fp32 on the CUDA cores: any type, any m and dv
+// up to 128, any strides.  The tensor-core kernels take the bf16 shapes that they fit.
+//
+// The sum o_t = sum_{j <= t} gamma^{t-j} (q_t . k_j) v_j is split by runs of tokens, so
+// that every run can be worked on at once although the state goes from token to token:
+//   1. states: what a run adds to the state, U_r = sum_j gamma^{e-1-j} k_j v_j^T
+//      (weights relative to the run's end e: all at most 1);
+//   2. join: the state entering each run, X_{r+1} = gamma^{len_r} X_r + U_r;
+//   3. reads: chunk by chunk inside a run, o = ((q k^T) * gamma^{i-j}) v + gamma^{i+1} q X,
+//      X carried on.
+// Every power of gamma is of a number of tokens >= 0, so none overflows, and heads that
+// forget within a chunk (gamma^64 = 0) need no care of their own.
+#include "linear.cuh"
+
+namespace falcon {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;         // rows and columns of a block's tile
+constexpr int kLd = kTile + 4;    // row stride in shared memory
+constexpr int kStep = 32;         // tokens (states) or keys (reads) staged at a time
+constexpr int kChunk = 64;        // tokens of a chunk
+
+// acc[i][j] += sum_{k < n} a[k][i] b[k][j] for this thread's 4 x 4 corner of the tile
+__device__ __forceinline__ void outer_sum(float (&acc)[4][4], const float* a, const float* b,
+                                          int n) {
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(a + k * kLd);
+    const float4 y = *reinterpret_cast<const float4*>(b + k * kLd);
+    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
+  }
+}
+
+// Four channels from c on of a row with `width` of them, zeros behind.
+template <typename E>
+__device__ __forceinline__ float4 row_quad(const E* row, int c, int width, bool vec) {
+  const int have = width - c;
+  return widen(load_quad<E>(row + c, vec && have >= 4, have < 0 ? 0 : (have < 4 ? have : 4)));
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kThreads)
+    decay_states_kernel(const __grid_constant__ DecayPass a) {
+  __shared__ float ks[kStep * kLd], vs[kStep * kLd];
+  const int run = blockIdx.x % a.runs;
+  const int64_t bh = blockIdx.x / a.runs, b = bh / a.H;
+  const int h = (int)(bh % a.H), tid = threadIdx.x;
+  const int tiles = (a.dv + kTile - 1) / kTile;
+  const int i0 = blockIdx.y / tiles * kTile, j0 = blockIdx.y % tiles * kTile;
+  const int64_t n = row_length(a.lengths, b, a.T);
+  const int64_t t0 = run * a.run_len, len = run_tokens(n, run, a.run_len);
+  const float g = decay_rate(a.log_decay, h);
+  const E* k = static_cast<const E*>(a.k) + b * a.ks.batch + h * a.ks.head;
+  const E* v = static_cast<const E*>(a.v) + b * a.vs.batch + h * a.vs.head;
+  const int ti = (tid >> 4) * 4, tj = (tid & 15) * 4;
+  float acc[4][4] = {};
+  for (int64_t s = 0; s < len; s += kStep) {
+    const int have = (int)(len - s < kStep ? len - s : kStep);
+    __syncthreads();
+    for (int e = tid; e < kStep * (kTile / 4); e += kThreads) {
+      const int r = e / (kTile / 4), c = e % (kTile / 4) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (r < have) {
+        const int64_t t = t0 + s + r;
+        const float wt = a.w * decay_power(g, (float)(a.rev ? s + r + 1 : len - 1 - s - r));
+        x = row_quad<E>(k + t * a.ks.time, i0 + c, a.m, a.vec_k);
+        y = row_quad<E>(v + t * a.vs.time, j0 + c, a.dv, a.vec_v);
+        x.x *= wt, x.y *= wt, x.z *= wt, x.w *= wt;
+      }
+      *reinterpret_cast<float4*>(ks + r * kLd + c) = x;
+      *reinterpret_cast<float4*>(vs + r * kLd + c) = y;
+    }
+    __syncthreads();
+    outer_sum(acc, ks + ti, vs + tj, have);
+  }
+  float* out = a.states + (bh * a.runs + run) * a.m * a.dv;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i0 + ti + i < a.m && j0 + tj + j < a.dv)
+        out[(i0 + ti + i) * a.dv + j0 + tj + j] = acc[i][j];
+}
+
+// The state entering each run, in the order of time (rev: from the last run back), in
+// place of what the run adds; one thread an element.  gamma^len X + U as
+// X + (gamma^len - 1) X + U: the power of a slow head is near 1, where its rounding
+// would repeat itself run after run (expm1 keeps it relative to what is lost).
+constexpr int kAhead = 8;
+__global__ void __launch_bounds__(kThreads)
+    decay_join_kernel(const __grid_constant__ DecayPass a) {
+  const int64_t size = (int64_t)a.m * a.dv;
+  const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (at >= a.B * a.H * size) return;
+  const int64_t bh = at / size, b = bh / a.H;
+  const int e = (int)(at % size), i = e / a.dv, j = e % a.dv;
+  const int64_t n = row_length(a.lengths, b, a.T);
+  const float g = decay_rate(a.log_decay, (int)(bh % a.H));
+  const int64_t seat = bh * size + (int64_t)i * a.si + (int64_t)j * a.sj;
+  float X = a.S_init ? a.S_init[seat] : 0.f;
+  float* st = a.states + bh * a.runs * size + e;
+  for (int s0 = 0; s0 < a.runs; s0 += kAhead) {
+    float U[kAhead];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+      if (s0 + s < a.runs) U[s] = st[(a.rev ? a.runs - 1 - s0 - s : s0 + s) * size];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      if (s0 + s >= a.runs) break;
+      const int r = a.rev ? a.runs - 1 - s0 - s : s0 + s;
+      st[r * size] = X;
+      const float len = (float)run_tokens(n, r, a.run_len);
+      X = fmaf(expm1f(g * len), X, X) + U[s];
+    }
+  }
+  if (a.S_out) a.S_out[seat] = X;
+}
+
+struct ReadSmem {
+  float q[kStep * kLd], k[kStep * kLd];  // transposed: [key][token]
+  float v[kChunk * kLd];                 // [token][value]
+  float p[kChunk * kLd];                 // [source][token]; then weighted keys [token][key]
+  float S[128 * kLd];                    // [key][value]
+};
+
+template <typename E>
+__global__ void __launch_bounds__(kThreads)
+    decay_read_kernel(const __grid_constant__ DecayPass a) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  ReadSmem& sm = *reinterpret_cast<ReadSmem*>(raw);
+  const int run = blockIdx.x % a.runs;
+  const int64_t bh = blockIdx.x / a.runs, b = bh / a.H;
+  const int h = (int)(bh % a.H), tid = threadIdx.x, j0 = blockIdx.y * kTile;
+  const int64_t n = row_length(a.lengths, b, a.T);
+  const float g = decay_rate(a.log_decay, h);
+  const E* q = static_cast<const E*>(a.q) + b * a.qs.batch + h * a.qs.head;
+  const E* k = static_cast<const E*>(a.k) + b * a.ks.batch + h * a.ks.head;
+  const E* v = static_cast<const E*>(a.v) + b * a.vs.batch + h * a.vs.head;
+  E* o = static_cast<E*>(a.o) + b * a.os.batch + h * a.os.head;
+  const int ti = (tid >> 4) * 4, tj = (tid & 15) * 4;
+  const int mpad = (a.m + kStep - 1) / kStep * kStep;
+  const int64_t first = run * a.run_len;
+  const int64_t end = first + a.run_len < a.T ? first + a.run_len : a.T;
+  const int chunks = (int)((end - first + kChunk - 1) / kChunk);
+  {
+    const float* X = a.states + (bh * a.runs + run) * a.m * a.dv;
+    for (int e = tid; e < mpad * kTile; e += kThreads) {
+      const int i = e / kTile, j = e % kTile;
+      sm.S[i * kLd + j] = i < a.m && j0 + j < a.dv ? X[i * a.dv + j0 + j] : 0.f;
+    }
+  }
+  for (int cc = 0; cc < chunks; ++cc) {
+    const int64_t t0 = first + (int64_t)(a.rev ? chunks - 1 - cc : cc) * kChunk;
+    const int have = (int)run_tokens(n, 0, t0 + kChunk) - (int)(n < t0 ? n : t0);
+    const int rows = (int)(end - t0 < kChunk ? end - t0 : kChunk);
+    float P[4][4] = {}, O[4][4] = {};
+    if (have > 0) {
+      for (int e = tid; e < kChunk * (kTile / 4); e += kThreads) {
+        const int r = e / (kTile / 4), c = e % (kTile / 4) * 4;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < have) y = row_quad<E>(v + (t0 + r) * a.vs.time, j0 + c, a.dv, a.vec_v);
+        *reinterpret_cast<float4*>(sm.v + r * kLd + c) = y;
+      }
+      for (int mk = 0; mk < a.m; mk += kStep) {
+        __syncthreads();
+        for (int e = tid; e < kChunk * (kStep / 4); e += kThreads) {
+          const int r = e % kChunk, c = e / kChunk * 4;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+          if (r < have) {
+            x = row_quad<E>(q + (t0 + r) * a.qs.time, mk + c, a.m, a.vec_q);
+            y = row_quad<E>(k + (t0 + r) * a.ks.time, mk + c, a.m, a.vec_k);
+          }
+          sm.q[c * kLd + r] = x.x, sm.q[(c + 1) * kLd + r] = x.y;
+          sm.q[(c + 2) * kLd + r] = x.z, sm.q[(c + 3) * kLd + r] = x.w;
+          sm.k[c * kLd + r] = y.x, sm.k[(c + 1) * kLd + r] = y.y;
+          sm.k[(c + 2) * kLd + r] = y.z, sm.k[(c + 3) * kLd + r] = y.w;
+        }
+        __syncthreads();
+        outer_sum(P, sm.q + ti, sm.k + tj, kStep);
+        outer_sum(O, sm.q + ti, sm.S + mk * kLd + tj, kStep);
+      }
+      const float intra = a.inter * a.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = ti + i;
+        const float far = a.inter * decay_power(g, (float)(a.rev ? max(have - 1 - r, 0) : r + 1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          O[i][j] *= far;
+          const int gap = a.rev ? tj + j - r : r - tj - j;
+          P[i][j] = gap >= 0 ? P[i][j] * intra * decay_power(g, (float)gap) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(sm.p + (tj + j) * kLd + ti) =
+            make_float4(P[0][j], P[1][j], P[2][j], P[3][j]);
+      __syncthreads();
+      outer_sum(O, sm.p + ti, sm.v + tj, kChunk);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ti + i;
+      if (r >= rows) break;
+      E* to = o + (t0 + r) * a.os.time + j0 + tj;
+      const int cols = a.dv - j0 - tj;
+      const bool live = r < have;
+      if (a.vec_o && cols >= 4) {
+        *reinterpret_cast<typename Raw<E>::Quad*>(to) =
+            narrow(live ? make_float4(O[i][0], O[i][1], O[i][2], O[i][3])
+                        : make_float4(0.f, 0.f, 0.f, 0.f),
+                   typename Raw<E>::Quad());
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < cols) store_vec<E, 1>(to + j, FloatV<1>{{live ? O[i][j] : 0.f}});
+      }
+    }
+    if (have > 0 && cc + 1 < chunks) {
+      const float lost = expm1f(g * (float)have);
+      for (int mk = 0; mk < a.m; mk += kTile) {
+        __syncthreads();
+        for (int e = tid; e < kChunk * (kTile / 4); e += kThreads) {
+          const int r = e / (kTile / 4), c = e % (kTile / 4) * 4;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < have) {
+            x = row_quad<E>(k + (t0 + r) * a.ks.time, mk + c, a.m, a.vec_k);
+            const float wt = a.w * decay_power(g, (float)(a.rev ? r + 1 : have - 1 - r));
+            x.x *= wt, x.y *= wt, x.z *= wt, x.w *= wt;
+          }
+          *reinterpret_cast<float4*>(sm.p + r * kLd + c) = x;
+        }
+        __syncthreads();
+        float U[4][4] = {};
+        outer_sum(U, sm.p + ti, sm.v + tj, kChunk);
+        if (mk + ti < mpad) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float& S = sm.S[(mk + ti + i) * kLd + tj + j];
+              S = fmaf(lost, S, S) + U[i][j];
+            }
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Runs of a row: enough for `want` blocks over all heads, of whole chunks.
+void split_runs(DecayPass* p, int chunk, int64_t want) {
+  const int64_t chunks = ceil_div(p->T, chunk);
+  const int64_t per = ceil_div(want, p->B * p->H);
+  const int64_t each = ceil_div(chunks, per < chunks ? per : (chunks ? chunks : 1));
+  p->run_len = (each ? each : 1) * chunk;
+  p->runs = (int)ceil_div(p->T, p->run_len);
+}
+
+constexpr int64_t kSimtBlocks = 608;  // four blocks for each of 152 SMs
+
+DecayPass shape_pass(const falcon_decay_shape& s, int m, int dv) {
+  DecayPass p = {};
+  p.B = s.B, p.H = s.H, p.T = s.T;
+  p.m = m, p.dv = dv, p.dtype = s.dtype;
+  split_runs(&p, kChunk, kSimtBlocks);
+  return p;
+}
+size_t pass_bytes(const DecayPass& p) {
+  return ((size_t)p.B * p.H * p.runs * p.m * p.dv * 4 + 255) / 256 * 256;
+}
+
+bool quads(const void* p, const falcon_strides& s, int dtype) {
+  const uintptr_t bytes = dtype == FALCON_BF16 ? 8 : 16;
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && s.batch % 4 == 0 && s.head % 4 == 0 &&
+         s.time % 4 == 0;
+}
+
+template <typename E>
+cudaError_t run_pass(DecayPass& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> allowed{0};
+  p.vec_q = quads(p.q, p.qs, p.dtype), p.vec_k = quads(p.k, p.ks, p.dtype);
+  p.vec_v = quads(p.v, p.vs, p.dtype), p.vec_o = quads(p.o, p.os, p.dtype);
+  const int64_t bh = p.B * p.H;
+  const unsigned grid = (unsigned)(bh * p.runs);
+  const unsigned vt = (unsigned)ceil_div(p.dv, kTile), mt = (unsigned)ceil_div(p.m, kTile);
+  if (p.runs > 0) decay_states_kernel<E><<<dim3(grid, mt * vt), kThreads, 0, stream>>>(p);
+  decay_join_kernel<<<(unsigned)ceil_div(bh * p.m * p.dv, kThreads), kThreads, 0, stream>>>(p);
+  if (p.runs > 0) {
+    cudaError_t e = allow_shared(decay_read_kernel<E>, sizeof(ReadSmem), &allowed);
+    if (e != cudaSuccess) return e;
+    decay_read_kernel<E><<<dim3(grid, vt), kThreads, sizeof(ReadSmem), stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t any_pass(DecayPass& p, cudaStream_t stream) {
+  return p.dtype == FALCON_BF16 ? run_pass<__nv_bfloat16>(p, stream) : run_pass<float>(p, stream);
+}
+
+}  // namespace
+
+size_t decay_workspace_bytes(const falcon_decay_shape& s, bool) {
+  return pass_bytes(shape_pass(s, s.m, s.dv));
+}
+
+cudaError_t launch_decay_fwd(const DecayCall& c, cudaStream_t stream) {
+  DecayPass p = shape_pass(c.s, c.s.m, c.s.dv);
+  p.q = c.q, p.k = c.k, p.v = c.v, p.o = c.o;
+  p.qs = c.qs, p.ks = c.ks, p.vs = c.vs, p.os = c.os;
+  p.log_decay = c.log_decay, p.lengths = c.lengths;
+  p.S_init = c.S0, p.S_out = c.S_out;
+  p.si = c.s.dv, p.sj = 1;
+  p.inter = c.s.scale, p.w = 1.f;
+  p.states = static_cast<float*>(c.ws);
+  return any_pass(p, stream);
+}
+
+cudaError_t launch_decay_bwd(const DecayCall& c, cudaStream_t stream) {
+  const int m = c.s.m, dv = c.s.dv;
+  // dq = scale S_t dO_t: the forward pass with (dO, v, k), its state transposed
+  DecayPass p = shape_pass(c.s, dv, m);
+  p.log_decay = c.log_decay, p.lengths = c.lengths;
+  p.states = static_cast<float*>(c.ws);
+  p.q = c.dO, p.k = c.v, p.v = c.k, p.o = c.dq;
+  p.qs = c.dos, p.ks = c.vs, p.vs = c.ks, p.os = c.dqs;
+  p.S_init = c.S0;
+  p.si = 1, p.sj = dv;
+  p.inter = c.s.scale, p.w = 1.f;
+  cudaError_t e = any_pass(p, stream);
+  if (e != cudaSuccess) return e;
+  // dk = G_t v_t, backward in time with (v, dO, q)
+  p.rev = 1;
+  p.q = c.v, p.k = c.dO, p.v = c.q, p.o = c.dk;
+  p.qs = c.vs, p.ks = c.dos, p.vs = c.qs, p.os = c.dks;
+  p.S_init = c.dS_T;
+  p.inter = 1.f, p.w = c.s.scale;
+  e = any_pass(p, stream);
+  if (e != cudaSuccess) return e;
+  // dv = G_t^T k_t, backward in time with (k, q, dO)
+  p.m = m, p.dv = dv;
+  p.q = c.k, p.k = c.q, p.v = c.dO, p.o = c.dv;
+  p.qs = c.ks, p.ks = c.qs, p.vs = c.dos, p.os = c.dvs;
+  p.S_out = c.dS0;
+  p.si = dv, p.sj = 1;
+  return any_pass(p, stream);
+}
+
+}  // namespace falcon

@@ -5,7 +5,8 @@
  * Falcon-3A (sliding window) in token-recurrent and chunk form, and the
  * single-token recurrent decode step.  Beside these, the operators of a
  * selective state space block (short causal convolution, selective scan,
- * clipping of a step's gradients), in a part of their own below.
+ * clipping of a step's gradients) and those of a linear attention block (attention with
+ * a fixed decay a head, gated norms), in parts of their own below.
  *
  * The operations are defined on the page hyper.ai/fr/papers/2608.27763
  * ("Fast Weight Attention for Continual Learning"):
@@ -605,6 +606,138 @@ typedef struct {
 size_t falcon_clip_workspace_bytes(const falcon_grad *grads, int64_t tensors);
 int falcon_clip_grad_norm(const falcon_grad *grads, int64_t tensors, float max_norm,
                           float eps, float *norm, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A linear attention block with a fixed decay for each head: the attention over
+ * prompts, its gradient and its single-token step, and the norms around a block.
+ *
+ * The conventions are those of the selective state space block above (strides,
+ * alignment, `lengths`, `slots`, `fresh`, overlap).  Strides of inputs may be zero
+ * (a broadcast head or row); the gradient of a broadcast input is returned for every
+ * head and row that reads it, to be summed by the caller. */
+
+/* B rows of T tokens, H heads with keys of m and values of dv channels (1 .. 128
+ * each); scale multiplies the reads. */
+typedef struct {
+  int64_t B, H, T;
+  int32_t m, dv, dtype;
+  float scale;
+} falcon_decay_shape;
+
+/* Attention with a decay: for each row and head, gamma = exp(log_decay),
+ *   S_t = gamma S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
+ *   q, k       [B,H,T,m] dtype;  v, o [B,H,T,dv] dtype
+ *   log_decay  [H] f32, at most 0 (a positive one counts as 0, minus infinity as
+ *              the lowest number: the state then holds the last token alone)
+ *   S0         [B,H,m,dv] f32, nullable (zeros);  S_out [B,H,m,dv] f32, out,
+ *              nullable, may be S0
+ *   workspace: at least falcon_decay_attn_workspace_bytes(shape) bytes, 256-byte
+ *   aligned: a state for every run of tokens that is worked on by itself.
+ * Errors: FALCON_ERR_NULL_PTR, _BAD_SHAPE, _BAD_DTYPE, _MISALIGNED, _WORKSPACE,
+ * _BAD_ARG (negative stride, o where an input starts or on itself, scale not
+ * finite), _DEVICE; _CUDA. */
+size_t falcon_decay_attn_workspace_bytes(const falcon_decay_shape *shape);
+int falcon_decay_attn_fwd(const falcon_decay_shape *shape, const void *q,
+                          const falcon_strides *q_strides, const void *k,
+                          const falcon_strides *k_strides, const void *v,
+                          const falcon_strides *v_strides, const float *log_decay,
+                          const float *S0, const int32_t *lengths, void *o,
+                          const falcon_strides *o_strides, float *S_out,
+                          void *workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/* Gradients of <dO, o> + <dS_T, S_T> of the call above (the decay is fixed and has
+ * none).  With G_t the adjoint of S_t, G_t = scale q_t dO_t^T + gamma G_{t+1}:
+ * dq_t = scale S_t dO_t, dk_t = G_t v_t, dv_t = G_t^T k_t, dS0 = gamma G_1.
+ *   dO [B,H,T,dv] dtype;  dS_T [B,H,m,dv] f32, nullable (zeros)
+ *   dq, dk [B,H,T,m] dtype, dv [B,H,T,dv] dtype, out;  dS0 [B,H,m,dv] f32, out,
+ *   nullable, may be dS_T (not S0)
+ *   workspace: at least falcon_decay_attn_bwd_workspace_bytes(shape) bytes, 256-byte
+ *   aligned. */
+size_t falcon_decay_attn_bwd_workspace_bytes(const falcon_decay_shape *shape);
+int falcon_decay_attn_bwd(const falcon_decay_shape *shape, const void *q,
+                          const falcon_strides *q_strides, const void *k,
+                          const falcon_strides *k_strides, const void *v,
+                          const falcon_strides *v_strides, const float *log_decay,
+                          const float *S0, const int32_t *lengths, const void *dO,
+                          const falcon_strides *dO_strides, const float *dS_T, void *dq,
+                          const falcon_strides *dq_strides, void *dk,
+                          const falcon_strides *dk_strides, void *dv,
+                          const falcon_strides *dv_strides, float *dS0, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/* One token of N sequences: q, k [N,H,m], v [N,H,dv] dtype (`batch` the row's stride,
+ * `head` the head's), o [N,H,dv] dtype dense, out; S [pool,H,m,dv] f32, updated in
+ * place.  The shape's B is N; its T is not read. */
+int falcon_decay_attn_step(const falcon_decay_shape *shape, const void *q,
+                           const falcon_strides *q_strides, const void *k,
+                           const falcon_strides *k_strides, const void *v,
+                           const falcon_strides *v_strides, const float *log_decay,
+                           float *S, int64_t pool, const int32_t *slots,
+                           const uint8_t *fresh, void *o, cudaStream_t stream);
+
+#define FALCON_ACT_SIGMOID 2 /* a gate of the norm below */
+
+/* B rows of T tokens with H heads of m channels (H*m at most 8192), each head
+ * normalised by itself; gate is the activation of z (FALCON_ACT_*), eps > 0 the norms'
+ * stabiliser. */
+typedef struct {
+  int64_t B, H, T;
+  int32_t m, dtype, gate;
+  float eps;
+} falcon_norm_shape;
+
+/* The norm behind a block, its gate, its scale and the residual, and the norm before
+ * the next block, in one pass over the rows:
+ *   out  = x + scale act(z) n(h) weight,   n(h) = h / sqrt(mean_head h^2 + eps)
+ *   next = out / sqrt(mean out^2 + eps) next_weight
+ * next is taken from out before its rounding.  Where h is NULL, out = x is not
+ * written, and next alone is the norm before the first block.
+ *   h           [B,H,T,m] dtype, any strides (an attention's head-major output, or
+ *               rows of channels: H = 1, or `head` = m)
+ *   z, x, out, next  [B,T,H*m] dtype (`head` unused)
+ *   weight, scale, next_weight  [H*m] f32
+ * Nullable: weight, scale (ones), z (no gate), x (zeros), next_weight together with
+ * next (no next norm); h together with out, weight, scale and z.
+ *   out may be x (with x's strides).
+ * No workspace.  Errors as for falcon_decay_attn_fwd; _BAD_ARG also for a gate code
+ * or eps out of range, and _NULL_PTR for a pointer without its partner. */
+int falcon_gated_norm_fwd(const falcon_norm_shape *shape, const void *h,
+                          const falcon_strides *h_strides, const float *weight,
+                          const void *z, const falcon_strides *z_strides,
+                          const float *scale, const void *x,
+                          const falcon_strides *x_strides, const float *next_weight,
+                          const int32_t *lengths, void *out,
+                          const falcon_strides *out_strides, void *next,
+                          const falcon_strides *next_strides, cudaStream_t stream);
+
+/* Gradients of <dout, out> + <dnext, next> of the call above.
+ *   out    [B,T,H*m] dtype: the stored output (where h is NULL: x); given where
+ *          next_weight is
+ *   dout, dnext  [B,T,H*m] dtype; dout nullable (zeros) where dnext is given, dnext
+ *          given where next_weight is
+ *   dx     [B,T,H*m] dtype, out, nullable: the gradient of x, may be dout (with
+ *          dout's strides)
+ *   dh     [B,H,T,m] dtype, out, given where h is;  dz [B,T,H*m] dtype, out, given
+ *          where z is
+ *   dweight, dscale, dnext_weight  [H*m] f32, out, nullable; dscale only where scale
+ *          is given, dnext_weight only where next_weight is
+ *   workspace: at least falcon_gated_norm_bwd_workspace_bytes(shape) bytes, 16-byte
+ *   aligned (per-block sums of the parameters' gradients, added in a fixed order). */
+size_t falcon_gated_norm_bwd_workspace_bytes(const falcon_norm_shape *shape);
+int falcon_gated_norm_bwd(const falcon_norm_shape *shape, const void *h,
+                          const falcon_strides *h_strides, const float *weight,
+                          const void *z, const falcon_strides *z_strides,
+                          const float *scale, const void *out,
+                          const falcon_strides *out_strides, const float *next_weight,
+                          const int32_t *lengths, const void *dout,
+                          const falcon_strides *dout_strides, const void *dnext,
+                          const falcon_strides *dnext_strides, void *dx,
+                          const falcon_strides *dx_strides, void *dh,
+                          const falcon_strides *dh_strides, void *dz,
+                          const falcon_strides *dz_strides, float *dweight,
+                          float *dscale, float *dnext_weight, void *workspace,
                           size_t workspace_bytes, cudaStream_t stream);
 
 /* Waits for `stream`, then reads and clears the library's device error word
