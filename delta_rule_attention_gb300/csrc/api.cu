@@ -322,6 +322,7 @@ int decode(int rule, int64_t N, int32_t m, int32_t dv, int32_t dtype, int32_t ph
 
 namespace falcon {
 int check_sm103_device() { return check_device(); }
+int* device_error_word_of_current() { return device_error_word(); }
 
 // Falcon-1 chunked forward over a workspace of workspace_bytes whose device
 // address `resolve` gives once the device check has passed.

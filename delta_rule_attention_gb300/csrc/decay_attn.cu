@@ -11,6 +11,7 @@
 // Every power of gamma is of a number of tokens >= 0, so none overflows, and heads that
 // forget within a chunk (gamma^64 = 0) need no care of their own.
 #include "linear.cuh"
+#include "linear_tc.cuh"
 
 namespace falcon {
 
@@ -267,15 +268,21 @@ void split_runs(DecayPass* p, int chunk, int64_t want) {
 
 constexpr int64_t kSimtBlocks = 608;  // four blocks for each of 152 SMs
 
-DecayPass shape_pass(const falcon_decay_shape& s, int m, int dv) {
+DecayPass shape_pass(const falcon_decay_shape& s, int m, int dv, bool tc) {
   DecayPass p = {};
   p.B = s.B, p.H = s.H, p.T = s.T;
   p.m = m, p.dv = dv, p.dtype = s.dtype;
-  split_runs(&p, kChunk, kSimtBlocks);
+  if (tc)
+    split_runs(&p, kDecayTcChunk, decay_tc_blocks(m, dv));
+  else
+    split_runs(&p, kChunk, kSimtBlocks);
   return p;
 }
-size_t pass_bytes(const DecayPass& p) {
-  return ((size_t)p.B * p.H * p.runs * p.m * p.dv * 4 + 255) / 256 * 256;
+// Room for either path: which one a pass takes goes by its pointers and strides too.
+size_t pass_bytes(const falcon_decay_shape& s) {
+  const int runs[2] = {shape_pass(s, s.m, s.dv, false).runs, shape_pass(s, s.m, s.dv, true).runs};
+  const size_t most = (size_t)(runs[0] > runs[1] ? runs[0] : runs[1]);
+  return ((size_t)s.B * s.H * most * s.m * s.dv * 4 + 255) / 256 * 256;
 }
 
 bool quads(const void* p, const falcon_strides& s, int dtype) {
@@ -293,27 +300,39 @@ cudaError_t run_pass(DecayPass& p, cudaStream_t stream) {
   const unsigned grid = (unsigned)(bh * p.runs);
   const unsigned vt = (unsigned)ceil_div(p.dv, kTile), mt = (unsigned)ceil_div(p.m, kTile);
   if (p.runs > 0) decay_states_kernel<E><<<dim3(grid, mt * vt), kThreads, 0, stream>>>(p);
-  decay_join_kernel<<<(unsigned)ceil_div(bh * p.m * p.dv, kThreads), kThreads, 0, stream>>>(p);
+  cudaError_t e = launch_decay_join(p, stream);
+  if (e != cudaSuccess) return e;
   if (p.runs > 0) {
-    cudaError_t e = allow_shared(decay_read_kernel<E>, sizeof(ReadSmem), &allowed);
+    e = allow_shared(decay_read_kernel<E>, sizeof(ReadSmem), &allowed);
     if (e != cudaSuccess) return e;
     decay_read_kernel<E><<<dim3(grid, vt), kThreads, sizeof(ReadSmem), stream>>>(p);
   }
   return cudaGetLastError();
 }
 
-cudaError_t any_pass(DecayPass& p, cudaStream_t stream) {
+// A pass with its tensors set: on the tensor cores where they fit.
+cudaError_t any_pass(const falcon_decay_shape& s, DecayPass p, cudaStream_t stream) {
+  const DecayPass split = shape_pass(s, p.m, p.dv, true);
+  p.runs = split.runs, p.run_len = split.run_len;
+  cudaError_t e = cudaSuccess;
+  if (decay_tc_pass(p, &e, stream)) return e;
+  const DecayPass other = shape_pass(s, p.m, p.dv, false);
+  p.runs = other.runs, p.run_len = other.run_len;
   return p.dtype == FALCON_BF16 ? run_pass<__nv_bfloat16>(p, stream) : run_pass<float>(p, stream);
 }
 
 }  // namespace
 
-size_t decay_workspace_bytes(const falcon_decay_shape& s, bool) {
-  return pass_bytes(shape_pass(s, s.m, s.dv));
+cudaError_t launch_decay_join(const DecayPass& p, cudaStream_t stream) {
+  const int64_t elements = p.B * p.H * p.m * p.dv;
+  decay_join_kernel<<<(unsigned)ceil_div(elements, kThreads), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
+size_t decay_workspace_bytes(const falcon_decay_shape& s, bool) { return pass_bytes(s); }
+
 cudaError_t launch_decay_fwd(const DecayCall& c, cudaStream_t stream) {
-  DecayPass p = shape_pass(c.s, c.s.m, c.s.dv);
+  DecayPass p = shape_pass(c.s, c.s.m, c.s.dv, false);
   p.q = c.q, p.k = c.k, p.v = c.v, p.o = c.o;
   p.qs = c.qs, p.ks = c.ks, p.vs = c.vs, p.os = c.os;
   p.log_decay = c.log_decay, p.lengths = c.lengths;
@@ -321,13 +340,13 @@ cudaError_t launch_decay_fwd(const DecayCall& c, cudaStream_t stream) {
   p.si = c.s.dv, p.sj = 1;
   p.inter = c.s.scale, p.w = 1.f;
   p.states = static_cast<float*>(c.ws);
-  return any_pass(p, stream);
+  return any_pass(c.s, p, stream);
 }
 
 cudaError_t launch_decay_bwd(const DecayCall& c, cudaStream_t stream) {
   const int m = c.s.m, dv = c.s.dv;
   // dq = scale S_t dO_t: the forward pass with (dO, v, k), its state transposed
-  DecayPass p = shape_pass(c.s, dv, m);
+  DecayPass p = shape_pass(c.s, dv, m, false);
   p.log_decay = c.log_decay, p.lengths = c.lengths;
   p.states = static_cast<float*>(c.ws);
   p.q = c.dO, p.k = c.v, p.v = c.k, p.o = c.dq;
@@ -335,7 +354,7 @@ cudaError_t launch_decay_bwd(const DecayCall& c, cudaStream_t stream) {
   p.S_init = c.S0;
   p.si = 1, p.sj = dv;
   p.inter = c.s.scale, p.w = 1.f;
-  cudaError_t e = any_pass(p, stream);
+  cudaError_t e = any_pass(c.s, p, stream);
   if (e != cudaSuccess) return e;
   // dk = G_t v_t, backward in time with (v, dO, q)
   p.rev = 1;
@@ -343,7 +362,7 @@ cudaError_t launch_decay_bwd(const DecayCall& c, cudaStream_t stream) {
   p.qs = c.vs, p.ks = c.dos, p.vs = c.qs, p.os = c.dks;
   p.S_init = c.dS_T;
   p.inter = 1.f, p.w = c.s.scale;
-  e = any_pass(p, stream);
+  e = any_pass(c.s, p, stream);
   if (e != cudaSuccess) return e;
   // dv = G_t^T k_t, backward in time with (k, q, dO)
   p.m = m, p.dv = dv;
@@ -351,7 +370,7 @@ cudaError_t launch_decay_bwd(const DecayCall& c, cudaStream_t stream) {
   p.qs = c.ks, p.ks = c.qs, p.vs = c.dos, p.os = c.dvs;
   p.S_out = c.dS0;
   p.si = dv, p.sj = 1;
-  return any_pass(p, stream);
+  return any_pass(c.s, p, stream);
 }
 
 }  // namespace falcon

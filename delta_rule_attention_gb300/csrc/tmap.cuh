@@ -18,4 +18,11 @@ namespace falcon {
 bool encode_rows_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                       uint64_t mats, uint32_t box_cols, uint32_t box_rows);
 
+// 4-D bf16 tensor of cols x rows x heads x batches with any strides (in elements; a
+// dimension of one entry needs none), boxes of 64 columns x box_rows rows with the same
+// swizzle and fill.
+bool encode_heads_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                       uint64_t heads, uint64_t batches, uint64_t row_stride,
+                       uint64_t head_stride, uint64_t batch_stride, uint32_t box_rows);
+
 }  // namespace falcon
