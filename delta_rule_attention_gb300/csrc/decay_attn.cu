@@ -257,12 +257,22 @@ __global__ void __launch_bounds__(kThreads)
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Runs of a row: enough for `want` blocks over all heads, of whole chunks.
-void split_runs(DecayPass* p, int chunk, int64_t want) {
-  const int64_t chunks = ceil_div(p->T, chunk);
-  const int64_t per = ceil_div(want, p->B * p->H);
-  const int64_t each = ceil_div(chunks, per < chunks ? per : (chunks ? chunks : 1));
-  p->run_len = (each ? each : 1) * chunk;
+// Runs of a row, of whole chunks: as many as make the last block's work shortest when
+// `want` blocks take the runs of all heads in turn, a run costing its chunks and `extra`
+// of one.
+void split_runs(DecayPass* p, int chunk, int64_t want, double extra) {
+  const int64_t chunks = ceil_div(p->T, chunk), heads = p->B * p->H;
+  int64_t best = chunks ? chunks : 1;
+  double least = -1.;
+  const int64_t first = ceil_div(heads, want);
+  for (int64_t t = first; t < first + 4 && chunks; ++t) {
+    const int64_t most = t * want / heads, runs = most < chunks ? (most ? most : 1) : chunks;
+    const int64_t each = ceil_div(chunks, runs);
+    const double cost =
+        (double)ceil_div(heads * ceil_div(chunks, each), want) * ((double)each + extra);
+    if (least < 0. || cost < least) least = cost, best = each;
+  }
+  p->run_len = best * chunk;
   p->runs = (int)ceil_div(p->T, p->run_len);
 }
 
@@ -273,9 +283,9 @@ DecayPass shape_pass(const falcon_decay_shape& s, int m, int dv, bool tc) {
   p.B = s.B, p.H = s.H, p.T = s.T;
   p.m = m, p.dv = dv, p.dtype = s.dtype;
   if (tc)
-    split_runs(&p, kDecayTcChunk, decay_tc_blocks(m, dv));
+    split_runs(&p, kDecayTcChunk, kDecayTcBlocks, 0.5);
   else
-    split_runs(&p, kChunk, kSimtBlocks);
+    split_runs(&p, kChunk, kSimtBlocks, 1.);
   return p;
 }
 // Room for either path: which one a pass takes goes by its pointers and strides too.

@@ -15,9 +15,9 @@
 // state), and is rounded once itself; weights, sums and states are fp32.
 //
 // Keys of up to 64 (M = 64) and up to 128 channels (M = 128), values likewise (N): TMA
-// fills the missing channels with zeros.  All accumulators have 128 lanes; for M = 64 the
-// A operand's second half is the tile behind it in shared memory, which lands in lanes
-// 64..127 that nobody reads.
+// fills the missing channels with zeros.  All accumulators have 128 lanes; for N = 64 the
+// second half of V^T as an A operand is the tile behind it in shared memory, which lands
+// in lanes 64..127 that nobody reads.
 #include <cuda_bf16.h>
 
 #include "linear.cuh"
@@ -33,31 +33,60 @@ using namespace tc;
 using tcu::align1024;
 using tcu::flag_error;
 
-constexpr int kThreads = 256;
 constexpr int kC = 128;                // tokens of a chunk
 constexpr uint32_t kTile = kC * 128;   // a chunk of 64 channels
+
+// A block's warps: two groups of eight that work on rows (a warp's TMEM lanes are its
+// number modulo 4, its half of the columns or channels the bit above), one warp that loads
+// and one or two that issue the products.
+constexpr int kStateThreads = 576, kReadThreads = 608;
+constexpr int kLoader = 16, kIssuer = 17;
 
 struct TcArgs {
   DecayPass p;
   int* err;
+  int items;  // runs of all heads
+  int wide_o;  // output rows lie on 32-byte boundaries
   // 0 where the tensor is broadcast along heads or batches
   int qh, qb, kh, kb, vh, vb;
 };
 struct TcMaps {
-  CUtensorMap q, k, v, o;
+  CUtensorMap q, k, v;
 };
 
+// Barriers of a block.  A wait that gave up sets `fail`, after which nobody waits.
+template <int BARS>
 struct Control {
-  uint64_t bar[4];
+  uint64_t bar[BARS];
   uint32_t tmem;
   volatile int fail;
 };
-
-__device__ __forceinline__ void wait(Control& c, int which, uint32_t phase) {
-  if (!c.fail && !mbar_wait(&c.bar[which], phase)) c.fail = 1;
+// A test suspends the thread for a while by itself: no sleep between tests, which would
+// add to every step of a chain.
+template <int BARS>
+__device__ __forceinline__ void wait(Control<BARS>& c, int which, uint32_t phase) {
+  if (mbar_try_wait(&c.bar[which], phase & 1)) return;
+  const uint64_t t0 = global_ns();
+  while (!c.fail) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(&c.bar[which], phase & 1)) return;
+    if (global_ns() - t0 > kWaitLimitNs) c.fail = 1;
+  }
+}
+// The same for all lanes of a warp, which go on together.
+template <int BARS>
+__device__ __forceinline__ void wait_warp(Control<BARS>& c, int which, uint32_t phase) {
+  wait(c, which, phase);
+  __syncwarp();
+}
+// A warp's part of a barrier that counts warps.
+template <int BARS>
+__device__ __forceinline__ void arrive_warp(Control<BARS>& c, int which) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&c.bar[which]);
 }
 
-// x as three bf16 terms; their sum keeps 24 bits.
+// a and b as sums of two or three bf16 terms; three keep all 24 bits.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& mid) {
   hi = pack_bf16(a, b);
   mid = pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
@@ -70,21 +99,23 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t&
   lo = pack_bf16(ra - bf16_lo(mid), rb - bf16_hi(mid));
 }
 
-// One row's share of a thread: 64 / (256 / 128) channels of every 64-wide tile.
+// 16-byte chunk c of row r of a swizzled tile.
 __device__ __forceinline__ unsigned char* chunk_of(unsigned char* tile, int r, int c) {
   return tile + r * 128 + ((c ^ (r & 7)) << 4);
 }
 
-// Weighted keys of row r (in place: the first term), and the terms behind it.
+// Half of row r of the keys times w: the first term, in place or elsewhere, and those
+// behind it.
 template <int ATOMS, int TERMS>
-__device__ __forceinline__ void weigh_keys(unsigned char* k, unsigned char* mid,
-                                           unsigned char* lo, int r, int half, float w) {
+__device__ __forceinline__ void weigh_keys(unsigned char* k, unsigned char* hi,
+                                           unsigned char* mid, unsigned char* lo, int r, int half,
+                                           float w) {
 #pragma unroll
   for (int at = 0; at < ATOMS; ++at)
 #pragma unroll
-    for (int c = 4 * half; c < 4 * half + 4; ++c) {
-      uint4* p = reinterpret_cast<uint4*>(chunk_of(k + at * kTile, r, c));
-      const uint4 x = *p;
+    for (int cc = 0; cc < 4; ++cc) {
+      const int c = 4 * half + cc;
+      const uint4 x = *reinterpret_cast<const uint4*>(chunk_of(k + at * kTile, r, c));
       const uint32_t in[4] = {x.x, x.y, x.z, x.w};
       uint32_t t[3][4];
 #pragma unroll
@@ -95,7 +126,8 @@ __device__ __forceinline__ void weigh_keys(unsigned char* k, unsigned char* mid,
         else
           split2(a, b, t[0][e], t[1][e]);
       }
-      *p = make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]);
+      *reinterpret_cast<uint4*>(chunk_of(hi + at * kTile, r, c)) =
+          make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]);
       *reinterpret_cast<uint4*>(chunk_of(mid + at * kTile, r, c)) =
           make_uint4(t[1][0], t[1][1], t[1][2], t[1][3]);
       if constexpr (TERMS == 3)
@@ -109,156 +141,129 @@ __device__ __forceinline__ void clear_row(unsigned char* tile, int r, int half) 
 #pragma unroll
   for (int at = 0; at < ATOMS; ++at)
 #pragma unroll
-    for (int c = 4 * half; c < 4 * half + 4; ++c)
-      *reinterpret_cast<uint4*>(chunk_of(tile + at * kTile, r, c)) = make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint4*>(chunk_of(tile + at * kTile, r, 4 * half + c)) =
+          make_uint4(0, 0, 0, 0);
 }
 
-// D += A^T B over 128 tokens: A and B tiles [token][channel], M (or 64) and N channels.
+// The issuing warp stays together (what it computes is then the same in all lanes, and
+// an operand's description costs one addition); one lane sends the products: sent by a
+// lane that runs by itself, a product of 128 x 64 x 16 took about 90 cycles, most of them
+// for its description.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+// Low word of a tile's description (the address moves by bytes / 16); the high word says
+// 1024 bytes between groups of eight rows, and the 128-byte swizzle.
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) {
+  return (saddr >> 4) | (lbo >> 4) << 16;
+}
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n"
+      " mov.b64 y, {%2, %5};\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}" ::"r"(d),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescHigh)
+      : "memory");
+}
+
+// D (+)= A^T B over the 128 tokens of tiles [token][channel]; N channels of B.
 template <int N>
 __device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
-  const uint32_t id = idesc_bf16(128, N, true, true);
-  const uint64_t da = sw128_desc(a, kTile, 1024), db = sw128_desc(b, kTile, 1024);
+  const uint32_t da = desc_low(a, kTile), db = desc_low(b, kTile);
 #pragma unroll
   for (int ks = 0; ks < kC / 16; ++ks)
-    mma_bf16(d, da + (uint64_t)(ks * kStepMN), db + (uint64_t)(ks * kStepMN), id,
-             accumulate || ks > 0);
+    mma_ss(d, da + ks * kStepMN, db + ks * kStepMN, idesc_bf16(128, N, true, true),
+           accumulate || ks > 0);
 }
+
+// A run of one head: where its tokens lie.
+struct Item {
+  int64_t bh;
+  int run, b, h, n, first, end, chunks;  // chunks that hold tokens
+  float g;
+  __device__ __forceinline__ Item(const DecayPass& p, int item) {
+    run = item % p.runs;
+    bh = item / p.runs;
+    b = (int)(bh / p.H), h = (int)(bh % p.H);
+    n = (int)row_length(p.lengths, b, p.T);
+    first = (int)(run * p.run_len);
+    end = (int)(first + p.run_len < p.T ? first + p.run_len : p.T);
+    const int left = min(n, end) - first;
+    chunks = left > 0 ? (left + kC - 1) / kC : 0;
+    g = decay_rate(p.log_decay, h);
+  }
+};
 
 // ---- states -----------------------------------------------------------------
+// D[value][key] = V^T (Diag(w) K), so that the three terms of a key share a thread's
+// lane.  A product of 128 rows costs at least 64 cycles for its A operand's bytes, however
+// few columns it has: with 64 keys the terms lie side by side and one product of 192
+// columns takes them all.
+//
+// The tensor cores add into an accumulator without rounding to nearest: over a long run
+// the error grows with the number of additions (1.3e-5 of a state of 65536 tokens at a rate
+// of 2^-12).  So sums are taken out after every chunk and added in registers; with 128
+// keys only the first term's, the other two, smaller by 2^8 and 2^16, stay in TMEM for
+// the whole run.
 template <int M, int N>
-struct StateSmem {
+struct StatePlan {
+  static constexpr bool kSide = M == 64;  // terms side by side
   static constexpr uint32_t kK = M / 64 * kTile, kV = N / 64 * kTile;
-  static constexpr uint32_t kMid = 0, kLo = kK, kStage = 2 * kK, kStageBytes = kK + kV;
-  static constexpr uint32_t kBytes = kStage + 2 * kStageBytes + 1024;
+  static constexpr int kStages = M + N == 128 ? 4 : 2;
+  static constexpr int kTerms = kSide ? 2 : 1;  // buffers for the terms
+  static constexpr uint32_t kT = (kSide ? 3 : 2) * kK;
+  static constexpr uint32_t V = 0, K = kStages * kV, T = K + kStages * kK;
+  static constexpr uint32_t kBytes = T + kTerms * kT + 1024;
+  // TMEM columns: two sums, and with 128 keys the smaller terms'
+  static constexpr uint32_t kSumCols = kSide ? 3 * M : M, kCols = 512;
+  static constexpr int kFull = 0, kEmpty = kStages, kSplit = 2 * kStages,
+                       kSplitFree = kSplit + 2, kSum = kSplit + 4, kSumFree = kSplit + 6,
+                       kBars = kSplit + 8;
 };
 
-template <int M, int N>
-__global__ void __launch_bounds__(kThreads, M + N == 128 ? 2 : 1)
-    decay_states_tc(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps) {
-  using L = StateSmem<M, N>;
-  extern __shared__ unsigned char raw[];
-  __shared__ Control ctl;
-  unsigned char* sm = align1024(raw);
-  const DecayPass& p = a.p;
-  const int tid = threadIdx.x, warp = tid >> 5;
-  const int run = blockIdx.x % p.runs;
-  const int64_t bh = blockIdx.x / p.runs;
-  const int b = (int)(bh / p.H), h = (int)(bh % p.H);
-  const int64_t n = row_length(p.lengths, b, p.T);
-  const int64_t t0 = run * p.run_len, len = run_tokens(n, run, p.run_len);
-  const int chunks = (int)((len + kC - 1) / kC);
-  if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(&ctl.bar[i], 1);
-    ctl.fail = 0;
-    fence_mbar_init();
-  }
-  if (warp == 0) tmem_alloc(&ctl.tmem, N);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
-  auto load = [&](int c) {
-    unsigned char* st = sm + L::kStage + (c & 1) * L::kStageBytes;
-    uint64_t* bar = &ctl.bar[c & 1];
-    mbar_expect_tx(bar, L::kStageBytes);
-    const int t = (int)t0 + c * kC;
-#pragma unroll
-    for (int i = 0; i < M / 64; ++i)
-      tma_load_4d(st + i * kTile, &maps.k, 64 * i, t, h * a.kh, b * a.kb, bar);
-#pragma unroll
-    for (int i = 0; i < N / 64; ++i)
-      tma_load_4d(st + L::kK + i * kTile, &maps.v, 64 * i, t, h * a.vh, b * a.vb, bar);
-  };
-  if (tid == 0)
-    for (int c = 0; c < 2 && c < chunks; ++c) load(c);
-  const float g = decay_rate(p.log_decay, h);
-  const int r = tid & (kC - 1), half = tid >> 7;
-  for (int c = 0; c < chunks; ++c) {
-    unsigned char* st = sm + L::kStage + (c & 1) * L::kStageBytes;
-    const int have = (int)(len - (int64_t)c * kC < kC ? len - (int64_t)c * kC : kC);
-    const float w = p.w * decay_power(g, (float)(p.rev ? (int64_t)c * kC + r + 1
-                                                       : len - 1 - (int64_t)c * kC - r));
-    wait(ctl, c & 1, (c >> 1) & 1);
-    if (c > 0) {
-      wait(ctl, 2, (c - 1) & 1);  // the products of the last chunk: its tiles are free
-      if (tid == 0 && c + 1 < chunks) load(c + 1);
-    }
-    if (r < have) {
-      weigh_keys<M / 64, 3>(st, sm + L::kMid, sm + L::kLo, r, half, w);
-    } else {  // rows that the sequence does not hold
-      clear_row<M / 64>(st, r, half);
-      clear_row<M / 64>(sm + L::kMid, r, half);
-      clear_row<M / 64>(sm + L::kLo, r, half);
-      clear_row<N / 64>(st + L::kK, r, half);
-    }
-    fence_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      tc_fence_after();
-      const uint32_t k = smem_addr(st), v = k + L::kK;
-      mma_tokens<N>(tmem, k, v, c > 0);
-      mma_tokens<N>(tmem, smem_addr(sm + L::kMid), v, true);
-      mma_tokens<N>(tmem, smem_addr(sm + L::kLo), v, true);
-      mma_commit(&ctl.bar[2]);
-    }
-  }
-  if (chunks > 0) wait(ctl, 2, (chunks - 1) & 1);
-  tc_fence_after();
-  const int i = 32 * (warp & 3) + (tid & 31);
-  float* out = p.states + ((bh * p.runs + run) * p.m + i) * p.dv;
-  if (32 * (warp & 3) < M) {
-#pragma unroll
-    for (int cb = 0; cb < N / 64; ++cb) {
-      const int j0 = (warp >> 2) * (N / 2) + cb * 32;
-      float v[32];
-      tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + j0, v);
-      if (i < p.m) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          if (j0 + j < p.dv)
-            *reinterpret_cast<float4*>(out + j0 + j) =
-                chunks > 0 ? make_float4(v[j], v[j + 1], v[j + 2], v[j + 3])
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, N);
-  if (tid == 0 && ctl.fail) flag_error(a.err);
+// Chunks [from, to) of a run whose weights are not all zero in fp32 (e^-104 is).
+__device__ __forceinline__ void weighed_chunks(const Item& it, bool rev, int len, int* from,
+                                               int* to) {
+  *from = 0, *to = it.chunks;
+  if (!(it.g < 0.f)) return;
+  const float reach = -104.f / it.g;
+  if (!(reach < (float)len)) return;
+  const int tokens = (int)reach + 2;
+  if (rev)
+    *to = min(it.chunks, (tokens + kC - 1) / kC);
+  else
+    *from = max(0, len - tokens) / kC;
 }
 
-// ---- reads --------------------------------------------------------------------
 template <int M, int N>
-struct ReadSmem {
-  static constexpr uint32_t kK = M / 64 * kTile, kV = N / 64 * kTile;
-  static constexpr uint32_t kSAtom = M * 128;  // 64 values of the state
-  static constexpr uint32_t Q = 0, K = kK, Lo = 2 * kK, V = 3 * kK, O = V + kV, S = O + kV;
-  static constexpr uint32_t kBytes = S + N / 64 * kSAtom + 1024;
-  // TMEM columns: P (fp32, then bf16), O, X
-  static constexpr uint32_t P = 0, Od = 128, X = Od + N, kCols = X + N <= 256 ? 256 : 512;
-};
-
-template <int M, int N>
-__global__ void __launch_bounds__(kThreads, M + N == 128 ? 2 : 1)
-    decay_read_tc(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps) {
-  using L = ReadSmem<M, N>;
+__global__ void __launch_bounds__(kStateThreads, 1)
+    decay_states_tc(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps) {
+  using L = StatePlan<M, N>;
   extern __shared__ unsigned char raw[];
-  __shared__ Control ctl;
+  __shared__ Control<L::kBars> ctl;
   unsigned char* sm = align1024(raw);
   const DecayPass& p = a.p;
-  const int tid = threadIdx.x, warp = tid >> 5;
-  const int run = blockIdx.x % p.runs;
-  const int64_t bh = blockIdx.x / p.runs;
-  const int b = (int)(bh / p.H), h = (int)(bh % p.H);
-  const int n = (int)row_length(p.lengths, b, p.T);
-  const int first = (int)(run * p.run_len);
-  const int end = (int)(first + p.run_len < p.T ? first + p.run_len : p.T);
-  const int chunks = (end - first + kC - 1) / kC;
-  const bool rev = p.rev;
-  enum { kQK = 0, kVb = 1, kMma = 2 };
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(&ctl.bar[i], 1);
+    for (int i = 0; i < L::kStages; ++i)
+      mbar_init(&ctl.bar[L::kFull + i], 1), mbar_init(&ctl.bar[L::kEmpty + i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.bar[L::kSplit + i], 8), mbar_init(&ctl.bar[L::kSplitFree + i], 1);
+      mbar_init(&ctl.bar[L::kSum + i], 1), mbar_init(&ctl.bar[L::kSumFree + i], 8);
+    }
     ctl.fail = 0;
     fence_mbar_init();
   }
@@ -266,255 +271,558 @@ __global__ void __launch_bounds__(kThreads, M + N == 128 ? 2 : 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0), base = smem_addr(sm);
 
-  auto token = [&](int c) { return first + (rev ? chunks - 1 - c : c) * kC; };
-  auto held = [&](int c) { return min(max(n - token(c), 0), kC); };
-  auto load_q = [&](int c) {
-    mbar_expect_tx(&ctl.bar[kQK], 2 * L::kK);
-#pragma unroll
-    for (int i = 0; i < M / 64; ++i)
-      tma_load_4d(sm + L::Q + i * kTile, &maps.q, 64 * i, token(c), h * a.qh, b * a.qb,
-                  &ctl.bar[kQK]);
-  };
-  auto load_kv = [&](int c) {
-#pragma unroll
-    for (int i = 0; i < M / 64; ++i)
-      tma_load_4d(sm + L::K + i * kTile, &maps.k, 64 * i, token(c), h * a.kh, b * a.kb,
-                  &ctl.bar[kQK]);
-    mbar_expect_tx(&ctl.bar[kVb], L::kV);
-#pragma unroll
-    for (int i = 0; i < N / 64; ++i)
-      tma_load_4d(sm + L::V + i * kTile, &maps.v, 64 * i, token(c), h * a.vh, b * a.vb,
-                  &ctl.bar[kVb]);
-  };
-  // chunks behind the row's last token come first (backward) or last (forward)
-  int live = 0, live0 = 0;
-  for (int c = 0; c < chunks; ++c)
-    if (held(c) > 0) {
-      if (live == 0) live0 = c;
-      ++live;
-    }
-  if (tid == 0 && live > 0) {
-    load_q(live0);
-    load_kv(live0);
-  }
-
-  const float g = decay_rate(p.log_decay, h);
-  const float g2 = fmaxf(g * kLog2e, -kLargest);
-  auto power = [&](int gap) { return exp2_approx(g2 * (float)gap); };
-  const float intra = p.inter * p.w;
-  const int lane = tid & 31, i = 32 * (warp & 3) + lane;  // TMEM lane: a token, or a key
-  const int part = warp >> 2;                             // half of the columns
-  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-  const int r = tid & (kC - 1), half = tid >> 7;  // a row of a staged tile, half of it
-
-  // the state entering the run: as an operand, and weighted for the sum
-  const bool state_row = 32 * (warp & 3) < M;
-  auto put_state = [&](float* x, int cb, float lost) {
-    // columns 32 cb .. of key i
-    unsigned char* tile = sm + L::S + (cb >> 1) * L::kSAtom;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint4*>(chunk_of(tile, i, 4 * (cb & 1) + c)) = tcu::pack8(x + 8 * c, 1.f);
-    uint32_t w[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(fmaf(lost, x[j], x[j]));
-    tmem_st32(tmem + lanes + L::X + 32 * cb, w);
-  };
-  if (live > 0 && state_row) {
-    const float lost = expm1f(g * (float)held(live0));
-    const float* X = p.states + ((bh * p.runs + run) * p.m + (i < p.m ? i : 0)) * p.dv;
-#pragma unroll
-    for (int q = 0; q < N / 64; ++q) {
-      const int cb = part * (N / 64) + q;
-      float x[32];
-#pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const int col = 32 * cb + j;
-        const float4 y = i < p.m && col < p.dv ? *reinterpret_cast<const float4*>(X + col)
-                                               : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[j] = y.x, x[j + 1] = y.y, x[j + 2] = y.z, x[j + 3] = y.w;
-      }
-      put_state(x, cb, lost);
-    }
-    tmem_st_wait();
-  }
-
-  float table[16];  // gamma^k, from the far end of 16 columns
-#pragma unroll
-  for (int j = 0; j < 16; ++j) table[j] = power(rev ? j : 15 - j);
-
-  int done = 0;         // chunks worked on
-  uint32_t mma = 0;     // phase of the products' barrier
-  for (int c = 0; c < chunks; ++c) {
-    const int t0 = token(c), have = held(c);
-    if (have > 0) {
-      const bool more = done + 1 < live;
-      wait(ctl, kQK, done & 1);
-      if (have < kC) {
-        wait(ctl, kVb, done & 1);
-        if (r >= have) {
-          clear_row<M / 64>(sm + L::Q, r, half);
-          clear_row<M / 64>(sm + L::K, r, half);
-          clear_row<N / 64>(sm + L::V, r, half);
+  int c = 0;  // chunks of all items so far
+  for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+    const Item it(p, item);
+    const int len = max(min(it.n, it.end) - it.first, 0);
+    int from, to;
+    weighed_chunks(it, p.rev, len, &from, &to);
+    if (warp < 8) {
+      // weighs and splits the keys
+      const int r = tid & (kC - 1), half = warp >> 2;
+      for (int k = from; k < to; ++k, ++c) {
+        const int s = c % L::kStages, t = c % L::kTerms;
+        const int at = k * kC + r;
+        const float w = p.w * decay_power(it.g, (float)(p.rev ? at + 1 : len - 1 - at));
+        unsigned char* key = sm + L::K + s * L::kK;
+        unsigned char* terms = sm + L::T + t * L::kT;
+        unsigned char* hi = L::kSide ? terms : key;
+        unsigned char* mid = L::kSide ? terms + L::kK : terms;
+        wait_warp(ctl, L::kFull + s, c / L::kStages);
+        if (c >= L::kTerms) wait_warp(ctl, L::kSplitFree + t, c / L::kTerms - 1);
+        if (at < len) {
+          weigh_keys<M / 64, 3>(key, hi, mid, mid + L::kK, r, half, w);
+        } else {  // rows that the sequence does not hold
+          clear_row<M / 64>(hi, r, half);
+          clear_row<M / 64>(mid, r, half);
+          clear_row<M / 64>(mid + L::kK, r, half);
+          clear_row<N / 64>(sm + L::V + s * L::kV, r, half);
         }
+        fence_async_smem();
+        arrive_warp(ctl, L::kSplit + t);
       }
-      fence_async_smem();
-      tc_fence_before();
-      __syncthreads();
-      if (tid == 0) {
+    } else if (warp < 16) {
+      // adds up the first term's sums, and writes the run's state
+      constexpr int kOwn = M / 2;
+      const int j = 32 * (warp & 3) + lane, i0 = (warp >> 2 & 1) * kOwn;
+      const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+      float sum[kOwn];
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) sum[i] = 0.f;
+      for (int k = from; k < to; ++k, ++c) {
+        wait_warp(ctl, L::kSum + (c & 1), c >> 1);
         tc_fence_after();
-        const uint32_t q = smem_addr(sm + L::Q), k = smem_addr(sm + L::K),
-                       s = smem_addr(sm + L::S);
+        auto add = [&](uint32_t col) {
 #pragma unroll
-        for (int ks = 0; ks < M / 16; ++ks) {
-          const uint32_t at = (ks >> 2) * kTile + (ks & 3) * 32;
-          mma_bf16(tmem + L::P, sw128_desc(q + at, 16, 1024), sw128_desc(k + at, 16, 1024),
-                   idesc_bf16(128, 128, false, false), ks > 0);
+          for (int q = 0; q < kOwn; q += 32) {
+            float x[32];
+            tmem_ld32(tmem + lanes + col + i0 + q, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[q + i] += x[i];
+          }
+        };
+        // the smallest first
+        if constexpr (L::kSide) {
+          add((c & 1) * L::kSumCols + 2 * M);
+          add((c & 1) * L::kSumCols + M);
+        } else if (k + 1 == to) {
+          add(2 * L::kSumCols);
         }
-#pragma unroll
-        for (int ks = 0; ks < M / 16; ++ks)
-          mma_bf16(tmem + L::Od,
-                   sw128_desc(q + (ks >> 2) * kTile + (ks & 3) * 32, 16, 1024),
-                   sw128_desc(s + ks * 2048, L::kSAtom, 1024), idesc_bf16(128, N, false, true),
-                   ks > 0);
-        mma_commit(&ctl.bar[kMma]);
+        add((c & 1) * L::kSumCols);
+        tc_fence_before();
+        arrive_warp(ctl, L::kSumFree + (c & 1));
       }
-      const float far = p.inter * power(rev ? max(have - 1 - i, 0) : i + 1);
-      const float wk = more ? p.w * power(rev ? r + 1 : max(have - 1 - r, 0)) : 0.f;
-      wait(ctl, kMma, mma);
-      mma ^= 1;
-      tc_fence_after();
-      if (tid == 0 && more) load_q(live0 + done + 1);
-      // O: the state's part
+      float* out = p.states + (it.bh * p.runs + it.run) * p.m * p.dv + j;
+      if (j < p.dv) {
 #pragma unroll
-      for (int q = 0; q < N / 64; ++q) {
-        const uint32_t at = tmem + lanes + L::Od + part * (N / 2) + 32 * q;
-        float x[32];
-        tmem_ld32(at, x);
-        uint32_t w[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(x[j] * far);
-        tmem_st32(at, w);
+        for (int i = 0; i < kOwn; ++i)
+          if (i0 + i < p.m) out[(i0 + i) * p.dv] = sum[i];
       }
-      // P: weights and mask, columns 64 part .. 64 part + 63, to bf16 in place
-      {
-        uint32_t w[32];
-        const int low = 32 * (warp & 3);
+    } else if (warp == kLoader) {
+      for (int k = from; k < to; ++k, ++c) {
+        const int s = c % L::kStages, t = it.first + k * kC;
+        if (lane != 0) continue;
+        if (c >= L::kStages) wait(ctl, L::kEmpty + s, c / L::kStages - 1);
+        uint64_t* bar = &ctl.bar[L::kFull + s];
+        mbar_expect_tx(bar, L::kK + L::kV);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float x[32];
-          tmem_ld32(tmem + lanes + L::P + 64 * part + 32 * q, x);
+        for (int i = 0; i < M / 64; ++i)
+          tma_load_4d(sm + L::K + s * L::kK + i * kTile, &maps.k, 64 * i, t, it.h * a.kh,
+                      it.b * a.kb, bar);
 #pragma unroll
-          for (int blk = 0; blk < 2; ++blk) {
-            const int j0 = 64 * part + 32 * q + 16 * blk;
-            float* y = x + 16 * blk;
-            uint32_t* to = w + 16 * q + 8 * blk;
-            const int least = rev ? j0 - low - 31 : low - j0 - 15;
-            const int most = rev ? j0 + 15 - low : low + 31 - j0;
-            if (most < 0) {
+        for (int i = 0; i < N / 64; ++i)
+          tma_load_4d(sm + L::V + s * L::kV + i * kTile, &maps.v, 64 * i, t, it.h * a.vh,
+                      it.b * a.vb, bar);
+      }
+    } else {
+      for (int k = from; k < to; ++k, ++c) {
+        const int s = c % L::kStages, t = c % L::kTerms;
+        wait_warp(ctl, L::kSplit + t, c / L::kTerms);
+        if (c >= 2) wait_warp(ctl, L::kSumFree + (c & 1), (c >> 1) - 1);
+        // the smaller terms' sums of the run before have been read
+        if (k == from && c >= 1) wait_warp(ctl, L::kSumFree + ((c - 1) & 1), (c - 1) >> 1);
+        tc_fence_after();
+        const uint32_t v = base + L::V + s * L::kV, terms = base + L::T + t * L::kT;
+        const uint32_t d = tmem + (c & 1) * L::kSumCols;
+        if (elect_one()) {
+          if constexpr (L::kSide) {
+            mma_tokens<3 * M>(d, v, terms, false);
+          } else {
+            mma_tokens<M>(d, v, base + L::K + s * L::kK, false);
+            mma_tokens<M>(tmem + 2 * L::kSumCols, v, terms, k > from);
+            mma_tokens<M>(tmem + 2 * L::kSumCols, v, terms + L::kK, true);
+          }
+          mma_commit(&ctl.bar[L::kEmpty + s]);
+          mma_commit(&ctl.bar[L::kSplitFree + t]);
+          mma_commit(&ctl.bar[L::kSum + (c & 1)]);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, L::kCols);
+  if (tid == 0 && ctl.fail) flag_error(a.err);
+}
+
+// ---- reads --------------------------------------------------------------------
+// Per chunk, four products, sent by two warps, so that neither chain waits for the other:
+//   A  P = Q K^T            -> weighted, masked and rounded by the first eight warps
+//   B  Oi = Q X             X the state entering the chunk, rounded to bf16
+//   C  X^T += V^T Kd        weighted keys in two terms; only where another chunk follows
+//   D  O = P V              P read from TMEM
+// One warp sends A and D, the other B and C.
+// The other eight warps write gamma^{i+1} Oi + O and carry X.
+template <int M, int N>
+struct ReadPlan {
+  static constexpr bool kSide = M == 64;  // the two terms side by side, one product
+  static constexpr uint32_t kQ = M / 64 * kTile, kK = kQ, kV = N / 64 * kTile;
+  static constexpr uint32_t kSAtom = N * 128;  // the state [value][key], 64 keys of it
+  static constexpr int kQs = M + N == 256 ? 1 : 2, kKs = M + N == 128 ? 3 : 2;  // stages
+  static constexpr int kPs = N == 64 ? 2 : 1;  // P: the next chunk's beside this one's
+  // V first: the tile behind its last one is read too (and ignored) where N = 64
+  static constexpr uint32_t V = 0, Q = kKs * kV, K = Q + kQs * kQ, Lo = K + kKs * kK,
+                            S = Lo + (kSide ? 2 : 1) * kK;
+  static constexpr uint32_t kBytes = S + M / 64 * kSAtom + 1024;
+  // TMEM columns: P (fp32, then bf16), O, Oi, X
+  static constexpr uint32_t P = 0, O = kPs * 128, Oi = O + N, X = Oi + N, kCols = 512;
+  static_assert(X + (kSide ? 2 * M : M) <= kCols, "columns of TMEM");
+  static constexpr int kFullQ = 0, kEmptyQ = 2, kFullK = 4, kEmptyK = 7, kFullV = 10,
+                       kEmptyV = 13, kA = 16, kB = 18, kC_ = 19, kD = 20, kClear = 21,
+                       kPReady = 25, kKReady = 27, kSReady = 28, kOFree = 29, kBars = 30;
+};
+// How far one warp runs ahead of another decides how many barriers a step needs (a wait
+// looks at a phase's parity): A, P's readiness and the clearing of padding may be one or
+// two chunks ahead of the warp that sends B, the others not one.
+
+// The chunks of an item in the order of the work, and whether rows of one have to be
+// cleared in shared memory (padding that is not the tensor's end).
+struct Chunk {
+  int t0, have;
+  bool clear;
+  __device__ __forceinline__ Chunk(const Item& it, const DecayPass& p, int i) {
+    t0 = it.first + (p.rev ? it.chunks - 1 - i : i) * kC;
+    have = min(it.n - t0, kC);
+    clear = have < kC && it.n < p.T;
+  }
+};
+
+template <int M, int N>
+__global__ void __launch_bounds__(kReadThreads, 1)
+    decay_read_tc(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps) {
+  using L = ReadPlan<M, N>;
+  extern __shared__ unsigned char raw[];
+  __shared__ Control<L::kBars> ctl;
+  __shared__ float nears[4][64];
+  unsigned char* sm = align1024(raw);
+  const DecayPass& p = a.p;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const bool rev = p.rev;
+  if (tid == 0) {
+    // what both issuing warps read is free when both have said so
+    for (int i = 0; i < L::kBars; ++i) {
+      const bool two = (i >= L::kEmptyQ && i < L::kFullK) || (i >= L::kEmptyK && i < L::kFullV) ||
+                       (i >= L::kEmptyV && i < L::kA);
+      mbar_init(&ctl.bar[i], i >= L::kClear ? 8 : two ? 2 : 1);
+    }
+    ctl.fail = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(&ctl.tmem, L::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0), base = smem_addr(sm);
+  const int row = 32 * (warp & 3) + lane;  // TMEM lane: a token, or a key
+  const int part = warp >> 2 & 1;          // half of the columns
+  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+
+  if (warp < 8) {
+    int c = 0, carried = 0, cleared = 0;
+    for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+      const Item it(p, item);
+      const float g2 = fmaxf(it.g * kLog2e, -kLargest);
+      auto power = [&](int gap) { return exp2_approx(g2 * (float)gap); };
+      const float intra = p.inter * p.w;
+      f32x2 table[8];  // gamma^k from the far end of 16 columns
 #pragma unroll
-              for (int j = 0; j < 8; ++j) to[j] = 0;
-            } else if (least >= 0) {
-              const float f = intra * power(rev ? j0 - i : i - j0 - 15);
+      for (int j = 0; j < 8; ++j)
+        table[j] = rev ? pack2(power(2 * j), power(2 * j + 1))
+                       : pack2(power(15 - 2 * j), power(14 - 2 * j));
+      // intra gamma^k, zero for k < 0, for the square of 32 tokens on the diagonal
+      // that half of these warps meet
+      float* near = nears[warp & 3];
+      __syncwarp();
+      if (part == (warp & 3) >> 1) {
+        near[lane] = lane == 31 ? intra : 0.f;
+        near[32 + lane] = lane == 31 ? 0.f : intra * power(lane + 1);
+      }
+      __syncwarp();
+      for (int i = 0; i < it.chunks; ++i, ++c) {
+        const Chunk ch(it, p, i);
+        const bool more = i + 1 < it.chunks;
+        const int ks = c % L::kKs, qs = c % L::kQs, ps = c % L::kPs;
+        const uint32_t at_p = tmem + lanes + L::P + ps * 128;
+        unsigned char* key = sm + L::K + ks * L::kK;
+        if (ch.clear) {
+          wait_warp(ctl, L::kFullQ + qs, c / L::kQs);
+          wait_warp(ctl, L::kFullK + ks, c / L::kKs);
+          wait_warp(ctl, L::kFullV + ks, c / L::kKs);
+          if (row >= ch.have) {
+            clear_row<M / 64>(sm + L::Q + qs * L::kQ, row, part);
+            clear_row<M / 64>(key, row, part);
+            clear_row<N / 64>(sm + L::V + ks * L::kV, row, part);
+          }
+          fence_async_smem();
+          arrive_warp(ctl, L::kClear + (cleared++ & 3));
+        }
+        wait_warp(ctl, L::kA + ps, c / L::kPs);
+        tc_fence_after();
+        {
+          // columns 64 part .. 64 part + 63, to bf16 in place
+          uint32_t w[32];
+          const int low = 32 * (warp & 3);
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                to[j] = pack_bf16(y[2 * j] * (f * table[2 * j]),
-                                  y[2 * j + 1] * (f * table[2 * j + 1]));
+          for (int q = 0; q < 2; ++q) {
+            const int c0 = 64 * part + 32 * q;  // against this warp's rows: one kind
+            uint32_t* to = w + 16 * q;
+            if (rev ? c0 < low : c0 > low) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) to[j] = 0;
+              continue;
+            }
+            float x[32];
+            tmem_ld32(at_p + c0, x);
+            if (c0 == low) {
+              const float* f = near + 31 + (rev ? -lane : lane);
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                to[j] = rev ? pack_bf16(x[2 * j] * f[2 * j], x[2 * j + 1] * f[2 * j + 1])
+                            : pack_bf16(x[2 * j] * f[-2 * j], x[2 * j + 1] * f[-2 * j - 1]);
             } else {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int gap = rev ? j0 + j - i : i - j0 - j;
-                y[j] = gap >= 0 ? y[j] * (intra * power(gap)) : 0.f;
-              }
+              for (int blk = 0; blk < 2; ++blk) {
+                const int j0 = c0 + 16 * blk;
+                const float f = intra * power(rev ? j0 - row : row - j0 - 15);
+                const f32x2 f2 = pack2(f, f);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) to[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+                for (int j = 0; j < 8; ++j) {
+                  const float2 z = unpack2(mul2(pack2(x[16 * blk + 2 * j], x[16 * blk + 2 * j + 1]),
+                                                mul2(f2, table[j])));
+                  to[8 * blk + j] = pack_bf16(z.x, z.y);
+                }
+              }
             }
           }
+          tmem_st32(at_p + 64 * part, w);
+          tmem_st_wait();
+          tc_fence_before();
+          arrive_warp(ctl, L::kPReady + ps);
         }
-        tmem_st32(tmem + lanes + L::P + 64 * part, w);
+        if (more) {
+          const float w = p.w * power(rev ? row + 1 : max(ch.have - 1 - row, 0));
+          if (carried > 0) wait_warp(ctl, L::kC_, carried - 1);  // the second terms are free
+          weigh_keys<M / 64, 2>(key, L::kSide ? sm + L::Lo : key,
+                                L::kSide ? sm + L::Lo + L::kK : sm + L::Lo, nullptr, row, part, w);
+          fence_async_smem();
+          arrive_warp(ctl, L::kKReady);
+          ++carried;
+        }
       }
-      if (more) weigh_keys<M / 64, 2>(sm + L::K, sm + L::Lo, nullptr, r, half, wk);
+    }
+  } else if (warp < 16) {
+    int c = 0, carried = 0;
+    const bool state_row = 32 * (warp & 3) < N;
+    // keys 32 cb .. of value `row`: an operand, and what the next sum starts from
+    auto put_state = [&](const float* x, int cb, float lost) {
+      unsigned char* tile = sm + L::S + (cb >> 1) * L::kSAtom;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint4*>(chunk_of(tile, row, 4 * (cb & 1) + e)) =
+            tcu::pack8(x + 8 * e, 1.f);
+      uint32_t w[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(fmaf(lost, x[j], x[j]));
+      tmem_st32(tmem + lanes + L::X + 32 * cb, w);
+      if constexpr (L::kSide) {  // the second term's sum
+#pragma unroll
+        for (int j = 0; j < 32; ++j) w[j] = 0u;
+        tmem_st32(tmem + lanes + L::X + M + 32 * cb, w);
+      }
+    };
+    auto state_ready = [&]() {
       tmem_st_wait();
       fence_async_smem();
       tc_fence_before();
-      __syncthreads();
-      wait(ctl, kVb, done & 1);
-      if (tid == 0) {
+      arrive_warp(ctl, L::kSReady);
+    };
+    for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+      const Item it(p, item);
+      const float g2 = fmaxf(it.g * kLog2e, -kLargest);
+      auto power = [&](int gap) { return exp2_approx(g2 * (float)gap); };
+      __nv_bfloat16* out =
+          static_cast<__nv_bfloat16*>(p.o) + it.b * p.os.batch + it.h * p.os.head;
+      if (it.chunks > 0) {
+        if (state_row) {
+          const float lost = expm1f(it.g * (float)Chunk(it, p, 0).have);
+          const float* X = p.states + (it.bh * p.runs + it.run) * p.m * p.dv + row;
+#pragma unroll
+          for (int q = 0; q < M / 64; ++q) {
+            const int cb = part * (M / 64) + q;
+            float x[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int i = 32 * cb + j;
+              x[j] = i < p.m && row < p.dv ? X[i * p.dv] : 0.f;
+            }
+            put_state(x, cb, lost);
+          }
+        }
+        state_ready();
+      }
+      // rows behind the last chunk that holds tokens
+      const int eighths = p.dv / 8;
+      const int64_t dead = (int64_t)max(it.end - it.first - it.chunks * kC, 0) * eighths;
+      for (int64_t e = tid - 256; e < dead; e += 256)
+        *reinterpret_cast<uint4*>(out + (it.first + it.chunks * kC + e / eighths) * p.os.time +
+                                  e % eighths * 8) = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < it.chunks; ++i, ++c) {
+        const Chunk ch(it, p, i);
+        const bool more = i + 1 < it.chunks;
+        const float far = p.inter * power(rev ? max(ch.have - 1 - row, 0) : row + 1);
+        const bool live = row < ch.have;
+        wait_warp(ctl, L::kD, c);
+        wait_warp(ctl, L::kB, c);
         tc_fence_after();
-        const uint64_t v = sw128_desc(smem_addr(sm + L::V), kTile, 1024);
-#pragma unroll
-        for (int ks = 0; ks < kC / 16; ++ks)
-          mma_bf16_ta(tmem + L::Od, tmem + L::P + (ks >> 2) * 64 + (ks & 3) * 8,
-                      v + (uint64_t)(ks * kStepMN), idesc_bf16(128, N, false, true), 1);
-        if (more) {
-          mma_tokens<N>(tmem + L::X, smem_addr(sm + L::K), smem_addr(sm + L::V), true);
-          mma_tokens<N>(tmem + L::X, smem_addr(sm + L::Lo), smem_addr(sm + L::V), true);
-        }
-        mma_commit(&ctl.bar[kMma]);
-        bulk_wait_read<0>();  // the last chunk's outputs have left their tiles
-      }
-      wait(ctl, kMma, mma);
-      mma ^= 1;
-      tc_fence_after();
-      if (tid == 0 && more) load_kv(live0 + done + 1);
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < N / 64; ++q) {
-        const int cb = part * (N / 64) + q;
-        float x[32];
-        tmem_ld32(tmem + lanes + L::Od + 32 * cb, x);
-        if (i >= have) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = 0.f;
-        }
-        unsigned char* tile = sm + L::O + (cb >> 1) * kTile;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4*>(chunk_of(tile, i, 4 * (cb & 1) + e)) =
-              tcu::pack8(x + 8 * e, 1.f);
-      }
-      if (more && state_row) {
-        const float lost = expm1f(g * (float)held(live0 + done + 1));
 #pragma unroll
         for (int q = 0; q < N / 64; ++q) {
-          const int cb = part * (N / 64) + q;
-          float x[32];
-          tmem_ld32(tmem + lanes + L::X + 32 * cb, x);
-          put_state(x, cb, lost);
-        }
-        tmem_st_wait();
-      }
-      ++done;
-    } else {  // no token: zeros
-      if (tid == 0) bulk_wait_read<0>();
-      __syncthreads();
-      clear_row<N / 64>(sm + L::O, r, half);
-    }
-    fence_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0) {
+          const int col = 32 * (part * (N / 64) + q);
+          float x[32], y[32];
+          tmem_ld32(tmem + lanes + L::O + col, x);
+          tmem_ld32(tmem + lanes + L::Oi + col, y);
+          if (q + 1 == N / 64) {
+            tc_fence_before();
+            arrive_warp(ctl, L::kOFree);
+          }
+          if (ch.t0 + row < it.end) {
+          uint32_t z[16];
 #pragma unroll
-      for (int q = 0; q < N / 64; ++q)
-        if (64 * q < p.dv) tma_store_4d(&maps.o, sm + L::O + q * kTile, 64 * q, t0, h, b);
-      bulk_commit();
+          for (int j = 0; j < 16; ++j)
+            z[j] = live ? pack_bf16(fmaf(far, y[2 * j], x[2 * j]),
+                                    fmaf(far, y[2 * j + 1], x[2 * j + 1]))
+                        : 0u;
+          __nv_bfloat16* to = out + (ch.t0 + row) * p.os.time + col;
+          if (a.wide_o) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (col + 16 * e < p.dv)
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(
+                                 to + 16 * e),
+                             "r"(z[8 * e]), "r"(z[8 * e + 1]), "r"(z[8 * e + 2]),
+                             "r"(z[8 * e + 3]), "r"(z[8 * e + 4]), "r"(z[8 * e + 5]),
+                             "r"(z[8 * e + 6]), "r"(z[8 * e + 7])
+                             : "memory");
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col + 8 * e < p.dv)
+                *reinterpret_cast<uint4*>(to + 8 * e) =
+                    make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+          }
+          }
+          __syncwarp();
+        }
+        if (more) {
+          const float lost = expm1f(it.g * (float)Chunk(it, p, i + 1).have);
+          wait_warp(ctl, L::kC_, carried);
+          ++carried;
+          tc_fence_after();
+          if (state_row) {
+#pragma unroll
+            for (int q = 0; q < M / 64; ++q) {
+              const int cb = part * (M / 64) + q;
+              float x[32];
+              tmem_ld32(tmem + lanes + L::X + 32 * cb, x);
+              if constexpr (L::kSide) {
+                float y[32];
+                tmem_ld32(tmem + lanes + L::X + M + 32 * cb, y);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] += y[j];
+              }
+              put_state(x, cb, lost);
+            }
+          }
+          state_ready();
+        }
+      }
+    }
+  } else if (warp == kLoader) {
+    int c = 0;
+    for (int item = blockIdx.x; item < a.items && lane == 0; item += gridDim.x) {
+      const Item it(p, item);
+      for (int i = 0; i < it.chunks; ++i, ++c) {
+        const int t = Chunk(it, p, i).t0;
+        if (L::kQs == 1) {  // its tile is still in use: as far as L2
+#pragma unroll
+          for (int x = 0; x < M / 64; ++x)
+            tma_prefetch_4d(&maps.q, 64 * x, t, it.h * a.qh, it.b * a.qb);
+        }
+        const int ks = c % L::kKs, qs = c % L::kQs;
+        if (c >= L::kKs) wait(ctl, L::kEmptyK + ks, c / L::kKs - 1);
+        mbar_expect_tx(&ctl.bar[L::kFullK + ks], L::kK);
+#pragma unroll
+        for (int x = 0; x < M / 64; ++x)
+          tma_load_4d(sm + L::K + ks * L::kK + x * kTile, &maps.k, 64 * x, t, it.h * a.kh,
+                      it.b * a.kb, &ctl.bar[L::kFullK + ks]);
+        if (c >= L::kKs) wait(ctl, L::kEmptyV + ks, c / L::kKs - 1);
+        mbar_expect_tx(&ctl.bar[L::kFullV + ks], L::kV);
+#pragma unroll
+        for (int x = 0; x < N / 64; ++x)
+          tma_load_4d(sm + L::V + ks * L::kV + x * kTile, &maps.v, 64 * x, t, it.h * a.vh,
+                      it.b * a.vb, &ctl.bar[L::kFullV + ks]);
+        if (c >= L::kQs) wait(ctl, L::kEmptyQ + qs, c / L::kQs - 1);
+        mbar_expect_tx(&ctl.bar[L::kFullQ + qs], L::kQ);
+#pragma unroll
+        for (int x = 0; x < M / 64; ++x)
+          tma_load_4d(sm + L::Q + qs * L::kQ + x * kTile, &maps.q, 64 * x, t, it.h * a.qh,
+                      it.b * a.qb, &ctl.bar[L::kFullQ + qs]);
+      }
+    }
+  } else if (warp == kIssuer) {
+    int c = 0, cleared = 0;
+    auto send_a = [&](int cc, bool clear) {
+      const int ks = cc % L::kKs, qs = cc % L::kQs, ps = cc % L::kPs;
+      wait_warp(ctl, L::kFullK + ks, cc / L::kKs);
+      wait_warp(ctl, L::kFullQ + qs, cc / L::kQs);
+      if (clear) wait_warp(ctl, L::kClear + (cleared & 3), cleared >> 2), ++cleared;
+      tc_fence_after();
+      const uint32_t q = desc_low(base + L::Q + qs * L::kQ, 16),
+                     k = desc_low(base + L::K + ks * L::kK, 16);
+        if (elect_one()) {  // behind the D that read this P
+#pragma unroll
+        for (int s = 0; s < M / 16; ++s) {
+          const uint32_t at = (s >> 2) * (kTile >> 4) + (s & 3) * kStepK;
+          mma_ss(tmem + L::P + ps * 128, q + at, k + at, idesc_bf16(128, 128, false, false),
+                 s > 0);
+        }
+        mma_commit(&ctl.bar[L::kA + ps]);
+        mma_commit(&ctl.bar[L::kEmptyQ + qs]);
+      }
+      __syncwarp();
+    };
+    for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+      const Item it(p, item);
+      if (it.chunks > 0) send_a(c, Chunk(it, p, 0).clear);
+      for (int i = 0; i < it.chunks; ++i, ++c) {
+        const int ks = c % L::kKs, ps = c % L::kPs;
+        const bool more = i + 1 < it.chunks;
+        if (L::kPs == 2 && more) send_a(c + 1, Chunk(it, p, i + 1).clear);
+        const uint32_t v = desc_low(base + L::V + ks * L::kV, kTile);
+        wait_warp(ctl, L::kFullV + ks, c / L::kKs);
+        if (c > 0) wait_warp(ctl, L::kOFree, c - 1);
+        wait_warp(ctl, L::kPReady + ps, c / L::kPs);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < kC / 16; ++s)
+            mma_ts(tmem + L::O, tmem + L::P + ps * 128 + (s >> 2) * 64 + (s & 3) * 8,
+                   v + s * kStepMN, idesc_bf16(128, N, false, true), s > 0);
+          mma_commit(&ctl.bar[L::kD]);
+          mma_commit(&ctl.bar[L::kEmptyK + ks]);
+          mma_commit(&ctl.bar[L::kEmptyV + ks]);
+        }
+        __syncwarp();
+        if (L::kPs == 1 && more) send_a(c + 1, Chunk(it, p, i + 1).clear);
+      }
+    }
+  } else {
+    int c = 0, carried = 0, cleared = 0;
+    for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+      const Item it(p, item);
+      for (int i = 0; i < it.chunks; ++i, ++c) {
+        const int ks = c % L::kKs, qs = c % L::kQs;
+        const uint32_t q = desc_low(base + L::Q + qs * L::kQ, 16),
+                       s = desc_low(base + L::S, 16);
+        wait_warp(ctl, L::kFullQ + qs, c / L::kQs);
+        if (Chunk(it, p, i).clear)
+          wait_warp(ctl, L::kClear + (cleared & 3), cleared >> 2), ++cleared;
+        if (c > 0) wait_warp(ctl, L::kOFree, c - 1);
+        wait_warp(ctl, L::kSReady, c);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < M / 16; ++k)
+            mma_ss(tmem + L::Oi, q + (k >> 2) * (kTile >> 4) + (k & 3) * kStepK,
+                   s + (k >> 2) * (L::kSAtom >> 4) + (k & 3) * kStepK,
+                   idesc_bf16(128, N, false, false), k > 0);
+          mma_commit(&ctl.bar[L::kB]);
+          mma_commit(&ctl.bar[L::kEmptyQ + qs]);
+        }
+        __syncwarp();
+        if (i + 1 < it.chunks) {
+          wait_warp(ctl, L::kFullV + ks, c / L::kKs);
+          wait_warp(ctl, L::kKReady, carried++);
+          tc_fence_after();
+          const uint32_t v = base + L::V + ks * L::kV;
+          if (elect_one()) {
+            if constexpr (L::kSide) {
+              mma_tokens<2 * M>(tmem + L::X, v, base + L::Lo, true);
+            } else {
+              mma_tokens<M>(tmem + L::X, v, base + L::K + ks * L::kK, true);
+              mma_tokens<M>(tmem + L::X, v, base + L::Lo, true);
+            }
+            mma_commit(&ctl.bar[L::kC_]);
+          }
+          __syncwarp();
+        }
+        if (elect_one()) {
+          mma_commit(&ctl.bar[L::kEmptyK + ks]);
+          mma_commit(&ctl.bar[L::kEmptyV + ks]);
+        }
+        __syncwarp();
+      }
     }
   }
-  if (tid == 0) bulk_wait<0>();
+  __syncwarp();
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, L::kCols);
   if (tid == 0 && ctl.fail) flag_error(a.err);
 }
 
 // ---- host -----------------------------------------------------------------------
 bool heads_map(CUtensorMap* map, const void* x, const falcon_strides& s, int64_t B, int64_t H,
-               int64_t T, int channels, bool output, int* by_head, int* by_row) {
+               int64_t T, int channels, int* by_head, int* by_row) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(x);
   if (at % 16 || s.batch % 8 || s.head % 8 || s.time % 8 || (T > 1 && s.time == 0)) return false;
   const bool hs = H > 1 && s.head != 0, bs = B > 1 && s.batch != 0;
-  *by_head = output || hs, *by_row = output || bs;
+  *by_head = hs, *by_row = bs;
   return encode_heads_bf16(map, x, channels, T, hs ? H : 1, bs ? B : 1, s.time, s.head, s.batch,
                            kC);
 }
@@ -522,16 +830,16 @@ bool heads_map(CUtensorMap* map, const void* x, const falcon_strides& s, int64_t
 template <int M, int N>
 cudaError_t run_tc(const TcArgs& a, const TcMaps& maps, bool reads, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed[2];
-  const unsigned grid = (unsigned)(a.p.B * a.p.H * a.p.runs);
-  constexpr int ss = StateSmem<M, N>::kBytes, rs = ReadSmem<M, N>::kBytes;
-  static_assert(ss <= 232448 && rs <= 232448, "shared memory of a block");
+  const unsigned grid = (unsigned)(a.items < kDecayTcBlocks ? a.items : kDecayTcBlocks);
+  constexpr int ss = StatePlan<M, N>::kBytes, rs = ReadPlan<M, N>::kBytes;
+  static_assert(ss + 1024 <= 232448 && rs + 1280 <= 232448, "shared memory of a block");
   cudaError_t e = reads ? allow_shared(decay_read_tc<M, N>, rs, &allowed[0])
                         : allow_shared(decay_states_tc<M, N>, ss, &allowed[1]);
   if (e != cudaSuccess) return e;
   if (reads)
-    decay_read_tc<M, N><<<grid, kThreads, rs, stream>>>(a, maps);
+    decay_read_tc<M, N><<<grid, kReadThreads, rs, stream>>>(a, maps);
   else
-    decay_states_tc<M, N><<<grid, kThreads, ss, stream>>>(a, maps);
+    decay_states_tc<M, N><<<grid, kStateThreads, ss, stream>>>(a, maps);
   return cudaGetLastError();
 }
 
@@ -545,20 +853,20 @@ cudaError_t run_tc_any(const TcArgs& a, const TcMaps& maps, bool reads, cudaStre
 
 }  // namespace
 
-int64_t decay_tc_blocks(int m, int dv) { return m <= 64 && dv <= 64 ? 2 * 152 : 152; }
-
 bool decay_tc_pass(const DecayPass& p, cudaError_t* status, cudaStream_t stream) {
   if (p.dtype != FALCON_BF16 || p.m % 8 || p.dv % 8 || p.runs == 0 || p.T > (1 << 30))
     return false;
   TcArgs a = {};
   TcMaps maps;
-  int oh, ob;
-  if (!heads_map(&maps.q, p.q, p.qs, p.B, p.H, p.T, p.m, false, &a.qh, &a.qb) ||
-      !heads_map(&maps.k, p.k, p.ks, p.B, p.H, p.T, p.m, false, &a.kh, &a.kb) ||
-      !heads_map(&maps.v, p.v, p.vs, p.B, p.H, p.T, p.dv, false, &a.vh, &a.vb) ||
-      !heads_map(&maps.o, p.o, p.os, p.B, p.H, p.T, p.dv, true, &oh, &ob))
+  if (!heads_map(&maps.q, p.q, p.qs, p.B, p.H, p.T, p.m, &a.qh, &a.qb) ||
+      !heads_map(&maps.k, p.k, p.ks, p.B, p.H, p.T, p.m, &a.kh, &a.kb) ||
+      !heads_map(&maps.v, p.v, p.vs, p.B, p.H, p.T, p.dv, &a.vh, &a.vb) ||
+      reinterpret_cast<uintptr_t>(p.o) % 16 || p.os.batch % 8 || p.os.head % 8 || p.os.time % 8)
     return false;
   a.p = p;
+  a.items = (int)(p.B * p.H * p.runs);
+  a.wide_o = reinterpret_cast<uintptr_t>(p.o) % 32 == 0 && p.os.batch % 16 == 0 &&
+             p.os.head % 16 == 0 && p.os.time % 16 == 0 && p.dv % 16 == 0;
   a.err = device_error_word_of_current();
   *status = run_tc_any(a, maps, false, stream);
   if (*status == cudaSuccess) *status = launch_decay_join(p, stream);

@@ -9,8 +9,7 @@ namespace falcon {
 int* device_error_word_of_current();  // api.cu
 
 constexpr int kDecayTcChunk = 128;
-// Blocks that one wave of the card holds, by key and value channels.
-int64_t decay_tc_blocks(int m, int dv);
+constexpr int kDecayTcBlocks = 152;  // one for each SM, each taking runs in turn
 // One pass, p.runs in chunks of kDecayTcChunk; false where the tensors do not fit it.
 bool decay_tc_pass(const DecayPass& p, cudaError_t* status, cudaStream_t stream);
 cudaError_t launch_decay_join(const DecayPass& p, cudaStream_t stream);

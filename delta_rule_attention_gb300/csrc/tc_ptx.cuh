@@ -169,6 +169,13 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, i
       : "memory");
 }
 
+// Hint: bring a box into L2.
+__device__ __forceinline__ void tma_prefetch_4d(const void* map, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
 // L2 cache policies for the copies below: evict_last keeps the lines over
 // others (data read again soon), evict_first lets them go first (read once).
 __device__ __forceinline__ uint64_t l2_evict_last() {
