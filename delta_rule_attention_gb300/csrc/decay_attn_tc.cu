@@ -61,17 +61,15 @@ struct Control {
   uint32_t tmem;
   volatile int fail;
 };
-// A test suspends the thread for a while by itself: no sleep between tests, which would
-// add to every step of a chain.
+// The part that waits is not inlined: the roles of a block run side by side, and with
+// everything unrolled their code did not fit the instruction cache (most of the warps'
+// time went into fetching it).
+__device__ __noinline__ void wait_on(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  if (!*fail && !mbar_wait(bar, parity)) *fail = 1;
+}
 template <int BARS>
 __device__ __forceinline__ void wait(Control<BARS>& c, int which, uint32_t phase) {
-  if (mbar_try_wait(&c.bar[which], phase & 1)) return;
-  const uint64_t t0 = global_ns();
-  while (!c.fail) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(&c.bar[which], phase & 1)) return;
-    if (global_ns() - t0 > kWaitLimitNs) c.fail = 1;
-  }
+  if (!mbar_try_wait(&c.bar[which], phase & 1)) wait_on(&c.bar[which], phase & 1, &c.fail);
 }
 // The same for all lanes of a warp, which go on together.
 template <int BARS>
@@ -110,9 +108,9 @@ template <int ATOMS, int TERMS>
 __device__ __forceinline__ void weigh_keys(unsigned char* k, unsigned char* hi,
                                            unsigned char* mid, unsigned char* lo, int r, int half,
                                            float w) {
-#pragma unroll
+#pragma unroll 1
   for (int at = 0; at < ATOMS; ++at)
-#pragma unroll
+#pragma unroll 2
     for (int cc = 0; cc < 4; ++cc) {
       const int c = 4 * half + cc;
       const uint4 x = *reinterpret_cast<const uint4*>(chunk_of(k + at * kTile, r, c));
@@ -138,9 +136,9 @@ __device__ __forceinline__ void weigh_keys(unsigned char* k, unsigned char* hi,
 
 template <int ATOMS>
 __device__ __forceinline__ void clear_row(unsigned char* tile, int r, int half) {
-#pragma unroll
+#pragma unroll 1
   for (int at = 0; at < ATOMS; ++at)
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 4; ++c)
       *reinterpret_cast<uint4*>(chunk_of(tile + at * kTile, r, 4 * half + c)) =
           make_uint4(0, 0, 0, 0);
@@ -422,27 +420,28 @@ struct ReadPlan {
 
 // The chunks of an item in the order of the work, and whether rows of one have to be
 // cleared in shared memory (padding that is not the tensor's end).
-struct Chunk {
+template <bool rev>
+struct ChunkOf {
   int t0, have;
   bool clear;
-  __device__ __forceinline__ Chunk(const Item& it, const DecayPass& p, int i) {
-    t0 = it.first + (p.rev ? it.chunks - 1 - i : i) * kC;
+  __device__ __forceinline__ ChunkOf(const Item& it, const DecayPass& p, int i) {
+    t0 = it.first + (rev ? it.chunks - 1 - i : i) * kC;
     have = min(it.n - t0, kC);
     clear = have < kC && it.n < p.T;
   }
 };
 
-template <int M, int N>
+template <int M, int N, bool rev>
 __global__ void __launch_bounds__(kReadThreads, 1)
     decay_read_tc(const __grid_constant__ TcArgs a, const __grid_constant__ TcMaps maps) {
   using L = ReadPlan<M, N>;
+  using Chunk = ChunkOf<rev>;
   extern __shared__ unsigned char raw[];
   __shared__ Control<L::kBars> ctl;
   __shared__ float nears[4][64];
   unsigned char* sm = align1024(raw);
   const DecayPass& p = a.p;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const bool rev = p.rev;
   if (tid == 0) {
     // what both issuing warps read is free when both have said so
     for (int i = 0; i < L::kBars; ++i) {
@@ -505,41 +504,41 @@ __global__ void __launch_bounds__(kReadThreads, 1)
         tc_fence_after();
         {
           // columns 64 part .. 64 part + 63, to bf16 in place
-          uint32_t w[32];
           const int low = 32 * (warp & 3);
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 2; ++q) {
             const int c0 = 64 * part + 32 * q;  // against this warp's rows: one kind
-            uint32_t* to = w + 16 * q;
+            uint32_t to[16];
             if (rev ? c0 < low : c0 > low) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) to[j] = 0;
-              continue;
-            }
-            float x[32];
-            tmem_ld32(at_p + c0, x);
-            if (c0 == low) {
-              const float* f = near + 31 + (rev ? -lane : lane);
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                to[j] = rev ? pack_bf16(x[2 * j] * f[2 * j], x[2 * j + 1] * f[2 * j + 1])
-                            : pack_bf16(x[2 * j] * f[-2 * j], x[2 * j + 1] * f[-2 * j - 1]);
             } else {
+              float x[32];
+              tmem_ld32(at_p + c0, x);
+              if (c0 == low) {
+                const float* f = near + 31 + (rev ? -lane : lane);
 #pragma unroll
-              for (int blk = 0; blk < 2; ++blk) {
-                const int j0 = c0 + 16 * blk;
-                const float f = intra * power(rev ? j0 - row : row - j0 - 15);
-                const f32x2 f2 = pack2(f, f);
+                for (int j = 0; j < 16; ++j)
+                  to[j] = rev ? pack_bf16(x[2 * j] * f[2 * j], x[2 * j + 1] * f[2 * j + 1])
+                              : pack_bf16(x[2 * j] * f[-2 * j], x[2 * j + 1] * f[-2 * j - 1]);
+              } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const float2 z = unpack2(mul2(pack2(x[16 * blk + 2 * j], x[16 * blk + 2 * j + 1]),
-                                                mul2(f2, table[j])));
-                  to[8 * blk + j] = pack_bf16(z.x, z.y);
+                for (int blk = 0; blk < 2; ++blk) {
+                  const int j0 = c0 + 16 * blk;
+                  const float f = intra * power(rev ? j0 - row : row - j0 - 15);
+                  const f32x2 f2 = pack2(f, f);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    const float2 z =
+                        unpack2(mul2(pack2(x[16 * blk + 2 * j], x[16 * blk + 2 * j + 1]),
+                                     mul2(f2, table[j])));
+                    to[8 * blk + j] = pack_bf16(z.x, z.y);
+                  }
                 }
               }
             }
+            tmem_st16(at_p + 64 * part + 16 * q, to);
           }
-          tmem_st32(at_p + 64 * part, w);
           tmem_st_wait();
           tc_fence_before();
           arrive_warp(ctl, L::kPReady + ps);
@@ -591,7 +590,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
         if (state_row) {
           const float lost = expm1f(it.g * (float)Chunk(it, p, 0).have);
           const float* X = p.states + (it.bh * p.runs + it.run) * p.m * p.dv + row;
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < M / 64; ++q) {
             const int cb = part * (M / 64) + q;
             float x[32];
@@ -619,7 +618,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
         wait_warp(ctl, L::kD, c);
         wait_warp(ctl, L::kB, c);
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < N / 64; ++q) {
           const int col = 32 * (part * (N / 64) + q);
           float x[32], y[32];
@@ -663,7 +662,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
           ++carried;
           tc_fence_after();
           if (state_row) {
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < M / 64; ++q) {
               const int cb = part * (M / 64) + q;
               float x[32];
@@ -829,15 +828,16 @@ bool heads_map(CUtensorMap* map, const void* x, const falcon_strides& s, int64_t
 
 template <int M, int N>
 cudaError_t run_tc(const TcArgs& a, const TcMaps& maps, bool reads, cudaStream_t stream) {
-  static std::atomic<uint64_t> allowed[2];
+  static std::atomic<uint64_t> allowed[3];
+  const auto read = a.p.rev ? decay_read_tc<M, N, true> : decay_read_tc<M, N, false>;
   const unsigned grid = (unsigned)(a.items < kDecayTcBlocks ? a.items : kDecayTcBlocks);
   constexpr int ss = StatePlan<M, N>::kBytes, rs = ReadPlan<M, N>::kBytes;
   static_assert(ss + 1024 <= 232448 && rs + 1280 <= 232448, "shared memory of a block");
-  cudaError_t e = reads ? allow_shared(decay_read_tc<M, N>, rs, &allowed[0])
-                        : allow_shared(decay_states_tc<M, N>, ss, &allowed[1]);
+  cudaError_t e = reads ? allow_shared(read, rs, &allowed[a.p.rev])
+                        : allow_shared(decay_states_tc<M, N>, ss, &allowed[2]);
   if (e != cudaSuccess) return e;
   if (reads)
-    decay_read_tc<M, N><<<grid, kReadThreads, rs, stream>>>(a, maps);
+    read<<<grid, kReadThreads, rs, stream>>>(a, maps);
   else
     decay_states_tc<M, N><<<grid, kStateThreads, ss, stream>>>(a, maps);
   return cudaGetLastError();
