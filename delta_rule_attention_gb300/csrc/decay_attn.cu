@@ -95,7 +95,9 @@ __global__ void __launch_bounds__(kThreads)
 // would repeat itself run after run (expm1 keeps it relative to what is lost).
 constexpr int kAhead = 8;
 __global__ void __launch_bounds__(kThreads)
-    decay_join_kernel(const __grid_constant__ DecayPass a) {
+    decay_join_kernel(const __grid_constant__ DecayPass a, int parts) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t size = (int64_t)a.m * a.dv;
   const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (at >= a.B * a.H * size) return;
@@ -105,17 +107,21 @@ __global__ void __launch_bounds__(kThreads)
   const float g = decay_rate(a.log_decay, (int)(bh % a.H));
   const int64_t seat = bh * size + (int64_t)i * a.si + (int64_t)j * a.sj;
   float X = a.S_init ? a.S_init[seat] : 0.f;
-  float* st = a.states + bh * a.runs * size + e;
+  float* st = a.states + bh * a.runs * parts * size + e;
+  const int64_t step = parts * size;
   for (int s0 = 0; s0 < a.runs; s0 += kAhead) {
     float U[kAhead];
 #pragma unroll
     for (int s = 0; s < kAhead; ++s)
-      if (s0 + s < a.runs) U[s] = st[(a.rev ? a.runs - 1 - s0 - s : s0 + s) * size];
+      if (s0 + s < a.runs) {
+        const float* from = st + (a.rev ? a.runs - 1 - s0 - s : s0 + s) * step;
+        U[s] = parts == 2 ? from[0] + from[size] : from[0];
+      }
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
       if (s0 + s >= a.runs) break;
       const int r = a.rev ? a.runs - 1 - s0 - s : s0 + s;
-      st[r * size] = X;
+      st[r * step] = X;
       const float len = (float)run_tokens(n, r, a.run_len);
       X = fmaf(expm1f(g * len), X, X) + U[s];
     }
@@ -291,7 +297,7 @@ DecayPass shape_pass(const falcon_decay_shape& s, int m, int dv, bool tc) {
 // Room for either path: which one a pass takes goes by its pointers and strides too.
 size_t pass_bytes(const falcon_decay_shape& s) {
   const int runs[2] = {shape_pass(s, s.m, s.dv, false).runs, shape_pass(s, s.m, s.dv, true).runs};
-  const size_t most = (size_t)(runs[0] > runs[1] ? runs[0] : runs[1]);
+  const size_t most = (size_t)(runs[0] > 2 * runs[1] ? runs[0] : 2 * runs[1]);
   return ((size_t)s.B * s.H * most * s.m * s.dv * 4 + 255) / 256 * 256;
 }
 
@@ -310,7 +316,7 @@ cudaError_t run_pass(DecayPass& p, cudaStream_t stream) {
   const unsigned grid = (unsigned)(bh * p.runs);
   const unsigned vt = (unsigned)ceil_div(p.dv, kTile), mt = (unsigned)ceil_div(p.m, kTile);
   if (p.runs > 0) decay_states_kernel<E><<<dim3(grid, mt * vt), kThreads, 0, stream>>>(p);
-  cudaError_t e = launch_decay_join(p, stream);
+  cudaError_t e = launch_decay_join(p, 1, false, stream);
   if (e != cudaSuccess) return e;
   if (p.runs > 0) {
     e = allow_shared(decay_read_kernel<E>, sizeof(ReadSmem), &allowed);
@@ -320,23 +326,24 @@ cudaError_t run_pass(DecayPass& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// A pass with its tensors set: on the tensor cores where they fit.
-cudaError_t any_pass(const falcon_decay_shape& s, DecayPass p, cudaStream_t stream) {
+// A pass with its tensors set, on the tensor cores; false where they do not fit.
+bool tc_pass(const falcon_decay_shape& s, DecayPass p, cudaError_t* e, cudaStream_t stream) {
   const DecayPass split = shape_pass(s, p.m, p.dv, true);
   p.runs = split.runs, p.run_len = split.run_len;
-  cudaError_t e = cudaSuccess;
-  if (decay_tc_pass(p, &e, stream)) return e;
-  const DecayPass other = shape_pass(s, p.m, p.dv, false);
-  p.runs = other.runs, p.run_len = other.run_len;
+  return decay_tc_pass(p, e, stream);
+}
+cudaError_t simt_pass(const falcon_decay_shape& s, DecayPass p, cudaStream_t stream) {
+  const DecayPass split = shape_pass(s, p.m, p.dv, false);
+  p.runs = split.runs, p.run_len = split.run_len;
   return p.dtype == FALCON_BF16 ? run_pass<__nv_bfloat16>(p, stream) : run_pass<float>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_decay_join(const DecayPass& p, cudaStream_t stream) {
+cudaError_t launch_decay_join(const DecayPass& p, int parts, bool early, cudaStream_t stream) {
   const int64_t elements = p.B * p.H * p.m * p.dv;
-  decay_join_kernel<<<(unsigned)ceil_div(elements, kThreads), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_behind(early, decay_join_kernel, (unsigned)ceil_div(elements, kThreads), kThreads,
+                       0, stream, p, parts);
 }
 
 size_t decay_workspace_bytes(const falcon_decay_shape& s, bool) { return pass_bytes(s); }
@@ -350,7 +357,10 @@ cudaError_t launch_decay_fwd(const DecayCall& c, cudaStream_t stream) {
   p.si = c.s.dv, p.sj = 1;
   p.inter = c.s.scale, p.w = 1.f;
   p.states = static_cast<float*>(c.ws);
-  return any_pass(c.s, p, stream);
+  p.sums = true, p.behind_reads = true;
+  p.xi = c.s.dv, p.xj = 1;
+  cudaError_t e = cudaSuccess;
+  return tc_pass(c.s, p, &e, stream) ? e : simt_pass(c.s, p, stream);
 }
 
 cudaError_t launch_decay_bwd(const DecayCall& c, cudaStream_t stream) {
@@ -364,23 +374,36 @@ cudaError_t launch_decay_bwd(const DecayCall& c, cudaStream_t stream) {
   p.S_init = c.S0;
   p.si = 1, p.sj = dv;
   p.inter = c.s.scale, p.w = 1.f;
-  cudaError_t e = any_pass(c.s, p, stream);
-  if (e != cudaSuccess) return e;
-  // dk = G_t v_t, backward in time with (v, dO, q)
-  p.rev = 1;
-  p.q = c.v, p.k = c.dO, p.v = c.q, p.o = c.dk;
-  p.qs = c.vs, p.ks = c.dos, p.vs = c.qs, p.os = c.dks;
-  p.S_init = c.dS_T;
-  p.inter = 1.f, p.w = c.s.scale;
-  e = any_pass(c.s, p, stream);
+  p.sums = true, p.behind_reads = true;
+  p.xi = m, p.xj = 1;
+  cudaError_t e = cudaSuccess;
+  const bool behind = tc_pass(c.s, p, &e, stream);
+  if (!behind) e = simt_pass(c.s, p, stream);
   if (e != cudaSuccess) return e;
   // dv = G_t^T k_t, backward in time with (k, q, dO)
+  p.rev = 1;
   p.m = m, p.dv = dv;
   p.q = c.k, p.k = c.q, p.v = c.dO, p.o = c.dv;
   p.qs = c.ks, p.ks = c.qs, p.vs = c.dos, p.os = c.dvs;
-  p.S_out = c.dS0;
+  p.S_init = c.dS_T, p.S_out = c.dS0;
   p.si = dv, p.sj = 1;
-  return any_pass(c.s, p, stream);
+  p.inter = 1.f, p.w = c.s.scale;
+  p.xi = dv, p.xj = 1;
+  p.behind_states = behind;
+  const bool kept = tc_pass(c.s, p, &e, stream);  // its states serve dk too
+  if (!kept) e = simt_pass(c.s, p, stream);
+  if (e != cudaSuccess) return e;
+  // dk = G_t v_t, backward in time with (v, dO, q)
+  p.m = dv, p.dv = m;
+  p.q = c.v, p.k = c.dO, p.v = c.q, p.o = c.dk;
+  p.qs = c.vs, p.ks = c.dos, p.vs = c.qs, p.os = c.dks;
+  p.S_out = nullptr;
+  p.si = 1, p.sj = dv;
+  p.behind_states = kept;
+  if (kept) p.sums = false, p.xi = 1, p.xj = dv;
+  if (tc_pass(c.s, p, &e, stream)) return e;
+  p.sums = true;
+  return simt_pass(c.s, p, stream);
 }
 
 }  // namespace falcon

@@ -51,7 +51,8 @@ struct TcArgs {
   int qh, qb, kh, kb, vh, vb;
 };
 struct TcMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v;    // boxes of 128 tokens
+  CUtensorMap ks, vs;     // of the states' chunks
 };
 
 // Barriers of a block.  A wait that gave up sets `fail`, after which nobody waits.
@@ -84,17 +85,27 @@ __device__ __forceinline__ void arrive_warp(Control<BARS>& c, int which) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(&c.bar[which]);
 }
 
-// a and b as sums of two or three bf16 terms; three keep all 24 bits.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& mid) {
-  hi = pack_bf16(a, b);
-  mid = pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
+// a and b (of x) as sums of two or three bf16 terms.  All but the last of two are cut
+// off, not rounded: each takes 8 of the 24 bits, so that three are exact.
+__device__ __forceinline__ uint32_t upper_halves(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid,
-                                       uint32_t& lo) {
-  hi = pack_bf16(a, b);
-  const float ra = a - bf16_lo(hi), rb = b - bf16_hi(hi);
-  mid = pack_bf16(ra, rb);
-  lo = pack_bf16(ra - bf16_lo(mid), rb - bf16_hi(mid));
+__device__ __forceinline__ float2 rest_of(float2 x) {
+  const f32x2 cut = pack2(-__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
+                          -__uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
+  return unpack2(add2(pair2(x), cut));
+}
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& mid) {
+  hi = upper_halves(x.x, x.y);
+  const float2 r = rest_of(x);
+  mid = pack_bf16(r.x, r.y);
+}
+__device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = upper_halves(x.x, x.y);
+  const float2 r = rest_of(x);
+  mid = upper_halves(r.x, r.y);
+  const float2 q = rest_of(r);
+  lo = upper_halves(q.x, q.y);
 }
 
 // 16-byte chunk c of row r of a swizzled tile.
@@ -102,46 +113,46 @@ __device__ __forceinline__ unsigned char* chunk_of(unsigned char* tile, int r, i
   return tile + r * 128 + ((c ^ (r & 7)) << 4);
 }
 
-// Half of row r of the keys times w: the first term, in place or elsewhere, and those
-// behind it.
-template <int ATOMS, int TERMS>
+// CHUNKS 16-byte chunks from `first` on of row r of every 64 keys, times w: the first
+// term, in place or elsewhere, and those behind it.  Tiles are TILE bytes apart.
+template <int ATOMS, int TERMS, int CHUNKS, uint32_t TILE>
 __device__ __forceinline__ void weigh_keys(unsigned char* k, unsigned char* hi,
-                                           unsigned char* mid, unsigned char* lo, int r, int half,
-                                           float w) {
+                                           unsigned char* mid, unsigned char* lo, int r,
+                                           int first, float w) {
+  const f32x2 w2 = pack2(w, w);
 #pragma unroll 1
   for (int at = 0; at < ATOMS; ++at)
 #pragma unroll 2
-    for (int cc = 0; cc < 4; ++cc) {
-      const int c = 4 * half + cc;
-      const uint4 x = *reinterpret_cast<const uint4*>(chunk_of(k + at * kTile, r, c));
+    for (int cc = 0; cc < CHUNKS; ++cc) {
+      const int c = first + cc;
+      const uint4 x = *reinterpret_cast<const uint4*>(chunk_of(k + at * TILE, r, c));
       const uint32_t in[4] = {x.x, x.y, x.z, x.w};
       uint32_t t[3][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float a = bf16_lo(in[e]) * w, b = bf16_hi(in[e]) * w;
+        const float2 y = unpack2(mul2(pack2(bf16_lo(in[e]), bf16_hi(in[e])), w2));
         if constexpr (TERMS == 3)
-          split3(a, b, t[0][e], t[1][e], t[2][e]);
+          split3(y, t[0][e], t[1][e], t[2][e]);
         else
-          split2(a, b, t[0][e], t[1][e]);
+          split2(y, t[0][e], t[1][e]);
       }
-      *reinterpret_cast<uint4*>(chunk_of(hi + at * kTile, r, c)) =
+      *reinterpret_cast<uint4*>(chunk_of(hi + at * TILE, r, c)) =
           make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]);
-      *reinterpret_cast<uint4*>(chunk_of(mid + at * kTile, r, c)) =
+      *reinterpret_cast<uint4*>(chunk_of(mid + at * TILE, r, c)) =
           make_uint4(t[1][0], t[1][1], t[1][2], t[1][3]);
       if constexpr (TERMS == 3)
-        *reinterpret_cast<uint4*>(chunk_of(lo + at * kTile, r, c)) =
+        *reinterpret_cast<uint4*>(chunk_of(lo + at * TILE, r, c)) =
             make_uint4(t[2][0], t[2][1], t[2][2], t[2][3]);
     }
 }
 
-template <int ATOMS>
-__device__ __forceinline__ void clear_row(unsigned char* tile, int r, int half) {
+template <int ATOMS, int CHUNKS = 4, uint32_t TILE = kTile>
+__device__ __forceinline__ void clear_row(unsigned char* tile, int r, int first) {
 #pragma unroll 1
   for (int at = 0; at < ATOMS; ++at)
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint4*>(chunk_of(tile + at * kTile, r, 4 * half + c)) =
-          make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < CHUNKS; ++c)
+      *reinterpret_cast<uint4*>(chunk_of(tile + at * TILE, r, first + c)) = make_uint4(0, 0, 0, 0);
 }
 
 // The issuing warp stays together (what it computes is then the same in all lanes, and
@@ -177,12 +188,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, 
       : "memory");
 }
 
-// D (+)= A^T B over the 128 tokens of tiles [token][channel]; N channels of B.
-template <int N>
+// D (+)= A^T B over the C tokens of tiles [token][channel]; N channels of B.
+template <int N, int C = kC>
 __device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
-  const uint32_t da = desc_low(a, kTile), db = desc_low(b, kTile);
+  const uint32_t da = desc_low(a, C * 128), db = desc_low(b, C * 128);
 #pragma unroll
-  for (int ks = 0; ks < kC / 16; ++ks)
+  for (int ks = 0; ks < C / 16; ++ks)
     mma_ss(d, da + ks * kStepMN, db + ks * kStepMN, idesc_bf16(128, N, true, true),
            accumulate || ks > 0);
 }
@@ -193,9 +204,10 @@ struct Item {
   int run, b, h, n, first, end, chunks;  // chunks that hold tokens
   float g;
   __device__ __forceinline__ Item(const DecayPass& p, int item) {
-    run = item % p.runs;
-    bh = item / p.runs;
-    b = (int)(bh / p.H), h = (int)(bh % p.H);
+    const unsigned head = (unsigned)item / (unsigned)p.runs, heads = (unsigned)p.H;
+    run = item - (int)head * p.runs;
+    bh = head;
+    b = (int)(head / heads), h = (int)(head - b * heads);
     n = (int)row_length(p.lengths, b, p.T);
     first = (int)(run * p.run_len);
     end = (int)(first + p.run_len < p.T ? first + p.run_len : p.T);
@@ -207,43 +219,47 @@ struct Item {
 
 // ---- states -----------------------------------------------------------------
 // D[value][key] = V^T (Diag(w) K), so that the three terms of a key share a thread's
-// lane.  A product of 128 rows costs at least 64 cycles for its A operand's bytes, however
-// few columns it has: with 64 keys the terms lie side by side and one product of 192
-// columns takes them all.
+// lane.  Shared memory's bandwidth is what these products take (4 KB of A and 32 bytes a
+// column of B for 16 tokens): terms lie side by side and one product takes as many of them
+// as it can, all three with 64 keys, the smaller two with 128.
 //
 // The tensor cores add into an accumulator without rounding to nearest: over a long run
 // the error grows with the number of additions (1.3e-5 of a state of 65536 tokens at a rate
 // of 2^-12).  So sums are taken out after every chunk and added in registers; with 128
 // keys only the first term's, the other two, smaller by 2^8 and 2^16, stay in TMEM for
 // the whole run.
+//
+// Two sets of eight warps take chunks in turn: while one waits for its products the
+// other weighs and splits keys.
 template <int M, int N>
 struct StatePlan {
-  static constexpr bool kSide = M == 64;  // terms side by side
+  static constexpr bool kSide = M == 64;        // terms side by side
+  static constexpr int kTokens = kSide ? 128 : 64;  // of a chunk here
+  static constexpr uint32_t kTile = kTokens * 128;
   static constexpr uint32_t kK = M / 64 * kTile, kV = N / 64 * kTile;
-  static constexpr int kStages = M + N == 128 ? 4 : 2;
-  static constexpr int kTerms = kSide ? 2 : 1;  // buffers for the terms
-  static constexpr uint32_t kT = (kSide ? 3 : 2) * kK;
+  static constexpr int kStages = M + N == 192 && kSide ? 2 : 4;
+  static constexpr uint32_t kT = (kSide ? 3 : 2) * kK;  // a set's terms
   static constexpr uint32_t V = 0, K = kStages * kV, T = K + kStages * kK;
-  static constexpr uint32_t kBytes = T + kTerms * kT + 1024;
-  // TMEM columns: two sums, and with 128 keys the smaller terms'
+  static constexpr uint32_t kBytes = T + 2 * kT + 1024;
+  // TMEM columns: a sum a set, and with 128 keys the smaller terms' two
   static constexpr uint32_t kSumCols = kSide ? 3 * M : M, kCols = 512;
-  static constexpr int kFull = 0, kEmpty = kStages, kSplit = 2 * kStages,
-                       kSplitFree = kSplit + 2, kSum = kSplit + 4, kSumFree = kSplit + 6,
-                       kBars = kSplit + 8;
+  static constexpr int kFull = 0, kEmpty = kStages, kSplit = 2 * kStages, kSum = kSplit + 2,
+                       kSumFree = kSplit + 4, kBars = kSplit + 6;
 };
 
 // Chunks [from, to) of a run whose weights are not all zero in fp32 (e^-104 is).
+template <int C>
 __device__ __forceinline__ void weighed_chunks(const Item& it, bool rev, int len, int* from,
                                                int* to) {
-  *from = 0, *to = it.chunks;
+  *from = 0, *to = (len + C - 1) / C;
   if (!(it.g < 0.f)) return;
   const float reach = -104.f / it.g;
   if (!(reach < (float)len)) return;
   const int tokens = (int)reach + 2;
   if (rev)
-    *to = min(it.chunks, (tokens + kC - 1) / kC);
+    *to = min(*to, (tokens + C - 1) / C);
   else
-    *from = max(0, len - tokens) / kC;
+    *from = max(0, len - tokens) / C;
 }
 
 template <int M, int N>
@@ -259,8 +275,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     for (int i = 0; i < L::kStages; ++i)
       mbar_init(&ctl.bar[L::kFull + i], 1), mbar_init(&ctl.bar[L::kEmpty + i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.bar[L::kSplit + i], 8), mbar_init(&ctl.bar[L::kSplitFree + i], 1);
-      mbar_init(&ctl.bar[L::kSum + i], 1), mbar_init(&ctl.bar[L::kSumFree + i], 8);
+      mbar_init(&ctl.bar[L::kSplit + i], 8), mbar_init(&ctl.bar[L::kSum + i], 1);
+      mbar_init(&ctl.bar[L::kSumFree + i], 8);
     }
     ctl.fail = 0;
     fence_mbar_init();
@@ -270,47 +286,48 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0), base = smem_addr(sm);
+  constexpr int C = L::kTokens;
+  // behind the pass before, which reads the states that this one writes
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   int c = 0;  // chunks of all items so far
   for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
     const Item it(p, item);
     const int len = max(min(it.n, it.end) - it.first, 0);
     int from, to;
-    weighed_chunks(it, p.rev, len, &from, &to);
-    if (warp < 8) {
-      // weighs and splits the keys
-      const int r = tid & (kC - 1), half = warp >> 2;
-      for (int k = from; k < to; ++k, ++c) {
-        const int s = c % L::kStages, t = c % L::kTerms;
-        const int at = k * kC + r;
-        const float w = p.w * decay_power(it.g, (float)(p.rev ? at + 1 : len - 1 - at));
-        unsigned char* key = sm + L::K + s * L::kK;
-        unsigned char* terms = sm + L::T + t * L::kT;
-        unsigned char* hi = L::kSide ? terms : key;
-        unsigned char* mid = L::kSide ? terms + L::kK : terms;
-        wait_warp(ctl, L::kFull + s, c / L::kStages);
-        if (c >= L::kTerms) wait_warp(ctl, L::kSplitFree + t, c / L::kTerms - 1);
-        if (at < len) {
-          weigh_keys<M / 64, 3>(key, hi, mid, mid + L::kK, r, half, w);
-        } else {  // rows that the sequence does not hold
-          clear_row<M / 64>(hi, r, half);
-          clear_row<M / 64>(mid, r, half);
-          clear_row<M / 64>(mid + L::kK, r, half);
-          clear_row<N / 64>(sm + L::V + s * L::kV, r, half);
-        }
-        fence_async_smem();
-        arrive_warp(ctl, L::kSplit + t);
-      }
-    } else if (warp < 16) {
-      // adds up the first term's sums, and writes the run's state
-      constexpr int kOwn = M / 2;
+    weighed_chunks<C>(it, p.rev, len, &from, &to);
+    if (warp < 16) {
+      const int set = warp >> 3;
+      constexpr int kOwn = M / 2;  // keys of a thread's sums
       const int j = 32 * (warp & 3) + lane, i0 = (warp >> 2 & 1) * kOwn;
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+      // a row of the keys, and the 16-byte chunks of it that this thread splits
+      constexpr int kChunks = 8 * C / 256;
+      const int r = tid & (C - 1), first = (tid & 255) / C * kChunks;
       float sum[kOwn];
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) sum[i] = 0.f;
       for (int k = from; k < to; ++k, ++c) {
-        wait_warp(ctl, L::kSum + (c & 1), c >> 1);
+        if ((c & 1) != set) continue;
+        const int s = c % L::kStages, at = k * C + r;
+        const float w = p.w * decay_power(it.g, (float)(p.rev ? at + 1 : len - 1 - at));
+        unsigned char* key = sm + L::K + s * L::kK;
+        unsigned char* terms = sm + L::T + set * L::kT;
+        unsigned char* hi = L::kSide ? terms : key;
+        unsigned char* mid = L::kSide ? terms + L::kK : terms;
+        wait_warp(ctl, L::kFull + s, c / L::kStages);
+        if (at < len) {
+          weigh_keys<M / 64, 3, kChunks, L::kTile>(key, hi, mid, mid + L::kK, r, first, w);
+        } else {  // rows that the sequence does not hold
+          clear_row<M / 64, kChunks, L::kTile>(hi, r, first);
+          clear_row<M / 64, kChunks, L::kTile>(mid, r, first);
+          clear_row<M / 64, kChunks, L::kTile>(mid + L::kK, r, first);
+          clear_row<N / 64, kChunks, L::kTile>(sm + L::V + s * L::kV, r, first);
+        }
+        fence_async_smem();
+        arrive_warp(ctl, L::kSplit + set);
+        wait_warp(ctl, L::kSum + set, c >> 1);
         tc_fence_after();
         auto add = [&](uint32_t col) {
 #pragma unroll
@@ -323,16 +340,18 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         };
         // the smallest first
         if constexpr (L::kSide) {
-          add((c & 1) * L::kSumCols + 2 * M);
-          add((c & 1) * L::kSumCols + M);
+          add(set * L::kSumCols + 2 * M);
+          add(set * L::kSumCols + M);
         } else if (k + 1 == to) {
+          add(2 * L::kSumCols + M);
           add(2 * L::kSumCols);
         }
-        add((c & 1) * L::kSumCols);
+        add(set * L::kSumCols);
         tc_fence_before();
-        arrive_warp(ctl, L::kSumFree + (c & 1));
+        arrive_warp(ctl, L::kSumFree + set);
       }
-      float* out = p.states + (it.bh * p.runs + it.run) * p.m * p.dv + j;
+      // each set's sums are a state of their own, which the join adds
+      float* out = p.states + ((it.bh * p.runs + it.run) * 2 + set) * p.m * p.dv + j;
       if (j < p.dv) {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i)
@@ -340,41 +359,39 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       }
     } else if (warp == kLoader) {
       for (int k = from; k < to; ++k, ++c) {
-        const int s = c % L::kStages, t = it.first + k * kC;
+        const int s = c % L::kStages, t = it.first + k * C;
         if (lane != 0) continue;
         if (c >= L::kStages) wait(ctl, L::kEmpty + s, c / L::kStages - 1);
         uint64_t* bar = &ctl.bar[L::kFull + s];
         mbar_expect_tx(bar, L::kK + L::kV);
 #pragma unroll
         for (int i = 0; i < M / 64; ++i)
-          tma_load_4d(sm + L::K + s * L::kK + i * kTile, &maps.k, 64 * i, t, it.h * a.kh,
+          tma_load_4d(sm + L::K + s * L::kK + i * L::kTile, &maps.ks, 64 * i, t, it.h * a.kh,
                       it.b * a.kb, bar);
 #pragma unroll
         for (int i = 0; i < N / 64; ++i)
-          tma_load_4d(sm + L::V + s * L::kV + i * kTile, &maps.v, 64 * i, t, it.h * a.vh,
+          tma_load_4d(sm + L::V + s * L::kV + i * L::kTile, &maps.vs, 64 * i, t, it.h * a.vh,
                       it.b * a.vb, bar);
       }
     } else {
       for (int k = from; k < to; ++k, ++c) {
-        const int s = c % L::kStages, t = c % L::kTerms;
-        wait_warp(ctl, L::kSplit + t, c / L::kTerms);
-        if (c >= 2) wait_warp(ctl, L::kSumFree + (c & 1), (c >> 1) - 1);
-        // the smaller terms' sums of the run before have been read
-        if (k == from && c >= 1) wait_warp(ctl, L::kSumFree + ((c - 1) & 1), (c - 1) >> 1);
+        const int s = c % L::kStages, set = c & 1;
+        wait_warp(ctl, L::kSplit + set, c >> 1);
+        // the sums of all chunks before have been read: a set's own by its order, the
+        // smaller terms' of the run before by this
+        if (k == from && c >= 1) wait_warp(ctl, L::kSumFree + (set ^ 1), (c - 1) >> 1);
         tc_fence_after();
-        const uint32_t v = base + L::V + s * L::kV, terms = base + L::T + t * L::kT;
-        const uint32_t d = tmem + (c & 1) * L::kSumCols;
+        const uint32_t v = base + L::V + s * L::kV, terms = base + L::T + set * L::kT;
+        const uint32_t d = tmem + set * L::kSumCols;
         if (elect_one()) {
           if constexpr (L::kSide) {
-            mma_tokens<3 * M>(d, v, terms, false);
+            mma_tokens<3 * M, C>(d, v, terms, false);
           } else {
-            mma_tokens<M>(d, v, base + L::K + s * L::kK, false);
-            mma_tokens<M>(tmem + 2 * L::kSumCols, v, terms, k > from);
-            mma_tokens<M>(tmem + 2 * L::kSumCols, v, terms + L::kK, true);
+            mma_tokens<M, C>(d, v, base + L::K + s * L::kK, false);
+            mma_tokens<2 * M, C>(tmem + 2 * L::kSumCols, v, terms, k > from);
           }
           mma_commit(&ctl.bar[L::kEmpty + s]);
-          mma_commit(&ctl.bar[L::kSplitFree + t]);
-          mma_commit(&ctl.bar[L::kSum + (c & 1)]);
+          mma_commit(&ctl.bar[L::kSum + set]);
         }
         __syncwarp();
       }
@@ -457,7 +474,10 @@ __global__ void __launch_bounds__(kReadThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0), base = smem_addr(sm);
-  const int row = 32 * (warp & 3) + lane;  // TMEM lane: a token, or a key
+  // behind the join; inputs that are read before were written before this pass began
+  if (warp >= 8 && warp < 16) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int row = 32 * (warp & 3) + lane;  // TMEM lane: a token, or a value
   const int part = warp >> 2 & 1;          // half of the columns
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
 
@@ -493,9 +513,9 @@ __global__ void __launch_bounds__(kReadThreads, 1)
           wait_warp(ctl, L::kFullK + ks, c / L::kKs);
           wait_warp(ctl, L::kFullV + ks, c / L::kKs);
           if (row >= ch.have) {
-            clear_row<M / 64>(sm + L::Q + qs * L::kQ, row, part);
-            clear_row<M / 64>(key, row, part);
-            clear_row<N / 64>(sm + L::V + ks * L::kV, row, part);
+            clear_row<M / 64>(sm + L::Q + qs * L::kQ, row, 4 * part);
+            clear_row<M / 64>(key, row, 4 * part);
+            clear_row<N / 64>(sm + L::V + ks * L::kV, row, 4 * part);
           }
           fence_async_smem();
           arrive_warp(ctl, L::kClear + (cleared++ & 3));
@@ -546,8 +566,9 @@ __global__ void __launch_bounds__(kReadThreads, 1)
         if (more) {
           const float w = p.w * power(rev ? row + 1 : max(ch.have - 1 - row, 0));
           if (carried > 0) wait_warp(ctl, L::kC_, carried - 1);  // the second terms are free
-          weigh_keys<M / 64, 2>(key, L::kSide ? sm + L::Lo : key,
-                                L::kSide ? sm + L::Lo + L::kK : sm + L::Lo, nullptr, row, part, w);
+          weigh_keys<M / 64, 2, 4, kTile>(key, L::kSide ? sm + L::Lo : key,
+                                          L::kSide ? sm + L::Lo + L::kK : sm + L::Lo, nullptr,
+                                          row, 4 * part, w);
           fence_async_smem();
           arrive_warp(ctl, L::kKReady);
           ++carried;
@@ -589,7 +610,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
       if (it.chunks > 0) {
         if (state_row) {
           const float lost = expm1f(it.g * (float)Chunk(it, p, 0).have);
-          const float* X = p.states + (it.bh * p.runs + it.run) * p.m * p.dv + row;
+          const float* X = p.states + (it.bh * p.runs + it.run) * 2 * p.m * p.dv + row * p.xj;
 #pragma unroll 1
           for (int q = 0; q < M / 64; ++q) {
             const int cb = part * (M / 64) + q;
@@ -597,7 +618,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int i = 32 * cb + j;
-              x[j] = i < p.m && row < p.dv ? X[i * p.dv] : 0.f;
+              x[j] = i < p.m && row < p.dv ? X[i * p.xi] : 0.f;
             }
             put_state(x, cb, lost);
           }
@@ -817,13 +838,13 @@ __global__ void __launch_bounds__(kReadThreads, 1)
 
 // ---- host -----------------------------------------------------------------------
 bool heads_map(CUtensorMap* map, const void* x, const falcon_strides& s, int64_t B, int64_t H,
-               int64_t T, int channels, int* by_head, int* by_row) {
+               int64_t T, int channels, int tokens, int* by_head, int* by_row) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(x);
   if (at % 16 || s.batch % 8 || s.head % 8 || s.time % 8 || (T > 1 && s.time == 0)) return false;
   const bool hs = H > 1 && s.head != 0, bs = B > 1 && s.batch != 0;
   *by_head = hs, *by_row = bs;
   return encode_heads_bf16(map, x, channels, T, hs ? H : 1, bs ? B : 1, s.time, s.head, s.batch,
-                           kC);
+                           tokens);
 }
 
 template <int M, int N>
@@ -836,11 +857,9 @@ cudaError_t run_tc(const TcArgs& a, const TcMaps& maps, bool reads, cudaStream_t
   cudaError_t e = reads ? allow_shared(read, rs, &allowed[a.p.rev])
                         : allow_shared(decay_states_tc<M, N>, ss, &allowed[2]);
   if (e != cudaSuccess) return e;
-  if (reads)
-    read<<<grid, kReadThreads, rs, stream>>>(a, maps);
-  else
-    decay_states_tc<M, N><<<grid, kStateThreads, ss, stream>>>(a, maps);
-  return cudaGetLastError();
+  return reads ? launch_behind(a.p.behind_reads, read, grid, kReadThreads, rs, stream, a, maps)
+               : launch_behind(a.p.behind_states, decay_states_tc<M, N>, grid, kStateThreads, ss,
+                               stream, a, maps);
 }
 
 cudaError_t run_tc_any(const TcArgs& a, const TcMaps& maps, bool reads, cudaStream_t stream) {
@@ -858,9 +877,13 @@ bool decay_tc_pass(const DecayPass& p, cudaError_t* status, cudaStream_t stream)
     return false;
   TcArgs a = {};
   TcMaps maps;
-  if (!heads_map(&maps.q, p.q, p.qs, p.B, p.H, p.T, p.m, &a.qh, &a.qb) ||
-      !heads_map(&maps.k, p.k, p.ks, p.B, p.H, p.T, p.m, &a.kh, &a.kb) ||
-      !heads_map(&maps.v, p.v, p.vs, p.B, p.H, p.T, p.dv, &a.vh, &a.vb) ||
+  const int sum_tokens =
+      p.m <= 64 ? StatePlan<64, 64>::kTokens : StatePlan<128, 64>::kTokens;
+  if (!heads_map(&maps.q, p.q, p.qs, p.B, p.H, p.T, p.m, kC, &a.qh, &a.qb) ||
+      !heads_map(&maps.k, p.k, p.ks, p.B, p.H, p.T, p.m, kC, &a.kh, &a.kb) ||
+      !heads_map(&maps.v, p.v, p.vs, p.B, p.H, p.T, p.dv, kC, &a.vh, &a.vb) ||
+      !heads_map(&maps.ks, p.k, p.ks, p.B, p.H, p.T, p.m, sum_tokens, &a.kh, &a.kb) ||
+      !heads_map(&maps.vs, p.v, p.vs, p.B, p.H, p.T, p.dv, sum_tokens, &a.vh, &a.vb) ||
       reinterpret_cast<uintptr_t>(p.o) % 16 || p.os.batch % 8 || p.os.head % 8 || p.os.time % 8)
     return false;
   a.p = p;
@@ -868,8 +891,8 @@ bool decay_tc_pass(const DecayPass& p, cudaError_t* status, cudaStream_t stream)
   a.wide_o = reinterpret_cast<uintptr_t>(p.o) % 32 == 0 && p.os.batch % 16 == 0 &&
              p.os.head % 16 == 0 && p.os.time % 16 == 0 && p.dv % 16 == 0;
   a.err = device_error_word_of_current();
-  *status = run_tc_any(a, maps, false, stream);
-  if (*status == cudaSuccess) *status = launch_decay_join(p, stream);
+  if (p.sums) *status = run_tc_any(a, maps, false, stream);
+  if (p.sums && *status == cudaSuccess) *status = launch_decay_join(p, 2, true, stream);
   if (*status == cudaSuccess) *status = run_tc_any(a, maps, true, stream);
   return true;
 }

@@ -27,10 +27,16 @@ struct DecayPass {
   int si, sj;
   float inter, w;
   // runs of tokens that are worked on by themselves: run_len tokens each (a multiple of
-  // the chunk), and a state [m, dv] for each, [B*H, runs, m, dv]
+  // the chunk), and a state for each, [B*H, runs, parts, m, dv]: what it adds, in one or
+  // two parts, then in the first part's place the state that enters it
   int64_t run_len;
   int runs;
   float* states;
+  // tensor-core passes: whether the states are formed (or taken as they are, key i and
+  // value j of one at i * xi + j * xj), and whether the kernels that form and read them
+  // may be set up while the kernel before them runs
+  bool sums, behind_states, behind_reads;
+  int xi, xj;
   bool vec_q, vec_k, vec_v, vec_o;  // quads of channels are one aligned access
 };
 

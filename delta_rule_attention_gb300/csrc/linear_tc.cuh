@@ -12,6 +12,25 @@ constexpr int kDecayTcChunk = 128;
 constexpr int kDecayTcBlocks = 152;  // one for each SM, each taking runs in turn
 // One pass, p.runs in chunks of kDecayTcChunk; false where the tensors do not fit it.
 bool decay_tc_pass(const DecayPass& p, cudaError_t* status, cudaStream_t stream);
-cudaError_t launch_decay_join(const DecayPass& p, cudaStream_t stream);
+// The join of states in `parts` parts; early: set up while the kernel before it runs.
+cudaError_t launch_decay_join(const DecayPass& p, int parts, bool early, cudaStream_t stream);
+
+// A launch that may be set up while the kernel before it on the stream runs (early): its
+// kernel waits for that one (griddepcontrol.wait) before it touches what that one writes
+// or reads.
+template <typename... P, typename... A>
+cudaError_t launch_behind(bool early, void (*kernel)(P...), unsigned grid, unsigned threads,
+                          size_t shared, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid), c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = shared;
+  c.stream = stream;
+  cudaLaunchAttribute attr[1] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
 
 }  // namespace falcon
