@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads)
 // would repeat itself run after run (expm1 keeps it relative to what is lost).
 constexpr int kAhead = 8;
 __global__ void __launch_bounds__(kThreads)
-    decay_join_kernel(const __grid_constant__ DecayPass a, int parts) {
+    decay_join_kernel(const __grid_constant__ DecayPass a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t size = (int64_t)a.m * a.dv;
@@ -107,21 +107,17 @@ __global__ void __launch_bounds__(kThreads)
   const float g = decay_rate(a.log_decay, (int)(bh % a.H));
   const int64_t seat = bh * size + (int64_t)i * a.si + (int64_t)j * a.sj;
   float X = a.S_init ? a.S_init[seat] : 0.f;
-  float* st = a.states + bh * a.runs * parts * size + e;
-  const int64_t step = parts * size;
+  float* st = a.states + bh * a.runs * size + e;
   for (int s0 = 0; s0 < a.runs; s0 += kAhead) {
     float U[kAhead];
 #pragma unroll
     for (int s = 0; s < kAhead; ++s)
-      if (s0 + s < a.runs) {
-        const float* from = st + (a.rev ? a.runs - 1 - s0 - s : s0 + s) * step;
-        U[s] = parts == 2 ? from[0] + from[size] : from[0];
-      }
+      if (s0 + s < a.runs) U[s] = st[(a.rev ? a.runs - 1 - s0 - s : s0 + s) * size];
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
       if (s0 + s >= a.runs) break;
       const int r = a.rev ? a.runs - 1 - s0 - s : s0 + s;
-      st[r * step] = X;
+      st[r * size] = X;
       const float len = (float)run_tokens(n, r, a.run_len);
       X = fmaf(expm1f(g * len), X, X) + U[s];
     }
@@ -297,7 +293,7 @@ DecayPass shape_pass(const falcon_decay_shape& s, int m, int dv, bool tc) {
 // Room for either path: which one a pass takes goes by its pointers and strides too.
 size_t pass_bytes(const falcon_decay_shape& s) {
   const int runs[2] = {shape_pass(s, s.m, s.dv, false).runs, shape_pass(s, s.m, s.dv, true).runs};
-  const size_t most = (size_t)(runs[0] > 2 * runs[1] ? runs[0] : 2 * runs[1]);
+  const size_t most = (size_t)(runs[0] > runs[1] ? runs[0] : runs[1]);
   return ((size_t)s.B * s.H * most * s.m * s.dv * 4 + 255) / 256 * 256;
 }
 
@@ -316,7 +312,7 @@ cudaError_t run_pass(DecayPass& p, cudaStream_t stream) {
   const unsigned grid = (unsigned)(bh * p.runs);
   const unsigned vt = (unsigned)ceil_div(p.dv, kTile), mt = (unsigned)ceil_div(p.m, kTile);
   if (p.runs > 0) decay_states_kernel<E><<<dim3(grid, mt * vt), kThreads, 0, stream>>>(p);
-  cudaError_t e = launch_decay_join(p, 1, false, stream);
+  cudaError_t e = launch_decay_join(p, false, stream);
   if (e != cudaSuccess) return e;
   if (p.runs > 0) {
     e = allow_shared(decay_read_kernel<E>, sizeof(ReadSmem), &allowed);
@@ -340,10 +336,10 @@ cudaError_t simt_pass(const falcon_decay_shape& s, DecayPass p, cudaStream_t str
 
 }  // namespace
 
-cudaError_t launch_decay_join(const DecayPass& p, int parts, bool early, cudaStream_t stream) {
+cudaError_t launch_decay_join(const DecayPass& p, bool early, cudaStream_t stream) {
   const int64_t elements = p.B * p.H * p.m * p.dv;
   return launch_behind(early, decay_join_kernel, (unsigned)ceil_div(elements, kThreads), kThreads,
-                       0, stream, p, parts);
+                       0, stream, p);
 }
 
 size_t decay_workspace_bytes(const falcon_decay_shape& s, bool) { return pass_bytes(s); }

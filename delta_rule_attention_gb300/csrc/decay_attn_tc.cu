@@ -225,26 +225,28 @@ struct Item {
 //
 // The tensor cores add into an accumulator without rounding to nearest: over a long run
 // the error grows with the number of additions (1.3e-5 of a state of 65536 tokens at a rate
-// of 2^-12).  So sums are taken out after every chunk and added in registers; with 128
-// keys only the first term's, the other two, smaller by 2^8 and 2^16, stay in TMEM for
-// the whole run.
+// of 2^-12).  So sums are taken out after every 256 tokens and added in registers; with
+// 128 keys only the first term's, the other two, smaller by 2^8 and 2^16, stay in TMEM
+// for the whole run.
 //
-// Two sets of eight warps take chunks in turn: while one waits for its products the
-// other weighs and splits keys.
+// Sixteen warps weigh and split the keys of a chunk while the products of the chunk before
+// run; the same warps take out the sums.
 template <int M, int N>
 struct StatePlan {
-  static constexpr bool kSide = M == 64;        // terms side by side
+  static constexpr bool kSide = M == 64;            // terms side by side
   static constexpr int kTokens = kSide ? 128 : 64;  // of a chunk here
+  static constexpr int kGroup = 256 / kTokens;      // chunks whose sums stay in TMEM
   static constexpr uint32_t kTile = kTokens * 128;
   static constexpr uint32_t kK = M / 64 * kTile, kV = N / 64 * kTile;
   static constexpr int kStages = M + N == 192 && kSide ? 2 : 4;
-  static constexpr uint32_t kT = (kSide ? 3 : 2) * kK;  // a set's terms
+  static constexpr uint32_t kT = (kSide ? 3 : 2) * kK;  // a chunk's terms
   static constexpr uint32_t V = 0, K = kStages * kV, T = K + kStages * kK;
   static constexpr uint32_t kBytes = T + 2 * kT + 1024;
-  // TMEM columns: a sum a set, and with 128 keys the smaller terms' two
+  // TMEM columns: two groups' sums, and with 128 keys the smaller terms' two
   static constexpr uint32_t kSumCols = kSide ? 3 * M : M, kCols = 512;
-  static constexpr int kFull = 0, kEmpty = kStages, kSplit = 2 * kStages, kSum = kSplit + 2,
-                       kSumFree = kSplit + 4, kBars = kSplit + 6;
+  static constexpr int kFull = 0, kEmpty = kStages, kSplit = 2 * kStages,
+                       kSplitFree = kSplit + 2, kSum = kSplit + 4, kSumFree = kSplit + 6,
+                       kBars = kSplit + 8;
 };
 
 // Chunks [from, to) of a run whose weights are not all zero in fp32 (e^-104 is).
@@ -275,8 +277,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     for (int i = 0; i < L::kStages; ++i)
       mbar_init(&ctl.bar[L::kFull + i], 1), mbar_init(&ctl.bar[L::kEmpty + i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.bar[L::kSplit + i], 8), mbar_init(&ctl.bar[L::kSum + i], 1);
-      mbar_init(&ctl.bar[L::kSumFree + i], 8);
+      mbar_init(&ctl.bar[L::kSplit + i], 16), mbar_init(&ctl.bar[L::kSplitFree + i], 1);
+      mbar_init(&ctl.bar[L::kSum + i], 1), mbar_init(&ctl.bar[L::kSumFree + i], 16);
     }
     ctl.fail = 0;
     fence_mbar_init();
@@ -291,32 +293,57 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  int c = 0;  // chunks of all items so far
+  int c = 0, group = 0;  // chunks, and groups of them, of all items so far
   for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
     const Item it(p, item);
     const int len = max(min(it.n, it.end) - it.first, 0);
     int from, to;
     weighed_chunks<C>(it, p.rev, len, &from, &to);
     if (warp < 16) {
-      const int set = warp >> 3;
-      constexpr int kOwn = M / 2;  // keys of a thread's sums
-      const int j = 32 * (warp & 3) + lane, i0 = (warp >> 2 & 1) * kOwn;
+      constexpr int kOwn = M / 4;  // keys of a thread's sums
+      const int j = 32 * (warp & 3) + lane, i0 = (warp >> 2) * kOwn;
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
       // a row of the keys, and the 16-byte chunks of it that this thread splits
-      constexpr int kChunks = 8 * C / 256;
-      const int r = tid & (C - 1), first = (tid & 255) / C * kChunks;
+      constexpr int kChunks = 8 * C / 512;
+      const int r = tid & (C - 1), first = tid / C * kChunks;
       float sum[kOwn];
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) sum[i] = 0.f;
+      auto add = [&](uint32_t col) {
+        float x[kOwn];
+        if constexpr (kOwn == 32)
+          tmem_ld32(tmem + lanes + col + i0, x);
+        else
+          tmem_ld16(tmem + lanes + col + i0, x);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) sum[i] += x[i];
+      };
+      auto take_out = [&](bool last) {
+        const int g = group & 1;
+        wait_warp(ctl, L::kSum + g, group >> 1);
+        ++group;
+        tc_fence_after();
+        // the smallest first
+        if constexpr (L::kSide) {
+          add(g * L::kSumCols + 2 * M);
+          add(g * L::kSumCols + M);
+        } else if (last) {
+          add(2 * L::kSumCols + M);
+          add(2 * L::kSumCols);
+        }
+        add(g * L::kSumCols);
+        tc_fence_before();
+        arrive_warp(ctl, L::kSumFree + g);
+      };
       for (int k = from; k < to; ++k, ++c) {
-        if ((c & 1) != set) continue;
-        const int s = c % L::kStages, at = k * C + r;
+        const int s = c % L::kStages, t = c & 1, at = k * C + r;
         const float w = p.w * decay_power(it.g, (float)(p.rev ? at + 1 : len - 1 - at));
         unsigned char* key = sm + L::K + s * L::kK;
-        unsigned char* terms = sm + L::T + set * L::kT;
+        unsigned char* terms = sm + L::T + t * L::kT;
         unsigned char* hi = L::kSide ? terms : key;
         unsigned char* mid = L::kSide ? terms + L::kK : terms;
         wait_warp(ctl, L::kFull + s, c / L::kStages);
+        if (c >= 2) wait_warp(ctl, L::kSplitFree + t, (c >> 1) - 1);
         if (at < len) {
           weigh_keys<M / 64, 3, kChunks, L::kTile>(key, hi, mid, mid + L::kK, r, first, w);
         } else {  // rows that the sequence does not hold
@@ -326,32 +353,11 @@ __global__ void __launch_bounds__(kStateThreads, 1)
           clear_row<N / 64, kChunks, L::kTile>(sm + L::V + s * L::kV, r, first);
         }
         fence_async_smem();
-        arrive_warp(ctl, L::kSplit + set);
-        wait_warp(ctl, L::kSum + set, c >> 1);
-        tc_fence_after();
-        auto add = [&](uint32_t col) {
-#pragma unroll
-          for (int q = 0; q < kOwn; q += 32) {
-            float x[32];
-            tmem_ld32(tmem + lanes + col + i0 + q, x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sum[q + i] += x[i];
-          }
-        };
-        // the smallest first
-        if constexpr (L::kSide) {
-          add(set * L::kSumCols + 2 * M);
-          add(set * L::kSumCols + M);
-        } else if (k + 1 == to) {
-          add(2 * L::kSumCols + M);
-          add(2 * L::kSumCols);
-        }
-        add(set * L::kSumCols);
-        tc_fence_before();
-        arrive_warp(ctl, L::kSumFree + set);
+        arrive_warp(ctl, L::kSplit + t);
+        if (k > from && (k - from) % L::kGroup == 0) take_out(false);  // the group before
       }
-      // each set's sums are a state of their own, which the join adds
-      float* out = p.states + ((it.bh * p.runs + it.run) * 2 + set) * p.m * p.dv + j;
+      if (to > from) take_out(true);
+      float* out = p.states + (it.bh * p.runs + it.run) * p.m * p.dv + j;
       if (j < p.dv) {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i)
@@ -375,25 +381,29 @@ __global__ void __launch_bounds__(kStateThreads, 1)
       }
     } else {
       for (int k = from; k < to; ++k, ++c) {
-        const int s = c % L::kStages, set = c & 1;
-        wait_warp(ctl, L::kSplit + set, c >> 1);
-        // the sums of all chunks before have been read: a set's own by its order, the
-        // smaller terms' of the run before by this
-        if (k == from && c >= 1) wait_warp(ctl, L::kSumFree + (set ^ 1), (c - 1) >> 1);
+        const int s = c % L::kStages, t = c & 1, g = group & 1;
+        const bool opens = (k - from) % L::kGroup == 0;
+        wait_warp(ctl, L::kSplit + t, c >> 1);
+        if (opens && group >= 2) wait_warp(ctl, L::kSumFree + g, (group >> 1) - 1);
+        // the smaller terms' sums of the run before have been read
+        if (k == from && group >= 1) wait_warp(ctl, L::kSumFree + (g ^ 1), (group - 1) >> 1);
         tc_fence_after();
-        const uint32_t v = base + L::V + s * L::kV, terms = base + L::T + set * L::kT;
-        const uint32_t d = tmem + set * L::kSumCols;
+        const uint32_t v = base + L::V + s * L::kV, terms = base + L::T + t * L::kT;
+        const uint32_t d = tmem + g * L::kSumCols;
+        const bool closes = (k + 1 - from) % L::kGroup == 0 || k + 1 == to;
         if (elect_one()) {
           if constexpr (L::kSide) {
-            mma_tokens<3 * M, C>(d, v, terms, false);
+            mma_tokens<3 * M, C>(d, v, terms, !opens);
           } else {
-            mma_tokens<M, C>(d, v, base + L::K + s * L::kK, false);
+            mma_tokens<M, C>(d, v, base + L::K + s * L::kK, !opens);
             mma_tokens<2 * M, C>(tmem + 2 * L::kSumCols, v, terms, k > from);
           }
           mma_commit(&ctl.bar[L::kEmpty + s]);
-          mma_commit(&ctl.bar[L::kSum + set]);
+          mma_commit(&ctl.bar[L::kSplitFree + t]);
+          if (closes) mma_commit(&ctl.bar[L::kSum + g]);
         }
         __syncwarp();
+        if (closes) ++group;
       }
     }
   }
@@ -610,7 +620,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
       if (it.chunks > 0) {
         if (state_row) {
           const float lost = expm1f(it.g * (float)Chunk(it, p, 0).have);
-          const float* X = p.states + (it.bh * p.runs + it.run) * 2 * p.m * p.dv + row * p.xj;
+          const float* X = p.states + (it.bh * p.runs + it.run) * p.m * p.dv + row * p.xj;
 #pragma unroll 1
           for (int q = 0; q < M / 64; ++q) {
             const int cb = part * (M / 64) + q;
@@ -892,7 +902,7 @@ bool decay_tc_pass(const DecayPass& p, cudaError_t* status, cudaStream_t stream)
              p.os.head % 16 == 0 && p.os.time % 16 == 0 && p.dv % 16 == 0;
   a.err = device_error_word_of_current();
   if (p.sums) *status = run_tc_any(a, maps, false, stream);
-  if (p.sums && *status == cudaSuccess) *status = launch_decay_join(p, 2, true, stream);
+  if (p.sums && *status == cudaSuccess) *status = launch_decay_join(p, true, stream);
   if (*status == cudaSuccess) *status = run_tc_any(a, maps, true, stream);
   return true;
 }

@@ -27,8 +27,8 @@ struct DecayPass {
   int si, sj;
   float inter, w;
   // runs of tokens that are worked on by themselves: run_len tokens each (a multiple of
-  // the chunk), and a state for each, [B*H, runs, parts, m, dv]: what it adds, in one or
-  // two parts, then in the first part's place the state that enters it
+  // the chunk), and a state [m, dv] for each, [B*H, runs, m, dv]: what it adds, then the
+  // state that enters it
   int64_t run_len;
   int runs;
   float* states;

@@ -12,8 +12,8 @@ constexpr int kDecayTcChunk = 128;
 constexpr int kDecayTcBlocks = 152;  // one for each SM, each taking runs in turn
 // One pass, p.runs in chunks of kDecayTcChunk; false where the tensors do not fit it.
 bool decay_tc_pass(const DecayPass& p, cudaError_t* status, cudaStream_t stream);
-// The join of states in `parts` parts; early: set up while the kernel before it runs.
-cudaError_t launch_decay_join(const DecayPass& p, int parts, bool early, cudaStream_t stream);
+// early: set up while the kernel before it runs.
+cudaError_t launch_decay_join(const DecayPass& p, bool early, cudaStream_t stream);
 
 // A launch that may be set up while the kernel before it on the stream runs (early): its
 // kernel waits for that one (griddepcontrol.wait) before it touches what that one writes
