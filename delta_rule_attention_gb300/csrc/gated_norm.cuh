@@ -1,0 +1,457 @@
+// Shared by the kernels of the gated norm (gated_norm.cu, gated_norm_bwd.cu): a row's
+// layout over threads, its sums, and the choice of a launch shape.
+#pragma once
+
+#include "linear.cuh"
+
+namespace falcon {
+namespace {
+
+// How a head's sum is formed.
+enum { kWhole = 0,   // one head: the threads of a row
+       kLanes = 1,   // m / V threads, a power of two up to 32, side by side in a warp
+       kStaged = 2   // any: products in shared memory, a warp a head
+};
+
+// V neighbouring elements as they lie in memory: a row's inputs wait in registers in half
+// the space that bf16 takes as fp32.
+template <typename E, int V>
+struct Held {
+  static constexpr bool kPairs = sizeof(E) == 2 && V > 1;
+  static constexpr int kWords = kPairs ? V / 2 : V;
+  uint32_t w[kWords];
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (kPairs) return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    return __uint_as_float(w[i]);
+  }
+};
+// As fp32.
+template <typename E, int V>
+__device__ __forceinline__ FloatV<V> wide(const Held<E, V>& h) {
+  FloatV<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = h.get(i);
+  return r;
+}
+template <int V>
+__device__ __forceinline__ FloatV<V> times(const FloatV<V>& x, float s) {
+  FloatV<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = x.v[i] * s;
+  return r;
+}
+template <int V>
+__device__ __forceinline__ FloatV<V> mul_of(const FloatV<V>& x, const FloatV<V>& y) {
+  FloatV<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = x.v[i] * y.v[i];
+  return r;
+}
+template <int V>
+__device__ __forceinline__ FloatV<V> fma_of(const FloatV<V>& x, const FloatV<V>& y,
+                                            const FloatV<V>& z) {
+  FloatV<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = fmaf(x.v[i], y.v[i], z.v[i]);
+  return r;
+}
+// x s + z
+template <int V>
+__device__ __forceinline__ FloatV<V> fma_of(const FloatV<V>& x, float s, const FloatV<V>& z) {
+  FloatV<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = fmaf(x.v[i], s, z.v[i]);
+  return r;
+}
+// acc + sum of a b, in two partial sums.
+template <int V>
+struct Dot {
+  float two[2] = {0.f, 0.f};
+  __device__ __forceinline__ void add(const FloatV<V>& a, const FloatV<V>& b) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) two[i & 1] = fmaf(a.v[i], b.v[i], two[i & 1]);
+  }
+  __device__ __forceinline__ float sum() const { return two[0] + two[1]; }
+};
+// V elements stored where `live`, zeros for a row that holds no token.
+template <typename E, int V>
+__device__ __forceinline__ void put_vec(E* p, const FloatV<V>& x, bool live, bool held) {
+  if (!live) return;
+  if constexpr (Held<E, V>::kPairs) {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = held ? pack_bf16(x.v[2 * i], x.v[2 * i + 1]) : 0u;
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    FloatV<V> y;
+#pragma unroll
+    for (int i = 0; i < V; ++i) y.v[i] = held ? x.v[i] : 0.f;
+    store_vec<E, V>(p, y);
+  }
+}
+
+// Inputs of the rows ahead wait in shared memory: a thread copies what it will read
+// itself (cp.async), so that nobody waits for another's copies, and registers hold one
+// row only.  Elements of two bytes that lie on no wider boundary are loaded when they are
+// needed instead.
+template <typename E, int V>
+struct Slot {
+  static constexpr int kBytes = V * sizeof(E);
+  static constexpr bool kAhead = kBytes >= 4;
+};
+template <typename E, int V>
+__device__ __forceinline__ void copy_ahead(unsigned char* to, const E* from, bool live) {
+  const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+  if constexpr (Slot<E, V>::kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+  else if constexpr (Slot<E, V>::kBytes == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from),
+                 "r"(live ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void ahead_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the newest `n` groups (0 .. 3) have arrived.
+__device__ __forceinline__ void ahead_wait(int n) {
+  if (n >= 3)
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (n == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+// An input's vector: out of its slot, or out of memory (two-byte elements, rows too wide
+// for shared memory).
+template <typename E, int V>
+__device__ __forceinline__ Held<E, V> held_vec(const unsigned char* slot, const E* from,
+                                               bool live, bool ahead) {
+  Held<E, V> r = {};
+  if constexpr (Slot<E, V>::kBytes == 16) {
+    if (ahead || live) {
+      const uint4 q = ahead ? *reinterpret_cast<const uint4*>(slot)
+                            : *reinterpret_cast<const uint4*>(from);
+      r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
+    }
+  } else if constexpr (Slot<E, V>::kBytes == 4) {
+    if (ahead || live)
+      r.w[0] = ahead ? *reinterpret_cast<const uint32_t*>(slot)
+                     : *reinterpret_cast<const uint32_t*>(from);
+  } else {
+    r.w[0] = live ? __float_as_uint(load_vec<E, 1>(from).v[0]) : 0u;
+  }
+  return r;
+}
+
+template <typename E, int V>
+__device__ __forceinline__ FloatV<V> zeros() {
+  FloatV<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = 0.f;
+  return r;
+}
+
+// The channels' parameters in shared memory, read for every row: weight times scale, and
+// next_weight (ones where there are none).
+__device__ __forceinline__ void stage_params(const NormArgs& a, float* to) {
+  const int threads = blockDim.x * blockDim.y;
+  for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < a.D; c += threads) {
+    const float w = a.weight ? a.weight[c] : 1.f;
+    to[c] = a.scale ? w * a.scale[c] : w;
+    if (a.next_weight) to[a.D + c] = a.next_weight[c];
+  }
+  __syncthreads();
+}
+template <int V>
+__device__ __forceinline__ FloatV<V> param_vec(const float* p) {
+  FloatV<V> r;
+  constexpr int Q = V < 4 ? V : 4;
+#pragma unroll
+  for (int i = 0; i < V; i += Q) {
+    const FloatV<Q> q = load_vec<float, Q>(p + i);
+#pragma unroll
+    for (int j = 0; j < Q; ++j) r.v[i + j] = q.v[j];
+  }
+  return r;
+}
+
+// The threads of one row of a block (rows of whole warps).
+__device__ __forceinline__ void row_sync(int nt) {
+  asm volatile("bar.sync %0, %1;" ::"r"((int)threadIdx.y + 1), "r"(nt) : "memory");
+}
+
+// Sums of N values over the nt threads of a row (a power of two up to 32, or whole
+// warps); `red` holds 2 x 32 pairs a row, `turn` says which were used last.
+template <int N>
+struct Sums {
+  float v[N];
+};
+template <int N>
+__device__ __forceinline__ Sums<N> row_sum(Sums<N> x, int nt, float2* red, int& turn) {
+  if (nt >= 32) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) x.v[i] += __shfl_xor_sync(0xffffffffu, x.v[i], o);
+  } else {
+    for (int o = nt / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) x.v[i] += __shfl_xor_sync(0xffffffffu, x.v[i], o);
+  }
+  if (nt <= 32) return x;
+  turn ^= 32;
+  red += turn;
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = make_float2(x.v[0], x.v[N - 1]);
+  row_sync(nt);
+  float2 s = red[0];
+  for (int w = 1; w < nt / 32; ++w) s.x += red[w].x, s.y += red[w].y;
+  x.v[0] = s.x;
+  if (N > 1) x.v[N - 1] = s.y;
+  return x;
+}
+
+// act(z), and act'(z)
+template <typename E, int V>
+__device__ __forceinline__ FloatV<V> gates(const Held<E, V>& z, int gate) {
+  FloatV<V> g;
+#pragma unroll
+  for (int i = 0; i < V; ++i) g.v[i] = z.get(i);
+  if (gate == FALCON_ACT_IDENTITY) return g;
+  if (gate == FALCON_ACT_SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) g.v[i] = sigmoid(g.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) g.v[i] *= sigmoid(g.v[i]);
+  }
+  return g;
+}
+template <typename E, int V>
+__device__ __forceinline__ FloatV<V> slopes(const Held<E, V>& z, int gate) {
+  FloatV<V> s;
+#pragma unroll
+  for (int i = 0; i < V; ++i) s.v[i] = 1.f;
+  if (gate == FALCON_ACT_IDENTITY) return s;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float x = z.get(i), p = sigmoid(x);
+    s.v[i] = gate == FALCON_ACT_SIGMOID ? p * (1.f - p) : p * fmaf(x, 1.f - p, 1.f);
+  }
+  return s;
+}
+
+// A row of the problem, and the way to the row `step` further on (no division in a loop).
+struct RowAt {
+  int b, t;
+  bool in, held;  // inside the problem; a token of its row
+  int step_b, step_t;
+  __device__ __forceinline__ RowAt(const NormArgs& a, int64_t row, int64_t step) {
+    const unsigned T = (unsigned)a.T;
+    b = (int)((uint64_t)row / T), t = (int)(row - (int64_t)b * T);
+    step_b = (int)((uint64_t)step / T), step_t = (int)(step - (int64_t)step_b * T);
+    look(a);
+  }
+  __device__ __forceinline__ void look(const NormArgs& a) {
+    in = b < a.B;
+    held = in && t < row_length(a.lengths, in ? b : 0, a.T);
+  }
+  __device__ __forceinline__ void advance(const NormArgs& a) {
+    b += step_b, t += step_t;
+    if (t >= a.T) t -= (int)a.T, ++b;
+    look(a);
+  }
+};
+
+// Channel and head of vector k of a thread.
+struct Place {
+  int c, head;
+  bool live;
+};
+template <int V, int MODE>
+__device__ __forceinline__ Place place_of(const NormArgs& a, int k) {
+  Place p;
+  p.c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+  p.live = p.c < a.D;
+  p.head = MODE == kWhole || !p.live ? 0 : p.c / a.m;
+  return p;
+}
+
+// Where the row's tensors begin, and vector `at` of a head-major one in it.
+template <typename E>
+__device__ __forceinline__ E* row_of(const void* p, const falcon_strides& s, const RowAt& r) {
+  return static_cast<E*>(const_cast<void*>(p)) + (r.in ? r.b * s.batch + r.t * s.time : 0);
+}
+template <int MODE>
+__device__ __forceinline__ int64_t in_heads(const NormArgs& a, const falcon_strides& s,
+                                            const Place& at) {
+  return MODE == kWhole ? at.c : at.head * s.head + (at.c - at.head * a.m);
+}
+
+// Sums over each vector's head of N values a vector, in place.
+template <int K, int MODE, int N>
+__device__ __forceinline__ void head_sums(const NormArgs& a, const Place (&at)[K],
+                                          Sums<N> (&x)[K], int V, float2* red, int& turn,
+                                          float2* staged) {
+  if constexpr (MODE == kWhole) {
+    Sums<N> s = x[0];
+#pragma unroll
+    for (int k = 1; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s.v[i] += x[k].v[i];
+    s = row_sum<N>(s, blockDim.x, red, turn);
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = s;
+  } else if constexpr (MODE == kLanes) {
+    const int lanes = a.m / V;
+    for (int o = lanes / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[k].v[i] += __shfl_xor_sync(0xffffffffu, x[k].v[i], o);
+  } else {
+    // a vector lies inside one head (V divides m)
+    const int vecs = a.D / V, each = a.m / V;
+    float2* mine = staged + (int)threadIdx.y * (vecs + a.H);
+    float2* sums = mine + vecs;
+    row_sync(blockDim.x);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (at[k].live) mine[at[k].c / V] = make_float2(x[k].v[0], x[k].v[N - 1]);
+    row_sync(blockDim.x);
+    const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
+    for (int h = threadIdx.x / 32; h < a.H; h += warps) {
+      float2 s = make_float2(0.f, 0.f);
+      for (int i = lane; i < each; i += 32) {
+        const float2 q = mine[h * each + i];
+        s.x += q.x, s.y += q.y;
+      }
+      s.x = warp_sum(s.x);
+      if (N > 1) s.y = warp_sum(s.y);
+      if (lane == 0) sums[h] = s;
+    }
+    row_sync(blockDim.x);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float2 s = sums[at[k].head];
+      x[k].v[0] = s.x;
+      if (N > 1) x[k].v[N - 1] = s.y;
+    }
+  }
+}
+
+// Launch shape: V channels a vector, K vectors a thread, nt threads a row, `rows` rows a
+// block.
+struct NormPlan {
+  int V, K, nt, rows, mode;
+  int blocks;  // at most
+  int ring;    // rows whose inputs are in shared memory at once, one of them being read; 0: none
+  // bytes: of a block's parameters, with its products (kStaged), and in all
+  size_t params, staged, shared;
+};
+
+bool fits(const void* p, const falcon_strides& s, int V, int esize, bool head) {
+  if (!p) return true;
+  return reinterpret_cast<uintptr_t>(p) % (uintptr_t)(V * esize) == 0 && s.batch % V == 0 &&
+         s.time % V == 0 && (!head || s.head % V == 0);
+}
+
+// How many vectors a thread may hold, the threads of a row (and block) at most, and the
+// threads of an SM that their registers leave room for.
+struct Width {
+  int K, threads, resident;
+};
+constexpr int kRowThreads = 128;  // threads a block aims at
+// Dynamic shared memory of each of `per` blocks of an SM, beside 5 KB of its own.
+constexpr size_t shared_for(int per) { return 228 * 1024 / per - 5 * 1024 - 256; }
+
+// widths: rising; the last one has to do for the widest row.  With many rows a thread holds as many as leave `enough` warps in all (a row's sums then
+// cost fewer steps, and more of its loads are under way at once), up to `prefer`; with few
+// rows a row is spread over more threads.
+template <int COUNTS>
+NormPlan plan_norm(const NormArgs& a, const Width (&widths)[COUNTS], int prefer, int64_t enough,
+                   int inputs, bool narrow) {
+  NormPlan p = {};
+  const int es = a.dtype == FALCON_BF16 ? 2 : 4;
+  p.V = 16 / es;
+  auto all = [&](int V) {
+    const bool heads = a.H > 1;
+    return a.m % V == 0 && fits(a.h, a.hs, V, es, heads) && fits(a.dh, a.dhs, V, es, heads) &&
+           fits(a.z, a.zs, V, es, false) && fits(a.x, a.xs, V, es, false) &&
+           fits(a.out, a.os, V, es, false) && fits(a.next, a.ns, V, es, false) &&
+           fits(a.y, a.os, V, es, false) && fits(a.dout, a.dos, V, es, false) &&
+           fits(a.dnext, a.dns, V, es, false) && fits(a.dx, a.dxs, V, es, false) &&
+           fits(a.dz, a.dzs, V, es, false);
+  };
+  if (narrow || !all(p.V)) p.V = 1;
+  const int vecs = a.D / p.V, each = a.m / p.V;
+  const bool lanes = each <= 32 && (each & (each - 1)) == 0;
+  p.mode = lanes ? kLanes : a.H == 1 ? kWhole : kStaged;
+  const int64_t rows = a.B * a.T;
+  int waste = 0, resident = 0;
+  for (int i = 0; i < COUNTS; ++i) {
+    const int K = widths[i].K;
+    if (p.V == 1 && K != 1 && K != 4 && i + 1 < COUNTS) continue;
+    int nt = (vecs + K - 1) / K;
+    if (nt <= 16 && p.mode != kStaged) {
+      int up = 1;
+      while (up < nt) up *= 2;
+      nt = up;
+    } else {
+      nt = (nt + 31) / 32 * 32;
+    }
+    if (nt > (p.V == 1 ? 1024 : widths[i].threads)) continue;
+    const int idle = nt * K - vecs;
+    const bool first = p.K == 0;
+    // a thread without work costs more than a shorter row saves
+    if (!first && (K > prefer || (rows * nt + 31) / 32 < enough || idle > waste + vecs / 8))
+      continue;
+    if (first || idle < waste) waste = idle;
+    p.K = K, p.nt = nt, resident = p.V == 1 ? 512 : widths[i].resident;
+  }
+  p.rows = kRowThreads / p.nt;
+  if (p.rows < 1) p.rows = 1;
+  if (p.rows > 8 && p.nt >= 32) p.rows = 8;
+  p.params = (size_t)(a.next_weight ? 2 : 1) * a.D * 4;
+  p.params = (p.params + 15) / 16 * 16;
+  p.staged = p.params;
+  if (p.mode == kStaged) {
+    const size_t one = (size_t)(vecs + a.H) * 8;
+    while (p.rows > 1 && p.rows * one > 40 * 1024) p.rows /= 2;
+    p.staged += (p.rows * one + 15) / 16 * 16;
+  }
+  // blocks that fit an SM with a row each at least; what is left of
+  // shared memory takes more rows ahead
+  const size_t row = (size_t)p.nt * p.rows * p.K * inputs * (p.V * es);
+  const bool ahead = p.V * es >= 4;
+  int per = resident / (p.nt * p.rows);
+  if (per < 1) per = 1;
+  if (per > 4) per = 4;  // a block takes all sixteen barriers
+  while (per > 1 && p.staged + (ahead ? row : 0) > shared_for(per)) --per;
+  if (ahead && shared_for(per) > p.staged) {
+    const size_t fit = (shared_for(per) - p.staged) / (row ? row : 1);
+    p.ring = fit > 4 ? 4 : (int)fit;
+  }
+  p.shared = p.staged + p.ring * row;
+  p.blocks = 152 * per;
+  return p;
+}
+
+template <typename F>
+cudaError_t start_norm(F kernel, const NormArgs& a, const NormPlan& p, unsigned grid,
+                       std::atomic<uint64_t>* allowed, cudaStream_t stream) {
+  // asked for with the most that any shape needs
+  if (p.shared > 40 * 1024) {
+    cudaError_t e = allow_shared(kernel, (int)shared_for(1), allowed);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, dim3(p.nt, p.rows), p.shared, stream>>>(a, p.ring, (int)p.params,
+                                                                (int)p.staged);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace falcon

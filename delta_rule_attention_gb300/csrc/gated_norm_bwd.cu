@@ -1,0 +1,264 @@
+// The gradient of the gated norm (formulas: gated_norm.cu).  A block takes rows in turn:
+// the next row's inputs are loaded while this row's sums are formed, and a thread keeps
+// the sums over rows of its channels for the parameters; a second kernel adds the blocks'
+// sums in a fixed order.
+#include "gated_norm.cuh"
+
+namespace falcon {
+namespace {
+
+// Inputs: h, z, dout, out and dnext, those that there are.
+template <typename E, int V, int K, int MODE>
+__global__ void __launch_bounds__(V == 1 ? 1024 : K == 3 || K == 4 ? 128 : 256,
+                                  V == 1 ? 1 : K == 3 || K == 4 ? 3 : K == 8 ? 1 : 2)
+    norm_bwd_kernel(const __grid_constant__ NormArgs a, int ring, int params_bytes,
+                    int staged_bytes) {
+  extern __shared__ __align__(16) unsigned char shared[];
+  float* par = reinterpret_cast<float*>(shared);
+  float2* staged = reinterpret_cast<float2*>(shared + params_bytes);
+  __shared__ float2 reds[8][64];
+  float2* red = reds[threadIdx.y & 7];
+  int turn = 0;
+  const int64_t rows = a.B * a.T, step = (int64_t)gridDim.x * blockDim.y;
+  constexpr int kBytes = Slot<E, V>::kBytes;
+  const int threads = blockDim.x * blockDim.y, vec = threads * kBytes;  // a vector of all threads
+  const int at_z = a.h ? K * vec : 0, at_d = at_z + (a.z ? K * vec : 0),
+            at_y = at_d + (a.dout ? K * vec : 0), at_e = at_y + (a.next_weight ? K * vec : 0),
+            row_bytes = at_e + (a.next_weight ? K * vec : 0);
+  unsigned char* mine =
+      shared + staged_bytes + (threadIdx.y * blockDim.x + threadIdx.x) * kBytes;
+  FloatV<V> each[K], nextw[K];  // sums for dweight and dscale, and for dnext_weight
+  Place at[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    each[k] = zeros<E, V>(), nextw[k] = zeros<E, V>();
+    at[k] = place_of<V, MODE>(a, k);
+  }
+  const bool ahead = Slot<E, V>::kAhead && ring > 0;
+  auto copy_row = [&](const RowAt& r, int slot) {
+    if constexpr (Slot<E, V>::kAhead) {
+      if (!ahead) return;
+      unsigned char* to = mine + slot * row_bytes;
+      const E *hp = row_of<E>(a.h, a.hs, r), *zp = row_of<E>(a.z, a.zs, r),
+              *dp = row_of<E>(a.dout, a.dos, r), *yp = row_of<E>(a.y, a.os, r),
+              *ep = row_of<E>(a.dnext, a.dns, r);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const bool on = at[k].live && r.held;
+        const int c = on ? at[k].c : 0;
+        if (a.h)
+          copy_ahead<E, V>(to + k * vec, hp + (on ? in_heads<MODE>(a, a.hs, at[k]) : 0), on);
+        if (a.z) copy_ahead<E, V>(to + at_z + k * vec, zp + c, on);
+        if (a.dout) copy_ahead<E, V>(to + at_d + k * vec, dp + c, on);
+        if (a.next_weight) {
+          copy_ahead<E, V>(to + at_y + k * vec, yp + c, on);
+          copy_ahead<E, V>(to + at_e + k * vec, ep + c, on);
+        }
+      }
+    }
+    ahead_commit();
+  };
+  const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  RowAt r(a, row0, step), next = r;
+  for (int i = 0; i < ring; ++i) {
+    copy_row(next, i);
+    next.advance(a);
+  }
+  stage_params(a, par);
+  int slot = 0;
+  // every thread takes part in every turn's barriers
+  for (int64_t row = row0; row - threadIdx.y < rows; row += step, r.advance(a)) {
+    if (ahead) ahead_wait(ring - 1);
+    const unsigned char* from = mine + slot * row_bytes;
+    auto input = [&](bool given, int off, const void* p, const falcon_strides& s, int64_t c,
+                     int k) {
+      Held<E, V> v = {};
+      if (given)
+        v = held_vec<E, V>(from + off + k * vec, row_of<E>(p, s, r) + c, at[k].live && r.held, ahead);
+      return v;
+    };
+    auto in_h = [&](int k) {
+      return wide(input(true, 0, a.h, a.hs, in_heads<MODE>(a, a.hs, at[k]), k));
+    };
+    auto in_z = [&](int k) { return input(true, at_z, a.z, a.zs, at[k].c, k); };
+    auto in_y = [&](int k) { return wide(input(true, at_y, a.y, a.os, at[k].c, k)); };
+    auto in_e = [&](int k) { return wide(input(true, at_e, a.dnext, a.dns, at[k].c, k)); };
+    auto ws = [&](int k) { return param_vec<V>(par + (at[k].live ? at[k].c : 0)); };
+    auto wn = [&](int k) { return param_vec<V>(par + a.D + (at[k].live ? at[k].c : 0)); };
+    FloatV<V> d[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) d[k] = wide(input(a.dout, at_d, a.dout, a.dos, at[k].c, k));
+    if (a.next_weight) {
+      Dot<V> yy, ey;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const FloatV<V> y = in_y(k);
+        yy.add(y, y);
+        ey.add(mul_of<V>(in_e(k), wn(k)), y);
+      }
+      const Sums<2> s = row_sum<2>({yy.sum(), ey.sum()}, blockDim.x, red, turn);
+      const float rn = rsqrtf(s.v[0] / (float)a.D + a.eps);
+      const float back = -rn * rn * s.v[1] / (float)a.D;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const FloatV<V> y = in_y(k), er = times<V>(in_e(k), rn);
+        nextw[k] = fma_of<V>(er, y, nextw[k]);
+        d[k] = fma_of<V>(er, wn(k), d[k]);
+        d[k] = fma_of<V>(y, rn * back, d[k]);
+      }
+    }
+    if (a.dx) {
+      E* p = row_of<E>(a.dx, a.dxs, r);
+#pragma unroll
+      for (int k = 0; k < K; ++k) put_vec<E, V>(p + at[k].c, d[k], at[k].live && r.in, r.held);
+    }
+    if (a.h) {
+      Sums<2> s[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        FloatV<V> f = mul_of<V>(d[k], ws(k));  // of n times the parameters
+        const FloatV<V> h = in_h(k);
+        Dot<V> hh, fh;
+        hh.add(h, h);
+        if (a.z) {
+          f = mul_of<V>(f, gates(in_z(k), a.gate));
+        }
+        fh.add(f, h);
+        s[k].v[0] = hh.sum(), s[k].v[1] = fh.sum();
+      }
+      head_sums<K, MODE, 2>(a, at, s, V, red, turn, staged);
+      E *hp = row_of<E>(a.dh, a.dhs, r), *zp = row_of<E>(a.dz, a.dzs, r);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float rn = rsqrtf(s[k].v[0] / (float)a.m + a.eps);
+        const float back = -rn * rn * s[k].v[1] / (float)a.m;
+        const FloatV<V> h = in_h(k), n = times<V>(h, rn);
+        FloatV<V> f = mul_of<V>(d[k], ws(k));
+        if (a.z) {
+          const FloatV<V> g = gates(in_z(k), a.gate);
+          const FloatV<V> dz = mul_of<V>(mul_of<V>(f, n), slopes(in_z(k), a.gate));
+          f = mul_of<V>(f, g);
+          d[k] = mul_of<V>(d[k], g);
+          put_vec<E, V>(zp + at[k].c, dz, at[k].live && r.in, r.held);
+        }
+        each[k] = fma_of<V>(d[k], n, each[k]);
+        put_vec<E, V>(hp + in_heads<MODE>(a, a.dhs, at[k]),
+                      times<V>(fma_of<V>(h, back, f), rn), at[k].live && r.in,
+                      r.held);
+      }
+    }
+    if (ahead) {  // this row's inputs are read
+      copy_row(next, slot);
+      next.advance(a);
+      slot = slot + 1 == ring ? 0 : slot + 1;
+    }
+  }
+  float* part = a.ws + ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * 2 * a.D;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (at[k].live) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        part[at[k].c + i] = each[k].v[i], part[a.D + at[k].c + i] = nextw[k].v[i];
+    }
+  }
+}
+
+// Adds the blocks' sums: 32 channels a block, 32 threads a channel, in a fixed order.
+constexpr int kPartThreads = 32;
+__global__ void __launch_bounds__(32 * kPartThreads)
+    norm_params_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float red[2][kPartThreads][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float s0 = 0.f, s1 = 0.f;
+  if (c < a.D) {
+#pragma unroll 4
+    for (int p = threadIdx.y; p < a.parts; p += kPartThreads) {
+      s0 += a.ws[(int64_t)p * 2 * a.D + c];
+      if (a.dnext_weight) s1 += a.ws[(int64_t)p * 2 * a.D + a.D + c];
+    }
+  }
+  red[0][threadIdx.y][threadIdx.x] = s0;
+  red[1][threadIdx.y][threadIdx.x] = s1;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < a.D) {
+    for (int p = 1; p < kPartThreads; ++p)
+      s0 += red[0][p][threadIdx.x], s1 += red[1][p][threadIdx.x];
+    if (a.dweight) a.dweight[c] = a.scale ? s0 * a.scale[c] : s0;
+    if (a.dscale) a.dscale[c] = a.weight ? s0 * a.weight[c] : s0;
+    if (a.dnext_weight) a.dnext_weight[c] = s1;
+  }
+}
+
+unsigned bwd_blocks(const NormArgs& a, const NormPlan& p) {
+  const int64_t blocks = (a.B * a.T + p.rows - 1) / p.rows;
+  return (unsigned)(blocks < p.blocks ? blocks : p.blocks);
+}
+
+NormPlan plan_bwd(const NormArgs& a, int inputs, bool narrow) {
+  const Width widths[] = {{1, 256, 512}, {2, 256, 512}, {3, 128, 384}, {4, 128, 384},
+                          {8, 256, 256}};
+  return plan_norm(a, widths, 4, 152 * 16, inputs, narrow);
+}
+
+template <typename E, int V, int K>
+cudaError_t start_mode(const NormArgs& a, const NormPlan& p, unsigned grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> allowed[3];  // one a kernel
+  if (p.mode == kWhole)
+    return start_norm(norm_bwd_kernel<E, V, K, kWhole>, a, p, grid, &allowed[0], stream);
+  if (p.mode == kLanes)
+    return start_norm(norm_bwd_kernel<E, V, K, kLanes>, a, p, grid, &allowed[1], stream);
+  return start_norm(norm_bwd_kernel<E, V, K, kStaged>, a, p, grid, &allowed[2], stream);
+}
+
+template <typename E, int V>
+cudaError_t start_count(const NormArgs& a, const NormPlan& p, unsigned grid,
+                        cudaStream_t stream) {
+  if (p.K == 1) return start_mode<E, V, 1>(a, p, grid, stream);
+  if constexpr (V > 1) {
+    if (p.K == 2) return start_mode<E, V, 2>(a, p, grid, stream);
+    if (p.K == 3) return start_mode<E, V, 3>(a, p, grid, stream);
+  }
+  if (p.K == 4) return start_mode<E, V, 4>(a, p, grid, stream);
+  return start_mode<E, V, 8>(a, p, grid, stream);
+}
+
+}  // namespace
+
+// Room for every launch that a call of this shape may make: it goes by its pointers.
+size_t norm_bwd_workspace_bytes(const falcon_norm_shape& s) {
+  NormArgs a = {};
+  a.B = s.B, a.T = s.T, a.H = (int)s.H, a.m = s.m, a.D = (int)(s.H * s.m), a.dtype = s.dtype;
+  int64_t most = 0;
+  for (int inputs = 1; inputs <= 5; ++inputs)
+    for (int narrow = 0; narrow < 2; ++narrow) {
+      const NormPlan p = plan_bwd(a, inputs, narrow != 0);
+      const int64_t parts = (int64_t)bwd_blocks(a, p) * p.rows;
+      most = parts > most ? parts : most;
+    }
+  return (size_t)most * 2 * a.D * 4;
+}
+
+cudaError_t launch_norm_bwd(const NormArgs& args, cudaStream_t stream) {
+  NormArgs a = args;
+  const int inputs =
+      (a.h ? 1 : 0) + (a.z ? 1 : 0) + (a.dout ? 1 : 0) + (a.next_weight ? 2 : 0);
+  const NormPlan p = plan_bwd(a, inputs, false);
+  const unsigned grid = bwd_blocks(a, p);
+  a.parts = (int)grid * p.rows;
+  if (grid > 0) {
+    cudaError_t e;
+    if (a.dtype == FALCON_BF16)
+      e = p.V == 8 ? start_count<__nv_bfloat16, 8>(a, p, grid, stream)
+                   : start_count<__nv_bfloat16, 1>(a, p, grid, stream);
+    else
+      e = p.V == 4 ? start_count<float, 4>(a, p, grid, stream)
+                   : start_count<float, 1>(a, p, grid, stream);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dweight || a.dscale || a.dnext_weight)
+    norm_params_kernel<<<(unsigned)((a.D + 31) / 32), dim3(32, kPartThreads), 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace falcon
