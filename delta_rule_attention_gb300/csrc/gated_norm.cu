@@ -18,7 +18,7 @@ namespace {
 
 // Inputs: h, z and x, those that there are.
 template <typename E, int V, int K, int MODE>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 256, V == 1 ? 1 : 2)
+__global__ void __launch_bounds__(V > 1 ? 256 : K == 8 ? 1024 : 512, V > 1 ? 2 : 1)
     norm_fwd_kernel(const __grid_constant__ NormArgs a, int ring, int params_bytes,
                     int staged_bytes) {
   extern __shared__ __align__(16) unsigned char shared[];

@@ -91,13 +91,12 @@ __device__ __forceinline__ void put_vec(E* p, const FloatV<V>& x, bool live, boo
 }
 
 // Inputs of the rows ahead wait in shared memory: a thread copies what it will read
-// itself (cp.async), so that nobody waits for another's copies, and registers hold one
-// row only.  Elements of two bytes that lie on no wider boundary are loaded when they are
-// needed instead.
+// itself (cp.async, 16 bytes), so that nobody waits for another's copies, and registers
+// hold one row only.  Rows on no such boundary are loaded when they are needed.
 template <typename E, int V>
 struct Slot {
   static constexpr int kBytes = V * sizeof(E);
-  static constexpr bool kAhead = kBytes >= 4;
+  static constexpr bool kAhead = kBytes == 16;
 };
 template <typename E, int V>
 __device__ __forceinline__ void copy_ahead(unsigned char* to, const E* from, bool live) {
@@ -105,10 +104,6 @@ __device__ __forceinline__ void copy_ahead(unsigned char* to, const E* from, boo
   if constexpr (Slot<E, V>::kBytes == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from),
                  "r"(live ? 16 : 0)
-                 : "memory");
-  else if constexpr (Slot<E, V>::kBytes == 4)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from),
-                 "r"(live ? 4 : 0)
                  : "memory");
 }
 __device__ __forceinline__ void ahead_commit() {
@@ -125,8 +120,8 @@ __device__ __forceinline__ void ahead_wait(int n) {
   else
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
-// An input's vector: out of its slot, or out of memory (two-byte elements, rows too wide
-// for shared memory).
+// An input's vector: out of its slot, or out of memory (also where rows are too wide for
+// shared memory).
 template <typename E, int V>
 __device__ __forceinline__ Held<E, V> held_vec(const unsigned char* slot, const E* from,
                                                bool live, bool ahead) {
@@ -137,12 +132,8 @@ __device__ __forceinline__ Held<E, V> held_vec(const unsigned char* slot, const 
                             : *reinterpret_cast<const uint4*>(from);
       r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
     }
-  } else if constexpr (Slot<E, V>::kBytes == 4) {
-    if (ahead || live)
-      r.w[0] = ahead ? *reinterpret_cast<const uint32_t*>(slot)
-                     : *reinterpret_cast<const uint32_t*>(from);
-  } else {
-    r.w[0] = live ? __float_as_uint(load_vec<E, 1>(from).v[0]) : 0u;
+  } else if (live) {
+    r.w[0] = __float_as_uint(load_vec<E, 1>(from).v[0]);
   }
   return r;
 }
@@ -364,13 +355,14 @@ bool fits(const void* p, const falcon_strides& s, int V, int esize, bool head) {
 struct Width {
   int K, threads, resident;
 };
-constexpr int kRowThreads = 128;  // threads a block aims at
+// Threads a block aims at.
+constexpr int kRowThreads = 128, kNarrowThreads = 256;
 // Dynamic shared memory of each of `per` blocks of an SM, beside 5 KB of its own.
 constexpr size_t shared_for(int per) { return 228 * 1024 / per - 5 * 1024 - 256; }
 
 // widths: rising; the last one has to do for the widest row.  With many rows a thread holds as many as leave `enough` warps in all (a row's sums then
-// cost fewer steps, and more of its loads are under way at once), up to `prefer`; with few
-// rows a row is spread over more threads.
+// cost fewer steps, and more of its loads are under way at once), up to `prefer`, or four
+// where that makes a row one warp's; with few rows a row is spread over more threads.
 template <int COUNTS>
 NormPlan plan_norm(const NormArgs& a, const Width (&widths)[COUNTS], int prefer, int64_t enough,
                    int inputs, bool narrow) {
@@ -403,16 +395,16 @@ NormPlan plan_norm(const NormArgs& a, const Width (&widths)[COUNTS], int prefer,
     } else {
       nt = (nt + 31) / 32 * 32;
     }
-    if (nt > (p.V == 1 ? 1024 : widths[i].threads)) continue;
+    if (nt > (p.V > 1 ? widths[i].threads : K == 8 ? 1024 : 512)) continue;
     const int idle = nt * K - vecs;
     const bool first = p.K == 0;
     // a thread without work costs more than a shorter row saves
-    if (!first && (K > prefer || (rows * nt + 31) / 32 < enough || idle > waste + vecs / 8))
+    if (!first && ((K > (p.V > 1 ? prefer : 4) && (nt > 32 || K > 4)) || (rows * nt + 31) / 32 < enough || idle > waste + vecs / 8))
       continue;
     if (first || idle < waste) waste = idle;
-    p.K = K, p.nt = nt, resident = p.V == 1 ? 512 : widths[i].resident;
+    p.K = K, p.nt = nt, resident = p.V > 1 ? widths[i].resident : K == 8 ? 1024 : 512;
   }
-  p.rows = kRowThreads / p.nt;
+  p.rows = (p.V == 1 ? kNarrowThreads : kRowThreads) / p.nt;
   if (p.rows < 1) p.rows = 1;
   if (p.rows > 8 && p.nt >= 32) p.rows = 8;
   p.params = (size_t)(a.next_weight ? 2 : 1) * a.D * 4;
@@ -426,7 +418,7 @@ NormPlan plan_norm(const NormArgs& a, const Width (&widths)[COUNTS], int prefer,
   // blocks that fit an SM with a row each at least; what is left of
   // shared memory takes more rows ahead
   const size_t row = (size_t)p.nt * p.rows * p.K * inputs * (p.V * es);
-  const bool ahead = p.V * es >= 4;
+  const bool ahead = p.V > 1;
   int per = resident / (p.nt * p.rows);
   if (per < 1) per = 1;
   if (per > 4) per = 4;  // a block takes all sixteen barriers

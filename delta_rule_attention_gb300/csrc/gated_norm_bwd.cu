@@ -9,7 +9,7 @@ namespace {
 
 // Inputs: h, z, dout, out and dnext, those that there are.
 template <typename E, int V, int K, int MODE>
-__global__ void __launch_bounds__(V == 1 ? 1024 : K == 3 || K == 4 ? 128 : 256,
+__global__ void __launch_bounds__(V == 1 ? (K == 8 ? 1024 : 512) : K == 3 || K == 4 ? 128 : 256,
                                   V == 1 ? 1 : K == 3 || K == 4 ? 3 : K == 8 ? 1 : 2)
     norm_bwd_kernel(const __grid_constant__ NormArgs a, int ring, int params_bytes,
                     int staged_bytes) {
@@ -198,7 +198,7 @@ unsigned bwd_blocks(const NormArgs& a, const NormPlan& p) {
 NormPlan plan_bwd(const NormArgs& a, int inputs, bool narrow) {
   const Width widths[] = {{1, 256, 512}, {2, 256, 512}, {3, 128, 384}, {4, 128, 384},
                           {8, 256, 256}};
-  return plan_norm(a, widths, 4, 152 * 16, inputs, narrow);
+  return plan_norm(a, widths, 2, 152 * 16, inputs, narrow);
 }
 
 template <typename E, int V, int K>
