@@ -396,6 +396,8 @@ NormPlan plan_norm(const NormArgs& a, const Width (&widths)[COUNTS], int prefer,
       nt = (nt + 31) / 32 * 32;
     }
     if (nt > (p.V > 1 ? widths[i].threads : K == 8 ? 1024 : 512)) continue;
+    // a head's lanes lie in one row, side by side
+    if (p.mode == kLanes && nt < each) continue;
     const int idle = nt * K - vecs;
     const bool first = p.K == 0;
     // a thread without work costs more than a shorter row saves
