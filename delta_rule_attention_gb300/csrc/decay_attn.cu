@@ -22,6 +22,8 @@ constexpr int kTile = 64;         // rows and columns of a block's tile
 constexpr int kLd = kTile + 4;    // row stride in shared memory
 constexpr int kStep = 32;         // tokens (states) or keys (reads) staged at a time
 constexpr int kChunk = 64;        // tokens of a chunk
+constexpr int kWholeTokens = 128;  // rows of at most so many are one run
+constexpr int kTcFrom = 64;        // longer rows go to the tensor cores
 
 // acc[i][j] += sum_{k < n} a[k][i] b[k][j] for this thread's 4 x 4 corner of the tile
 __device__ __forceinline__ void outer_sum(float (&acc)[4][4], const float* a, const float* b,
@@ -151,12 +153,14 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t first = run * a.run_len;
   const int64_t end = first + a.run_len < a.T ? first + a.run_len : a.T;
   const int chunks = (int)((end - first + kChunk - 1) / kChunk);
-  {
-    const float* X = a.states + (bh * a.runs + run) * a.m * a.dv;
-    for (int e = tid; e < mpad * kTile; e += kThreads) {
-      const int i = e / kTile, j = e % kTile;
-      sm.S[i * kLd + j] = i < a.m && j0 + j < a.dv ? X[i * a.dv + j0 + j] : 0.f;
-    }
+  // the state entering the run; where a row is one run, the call's own
+  const float* X = a.whole ? a.S_init : a.states + (bh * a.runs + run) * a.m * a.dv;
+  const int si = a.whole ? a.si : a.dv, sj = a.whole ? a.sj : 1;
+  const int64_t seat = a.whole ? bh * a.m * a.dv : 0;
+  for (int e = tid; e < mpad * kTile; e += kThreads) {
+    const int i = e / kTile, j = e % kTile;
+    sm.S[i * kLd + j] =
+        X && i < a.m && j0 + j < a.dv ? X[seat + i * si + (j0 + j) * sj] : 0.f;
   }
   for (int cc = 0; cc < chunks; ++cc) {
     const int64_t t0 = first + (int64_t)(a.rev ? chunks - 1 - cc : cc) * kChunk;
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(kThreads)
           if (j < cols) store_vec<E, 1>(to + j, FloatV<1>{{live ? O[i][j] : 0.f}});
       }
     }
-    if (have > 0 && cc + 1 < chunks) {
+    if (have > 0 && (cc + 1 < chunks || (a.whole && a.S_out))) {
       const float lost = expm1f(g * (float)have);
       for (int mk = 0; mk < a.m; mk += kTile) {
         __syncthreads();
@@ -253,6 +257,13 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
       __syncthreads();
+    }
+  }
+  if (a.whole && a.S_out) {
+    __syncthreads();
+    for (int e = tid; e < a.m * kTile; e += kThreads) {
+      const int i = e / kTile, j = e % kTile;
+      if (j0 + j < a.dv) a.S_out[seat + i * si + (j0 + j) * sj] = sm.S[i * kLd + j];
     }
   }
 }
@@ -309,10 +320,14 @@ cudaError_t run_pass(DecayPass& p, cudaStream_t stream) {
   p.vec_q = quads(p.q, p.qs, p.dtype), p.vec_k = quads(p.k, p.ks, p.dtype);
   p.vec_v = quads(p.v, p.vs, p.dtype), p.vec_o = quads(p.o, p.os, p.dtype);
   const int64_t bh = p.B * p.H;
+  // a row of few chunks as one run, whose state the reads carry themselves: one launch
+  // instead of three (T 64: a call 25 -> 18 us, all of it the host's)
+  if (p.T > 0 && p.T <= kWholeTokens) p.runs = 1, p.run_len = kWholeTokens, p.whole = true;
   const unsigned grid = (unsigned)(bh * p.runs);
   const unsigned vt = (unsigned)ceil_div(p.dv, kTile), mt = (unsigned)ceil_div(p.m, kTile);
-  if (p.runs > 0) decay_states_kernel<E><<<dim3(grid, mt * vt), kThreads, 0, stream>>>(p);
-  cudaError_t e = launch_decay_join(p, false, stream);
+  if (p.runs > 0 && !p.whole)
+    decay_states_kernel<E><<<dim3(grid, mt * vt), kThreads, 0, stream>>>(p);
+  cudaError_t e = p.whole ? cudaSuccess : launch_decay_join(p, false, stream);
   if (e != cudaSuccess) return e;
   if (p.runs > 0) {
     e = allow_shared(decay_read_kernel<E>, sizeof(ReadSmem), &allowed);
@@ -323,7 +338,9 @@ cudaError_t run_pass(DecayPass& p, cudaStream_t stream) {
 }
 
 // A pass with its tensors set, on the tensor cores; false where they do not fit.
+// Rows that are one run here take one launch, against three there.
 bool tc_pass(const falcon_decay_shape& s, DecayPass p, cudaError_t* e, cudaStream_t stream) {
+  if (p.T <= kTcFrom) return false;
   const DecayPass split = shape_pass(s, p.m, p.dv, true);
   p.runs = split.runs, p.run_len = split.run_len;
   return decay_tc_pass(p, e, stream);
@@ -376,30 +393,42 @@ cudaError_t launch_decay_bwd(const DecayCall& c, cudaStream_t stream) {
   const bool behind = tc_pass(c.s, p, &e, stream);
   if (!behind) e = simt_pass(c.s, p, stream);
   if (e != cudaSuccess) return e;
-  // dv = G_t^T k_t, backward in time with (k, q, dO)
   p.rev = 1;
-  p.m = m, p.dv = dv;
-  p.q = c.k, p.k = c.q, p.v = c.dO, p.o = c.dv;
-  p.qs = c.ks, p.ks = c.qs, p.vs = c.dos, p.os = c.dvs;
-  p.S_init = c.dS_T, p.S_out = c.dS0;
-  p.si = dv, p.sj = 1;
   p.inter = 1.f, p.w = c.s.scale;
-  p.xi = dv, p.xj = 1;
-  p.behind_states = behind;
-  const bool kept = tc_pass(c.s, p, &e, stream);  // its states serve dk too
-  if (!kept) e = simt_pass(c.s, p, stream);
-  if (e != cudaSuccess) return e;
+  p.S_init = c.dS_T;
+  // dv = G_t^T k_t, backward in time with (k, q, dO)
+  DecayPass v = p;
+  v.m = m, v.dv = dv;
+  v.q = c.k, v.k = c.q, v.v = c.dO, v.o = c.dv;
+  v.qs = c.ks, v.ks = c.qs, v.vs = c.dos, v.os = c.dvs;
+  v.S_out = c.dS0;
+  v.si = dv, v.sj = 1;
+  v.xi = dv, v.xj = 1;
   // dk = G_t v_t, backward in time with (v, dO, q)
-  p.m = dv, p.dv = m;
-  p.q = c.v, p.k = c.dO, p.v = c.q, p.o = c.dk;
-  p.qs = c.vs, p.ks = c.dos, p.vs = c.qs, p.os = c.dks;
-  p.S_out = nullptr;
-  p.si = 1, p.sj = dv;
-  p.behind_states = kept;
-  if (kept) p.sums = false, p.xi = 1, p.xj = dv;
-  if (tc_pass(c.s, p, &e, stream)) return e;
-  p.sums = true;
-  return simt_pass(c.s, p, stream);
+  DecayPass k = p;
+  k.m = dv, k.dv = m;
+  k.q = c.v, k.k = c.dO, k.v = c.q, k.o = c.dk;
+  k.qs = c.vs, k.ks = c.dos, k.vs = c.qs, k.os = c.dks;
+  k.si = 1, k.sj = dv;
+  k.xi = m, k.xj = 1;
+  if (c.dS_T && c.dS0 == c.dS_T) {  // in place: nothing reads dS_T behind the pass that writes dS0
+    k.behind_states = behind;
+    const bool first = tc_pass(c.s, k, &e, stream);
+    if (!first) e = simt_pass(c.s, k, stream);
+    if (e != cudaSuccess) return e;
+    v.behind_states = first;
+    return tc_pass(c.s, v, &e, stream) ? e : simt_pass(c.s, v, stream);
+  }
+  v.behind_states = behind;
+  const bool kept = tc_pass(c.s, v, &e, stream);  // its states serve dk too
+  if (!kept) e = simt_pass(c.s, v, stream);
+  if (e != cudaSuccess) return e;
+  if (kept) {
+    DecayPass shared = k;
+    shared.sums = false, shared.xi = 1, shared.xj = dv;
+    if (tc_pass(c.s, shared, &e, stream)) return e;
+  }
+  return simt_pass(c.s, k, stream);
 }
 
 }  // namespace falcon

@@ -31,6 +31,7 @@ struct DecayPass {
   // state that enters it
   int64_t run_len;
   int runs;
+  bool whole;  // CUDA cores: one run a row, from S_init to S_out in one launch
   float* states;
   // tensor-core passes: whether the states are formed (or taken as they are, key i and
   // value j of one at i * xi + j * xj), and whether the kernels that form and read them

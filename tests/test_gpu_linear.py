@@ -398,3 +398,34 @@ def test_norm_many_rows(falcon):
             # summed by thousands of threads: a tree of at most rows / 608 + 608 terms
             once(got[name], want[name], size[name], 0.0, H * m + 1024, name)
         once(got["dh"], want["dh"], size["dh"], HALF[dtype], H * m + 64, "dh")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [1, 64, 65, 128, 129, 700])
+def test_decay_gradient_of_the_state_in_place(falcon, T, dtype):
+    """dS0 over dS_T, which the gradients of keys and values read."""
+    c = decay_case(2, 3, T, 64, 64, dtype, seed=T, lengths=[T, T // 2])
+    c["dO"], dS = randn(gen(1), 2, 3, T, 64, dtype=dtype), randn(gen(2), 2, 3, 64, 64)
+    want = falcon.falcon_decay_attn_bwd(**c, dS_T=dS)
+    held = dS.clone()
+    got = falcon.falcon_decay_attn_bwd(**c, dS_T=held, grads=dict(dS0=held))
+    assert got["dS0"] is held
+    for name in ("dq", "dk", "dv", "dS0"):
+        # the runs' states may be formed by another pass: the same sums in another order
+        off = (got[name].double() - want[name].double()).abs()
+        assert float(off.max()) <= 2 * HALF[dtype] * float(want[name].double().abs().max()) + 1e-4
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_decay_mixed_layouts_in_the_gradient(falcon, dtype):
+    """Results of which one lies where TMA cannot write or read: passes on both paths."""
+    T, m = 300, 64
+    c = decay_case(2, 2, T, m, m, dtype, seed=8)
+    c["dO"], c["dS_T"] = randn(gen(1), 2, 2, T, m, dtype=dtype), randn(gen(2), 2, 2, m, m)
+    want, size = ref.decay_gradient(**c), ref.decay_gradient_size(**c)
+    odd = lambda: torch.empty(2, 2, T, m + 1, dtype=dtype, device="cuda")[..., 1:]  # noqa: E731
+    for names in (("dq",), ("dk",), ("dv",), ("dq", "dv"), ("dk", "dv")):
+        got = falcon.falcon_decay_attn_bwd(**c, grads={n: odd() for n in names})
+        for name in ("dq", "dk", "dv"):
+            near(got[name], want[name], size[name], HALF[dtype], 2 * m + T + 256, name)
+        near(got["dS0"], want["dS0"], size["dS0"], 0.0, T + 256, "dS0")
