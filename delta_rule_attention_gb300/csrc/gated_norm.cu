@@ -37,10 +37,9 @@ __global__ void __launch_bounds__(V > 1 ? 256 : K == 8 ? 1024 : 512, V > 1 ? 2 :
   Place at[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) at[k] = place_of<V, MODE>(a, k);
-  const bool ahead = Slot<E, V>::kAhead && ring > 0;
+  constexpr bool ahead = Slot<E, V>::kAhead;
   auto copy_row = [&](const RowAt& r, int slot) {
-    if constexpr (Slot<E, V>::kAhead) {
-      if (!ahead) return;
+    if constexpr (ahead) {
       unsigned char* to = mine + slot * row_bytes;
       const E *hp = row_of<E>(a.h, a.hs, r), *zp = row_of<E>(a.z, a.zs, r),
               *xp = row_of<E>(a.x, a.xs, r);
@@ -53,8 +52,8 @@ __global__ void __launch_bounds__(V > 1 ? 256 : K == 8 ? 1024 : 512, V > 1 ? 2 :
         if (a.z) copy_ahead<E, V>(to + at_z + k * vec, zp + c, on);
         if (a.x) copy_ahead<E, V>(to + at_x + k * vec, xp + c, on);
       }
+      ahead_commit();
     }
-    ahead_commit();
   };
   const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   RowAt r(a, row0, step), next = r;
@@ -72,7 +71,7 @@ __global__ void __launch_bounds__(V > 1 ? 256 : K == 8 ? 1024 : 512, V > 1 ? 2 :
             *xp = row_of<E>(a.x, a.xs, r);
     auto input = [&](bool given, int off, const E* p, int64_t c, int k) {
       Held<E, V> v = {};
-      if (given) v = held_vec<E, V>(from + off + k * vec, p + c, at[k].live && r.held, ahead);
+      if (given) v = held_vec<E, V>(from + off + k * vec, p + c, at[k].live && r.held);
       return v;
     };
     auto in_h = [&](int k) {

@@ -120,18 +120,14 @@ __device__ __forceinline__ void ahead_wait(int n) {
   else
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
-// An input's vector: out of its slot, or out of memory (also where rows are too wide for
-// shared memory).
+// An input's vector: out of its slot, or out of memory.
 template <typename E, int V>
 __device__ __forceinline__ Held<E, V> held_vec(const unsigned char* slot, const E* from,
-                                               bool live, bool ahead) {
+                                               bool live) {
   Held<E, V> r = {};
-  if constexpr (Slot<E, V>::kBytes == 16) {
-    if (ahead || live) {
-      const uint4 q = ahead ? *reinterpret_cast<const uint4*>(slot)
-                            : *reinterpret_cast<const uint4*>(from);
-      r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
-    }
+  if constexpr (Slot<E, V>::kAhead) {
+    const uint4 q = *reinterpret_cast<const uint4*>(slot);
+    r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
   } else if (live) {
     r.w[0] = __float_as_uint(load_vec<E, 1>(from).v[0]);
   }
@@ -339,7 +335,7 @@ __device__ __forceinline__ void head_sums(const NormArgs& a, const Place (&at)[K
 struct NormPlan {
   int V, K, nt, rows, mode;
   int blocks;  // at most
-  int ring;    // rows whose inputs are in shared memory at once, one of them being read; 0: none
+  int ring;    // rows whose inputs are in shared memory at once, one of them being read (V > 1)
   // bytes: of a block's parameters, with its products (kStaged), and in all
   size_t params, staged, shared;
 };
@@ -429,6 +425,8 @@ NormPlan plan_norm(const NormArgs& a, const Width (&widths)[COUNTS], int prefer,
     const size_t fit = (shared_for(per) - p.staged) / (row ? row : 1);
     p.ring = fit > 4 ? 4 : (int)fit;
   }
+  // no room for a single row: one that is loaded when needed
+  if (ahead && p.ring == 0) return plan_norm(a, widths, prefer, enough, inputs, true);
   p.shared = p.staged + p.ring * row;
   p.blocks = 152 * per;
   return p;

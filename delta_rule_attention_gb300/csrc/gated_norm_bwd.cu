@@ -34,10 +34,9 @@ __global__ void __launch_bounds__(V == 1 ? (K == 8 ? 1024 : 512) : K == 3 || K =
     each[k] = zeros<E, V>(), nextw[k] = zeros<E, V>();
     at[k] = place_of<V, MODE>(a, k);
   }
-  const bool ahead = Slot<E, V>::kAhead && ring > 0;
+  constexpr bool ahead = Slot<E, V>::kAhead;
   auto copy_row = [&](const RowAt& r, int slot) {
-    if constexpr (Slot<E, V>::kAhead) {
-      if (!ahead) return;
+    if constexpr (ahead) {
       unsigned char* to = mine + slot * row_bytes;
       const E *hp = row_of<E>(a.h, a.hs, r), *zp = row_of<E>(a.z, a.zs, r),
               *dp = row_of<E>(a.dout, a.dos, r), *yp = row_of<E>(a.y, a.os, r),
@@ -55,8 +54,8 @@ __global__ void __launch_bounds__(V == 1 ? (K == 8 ? 1024 : 512) : K == 3 || K =
           copy_ahead<E, V>(to + at_e + k * vec, ep + c, on);
         }
       }
+      ahead_commit();
     }
-    ahead_commit();
   };
   const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   RowAt r(a, row0, step), next = r;
@@ -74,7 +73,7 @@ __global__ void __launch_bounds__(V == 1 ? (K == 8 ? 1024 : 512) : K == 3 || K =
                      int k) {
       Held<E, V> v = {};
       if (given)
-        v = held_vec<E, V>(from + off + k * vec, row_of<E>(p, s, r) + c, at[k].live && r.held, ahead);
+        v = held_vec<E, V>(from + off + k * vec, row_of<E>(p, s, r) + c, at[k].live && r.held);
       return v;
     };
     auto in_h = [&](int k) {
