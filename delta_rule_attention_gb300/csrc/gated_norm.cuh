@@ -35,43 +35,42 @@ __device__ __forceinline__ FloatV<V> wide(const Held<E, V>& h) {
 }
 template <int V>
 __device__ __forceinline__ FloatV<V> times(const FloatV<V>& x, float s) {
-  FloatV<V> r;
+  FloatV<V> t;
 #pragma unroll
-  for (int i = 0; i < V; ++i) r.v[i] = x.v[i] * s;
-  return r;
+  for (int i = 0; i < V; ++i) t.v[i] = s;
+  return mul_vec<V>(x, t);
 }
 template <int V>
 __device__ __forceinline__ FloatV<V> mul_of(const FloatV<V>& x, const FloatV<V>& y) {
-  FloatV<V> r;
-#pragma unroll
-  for (int i = 0; i < V; ++i) r.v[i] = x.v[i] * y.v[i];
-  return r;
+  return mul_vec<V>(x, y);
 }
 template <int V>
 __device__ __forceinline__ FloatV<V> fma_of(const FloatV<V>& x, const FloatV<V>& y,
                                             const FloatV<V>& z) {
-  FloatV<V> r;
-#pragma unroll
-  for (int i = 0; i < V; ++i) r.v[i] = fmaf(x.v[i], y.v[i], z.v[i]);
-  return r;
+  return fma_vec<V>(x, y, z);
 }
 // x s + z
 template <int V>
 __device__ __forceinline__ FloatV<V> fma_of(const FloatV<V>& x, float s, const FloatV<V>& z) {
-  FloatV<V> r;
+  FloatV<V> t;
 #pragma unroll
-  for (int i = 0; i < V; ++i) r.v[i] = fmaf(x.v[i], s, z.v[i]);
-  return r;
+  for (int i = 0; i < V; ++i) t.v[i] = s;
+  return fma_vec<V>(x, t, z);
 }
 // acc + sum of a b, in two partial sums.
 template <int V>
 struct Dot {
-  float two[2] = {0.f, 0.f};
+  FloatV<2> two = {{0.f, 0.f}};
   __device__ __forceinline__ void add(const FloatV<V>& a, const FloatV<V>& b) {
+    if constexpr (V == 1) {
+      two.v[0] = fmaf(a.v[0], b.v[0], two.v[0]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) two[i & 1] = fmaf(a.v[i], b.v[i], two[i & 1]);
+      for (int i = 0; i < V; i += 2)
+        two = fma_vec<2>({{a.v[i], a.v[i + 1]}}, {{b.v[i], b.v[i + 1]}}, two);
+    }
   }
-  __device__ __forceinline__ float sum() const { return two[0] + two[1]; }
+  __device__ __forceinline__ float sum() const { return two.v[0] + two.v[1]; }
 };
 // V elements stored where `live`, zeros for a row that holds no token.
 template <typename E, int V>
