@@ -163,26 +163,32 @@ __global__ void __launch_bounds__(V == 1 ? (K == 8 ? 1024 : 512) : K == 3 || K =
   }
 }
 
-// Adds the blocks' sums: 32 channels a block, 32 threads a channel, in a fixed order.
-constexpr int kPartThreads = 32;
-__global__ void __launch_bounds__(32 * kPartThreads)
+// Adds the blocks' sums: 8 channels a block, 128 threads a channel, in a fixed order.
+constexpr int kPartThreads = 128, kPartChannels = 8;
+__global__ void __launch_bounds__(kPartChannels* kPartThreads)
     norm_params_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float red[2][kPartThreads][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  constexpr int kWarps = kPartChannels * kPartThreads / 32;
+  __shared__ float red[2][kWarps][kPartChannels];
+  const int c = blockIdx.x * kPartChannels + threadIdx.x;
   float s0 = 0.f, s1 = 0.f;
   if (c < a.D) {
-#pragma unroll 4
     for (int p = threadIdx.y; p < a.parts; p += kPartThreads) {
       s0 += a.ws[(int64_t)p * 2 * a.D + c];
       if (a.dnext_weight) s1 += a.ws[(int64_t)p * 2 * a.D + a.D + c];
     }
   }
-  red[0][threadIdx.y][threadIdx.x] = s0;
-  red[1][threadIdx.y][threadIdx.x] = s1;
+#pragma unroll
+  for (int o = kPartChannels; o < 32; o *= 2) {
+    s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+  }
+  const int lane = (threadIdx.y * kPartChannels + threadIdx.x) % 32,
+            warp = (threadIdx.y * kPartChannels + threadIdx.x) / 32;
+  if (lane < kPartChannels) red[0][warp][lane] = s0, red[1][warp][lane] = s1;
   __syncthreads();
   if (threadIdx.y == 0 && c < a.D) {
-    for (int p = 1; p < kPartThreads; ++p)
-      s0 += red[0][p][threadIdx.x], s1 += red[1][p][threadIdx.x];
+    s0 = s1 = 0.f;
+    for (int w = 0; w < kWarps; ++w) s0 += red[0][w][threadIdx.x], s1 += red[1][w][threadIdx.x];
     if (a.dweight) a.dweight[c] = a.scale ? s0 * a.scale[c] : s0;
     if (a.dscale) a.dscale[c] = a.weight ? s0 * a.weight[c] : s0;
     if (a.dnext_weight) a.dnext_weight[c] = s1;
@@ -256,7 +262,8 @@ cudaError_t launch_norm_bwd(const NormArgs& args, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   if (a.dweight || a.dscale || a.dnext_weight)
-    norm_params_kernel<<<(unsigned)((a.D + 31) / 32), dim3(32, kPartThreads), 0, stream>>>(a);
+    norm_params_kernel<<<(unsigned)((a.D + kPartChannels - 1) / kPartChannels),
+                         dim3(kPartChannels, kPartThreads), 0, stream>>>(a);
   return cudaGetLastError();
 }
 
