@@ -100,26 +100,26 @@ __global__ void __launch_bounds__(kThreads)
     decay_join_kernel(const __grid_constant__ DecayPass a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t size = (int64_t)a.m * a.dv;
-  const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (at >= a.B * a.H * size) return;
-  const int64_t bh = at / size, b = bh / a.H;
-  const int e = (int)(at % size), i = e / a.dv, j = e % a.dv;
+  const unsigned size = a.m * a.dv, tiles = (size + kThreads - 1) / kThreads;
+  const unsigned bh = blockIdx.x / tiles, b = bh / (unsigned)a.H;
+  const unsigned e = (blockIdx.x - bh * tiles) * kThreads + threadIdx.x;
+  if (e >= size) return;
+  const unsigned i = e / (unsigned)a.dv, j = e - i * a.dv;
   const int64_t n = row_length(a.lengths, b, a.T);
-  const float g = decay_rate(a.log_decay, (int)(bh % a.H));
-  const int64_t seat = bh * size + (int64_t)i * a.si + (int64_t)j * a.sj;
+  const float g = decay_rate(a.log_decay, (int)(bh - b * (unsigned)a.H));
+  const int64_t seat = (int64_t)bh * size + i * a.si + j * a.sj;
   float X = a.S_init ? a.S_init[seat] : 0.f;
-  float* st = a.states + bh * a.runs * size + e;
+  float* st = a.states + (int64_t)bh * a.runs * size + e;
   for (int s0 = 0; s0 < a.runs; s0 += kAhead) {
     float U[kAhead];
 #pragma unroll
     for (int s = 0; s < kAhead; ++s)
-      if (s0 + s < a.runs) U[s] = st[(a.rev ? a.runs - 1 - s0 - s : s0 + s) * size];
+      if (s0 + s < a.runs) U[s] = st[(int64_t)(a.rev ? a.runs - 1 - s0 - s : s0 + s) * size];
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
       if (s0 + s >= a.runs) break;
       const int r = a.rev ? a.runs - 1 - s0 - s : s0 + s;
-      st[r * size] = X;
+      st[(int64_t)r * size] = X;
       const float len = (float)run_tokens(n, r, a.run_len);
       X = fmaf(expm1f(g * len), X, X) + U[s];
     }
@@ -354,9 +354,8 @@ cudaError_t simt_pass(const falcon_decay_shape& s, DecayPass p, cudaStream_t str
 }  // namespace
 
 cudaError_t launch_decay_join(const DecayPass& p, bool early, cudaStream_t stream) {
-  const int64_t elements = p.B * p.H * p.m * p.dv;
-  return launch_behind(early, decay_join_kernel, (unsigned)ceil_div(elements, kThreads), kThreads,
-                       0, stream, p);
+  const int64_t blocks = p.B * p.H * ceil_div((int64_t)p.m * p.dv, kThreads);
+  return launch_behind(early, decay_join_kernel, (unsigned)blocks, kThreads, 0, stream, p);
 }
 
 size_t decay_workspace_bytes(const falcon_decay_shape& s, bool) { return pass_bytes(s); }
