@@ -20,7 +20,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 64;         // rows and columns of a block's tile
 constexpr int kLd = kTile + 4;    // row stride in shared memory
-constexpr int kStep = 32;         // tokens (states) or keys (reads) staged at a time
+constexpr int kStep = 32;         // tokens staged at a time (states)
+constexpr int kKeys = 64;         // keys staged at a time (reads)
 constexpr int kChunk = 64;        // tokens of a chunk
 constexpr int kWholeTokens = 128;  // rows of at most so many are one run
 constexpr int kTcFrom = 64;        // longer rows go to the tensor cores
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 struct ReadSmem {
-  float q[kStep * kLd], k[kStep * kLd];  // transposed: [key][token]
+  float q[kKeys * kLd], k[kKeys * kLd];  // transposed: [key][token]
   float v[kChunk * kLd];                 // [token][value]
   float p[kChunk * kLd];                 // [source][token]; then weighted keys [token][key]
   float S[128 * kLd];                    // [key][value]
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kThreads)
   const E* v = static_cast<const E*>(a.v) + b * a.vs.batch + h * a.vs.head;
   E* o = static_cast<E*>(a.o) + b * a.os.batch + h * a.os.head;
   const int ti = (tid >> 4) * 4, tj = (tid & 15) * 4;
-  const int mpad = (a.m + kStep - 1) / kStep * kStep;
+  const int mpad = (a.m + kKeys - 1) / kKeys * kKeys;
   const int64_t first = run * a.run_len;
   const int64_t end = first + a.run_len < a.T ? first + a.run_len : a.T;
   const int chunks = (int)((end - first + kChunk - 1) / kChunk);
@@ -168,29 +169,37 @@ __global__ void __launch_bounds__(kThreads)
     const int rows = (int)(end - t0 < kChunk ? end - t0 : kChunk);
     float P[4][4] = {}, O[4][4] = {};
     if (have > 0) {
-      for (int e = tid; e < kChunk * (kTile / 4); e += kThreads) {
-        const int r = e / (kTile / 4), c = e % (kTile / 4) * 4;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < have) y = row_quad<E>(v + (t0 + r) * a.vs.time, j0 + c, a.dv, a.vec_v);
-        *reinterpret_cast<float4*>(sm.v + r * kLd + c) = y;
-      }
-      for (int mk = 0; mk < a.m; mk += kStep) {
-        __syncthreads();
-        for (int e = tid; e < kChunk * (kStep / 4); e += kThreads) {
-          const int r = e % kChunk, c = e / kChunk * 4;
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      constexpr int kEach = kChunk * kTile / 4 / kThreads;  // quads of a thread
+      for (int mk = 0; mk < a.m; mk += kKeys) {
+        // all loads under way before the first is stored
+        float4 x[kEach], y[kEach], z[kEach];
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+          const int e = tid + u * kThreads, r = e % kChunk, c = e / kChunk * 4;
+          const int vr = e / (kTile / 4), vc = e % (kTile / 4) * 4;
+          x[u] = y[u] = z[u] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (r < have) {
-            x = row_quad<E>(q + (t0 + r) * a.qs.time, mk + c, a.m, a.vec_q);
-            y = row_quad<E>(k + (t0 + r) * a.ks.time, mk + c, a.m, a.vec_k);
+            x[u] = row_quad<E>(q + (t0 + r) * a.qs.time, mk + c, a.m, a.vec_q);
+            y[u] = row_quad<E>(k + (t0 + r) * a.ks.time, mk + c, a.m, a.vec_k);
           }
-          sm.q[c * kLd + r] = x.x, sm.q[(c + 1) * kLd + r] = x.y;
-          sm.q[(c + 2) * kLd + r] = x.z, sm.q[(c + 3) * kLd + r] = x.w;
-          sm.k[c * kLd + r] = y.x, sm.k[(c + 1) * kLd + r] = y.y;
-          sm.k[(c + 2) * kLd + r] = y.z, sm.k[(c + 3) * kLd + r] = y.w;
+          if (mk == 0 && vr < have)
+            z[u] = row_quad<E>(v + (t0 + vr) * a.vs.time, j0 + vc, a.dv, a.vec_v);
         }
         __syncthreads();
-        outer_sum(P, sm.q + ti, sm.k + tj, kStep);
-        outer_sum(O, sm.q + ti, sm.S + mk * kLd + tj, kStep);
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+          const int e = tid + u * kThreads, r = e % kChunk, c = e / kChunk * 4;
+          sm.q[c * kLd + r] = x[u].x, sm.q[(c + 1) * kLd + r] = x[u].y;
+          sm.q[(c + 2) * kLd + r] = x[u].z, sm.q[(c + 3) * kLd + r] = x[u].w;
+          sm.k[c * kLd + r] = y[u].x, sm.k[(c + 1) * kLd + r] = y[u].y;
+          sm.k[(c + 2) * kLd + r] = y[u].z, sm.k[(c + 3) * kLd + r] = y[u].w;
+          if (mk == 0)
+            *reinterpret_cast<float4*>(sm.v + e / (kTile / 4) * kLd + e % (kTile / 4) * 4) = z[u];
+        }
+        __syncthreads();
+        const int keys = a.m - mk < kKeys ? a.m - mk : kKeys;
+        outer_sum(P, sm.q + ti, sm.k + tj, keys);
+        outer_sum(O, sm.q + ti, sm.S + mk * kLd + tj, keys);
       }
       const float intra = a.inter * a.w;
 #pragma unroll
