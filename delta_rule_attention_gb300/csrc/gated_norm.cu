@@ -18,7 +18,7 @@ namespace {
 
 // Inputs: h, z and x, those that there are.
 template <typename E, int V, int K, int MODE>
-__global__ void __launch_bounds__(V > 1 ? 256 : K == 8 ? 1024 : 512, V > 1 ? 2 : 1)
+__global__ void __launch_bounds__(K == 16 ? 512 : 256, K == 16 ? 1 : 2)
     norm_fwd_kernel(const __grid_constant__ NormArgs a, int ring, int params_bytes,
                     int staged_bytes) {
   extern __shared__ __align__(16) unsigned char shared[];
@@ -41,16 +41,15 @@ __global__ void __launch_bounds__(V > 1 ? 256 : K == 8 ? 1024 : 512, V > 1 ? 2 :
   auto copy_row = [&](const RowAt& r, int slot) {
     if constexpr (ahead) {
       unsigned char* to = mine + slot * row_bytes;
-      const E *hp = row_of<E>(a.h, a.hs, r), *zp = row_of<E>(a.z, a.zs, r),
-              *xp = row_of<E>(a.x, a.xs, r);
+      const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
+              *xp = row_in<E>(a.x, a.xs, r);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const bool on = at[k].live && r.held;
-        const int c = on ? at[k].c : 0;
         if (a.h)
-          copy_ahead<E, V>(to + k * vec, hp + (on ? in_heads<MODE>(a, a.hs, at[k]) : 0), on);
-        if (a.z) copy_ahead<E, V>(to + at_z + k * vec, zp + c, on);
-        if (a.x) copy_ahead<E, V>(to + at_x + k * vec, xp + c, on);
+          copy_ahead<E, V>(to + k * vec, hp + in_heads<MODE>(a, a.hs, at[k]), on);
+        if (a.z) copy_ahead<E, V>(to + at_z + k * vec, zp + at[k].c, on);
+        if (a.x) copy_ahead<E, V>(to + at_x + k * vec, xp + at[k].c, on);
       }
       ahead_commit();
     }
@@ -67,8 +66,8 @@ __global__ void __launch_bounds__(V > 1 ? 256 : K == 8 ? 1024 : 512, V > 1 ? 2 :
   for (int64_t row = row0; row - threadIdx.y < rows; row += step, r.advance(a)) {
     if (ahead) ahead_wait(ring - 1);
     const unsigned char* from = mine + slot * row_bytes;
-    const E *hp = row_of<E>(a.h, a.hs, r), *zp = row_of<E>(a.z, a.zs, r),
-            *xp = row_of<E>(a.x, a.xs, r);
+    const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
+            *xp = row_in<E>(a.x, a.xs, r);
     auto input = [&](bool given, int off, const E* p, int64_t c, int k) {
       Held<E, V> v = {};
       if (given) v = held_vec<E, V>(from + off + k * vec, p + c, at[k].live && r.held);
@@ -96,7 +95,7 @@ __global__ void __launch_bounds__(V > 1 ? 256 : K == 8 ? 1024 : 512, V > 1 ? 2 :
           n = mul_of<V>(n, gates(input(true, at_z, zp, at[k].c, k), a.gate));
         }
         const FloatV<V> x = wide(input(a.x, at_x, xp, at[k].c, k));
-        n = fma_of<V>(n, param_vec<V>(par + (at[k].live ? at[k].c : 0)), x);
+        n = fma_of<V>(n, param_vec<V>(par + at[k].c), x);
         y[k] = n;
         put_vec<E, V>(op + at[k].c, n, at[k].live && r.in, r.held);
       }
@@ -119,8 +118,8 @@ __global__ void __launch_bounds__(V > 1 ? 256 : K == 8 ? 1024 : 512, V > 1 ? 2 :
 #pragma unroll
       for (int k = 0; k < K; ++k)
         put_vec<E, V>(np + at[k].c,
-                      mul_of<V>(times<V>(y[k], rn),
-                                 param_vec<V>(par + a.D + (at[k].live ? at[k].c : 0))), at[k].live && r.in, r.held);
+                      mul_of<V>(times<V>(y[k], rn), param_vec<V>(par + a.D + at[k].c)),
+                      at[k].live && r.in, r.held);
     }
   }
 }
@@ -142,6 +141,8 @@ cudaError_t start_count(const NormArgs& a, const NormPlan& p, unsigned grid,
   if constexpr (V > 1) {
     if (p.K == 2) return start_mode<E, V, 2>(a, p, grid, stream);
     if (p.K == 3) return start_mode<E, V, 3>(a, p, grid, stream);
+  } else {
+    if (p.K == 16) return start_mode<E, V, 16>(a, p, grid, stream);
   }
   if (p.K == 4) return start_mode<E, V, 4>(a, p, grid, stream);
   return start_mode<E, V, 8>(a, p, grid, stream);

@@ -127,8 +127,9 @@ __device__ __forceinline__ Held<E, V> held_vec(const unsigned char* slot, const 
   if constexpr (Slot<E, V>::kAhead) {
     const uint4 q = *reinterpret_cast<const uint4*>(slot);
     r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
-  } else if (live) {
-    r.w[0] = __float_as_uint(load_vec<E, 1>(from).v[0]);
+  } else {
+    const float x = load_vec<E, 1>(from).v[0];  // no branch: all loads under way at once
+    r.w[0] = live ? __float_as_uint(x) : 0u;
   }
   return r;
 }
@@ -252,7 +253,7 @@ struct RowAt {
   }
 };
 
-// Channel and head of vector k of a thread.
+// Channel and head of vector k of a thread (the row's first where it has none).
 struct Place {
   int c, head;
   bool live;
@@ -262,11 +263,18 @@ __device__ __forceinline__ Place place_of(const NormArgs& a, int k) {
   Place p;
   p.c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
   p.live = p.c < a.D;
-  p.head = MODE == kWhole || !p.live ? 0 : p.c / a.m;
+  if (!p.live) p.c = 0;
+  p.head = MODE == kWhole ? 0 : p.c / a.m;
   return p;
 }
 
-// Where the row's tensors begin, and vector `at` of a head-major one in it.
+// Where the row's tensors begin (the first row's where none is to be read), and vector
+// `at` of a head-major one in it.
+template <typename E>
+__device__ __forceinline__ const E* row_in(const void* p, const falcon_strides& s,
+                                           const RowAt& r) {
+  return static_cast<const E*>(p) + (r.held ? r.b * s.batch + r.t * s.time : 0);
+}
 template <typename E>
 __device__ __forceinline__ E* row_of(const void* p, const falcon_strides& s, const RowAt& r) {
   return static_cast<E*>(const_cast<void*>(p)) + (r.in ? r.b * s.batch + r.t * s.time : 0);
@@ -355,9 +363,15 @@ constexpr int kRowThreads = 128, kNarrowThreads = 256;
 // Dynamic shared memory of each of `per` blocks of an SM, beside 5 KB of its own.
 constexpr size_t shared_for(int per) { return 228 * 1024 / per - 5 * 1024 - 256; }
 
-// widths: rising; the last one has to do for the widest row.  With many rows a thread holds as many as leave `enough` warps in all (a row's sums then
-// cost fewer steps, and more of its loads are under way at once), up to `prefer`, or four
-// where that makes a row one warp's; with few rows a row is spread over more threads.
+// Those of single elements; the last is for the widest rows.
+constexpr Width kNarrow[] = {{1, 256, 512}, {4, 256, 512}, {8, 256, 512}, {16, 512, 512}};
+
+// widths: rising; the last one has to do for the widest row.  Of those that leave `enough`
+// warps in all, the one whose row takes the fewest instructions: about as many for a warp's
+// sums and addresses as for 24 values a thread (2048 channels in 128 threads: 107 us, in
+// 32: 53 us).  With few rows the narrowest, which spreads a row over the most threads.
+// More than `prefer` (single elements: two more) only where that makes a row one warp's, up
+// to four (eight), or nothing less will do: a thread's registers.
 template <int COUNTS>
 NormPlan plan_norm(const NormArgs& a, const Width (&widths)[COUNTS], int prefer, int64_t enough,
                    int inputs, bool narrow) {
@@ -378,10 +392,11 @@ NormPlan plan_norm(const NormArgs& a, const Width (&widths)[COUNTS], int prefer,
   const bool lanes = each <= 32 && (each & (each - 1)) == 0;
   p.mode = lanes ? kLanes : a.H == 1 ? kWhole : kStaged;
   const int64_t rows = a.B * a.T;
-  int waste = 0, resident = 0;
-  for (int i = 0; i < COUNTS; ++i) {
-    const int K = widths[i].K;
-    if (p.V == 1 && K != 1 && K != 4 && i + 1 < COUNTS) continue;
+  int resident = 0, least = 0;
+  const int counts = p.V > 1 ? COUNTS : 4;
+  for (int i = 0; i < counts; ++i) {
+    const Width& w = p.V > 1 ? widths[i] : kNarrow[i];
+    const int K = w.K;
     int nt = (vecs + K - 1) / K;
     if (nt <= 16 && p.mode != kStaged) {
       int up = 1;
@@ -390,16 +405,15 @@ NormPlan plan_norm(const NormArgs& a, const Width (&widths)[COUNTS], int prefer,
     } else {
       nt = (nt + 31) / 32 * 32;
     }
-    if (nt > (p.V > 1 ? widths[i].threads : K == 8 ? 1024 : 512)) continue;
+    if (nt > w.threads) continue;
     // a head's lanes lie in one row, side by side
     if (p.mode == kLanes && nt < each) continue;
-    const int idle = nt * K - vecs;
-    const bool first = p.K == 0;
-    // a thread without work costs more than a shorter row saves
-    if (!first && ((K > (p.V > 1 ? prefer : 4) && (nt > 32 || K > 4)) || (rows * nt + 31) / 32 < enough || idle > waste + vecs / 8))
+    const int cost = (nt < 32 ? 1 : nt / 32) * (24 + K * p.V);
+    if (p.K && (cost >= least || (rows * nt + 31) / 32 < enough ||
+                (p.V > 1 ? K > prefer && (nt > 32 || K > 4)
+                         : K > prefer + 2 && (nt > 32 || K > 8))))
       continue;
-    if (first || idle < waste) waste = idle;
-    p.K = K, p.nt = nt, resident = p.V > 1 ? widths[i].resident : K == 8 ? 1024 : 512;
+    p.K = K, p.nt = nt, least = cost, resident = w.resident;
   }
   p.rows = (p.V == 1 ? kNarrowThreads : kRowThreads) / p.nt;
   if (p.rows < 1) p.rows = 1;

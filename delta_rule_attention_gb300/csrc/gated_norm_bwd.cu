@@ -9,8 +9,11 @@ namespace {
 
 // Inputs: h, z, dout, out and dnext, those that there are.
 template <typename E, int V, int K, int MODE>
-__global__ void __launch_bounds__(V == 1 ? (K == 8 ? 1024 : 512) : K == 3 || K == 4 ? 128 : 256,
-                                  V == 1 ? 1 : K == 3 || K == 4 ? 3 : K == 8 ? 1 : 2)
+__global__ void __launch_bounds__(V == 1 ? (K == 16 ? 512 : 256) : K == 3 || K == 4 ? 128 : 256,
+                                  V == 1 ? (K == 16 ? 1 : 2)
+                                  : K == 3 || K == 4 ? 3
+                                  : K == 8           ? 1
+                                                     : 2)
     norm_bwd_kernel(const __grid_constant__ NormArgs a, int ring, int params_bytes,
                     int staged_bytes) {
   extern __shared__ __align__(16) unsigned char shared[];
@@ -38,20 +41,19 @@ __global__ void __launch_bounds__(V == 1 ? (K == 8 ? 1024 : 512) : K == 3 || K =
   auto copy_row = [&](const RowAt& r, int slot) {
     if constexpr (ahead) {
       unsigned char* to = mine + slot * row_bytes;
-      const E *hp = row_of<E>(a.h, a.hs, r), *zp = row_of<E>(a.z, a.zs, r),
-              *dp = row_of<E>(a.dout, a.dos, r), *yp = row_of<E>(a.y, a.os, r),
-              *ep = row_of<E>(a.dnext, a.dns, r);
+      const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
+              *dp = row_in<E>(a.dout, a.dos, r), *yp = row_in<E>(a.y, a.os, r),
+              *ep = row_in<E>(a.dnext, a.dns, r);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const bool on = at[k].live && r.held;
-        const int c = on ? at[k].c : 0;
         if (a.h)
-          copy_ahead<E, V>(to + k * vec, hp + (on ? in_heads<MODE>(a, a.hs, at[k]) : 0), on);
-        if (a.z) copy_ahead<E, V>(to + at_z + k * vec, zp + c, on);
-        if (a.dout) copy_ahead<E, V>(to + at_d + k * vec, dp + c, on);
+          copy_ahead<E, V>(to + k * vec, hp + in_heads<MODE>(a, a.hs, at[k]), on);
+        if (a.z) copy_ahead<E, V>(to + at_z + k * vec, zp + at[k].c, on);
+        if (a.dout) copy_ahead<E, V>(to + at_d + k * vec, dp + at[k].c, on);
         if (a.next_weight) {
-          copy_ahead<E, V>(to + at_y + k * vec, yp + c, on);
-          copy_ahead<E, V>(to + at_e + k * vec, ep + c, on);
+          copy_ahead<E, V>(to + at_y + k * vec, yp + at[k].c, on);
+          copy_ahead<E, V>(to + at_e + k * vec, ep + at[k].c, on);
         }
       }
       ahead_commit();
@@ -73,7 +75,7 @@ __global__ void __launch_bounds__(V == 1 ? (K == 8 ? 1024 : 512) : K == 3 || K =
                      int k) {
       Held<E, V> v = {};
       if (given)
-        v = held_vec<E, V>(from + off + k * vec, row_of<E>(p, s, r) + c, at[k].live && r.held);
+        v = held_vec<E, V>(from + off + k * vec, row_in<E>(p, s, r) + c, at[k].live && r.held);
       return v;
     };
     auto in_h = [&](int k) {
@@ -82,8 +84,8 @@ __global__ void __launch_bounds__(V == 1 ? (K == 8 ? 1024 : 512) : K == 3 || K =
     auto in_z = [&](int k) { return input(true, at_z, a.z, a.zs, at[k].c, k); };
     auto in_y = [&](int k) { return wide(input(true, at_y, a.y, a.os, at[k].c, k)); };
     auto in_e = [&](int k) { return wide(input(true, at_e, a.dnext, a.dns, at[k].c, k)); };
-    auto ws = [&](int k) { return param_vec<V>(par + (at[k].live ? at[k].c : 0)); };
-    auto wn = [&](int k) { return param_vec<V>(par + a.D + (at[k].live ? at[k].c : 0)); };
+    auto ws = [&](int k) { return param_vec<V>(par + at[k].c); };
+    auto wn = [&](int k) { return param_vec<V>(par + a.D + at[k].c); };
     FloatV<V> d[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) d[k] = wide(input(a.dout, at_d, a.dout, a.dos, at[k].c, k));
@@ -223,6 +225,8 @@ cudaError_t start_count(const NormArgs& a, const NormPlan& p, unsigned grid,
   if constexpr (V > 1) {
     if (p.K == 2) return start_mode<E, V, 2>(a, p, grid, stream);
     if (p.K == 3) return start_mode<E, V, 3>(a, p, grid, stream);
+  } else {
+    if (p.K == 16) return start_mode<E, V, 16>(a, p, grid, stream);
   }
   if (p.K == 4) return start_mode<E, V, 4>(a, p, grid, stream);
   return start_mode<E, V, 8>(a, p, grid, stream);
