@@ -329,9 +329,12 @@ cudaError_t run_pass(DecayPass& p, cudaStream_t stream) {
   p.vec_q = quads(p.q, p.qs, p.dtype), p.vec_k = quads(p.k, p.ks, p.dtype);
   p.vec_v = quads(p.v, p.vs, p.dtype), p.vec_o = quads(p.o, p.os, p.dtype);
   const int64_t bh = p.B * p.H;
-  // a row of few chunks as one run, whose state the reads carry themselves: one launch
-  // instead of three (T 64: a call 25 -> 18 us, all of it the host's)
-  if (p.T > 0 && p.T <= kWholeTokens) p.runs = 1, p.run_len = kWholeTokens, p.whole = true;
+  // Rows that are one run carry their state themselves: one launch instead of three.  Of
+  // few chunks they are made one (fp32, 2 heads of 64: T 64 13.8 us for 18.3 in a graph, T
+  // 128 25.1 for 18.5, but a call by itself 18.5 for the host's 25; 1024 heads 82.7 for 128 and
+  // 166 for 229).
+  if (p.T > 0 && p.T <= kWholeTokens) p.runs = 1, p.run_len = kWholeTokens;
+  p.whole = p.runs == 1;
   const unsigned grid = (unsigned)(bh * p.runs);
   const unsigned vt = (unsigned)ceil_div(p.dv, kTile), mt = (unsigned)ceil_div(p.m, kTile);
   if (p.runs > 0 && !p.whole)
@@ -347,7 +350,9 @@ cudaError_t run_pass(DecayPass& p, cudaStream_t stream) {
 }
 
 // A pass with its tensors set, on the tensor cores; false where they do not fit.
-// Rows that are one run here take one launch, against three there.
+// Rows of one chunk here take one launch, against three there: a call by itself takes the
+// host 19 us for 26 (in a graph 15 us here for 9 there with 2 heads of 64, 83 for 75 with
+// 1024; longer rows 27 for 9.6 and 156 for 77).
 bool tc_pass(const falcon_decay_shape& s, DecayPass p, cudaError_t* e, cudaStream_t stream) {
   if (p.T <= kTcFrom) return false;
   const DecayPass split = shape_pass(s, p.m, p.dv, true);
