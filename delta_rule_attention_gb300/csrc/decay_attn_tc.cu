@@ -18,6 +18,13 @@
 // fills the missing channels with zeros.  All accumulators have 128 lanes; for N = 64 the
 // second half of V^T as an A operand is the tile behind it in shared memory, which lands
 // in lanes 64..127 that nobody reads.
+//
+// Measured (96 heads of 64, 2048 tokens; 16 heads of 128, 65536 tokens): a call 50 us, of
+// which the states take 19 and the reads 29 (floor of the call's bytes: 15); 293 us, 99 and
+// 175 (158).  The states are bound by shared memory, through which three terms of every
+// key go to the tensor cores, the reads by the chain from one chunk's state to the next
+// (3300 cycles a chunk of 64 channels).  One block an SM whose warps have roles took the place
+// of two blocks an SM that went through the phases together: 68 us and 609.
 #include <cuda_bf16.h>
 
 #include "linear.cuh"
@@ -230,7 +237,8 @@ struct Item {
 // for the whole run.
 //
 // Sixteen warps weigh and split the keys of a chunk while the products of the chunk before
-// run; the same warps take out the sums.
+// run; the same warps take out the sums.  (Two sets of eight, a chunk each: 20.7 us for
+// 18.7.)
 template <int M, int N>
 struct StatePlan {
   static constexpr bool kSide = M == 64;            // terms side by side
@@ -422,7 +430,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 //   C  X^T += V^T Kd        weighted keys in two terms; only where another chunk follows
 //   D  O = P V              P read from TMEM
 // One warp sends A and D, the other B and C.
-// The other eight warps write gamma^{i+1} Oi + O and carry X.
+// The other eight warps write gamma^{i+1} Oi + O and carry X.  (C sent before B, and the state
+// taken out before the outputs: 208 us for 175 with 128 channels, 29.6 for 28.5 with 64.)
 template <int M, int N>
 struct ReadPlan {
   static constexpr bool kSide = M == 64;  // the two terms side by side, one product
@@ -660,30 +669,30 @@ __global__ void __launch_bounds__(kReadThreads, 1)
             arrive_warp(ctl, L::kOFree);
           }
           if (ch.t0 + row < it.end) {
-          uint32_t z[16];
+            uint32_t z[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            z[j] = live ? pack_bf16(fmaf(far, y[2 * j], x[2 * j]),
-                                    fmaf(far, y[2 * j + 1], x[2 * j + 1]))
-                        : 0u;
-          __nv_bfloat16* to = out + (ch.t0 + row) * p.os.time + col;
-          if (a.wide_o) {
+            for (int j = 0; j < 16; ++j)
+              z[j] = live ? pack_bf16(fmaf(far, y[2 * j], x[2 * j]),
+                                      fmaf(far, y[2 * j + 1], x[2 * j + 1]))
+                          : 0u;
+            __nv_bfloat16* to = out + (ch.t0 + row) * p.os.time + col;
+            if (a.wide_o) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (col + 16 * e < p.dv)
-                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(
-                                 to + 16 * e),
-                             "r"(z[8 * e]), "r"(z[8 * e + 1]), "r"(z[8 * e + 2]),
-                             "r"(z[8 * e + 3]), "r"(z[8 * e + 4]), "r"(z[8 * e + 5]),
-                             "r"(z[8 * e + 6]), "r"(z[8 * e + 7])
-                             : "memory");
-          } else {
+              for (int e = 0; e < 2; ++e)
+                if (col + 16 * e < p.dv)
+                  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(
+                                   to + 16 * e),
+                               "r"(z[8 * e]), "r"(z[8 * e + 1]), "r"(z[8 * e + 2]),
+                               "r"(z[8 * e + 3]), "r"(z[8 * e + 4]), "r"(z[8 * e + 5]),
+                               "r"(z[8 * e + 6]), "r"(z[8 * e + 7])
+                               : "memory");
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (col + 8 * e < p.dv)
-                *reinterpret_cast<uint4*>(to + 8 * e) =
-                    make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
-          }
+              for (int e = 0; e < 4; ++e)
+                if (col + 8 * e < p.dv)
+                  *reinterpret_cast<uint4*>(to + 8 * e) =
+                      make_uint4(z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+            }
           }
           __syncwarp();
         }
@@ -753,7 +762,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
       tc_fence_after();
       const uint32_t q = desc_low(base + L::Q + qs * L::kQ, 16),
                      k = desc_low(base + L::K + ks * L::kK, 16);
-        if (elect_one()) {  // behind the D that read this P
+      if (elect_one()) {  // behind the D that read this P
 #pragma unroll
         for (int s = 0; s < M / 16; ++s) {
           const uint32_t at = (s >> 2) * (kTile >> 4) + (s & 3) * kStepK;

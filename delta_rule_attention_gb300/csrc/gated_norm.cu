@@ -11,6 +11,12 @@
 //   dh = r (f - h r^2 mean_head(f h))
 //   dw = scale sum(d act(z) n),  dscale = w sum(d act(z) n),  dw' = sum(du y s)
 // whose kernel is in gated_norm_bwd.cu.
+//
+// Measured: 16384 rows of 2048 channels with gate, residual and next norm (bf16, 268 MB)
+// 52.7 us, 5.1 TB/s; 16384 rows of 12 heads of 64 (75 MB) 23 us.  With many rows a row is one
+// warp's: a row costs a warp about 450 instructions for sums and addresses whatever its
+// width, so 2048 channels in four warps took 107 us.  What is left is issue slots (49%) and
+// the shared-memory pipe (62%), through which the inputs and parameters pass.
 #include "gated_norm.cuh"
 
 namespace falcon {

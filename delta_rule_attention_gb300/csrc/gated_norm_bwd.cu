@@ -2,6 +2,11 @@
 // the next row's inputs are loaded while this row's sums are formed, and a thread keeps
 // the sums over rows of its channels for the parameters; a second kernel adds the blocks'
 // sums in a fixed order.
+//
+// Bound by instructions, about 45 a value: 16384 rows of 2048 channels (bf16, 403 MB) 110 us,
+// 3.7 TB/s, of which the blocks' sums take 6 (8 with a block for every 32 channels).  The
+// plan's limit of two vectors a thread: with four, 384 threads an SM hold the registers and
+// the same rows take 118 us; one instruction for two values (112 us before: 114).
 #include "gated_norm.cuh"
 
 namespace falcon {

@@ -64,7 +64,7 @@ struct DecayCall {
   float *S_out, *dS0;
   void* ws;
 };
-size_t decay_workspace_bytes(const falcon_decay_shape& s, bool backward);
+size_t decay_workspace_bytes(const falcon_decay_shape& s);
 cudaError_t launch_decay_fwd(const DecayCall& c, cudaStream_t stream);
 cudaError_t launch_decay_bwd(const DecayCall& c, cudaStream_t stream);
 

@@ -87,7 +87,7 @@ extern "C" {
 
 size_t falcon_decay_attn_workspace_bytes(const falcon_decay_shape* s) {
   if (check_decay(s) != FALCON_OK || s->B == 0 || s->H == 0) return 0;
-  return falcon::decay_workspace_bytes(*s, false);
+  return falcon::decay_workspace_bytes(*s);
 }
 
 int falcon_decay_attn_fwd(const falcon_decay_shape* s, const void* q, const falcon_strides* qs,
@@ -128,7 +128,7 @@ int falcon_decay_attn_fwd(const falcon_decay_shape* s, const void* q, const falc
 
 size_t falcon_decay_attn_bwd_workspace_bytes(const falcon_decay_shape* s) {
   if (check_decay(s) != FALCON_OK || s->B == 0 || s->H == 0) return 0;
-  return falcon::decay_workspace_bytes(*s, true);
+  return falcon::decay_workspace_bytes(*s);
 }
 
 int falcon_decay_attn_bwd(const falcon_decay_shape* s, const void* q, const falcon_strides* qs,

@@ -152,14 +152,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
 }
 
 // The same for 4-D tensor maps, coordinates (x, y, z, w).
-__device__ __forceinline__ void tma_store_4d(const void* map, const void* src, int x, int y,
-                                             int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-          map),
-      "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(src))
-      : "memory");
-}
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, int y, int z,
                                             int w, uint64_t* bar) {
   asm volatile(
@@ -281,17 +273,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The same with A in TMEM (K-major: a lane holds a row, a 32-bit column two neighbouring
-// bf16 of it; one instruction reads 8 columns).
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 

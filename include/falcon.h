@@ -634,6 +634,9 @@ typedef struct {
  *              nullable, may be S0
  *   workspace: at least falcon_decay_attn_workspace_bytes(shape) bytes, 256-byte
  *   aligned: a state for every run of tokens that is worked on by itself.
+ * A NaN or infinity in a token reaches the tokens behind it, and may reach those before
+ * it among the 128 that are worked on together; a token whose weight in a state is zero
+ * in float32 (gamma^n below 2^-149) is left out of it, whatever it holds.
  * Errors: FALCON_ERR_NULL_PTR, _BAD_SHAPE, _BAD_DTYPE, _MISALIGNED, _WORKSPACE,
  * _BAD_ARG (negative stride, o where an input starts or on itself, scale not
  * finite), _DEVICE; _CUDA. */

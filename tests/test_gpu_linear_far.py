@@ -74,6 +74,15 @@ def test_many_narrow_rows(falcon, rows, H, m, dtype):  # noqa: F811
         assert (off <= 2.0 ** -23 * 1024 * t.abs().sum((0, 1))).all(), name
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,H,m", [(5000, 1, 1051), (2500, 1, 2055), (2500, 1, 4099), (2500, 1, 8191),
+                                      (2500, 1, 8192), (2500, 12, 111), (2500, 11, 97),
+                                      (9000, 1, 130), (2500, 2, 2048)])
+def test_many_wide_rows(falcon, rows, H, m, dtype):  # noqa: F811
+    """Rows that leave room for none ahead, or lie on no 16-byte boundary."""
+    test_many_narrow_rows(falcon, rows, H, m, dtype)
+
+
 def test_step_and_norms_off_their_boundaries(falcon):  # noqa: F811
     g = gen(3)
     N, H, m, dv = 3, 2, 64, 64
