@@ -43,8 +43,20 @@ __global__ void __launch_bounds__(K == 16 ? 512 : 256, K == 16 ? 1 : 2)
   Place at[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) at[k] = place_of<V, MODE>(a, k);
-  constexpr bool ahead = Slot<E, V>::kAhead;
+  constexpr bool ahead = Slot<E, V>::kAhead, early = !ahead && K <= 8;
+  Held<E, V> own[3][early ? K : 1];
   auto copy_row = [&](const RowAt& r, int slot) {
+    if constexpr (early) {
+      const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
+              *xp = row_in<E>(a.x, a.xs, r);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const bool on = at[k].live && r.held;
+        if (a.h) own[0][k] = held_vec<E, V>(nullptr, hp + in_heads<MODE>(a, a.hs, at[k]), on);
+        if (a.z) own[1][k] = held_vec<E, V>(nullptr, zp + at[k].c, on);
+        if (a.x) own[2][k] = held_vec<E, V>(nullptr, xp + at[k].c, on);
+      }
+    }
     if constexpr (ahead) {
       unsigned char* to = mine + slot * row_bytes;
       const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
@@ -62,7 +74,7 @@ __global__ void __launch_bounds__(K == 16 ? 512 : 256, K == 16 ? 1 : 2)
   };
   const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   RowAt r(a, row0, step), next = r;
-  for (int i = 0; i < ring; ++i) {
+  for (int i = 0; i < (early ? 1 : ring); ++i) {
     copy_row(next, i);
     next.advance(a);
   }
@@ -74,13 +86,17 @@ __global__ void __launch_bounds__(K == 16 ? 512 : 256, K == 16 ? 1 : 2)
     const unsigned char* from = mine + slot * row_bytes;
     const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
             *xp = row_in<E>(a.x, a.xs, r);
-    auto input = [&](bool given, int off, const E* p, int64_t c, int k) {
+    auto input = [&](bool given, int off, int which, const E* p, int64_t c, int k) {
       Held<E, V> v = {};
+      if constexpr (early) {
+        if (given) v = own[which][k];
+        return v;
+      }
       if (given) v = held_vec<E, V>(from + off + k * vec, p + c, at[k].live && r.held);
       return v;
     };
     auto in_h = [&](int k) {
-      return wide(input(true, 0, hp, in_heads<MODE>(a, a.hs, at[k]), k));
+      return wide(input(true, 0, 0, hp, in_heads<MODE>(a, a.hs, at[k]), k));
     };
     FloatV<V> y[K];
     if (a.h) {
@@ -98,18 +114,18 @@ __global__ void __launch_bounds__(K == 16 ? 512 : 256, K == 16 ? 1 : 2)
       for (int k = 0; k < K; ++k) {
         FloatV<V> n = times<V>(in_h(k), rsqrtf(ss[k].v[0] / (float)a.m + a.eps));
         if (a.z) {
-          n = mul_of<V>(n, gates(input(true, at_z, zp, at[k].c, k), a.gate));
+          n = mul_of<V>(n, gates(input(true, at_z, 1, zp, at[k].c, k), a.gate));
         }
-        const FloatV<V> x = wide(input(a.x, at_x, xp, at[k].c, k));
+        const FloatV<V> x = wide(input(a.x, at_x, 2, xp, at[k].c, k));
         n = fma_of<V>(n, param_vec<V>(par + at[k].c), x);
         y[k] = n;
         put_vec<E, V>(op + at[k].c, n, at[k].live && r.in, r.held);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < K; ++k) y[k] = wide(input(true, at_x, xp, at[k].c, k));
+      for (int k = 0; k < K; ++k) y[k] = wide(input(true, at_x, 2, xp, at[k].c, k));
     }
-    if (ahead) {  // this row's inputs are read
+    if (ahead || early) {  // this row's inputs are read
       copy_row(next, slot);
       next.advance(a);
       slot = slot + 1 == ring ? 0 : slot + 1;

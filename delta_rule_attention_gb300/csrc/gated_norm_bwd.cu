@@ -42,8 +42,25 @@ __global__ void __launch_bounds__(V == 1 ? (K == 16 ? 512 : 256) : K == 3 || K =
     each[k] = zeros<E, V>(), nextw[k] = zeros<E, V>();
     at[k] = place_of<V, MODE>(a, k);
   }
-  constexpr bool ahead = Slot<E, V>::kAhead;
+  constexpr bool ahead = Slot<E, V>::kAhead, early = !ahead && K <= 4;
+  Held<E, V> own[5][early ? K : 1];
   auto copy_row = [&](const RowAt& r, int slot) {
+    if constexpr (early) {
+      const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
+              *dp = row_in<E>(a.dout, a.dos, r), *yp = row_in<E>(a.y, a.os, r),
+              *ep = row_in<E>(a.dnext, a.dns, r);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const bool on = at[k].live && r.held;
+        if (a.h) own[0][k] = held_vec<E, V>(nullptr, hp + in_heads<MODE>(a, a.hs, at[k]), on);
+        if (a.z) own[1][k] = held_vec<E, V>(nullptr, zp + at[k].c, on);
+        if (a.dout) own[2][k] = held_vec<E, V>(nullptr, dp + at[k].c, on);
+        if (a.next_weight) {
+          own[3][k] = held_vec<E, V>(nullptr, yp + at[k].c, on);
+          own[4][k] = held_vec<E, V>(nullptr, ep + at[k].c, on);
+        }
+      }
+    }
     if constexpr (ahead) {
       unsigned char* to = mine + slot * row_bytes;
       const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
@@ -66,7 +83,7 @@ __global__ void __launch_bounds__(V == 1 ? (K == 16 ? 512 : 256) : K == 3 || K =
   };
   const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   RowAt r(a, row0, step), next = r;
-  for (int i = 0; i < ring; ++i) {
+  for (int i = 0; i < (early ? 1 : ring); ++i) {
     copy_row(next, i);
     next.advance(a);
   }
@@ -76,24 +93,28 @@ __global__ void __launch_bounds__(V == 1 ? (K == 16 ? 512 : 256) : K == 3 || K =
   for (int64_t row = row0; row - threadIdx.y < rows; row += step, r.advance(a)) {
     if (ahead) ahead_wait(ring - 1);
     const unsigned char* from = mine + slot * row_bytes;
-    auto input = [&](bool given, int off, const void* p, const falcon_strides& s, int64_t c,
-                     int k) {
+    auto input = [&](bool given, int off, int which, const void* p, const falcon_strides& s,
+                     int64_t c, int k) {
       Held<E, V> v = {};
+      if constexpr (early) {
+        if (given) v = own[which][k];
+        return v;
+      }
       if (given)
         v = held_vec<E, V>(from + off + k * vec, row_in<E>(p, s, r) + c, at[k].live && r.held);
       return v;
     };
     auto in_h = [&](int k) {
-      return wide(input(true, 0, a.h, a.hs, in_heads<MODE>(a, a.hs, at[k]), k));
+      return wide(input(true, 0, 0, a.h, a.hs, in_heads<MODE>(a, a.hs, at[k]), k));
     };
-    auto in_z = [&](int k) { return input(true, at_z, a.z, a.zs, at[k].c, k); };
-    auto in_y = [&](int k) { return wide(input(true, at_y, a.y, a.os, at[k].c, k)); };
-    auto in_e = [&](int k) { return wide(input(true, at_e, a.dnext, a.dns, at[k].c, k)); };
+    auto in_z = [&](int k) { return input(true, at_z, 1, a.z, a.zs, at[k].c, k); };
+    auto in_y = [&](int k) { return wide(input(true, at_y, 3, a.y, a.os, at[k].c, k)); };
+    auto in_e = [&](int k) { return wide(input(true, at_e, 4, a.dnext, a.dns, at[k].c, k)); };
     auto ws = [&](int k) { return param_vec<V>(par + at[k].c); };
     auto wn = [&](int k) { return param_vec<V>(par + a.D + at[k].c); };
     FloatV<V> d[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) d[k] = wide(input(a.dout, at_d, a.dout, a.dos, at[k].c, k));
+    for (int k = 0; k < K; ++k) d[k] = wide(input(a.dout, at_d, 2, a.dout, a.dos, at[k].c, k));
     if (a.next_weight) {
       Dot<V> yy, ey;
 #pragma unroll
@@ -153,7 +174,7 @@ __global__ void __launch_bounds__(V == 1 ? (K == 16 ? 512 : 256) : K == 3 || K =
                       r.held);
       }
     }
-    if (ahead) {  // this row's inputs are read
+    if (ahead || early) {  // this row's inputs are read
       copy_row(next, slot);
       next.advance(a);
       slot = slot + 1 == ring ? 0 : slot + 1;
