@@ -24,7 +24,7 @@ namespace {
 
 // Inputs: h, z and x, those that there are.
 template <typename E, int V, int K, int MODE>
-__global__ void __launch_bounds__(K == 16 ? 512 : 256, K == 16 ? 1 : 2)
+__global__ void __launch_bounds__(V == 1 && K > 1 ? 512 : 256, V == 1 && K > 1 ? 1 : 2)
     norm_fwd_kernel(const __grid_constant__ NormArgs a, int ring, int params_bytes,
                     int staged_bytes) {
   extern __shared__ __align__(16) unsigned char shared[];
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(K == 16 ? 512 : 256, K == 16 ? 1 : 2)
   Place at[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) at[k] = place_of<V, MODE>(a, k);
-  constexpr bool ahead = Slot<E, V>::kAhead, early = !ahead && K <= 8;
+  constexpr bool ahead = Slot<E, V>::kAhead, early = !ahead;
   Held<E, V> own[3][early ? K : 1];
   auto copy_row = [&](const RowAt& r, int slot) {
     if constexpr (early) {

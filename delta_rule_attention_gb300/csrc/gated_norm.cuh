@@ -368,7 +368,7 @@ constexpr size_t shared_for(int per) { return 228 * 1024 / per - 5 * 1024 - 256;
 // gradient 382 us; 32 elements of 256 threads: 618).  Two blocks an SM and loads without
 // branches: 7312 bf16 rows of 1051 channels 51 us, 158 with one block and branches.  Copies
 // ahead of 4 bytes were slower than plain loads (90 us for 40).
-constexpr Width kNarrow[] = {{1, 256, 512}, {4, 256, 512}, {8, 256, 512}, {16, 512, 512}};
+constexpr Width kNarrow[] = {{1, 256, 512}, {4, 512, 512}, {8, 512, 512}, {16, 512, 512}};
 
 // widths: rising; the last one has to do for the widest row.  Of those that leave `enough`
 // warps in all, the one whose row takes the fewest instructions: about as many for a warp's

@@ -14,8 +14,8 @@ namespace {
 
 // Inputs: h, z, dout, out and dnext, those that there are.
 template <typename E, int V, int K, int MODE>
-__global__ void __launch_bounds__(V == 1 ? (K == 16 ? 512 : 256) : K == 3 || K == 4 ? 128 : 256,
-                                  V == 1 ? (K == 16 ? 1 : 2)
+__global__ void __launch_bounds__(V == 1 ? (K > 1 ? 512 : 256) : K == 3 || K == 4 ? 128 : 256,
+                                  V == 1 ? (K > 1 ? 1 : 2)
                                   : K == 3 || K == 4 ? 3
                                   : K == 8           ? 1
                                                      : 2)
