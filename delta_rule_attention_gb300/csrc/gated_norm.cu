@@ -43,38 +43,30 @@ __global__ void __launch_bounds__(V == 1 && K > 1 ? 512 : 256, V == 1 && K > 1 ?
   Place at[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) at[k] = place_of<V, MODE>(a, k);
-  constexpr bool ahead = Slot<E, V>::kAhead, early = !ahead;
-  Held<E, V> own[3][early ? K : 1];
+  constexpr bool ahead = Slot<E, V>::kAhead;
+  Held<E, V> own[3][ahead ? 1 : K];  // without slots: the next row's h, z and x
   auto copy_row = [&](const RowAt& r, int slot) {
-    if constexpr (early) {
-      const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
-              *xp = row_in<E>(a.x, a.xs, r);
+    unsigned char* to = mine + slot * row_bytes;
+    const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
+            *xp = row_in<E>(a.x, a.xs, r);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const bool on = at[k].live && r.held;
-        if (a.h) own[0][k] = held_vec<E, V>(nullptr, hp + in_heads<MODE>(a, a.hs, at[k]), on);
-        if (a.z) own[1][k] = held_vec<E, V>(nullptr, zp + at[k].c, on);
-        if (a.x) own[2][k] = held_vec<E, V>(nullptr, xp + at[k].c, on);
-      }
+    for (int k = 0; k < K; ++k) {
+      const bool on = at[k].live && r.held;
+      auto copy = [&](int which, int off, const E* p) {
+        if constexpr (ahead)
+          copy_ahead<E>(to + off + k * vec, p, on);
+        else
+          own[which][k] = load_own<E>(p, on);
+      };
+      if (a.h) copy(0, 0, hp + in_heads<MODE>(a, a.hs, at[k]));
+      if (a.z) copy(1, at_z, zp + at[k].c);
+      if (a.x) copy(2, at_x, xp + at[k].c);
     }
-    if constexpr (ahead) {
-      unsigned char* to = mine + slot * row_bytes;
-      const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
-              *xp = row_in<E>(a.x, a.xs, r);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const bool on = at[k].live && r.held;
-        if (a.h)
-          copy_ahead<E, V>(to + k * vec, hp + in_heads<MODE>(a, a.hs, at[k]), on);
-        if (a.z) copy_ahead<E, V>(to + at_z + k * vec, zp + at[k].c, on);
-        if (a.x) copy_ahead<E, V>(to + at_x + k * vec, xp + at[k].c, on);
-      }
-      ahead_commit();
-    }
+    if (ahead) ahead_commit();
   };
   const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   RowAt r(a, row0, step), next = r;
-  for (int i = 0; i < (early ? 1 : ring); ++i) {
+  for (int i = 0; i < (ahead ? ring : 1); ++i) {
     copy_row(next, i);
     next.advance(a);
   }
@@ -84,20 +76,16 @@ __global__ void __launch_bounds__(V == 1 && K > 1 ? 512 : 256, V == 1 && K > 1 ?
   for (int64_t row = row0; row - threadIdx.y < rows; row += step, r.advance(a)) {
     if (ahead) ahead_wait(ring - 1);
     const unsigned char* from = mine + slot * row_bytes;
-    const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
-            *xp = row_in<E>(a.x, a.xs, r);
-    auto input = [&](bool given, int off, int which, const E* p, int64_t c, int k) {
+    auto input = [&](bool given, int which, int off, int k) {
       Held<E, V> v = {};
-      if constexpr (early) {
+      if constexpr (ahead) {
+        if (given) v = slot_vec<E, V>(from + off + k * vec);
+      } else {
         if (given) v = own[which][k];
-        return v;
       }
-      if (given) v = held_vec<E, V>(from + off + k * vec, p + c, at[k].live && r.held);
       return v;
     };
-    auto in_h = [&](int k) {
-      return wide(input(true, 0, 0, hp, in_heads<MODE>(a, a.hs, at[k]), k));
-    };
+    auto in_h = [&](int k) { return wide(input(true, 0, 0, k)); };
     FloatV<V> y[K];
     if (a.h) {
       Sums<1> ss[K];
@@ -114,22 +102,21 @@ __global__ void __launch_bounds__(V == 1 && K > 1 ? 512 : 256, V == 1 && K > 1 ?
       for (int k = 0; k < K; ++k) {
         FloatV<V> n = times<V>(in_h(k), rsqrtf(ss[k].v[0] / (float)a.m + a.eps));
         if (a.z) {
-          n = mul_of<V>(n, gates(input(true, at_z, 1, zp, at[k].c, k), a.gate));
+          n = mul_of<V>(n, gates(input(true, 1, at_z, k), a.gate));
         }
-        const FloatV<V> x = wide(input(a.x, at_x, 2, xp, at[k].c, k));
+        const FloatV<V> x = wide(input(a.x, 2, at_x, k));
         n = fma_of<V>(n, param_vec<V>(par + at[k].c), x);
         y[k] = n;
         put_vec<E, V>(op + at[k].c, n, at[k].live && r.in, r.held);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < K; ++k) y[k] = wide(input(true, at_x, 2, xp, at[k].c, k));
+      for (int k = 0; k < K; ++k) y[k] = wide(input(true, 2, at_x, k));
     }
-    if (ahead || early) {  // this row's inputs are read
-      copy_row(next, slot);
-      next.advance(a);
-      slot = slot + 1 == ring ? 0 : slot + 1;
-    }
+    // this row's inputs are read
+    copy_row(next, slot);
+    next.advance(a);
+    slot = slot + 1 < ring ? slot + 1 : 0;
     if (a.next) {
       Dot<V> dot;
 #pragma unroll

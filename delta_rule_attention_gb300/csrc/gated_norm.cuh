@@ -91,19 +91,18 @@ __device__ __forceinline__ void put_vec(E* p, const FloatV<V>& x, bool live, boo
 
 // Inputs of the rows ahead wait in shared memory: a thread copies what it will read
 // itself (cp.async, 16 bytes), so that nobody waits for another's copies, and registers
-// hold one row only.  Rows on no such boundary are loaded when they are needed.
+// hold one row only.  Rows on no such boundary are loaded into registers, one row ahead.
 template <typename E, int V>
 struct Slot {
   static constexpr int kBytes = V * sizeof(E);
   static constexpr bool kAhead = kBytes == 16;
 };
-template <typename E, int V>
+template <typename E>
 __device__ __forceinline__ void copy_ahead(unsigned char* to, const E* from, bool live) {
   const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-  if constexpr (Slot<E, V>::kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from),
-                 "r"(live ? 16 : 0)
-                 : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from),
+               "r"(live ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ void ahead_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -119,19 +118,17 @@ __device__ __forceinline__ void ahead_wait(int n) {
   else
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
-// An input's vector: out of its slot, or out of memory.
+// An input's vector out of its slot.
 template <typename E, int V>
-__device__ __forceinline__ Held<E, V> held_vec(const unsigned char* slot, const E* from,
-                                               bool live) {
-  Held<E, V> r = {};
-  if constexpr (Slot<E, V>::kAhead) {
-    const uint4 q = *reinterpret_cast<const uint4*>(slot);
-    r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
-  } else {
-    const float x = load_vec<E, 1>(from).v[0];  // no branch: all loads under way at once
-    r.w[0] = live ? __float_as_uint(x) : 0u;
-  }
-  return r;
+__device__ __forceinline__ Held<E, V> slot_vec(const unsigned char* slot) {
+  const uint4 q = *reinterpret_cast<const uint4*>(slot);
+  return {{q.x, q.y, q.z, q.w}};
+}
+// An input's element out of memory, without a branch: all loads are under way at once.
+template <typename E>
+__device__ __forceinline__ Held<E, 1> load_own(const E* from, bool live) {
+  const float x = load_vec<E, 1>(from).v[0];
+  return {{live ? __float_as_uint(x) : 0u}};
 }
 
 template <typename E, int V>
@@ -365,9 +362,9 @@ constexpr int kRowThreads = 128, kNarrowThreads = 256;
 constexpr size_t shared_for(int per) { return 228 * 1024 / per - 5 * 1024 - 256; }
 
 // Those of single elements; the last is for the widest rows (2048 fp32 rows of 8190 channels:
-// gradient 382 us; 32 elements of 256 threads: 618).  Two blocks an SM and loads without
-// branches: 7312 bf16 rows of 1051 channels 51 us, 158 with one block and branches.  Copies
-// ahead of 4 bytes were slower than plain loads (90 us for 40).
+// gradient 296 us, 618 with 32 elements in each of 256 threads).  A row ahead in registers
+// and loads without branches: 7312 bf16 rows of 1051 channels 38 us, 51 without the row ahead,
+// 158 with branches.  Copies of 4 bytes into shared memory were slower still.
 constexpr Width kNarrow[] = {{1, 256, 512}, {4, 512, 512}, {8, 512, 512}, {16, 512, 512}};
 
 // widths: rising; the last one has to do for the widest row.  Of those that leave `enough`

@@ -42,48 +42,32 @@ __global__ void __launch_bounds__(V == 1 ? (K > 1 ? 512 : 256) : K == 3 || K == 
     each[k] = zeros<E, V>(), nextw[k] = zeros<E, V>();
     at[k] = place_of<V, MODE>(a, k);
   }
-  constexpr bool ahead = Slot<E, V>::kAhead, early = !ahead && K <= 4;
-  Held<E, V> own[5][early ? K : 1];
+  constexpr bool ahead = Slot<E, V>::kAhead;
+  Held<E, V> own[5][ahead ? 1 : K];  // without slots: the next row's h, z, dout, out and dnext
   auto copy_row = [&](const RowAt& r, int slot) {
-    if constexpr (early) {
-      const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
-              *dp = row_in<E>(a.dout, a.dos, r), *yp = row_in<E>(a.y, a.os, r),
-              *ep = row_in<E>(a.dnext, a.dns, r);
+    unsigned char* to = mine + slot * row_bytes;
+    const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
+            *dp = row_in<E>(a.dout, a.dos, r), *yp = row_in<E>(a.y, a.os, r),
+            *ep = row_in<E>(a.dnext, a.dns, r);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const bool on = at[k].live && r.held;
-        if (a.h) own[0][k] = held_vec<E, V>(nullptr, hp + in_heads<MODE>(a, a.hs, at[k]), on);
-        if (a.z) own[1][k] = held_vec<E, V>(nullptr, zp + at[k].c, on);
-        if (a.dout) own[2][k] = held_vec<E, V>(nullptr, dp + at[k].c, on);
-        if (a.next_weight) {
-          own[3][k] = held_vec<E, V>(nullptr, yp + at[k].c, on);
-          own[4][k] = held_vec<E, V>(nullptr, ep + at[k].c, on);
-        }
-      }
+    for (int k = 0; k < K; ++k) {
+      const bool on = at[k].live && r.held;
+      auto copy = [&](int which, int off, const E* p) {
+        if constexpr (ahead)
+          copy_ahead<E>(to + off + k * vec, p, on);
+        else
+          own[which][k] = load_own<E>(p, on);
+      };
+      if (a.h) copy(0, 0, hp + in_heads<MODE>(a, a.hs, at[k]));
+      if (a.z) copy(1, at_z, zp + at[k].c);
+      if (a.dout) copy(2, at_d, dp + at[k].c);
+      if (a.next_weight) copy(3, at_y, yp + at[k].c), copy(4, at_e, ep + at[k].c);
     }
-    if constexpr (ahead) {
-      unsigned char* to = mine + slot * row_bytes;
-      const E *hp = row_in<E>(a.h, a.hs, r), *zp = row_in<E>(a.z, a.zs, r),
-              *dp = row_in<E>(a.dout, a.dos, r), *yp = row_in<E>(a.y, a.os, r),
-              *ep = row_in<E>(a.dnext, a.dns, r);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const bool on = at[k].live && r.held;
-        if (a.h)
-          copy_ahead<E, V>(to + k * vec, hp + in_heads<MODE>(a, a.hs, at[k]), on);
-        if (a.z) copy_ahead<E, V>(to + at_z + k * vec, zp + at[k].c, on);
-        if (a.dout) copy_ahead<E, V>(to + at_d + k * vec, dp + at[k].c, on);
-        if (a.next_weight) {
-          copy_ahead<E, V>(to + at_y + k * vec, yp + at[k].c, on);
-          copy_ahead<E, V>(to + at_e + k * vec, ep + at[k].c, on);
-        }
-      }
-      ahead_commit();
-    }
+    if (ahead) ahead_commit();
   };
   const int64_t row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   RowAt r(a, row0, step), next = r;
-  for (int i = 0; i < (early ? 1 : ring); ++i) {
+  for (int i = 0; i < (ahead ? ring : 1); ++i) {
     copy_row(next, i);
     next.advance(a);
   }
@@ -93,28 +77,24 @@ __global__ void __launch_bounds__(V == 1 ? (K > 1 ? 512 : 256) : K == 3 || K == 
   for (int64_t row = row0; row - threadIdx.y < rows; row += step, r.advance(a)) {
     if (ahead) ahead_wait(ring - 1);
     const unsigned char* from = mine + slot * row_bytes;
-    auto input = [&](bool given, int off, int which, const void* p, const falcon_strides& s,
-                     int64_t c, int k) {
+    auto input = [&](bool given, int which, int off, int k) {
       Held<E, V> v = {};
-      if constexpr (early) {
+      if constexpr (ahead) {
+        if (given) v = slot_vec<E, V>(from + off + k * vec);
+      } else {
         if (given) v = own[which][k];
-        return v;
       }
-      if (given)
-        v = held_vec<E, V>(from + off + k * vec, row_in<E>(p, s, r) + c, at[k].live && r.held);
       return v;
     };
-    auto in_h = [&](int k) {
-      return wide(input(true, 0, 0, a.h, a.hs, in_heads<MODE>(a, a.hs, at[k]), k));
-    };
-    auto in_z = [&](int k) { return input(true, at_z, 1, a.z, a.zs, at[k].c, k); };
-    auto in_y = [&](int k) { return wide(input(true, at_y, 3, a.y, a.os, at[k].c, k)); };
-    auto in_e = [&](int k) { return wide(input(true, at_e, 4, a.dnext, a.dns, at[k].c, k)); };
+    auto in_h = [&](int k) { return wide(input(true, 0, 0, k)); };
+    auto in_z = [&](int k) { return input(true, 1, at_z, k); };
+    auto in_y = [&](int k) { return wide(input(true, 3, at_y, k)); };
+    auto in_e = [&](int k) { return wide(input(true, 4, at_e, k)); };
     auto ws = [&](int k) { return param_vec<V>(par + at[k].c); };
     auto wn = [&](int k) { return param_vec<V>(par + a.D + at[k].c); };
     FloatV<V> d[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) d[k] = wide(input(a.dout, at_d, 2, a.dout, a.dos, at[k].c, k));
+    for (int k = 0; k < K; ++k) d[k] = wide(input(a.dout, 2, at_d, k));
     if (a.next_weight) {
       Dot<V> yy, ey;
 #pragma unroll
@@ -174,11 +154,10 @@ __global__ void __launch_bounds__(V == 1 ? (K > 1 ? 512 : 256) : K == 3 || K == 
                       r.held);
       }
     }
-    if (ahead || early) {  // this row's inputs are read
-      copy_row(next, slot);
-      next.advance(a);
-      slot = slot + 1 == ring ? 0 : slot + 1;
-    }
+    // this row's inputs are read
+    copy_row(next, slot);
+    next.advance(a);
+    slot = slot + 1 < ring ? slot + 1 : 0;
   }
   float* part = a.ws + ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * 2 * a.D;
 #pragma unroll
