@@ -288,8 +288,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Runs of a row, of whole chunks: as many as make the last block's work shortest when
 // `want` blocks take the runs of all heads in turn, a run costing its chunks and `extra`
 // of one: its set-up, and the state that is written, joined and read back.  96 heads of 16
-// chunks over 152 blocks: 3 runs of 6 chunks, the last block takes two of them (10.1 chunks would be
-// even).
+// chunks over 152 blocks: 3 runs of 6 chunks, of which a block takes up to two (10.1 chunks
+// a block would be even).
 void split_runs(DecayPass* p, int chunk, int64_t want, double extra) {
   const int64_t chunks = ceil_div(p->T, chunk), heads = p->B * p->H;
   int64_t best = chunks ? chunks : 1;
