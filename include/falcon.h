@@ -637,6 +637,10 @@ typedef struct {
  * A NaN or infinity in a token reaches the tokens behind it, and may reach those before
  * it among the 128 that are worked on together; a token whose weight in a state is zero
  * in float32 (gamma^n below 2^-149) is left out of it, whatever it holds.
+ *   Behind a call's first kernel, an ordinary launch, the others are programmatic
+ * dependent ones; they read the call's inputs, not what its kernels write, before they
+ * wait for the one before them.  What is said above of a caller's kernel launched in
+ * that way behind a chunked forward holds behind these calls too.
  * Errors: FALCON_ERR_NULL_PTR, _BAD_SHAPE, _BAD_DTYPE, _MISALIGNED, _WORKSPACE,
  * _BAD_ARG (negative stride, o where an input starts or on itself, scale not
  * finite), _DEVICE; _CUDA. */
