@@ -92,6 +92,20 @@ __device__ __forceinline__ void arrive_warp(Control<BARS>& c, int which) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(&c.bar[which]);
 }
 
+// At a block's end: the last phases of a ring of barriers that n uses went through.  Copies
+// and the arrivals that products send are asynchronous, and the shared memory that they
+// come to is the next block's once this one has ended.  After a wait that gave up, what is
+// on its way still gets a while to land.
+constexpr uint64_t kSettleNs = 10000000ull;
+template <int BARS>
+__device__ __forceinline__ void settle(Control<BARS>& c, int ring, int stages, int n) {
+#pragma unroll 1
+  for (int s = 0; s < stages && s < n; ++s)
+    if (!mbar_wait(&c.bar[ring + s], last_phase(n, stages, s) & 1,
+                   c.fail ? kSettleNs : kWaitLimitNs))
+      c.fail = 1;
+}
+
 // a and b (of x) as sums of two or three bf16 terms.  All but the last of two are cut
 // off, not rounded: each takes 8 of the 24 bits, so that three are exact.
 __device__ __forceinline__ uint32_t upper_halves(float a, float b) {
@@ -302,6 +316,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   int c = 0, group = 0;  // chunks, and groups of them, of all items so far
+  int loaded = 0;        // chunks that were copied
   for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
     const Item it(p, item);
     const int len = max(min(it.n, it.end) - it.first, 0);
@@ -376,6 +391,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         const int s = c % L::kStages, t = it.first + k * C;
         if (lane != 0) continue;
         if (c >= L::kStages) wait(ctl, L::kEmpty + s, c / L::kStages - 1);
+        if (ctl.fail) continue;
+        loaded = c + 1;
         uint64_t* bar = &ctl.bar[L::kFull + s];
         mbar_expect_tx(bar, L::kK + L::kV);
 #pragma unroll
@@ -414,6 +431,11 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         if (closes) ++group;
       }
     }
+  }
+  if (warp == kLoader && lane == 0) {
+    settle(ctl, L::kFull, L::kStages, loaded);
+    settle(ctl, L::kEmpty, L::kStages, c);
+    settle(ctl, L::kSplitFree, 2, c);
   }
   __syncwarp();
   tc_fence_before();
@@ -721,7 +743,11 @@ __global__ void __launch_bounds__(kReadThreads, 1)
       }
     }
   } else if (warp == kLoader) {
-    int c = 0;
+    int c = 0, loaded_k = 0, loaded_v = 0, loaded_q = 0;
+    auto free = [&](int ring, int stages) {
+      if (c >= stages) wait(ctl, ring + c % stages, c / stages - 1);
+      return ctl.fail == 0;
+    };
     for (int item = blockIdx.x; item < a.items && lane == 0; item += gridDim.x) {
       const Item it(p, item);
       for (int i = 0; i < it.chunks; ++i, ++c) {
@@ -732,25 +758,39 @@ __global__ void __launch_bounds__(kReadThreads, 1)
             tma_prefetch_4d(&maps.q, 64 * x, t, it.h * a.qh, it.b * a.qb);
         }
         const int ks = c % L::kKs, qs = c % L::kQs;
-        if (c >= L::kKs) wait(ctl, L::kEmptyK + ks, c / L::kKs - 1);
-        mbar_expect_tx(&ctl.bar[L::kFullK + ks], L::kK);
+        if (free(L::kEmptyK, L::kKs)) {
+          loaded_k = c + 1;
+          mbar_expect_tx(&ctl.bar[L::kFullK + ks], L::kK);
 #pragma unroll
-        for (int x = 0; x < M / 64; ++x)
-          tma_load_4d(sm + L::K + ks * L::kK + x * kTile, &maps.k, 64 * x, t, it.h * a.kh,
-                      it.b * a.kb, &ctl.bar[L::kFullK + ks]);
-        if (c >= L::kKs) wait(ctl, L::kEmptyV + ks, c / L::kKs - 1);
-        mbar_expect_tx(&ctl.bar[L::kFullV + ks], L::kV);
+          for (int x = 0; x < M / 64; ++x)
+            tma_load_4d(sm + L::K + ks * L::kK + x * kTile, &maps.k, 64 * x, t, it.h * a.kh,
+                        it.b * a.kb, &ctl.bar[L::kFullK + ks]);
+        }
+        if (free(L::kEmptyV, L::kKs)) {
+          loaded_v = c + 1;
+          mbar_expect_tx(&ctl.bar[L::kFullV + ks], L::kV);
 #pragma unroll
-        for (int x = 0; x < N / 64; ++x)
-          tma_load_4d(sm + L::V + ks * L::kV + x * kTile, &maps.v, 64 * x, t, it.h * a.vh,
-                      it.b * a.vb, &ctl.bar[L::kFullV + ks]);
-        if (c >= L::kQs) wait(ctl, L::kEmptyQ + qs, c / L::kQs - 1);
-        mbar_expect_tx(&ctl.bar[L::kFullQ + qs], L::kQ);
+          for (int x = 0; x < N / 64; ++x)
+            tma_load_4d(sm + L::V + ks * L::kV + x * kTile, &maps.v, 64 * x, t, it.h * a.vh,
+                        it.b * a.vb, &ctl.bar[L::kFullV + ks]);
+        }
+        if (free(L::kEmptyQ, L::kQs)) {
+          loaded_q = c + 1;
+          mbar_expect_tx(&ctl.bar[L::kFullQ + qs], L::kQ);
 #pragma unroll
-        for (int x = 0; x < M / 64; ++x)
-          tma_load_4d(sm + L::Q + qs * L::kQ + x * kTile, &maps.q, 64 * x, t, it.h * a.qh,
-                      it.b * a.qb, &ctl.bar[L::kFullQ + qs]);
+          for (int x = 0; x < M / 64; ++x)
+            tma_load_4d(sm + L::Q + qs * L::kQ + x * kTile, &maps.q, 64 * x, t, it.h * a.qh,
+                        it.b * a.qb, &ctl.bar[L::kFullQ + qs]);
+        }
       }
+    }
+    if (lane == 0) {
+      settle(ctl, L::kFullK, L::kKs, loaded_k);
+      settle(ctl, L::kFullV, L::kKs, loaded_v);
+      settle(ctl, L::kFullQ, L::kQs, loaded_q);
+      settle(ctl, L::kEmptyK, L::kKs, c);
+      settle(ctl, L::kEmptyV, L::kKs, c);
+      settle(ctl, L::kEmptyQ, L::kQs, c);
     }
   } else if (warp == kIssuer) {
     int c = 0, cleared = 0;

@@ -15,6 +15,12 @@ bool decay_tc_pass(const DecayPass& p, cudaError_t* status, cudaStream_t stream)
 // early: set up while the kernel before it runs.
 cudaError_t launch_decay_join(const DecayPass& p, bool early, cudaStream_t stream);
 
+// A ring of `stages` barriers that n uses went through in turn: the phase that the last
+// use of barrier s completed (s < n).
+__host__ __device__ constexpr int last_phase(int n, int stages, int s) {
+  return (n - 1 - s) / stages;
+}
+
 // A launch that may be set up while the kernel before it on the stream runs (early): its
 // kernel waits for that one (griddepcontrol.wait) before it touches what that one writes
 // or reads.

@@ -1,0 +1,37 @@
+"""Attention with a decay over the ways in which rows are split: blocks of few and of many
+chunks, many heads, calls one behind another."""
+import pytest
+import torch
+
+import linear_reference as ref
+from test_gpu_linear import (BF16, F32, HALF, decay_case, falcon, gen, near,  # noqa: F401
+                             no_timeout, randn)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("m,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+def test_blocks_of_few_and_many_chunks(falcon, m, dv):  # noqa: F811
+    """Rings of barriers that are used not at all, once, as often as they have stages, and
+    more often, by calls that follow one another without a pause."""
+    for B, H, T, lengths in ((1, 1, 65, None), (1, 2, 128, None), (1, 1, 129, None),
+                             (2, 1, 300, [300, 0]), (1, 160, 500, None), (2, 80, 400, [129, 400])):
+        c = decay_case(B, H, T, m, dv, BF16, seed=T, lengths=lengths)
+        dO = randn(gen(T), B, H, T, dv, dtype=BF16)
+        calls = [(falcon.falcon_decay_attn_fwd(**c), falcon.falcon_decay_attn_bwd(**c, dO=dO))
+                 for _ in range(6)]
+        (o, S), g = calls[0]
+        for (o1, S1), g1 in calls[1:]:
+            assert torch.equal(o, o1) and torch.equal(S, S1)
+            assert all(torch.equal(g[n], g1[n]) for n in g)
+        hs = slice(0, H, max(1, H // 2))
+        one = {n: t[:, hs] if n in ("q", "k", "v", "S0") else t[hs] if n == "log_decay" else t
+               for n, t in c.items()}
+        want, want_S = ref.decay_forward(**one)
+        size, size_S = ref.decay_forward_size(**one)
+        near(o[:, hs], want, size, HALF[BF16], m + T + 256, "o")
+        near(S[:, hs], want_S, size_S, 0.0, T + 256, "S")
+        want = ref.decay_gradient(**one, dO=dO[:, hs])
+        size = ref.decay_gradient_size(**one, dO=dO[:, hs])
+        for name in ("dq", "dk", "dv"):
+            near(g[name][:, hs], want[name], size[name], HALF[BF16], m + dv + T + 256, name)
