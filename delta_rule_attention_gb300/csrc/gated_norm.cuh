@@ -228,6 +228,17 @@ __device__ __forceinline__ FloatV<V> slopes(const Held<E, V>& z, int gate) {
   return s;
 }
 
+// (b, t) of the row that lies step_b batches and step_t < T tokens further on; no sum passes
+// 2^31 on the way, however long a row.
+__host__ __device__ __forceinline__ void advance_row(unsigned& b, int& t, int step_b, int step_t,
+                                                     int T) {
+  b += step_b;
+  if (t >= T - step_t)
+    t -= T - step_t, ++b;
+  else
+    t += step_t;
+}
+
 // A row of the problem, and the way to the row `step` further on (no division in a loop).
 struct RowAt {
   unsigned b;  // runs past 2^31 behind the last row of the largest problem
@@ -245,8 +256,7 @@ struct RowAt {
     held = in && t < row_length(a.lengths, in ? b : 0, a.T);
   }
   __device__ __forceinline__ void advance(const NormArgs& a) {
-    b += step_b, t += step_t;
-    if (t >= a.T) t -= (int)a.T, ++b;
+    advance_row(b, t, step_b, step_t, (int)a.T);
     look(a);
   }
 };

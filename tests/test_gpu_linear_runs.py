@@ -35,3 +35,34 @@ def test_blocks_of_few_and_many_chunks(falcon, m, dv):  # noqa: F811
         size = ref.decay_gradient_size(**one, dO=dO[:, hs])
         for name in ("dq", "dk", "dv"):
             near(g[name][:, hs], want[name], size[name], HALF[BF16], m + dv + T + 256, name)
+
+
+def test_norm_of_a_row_of_as_many_tokens_as_there_may_be(falcon):  # noqa: F811
+    """One row of 2^31 - 1 tokens of a channel each: the last block's rows lie partly behind it."""
+    T, eps = 2 ** 31 - 1, 0.5
+    h = torch.empty(1, T, 1, dtype=BF16, device="cuda").normal_(generator=gen(1))
+    room = torch.full((1, T + 512, 1), 7.0, dtype=BF16, device="cuda")
+    out = room[:, 256:-256]
+    w = torch.tensor([0.75], device="cuda")
+
+    def n(at):
+        x = h[0, at].double().cpu()
+        return x, 0.75 * x / torch.sqrt(x * x + eps), 0.75 * eps / (x * x + eps) ** 1.5
+
+    falcon.falcon_gated_norm_fwd(h, weight=w, eps=eps, out=out)
+    parts = [slice(a, a + 100000) for a in (0, 2 ** 30, T - 100000)]
+    for at in parts:
+        off = (out[0, at].double().cpu() - n(at)[1]).abs()
+        assert (off <= n(at)[1].abs() * (HALF[BF16] * 1.01 + 2.0 ** -18)).all()
+    dout = out.clone()
+    g = falcon.falcon_gated_norm_bwd(h, dout, weight=w, eps=eps, residual=False,
+                                     grads=dict(dh=out))
+    assert g["dh"] is out
+    for at in parts:
+        x, _, slope = n(at)
+        d = dout[0, at].double().cpu()
+        # dh = r (d w - x^2 r^2 d w): terms of the size r |d w|, at most (1 + x^2 / eps) of dh
+        size = 0.75 * d.abs() / torch.sqrt(x * x + eps)
+        off = (out[0, at].double().cpu() - d * slope).abs()
+        assert (off <= (d * slope).abs() * HALF[BF16] * 1.01 + 2.0 ** -18 * size).all()
+    assert (room[:, :256] == 7).all() and (room[:, -256:] == 7).all()

@@ -42,3 +42,28 @@ def test_last_phase_of_a_ring(tmp_path):
         if (phases[s]) return 2;
     }
   return 0;""", "linear_tc.cuh")
+
+
+@pytest.mark.parametrize("T", [1, 2, 7, 128, 77824, 2 ** 30 + 1, 2 ** 31 - 1])
+def test_rows_further_on(tmp_path, T):
+    """A block's way through the rows of a norm, to the end of the problem and a few rows
+    behind it, against division in 64 bits: rows of up to 2^31 - 1 tokens."""
+    B = (2 ** 31 - 1) // T
+    run_on_host(tmp_path, f"""
+  const long long T = {T}LL, B = {B}LL;
+  for (long long step : {{1LL, 2LL, 19456LL, 38912LL, 77824LL}})
+    for (long long row : {{0LL, 1LL, step - 1, T / 2, T - 2 * step, T - step, T - 1,
+                           B * T - 3 * step, B * T - step, B * T - 1}}) {{
+      if (row < 0) continue;
+      unsigned b = (unsigned)(row / T);
+      int t = (int)(row % T);
+      for (int i = 0; i < 8 && row < B * T; ++i) {{
+        row += step;
+        falcon::advance_row(b, t, (int)(step / T), (int)(step % T), (int)T);
+        if (b != row / T || t != row % T) {{
+          printf("step %lld row %lld: (%u, %d)\\n", step, row, b, t);
+          return 1;
+        }}
+      }}
+    }}
+  return 0;""", "gated_norm.cuh")
