@@ -99,9 +99,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // The state entering each run, in the order of time (rev: from the last run back), in
-// place of what the run adds; one thread an element.  gamma^len X + U as
-// X + (gamma^len - 1) X + U: the power of a slow head is near 1, where its rounding
-// would repeat itself run after run (expm1 keeps it relative to what is lost).
+// place of what the run adds; one thread an element.
 constexpr int kAhead = 8;
 __global__ void __launch_bounds__(kThreads)
     decay_join_kernel(const __grid_constant__ DecayPass a) {
@@ -127,8 +125,7 @@ __global__ void __launch_bounds__(kThreads)
       if (s0 + s >= a.runs) break;
       const int r = a.rev ? a.runs - 1 - s0 - s : s0 + s;
       st[(int64_t)r * size] = X;
-      const float len = (float)run_tokens(n, r, a.run_len);
-      X = fmaf(expm1f(g * len), X, X) + U[s];
+      X = Carry(g, (float)run_tokens(n, r, a.run_len)).of(X) + U[s];
     }
   }
   if (a.S_out) a.S_out[seat] = X;
@@ -245,7 +242,7 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     if (have > 0 && (cc + 1 < chunks || (a.whole && a.S_out))) {
-      const float lost = expm1f(g * (float)have);
+      const Carry carry(g, (float)have);
       for (int mk = 0; mk < a.m; mk += kTile) {
         __syncthreads();
         for (int e = tid; e < kChunk * (kTile / 4); e += kThreads) {
@@ -267,7 +264,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float& S = sm.S[(mk + ti + i) * kLd + tj + j];
-              S = fmaf(lost, S, S) + U[i][j];
+              S = carry.of(S) + U[i][j];
             }
         }
       }

@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
     int c = 0, carried = 0;
     const bool state_row = 32 * (warp & 3) < N;
     // keys 32 cb .. of value `row`: an operand, and what the next sum starts from
-    auto put_state = [&](const float* x, int cb, float lost) {
+    auto put_state = [&](const float* x, int cb, const Carry& carry) {
       unsigned char* tile = sm + L::S + (cb >> 1) * L::kSAtom;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
             tcu::pack8(x + 8 * e, 1.f);
       uint32_t w[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(fmaf(lost, x[j], x[j]));
+      for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(carry.of(x[j]));
       tmem_st32(tmem + lanes + L::X + 32 * cb, w);
       if constexpr (L::kSide) {  // the second term's sum
 #pragma unroll
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
           static_cast<__nv_bfloat16*>(p.o) + it.b * p.os.batch + it.h * p.os.head;
       if (it.chunks > 0) {
         if (state_row) {
-          const float lost = expm1f(it.g * (float)Chunk(it, p, 0).have);
+          const Carry carry(it.g, (float)Chunk(it, p, 0).have);
           const float* X = p.states + (it.bh * p.runs + it.run) * p.m * p.dv + row * p.xj;
 #pragma unroll 1
           for (int q = 0; q < M / 64; ++q) {
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
               const int i = 32 * cb + j;
               x[j] = i < p.m && row < p.dv ? X[i * p.xi] : 0.f;
             }
-            put_state(x, cb, lost);
+            put_state(x, cb, carry);
           }
         }
         state_ready();
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
           __syncwarp();
         }
         if (more) {
-          const float lost = expm1f(it.g * (float)Chunk(it, p, i + 1).have);
+          const Carry carry(it.g, (float)Chunk(it, p, i + 1).have);
           wait_warp(ctl, L::kC_, carried);
           ++carried;
           tc_fence_after();
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) x[j] += y[j];
               }
-              put_state(x, cb, lost);
+              put_state(x, cb, carry);
             }
           }
           state_ready();

@@ -48,6 +48,20 @@ __device__ __forceinline__ float decay_rate(const float* log_decay, int h) {
 }
 __device__ __forceinline__ float decay_power(float g, float n) { return expf(g * n); }
 
+// A state n tokens later.  Where gamma^n is near 1 its rounding would repeat itself run
+// after run, so what is lost is subtracted (expm1); where it is small, that difference
+// would cancel: off by 2^-25 of X where gamma^n X is left (exactly zero for gamma^n < 2^-25).
+struct Carry {
+  float f;
+  bool near;
+  __device__ __forceinline__ Carry(float g, float n) {
+    const float x = g * n;
+    near = !(x < -0.69314718f);
+    f = near ? expm1f(x) : expf(x);
+  }
+  __device__ __forceinline__ float of(float X) const { return fmaf(f, X, near ? X : 0.f); }
+};
+
 // Tokens of run r of a row of n.
 __device__ __forceinline__ int64_t run_tokens(int64_t n, int64_t r, int64_t run_len) {
   const int64_t left = n - r * run_len;
