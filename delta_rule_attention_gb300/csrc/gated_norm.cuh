@@ -222,8 +222,10 @@ __device__ __forceinline__ FloatV<V> slopes(const Held<E, V>& z, int gate) {
   if (gate == FALCON_ACT_IDENTITY) return s;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
+    // 1 - p is e^{-x} p where x > 0: the difference would be p's rounding there
     const float x = z.get(i), p = sigmoid(x);
-    s.v[i] = gate == FALCON_ACT_SIGMOID ? p * (1.f - p) : p * fmaf(x, 1.f - p, 1.f);
+    const float q = x > 0.f ? exp2_approx(-x * kLog2e) * p : 1.f - p;
+    s.v[i] = gate == FALCON_ACT_SIGMOID ? p * q : p * fmaf(x, q, 1.f);
   }
   return s;
 }
