@@ -285,7 +285,8 @@ def falcon_gated_norm_bwd(h, dout, dnext=None, out=None, weight=None, z=None, ga
     stored output (x where h is None), needed with next_weight; dout may be None where
     dnext is given; ``residual`` says whether x was.  Returns a dict with dx, dh, dz
     (dense, h's type, dh of h's shape) and dweight, dscale, dnext_weight (fp32); those of
-    what was not given are None.  ``grads`` may pass preallocated outputs."""
+    what was not given are None.  ``grads`` may pass preallocated outputs of those that
+    there are."""
     if stream is not None:
         return elsewhere(stream, falcon_gated_norm_bwd, h, dout, dnext, out, weight, z, gate,
                          scale, residual, next_weight, lengths, eps, grads, workspace)
@@ -307,21 +308,23 @@ def falcon_gated_norm_bwd(h, dout, dnext=None, out=None, weight=None, z=None, ga
     _norm_params(row[2], dev, weight=weight, scale=scale, next_weight=next_weight)
     _dense(lengths, "lengths", torch.int32, row[:1], dev)
     g = {} if grads is None else grads
-    for name, like, shape in (("dx", residual or h is None or None, row),
-                              ("dh", h, None if h is None else h.shape), ("dz", z, row)):
-        if like is None or like is False:
+    # each result with what it is the gradient of; `grads` may hold the None of an earlier call
+    given = dict(dx=residual or h is None, dh=h is not None, dz=z is not None,
+                 dweight=weight is not None, dscale=scale is not None,
+                 dnext_weight=next_weight is not None)
+    for name, on in given.items():
+        if not on and g.get(name) is not None:
+            raise ValueError(f"grads has {name}, whose argument was not given")
+    for name, on in given.items():
+        if not on:
             g[name] = None
-        elif name in g:
-            _rows(g[name], name, dt, shape, dev)
+        elif name in ("dx", "dh", "dz"):
+            shape = h.shape if name == "dh" else row
+            g[name] = block._empty(shape, dt, dev) if g.get(name) is None else \
+                _rows(g[name], name, dt, shape, dev)
         else:
-            g[name] = block._empty(shape, dt, dev)
-    for name, p in (("dweight", weight), ("dscale", scale), ("dnext_weight", next_weight)):
-        if p is None:
-            g[name] = None
-        elif name in g:
-            _dense(g[name], name, torch.float32, (row[2],), dev)
-        else:
-            g[name] = block._empty((row[2],), torch.float32, dev)
+            g[name] = block._empty((row[2],), torch.float32, dev) if g.get(name) is None else \
+                _dense(g[name], name, torch.float32, (row[2],), dev)
     workspace, have = block._workspace(_need("falcon_gated_norm_bwd_workspace_bytes",
                                              _norm_shape, *fields), workspace, dev)
     rc = lib.falcon_gated_norm_bwd(

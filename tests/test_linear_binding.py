@@ -137,3 +137,29 @@ def test_results_of_what_was_not_given(world):
     x = _gpu(2, 4, 24)
     out, nxt = norm(h=None, weight=None, z=None, x=x)
     assert out is x and nxt.shape == (2, 4, 24)
+
+
+@pytest.mark.parametrize("name,without", [
+    ("dx", dict(residual=False)), ("dz", dict(z=None)), ("dweight", dict(weight=None)),
+    ("dscale", dict(scale=None)),
+    ("dnext_weight", dict(next_weight=None, dnext=None)),
+    ("dh", dict(h=None, weight=None, z=None)),
+])
+def test_a_result_of_what_was_not_given_is_refused(world, name, without):
+    """It would be left as it is; the caller's dict keeps it."""
+    t = _gpu(2, 3, 4, 8) if name == "dh" else _gpu(2, 4, 24) if name in ("dx", "dz") else _gpu(24)
+    grads = {name: t}
+    with pytest.raises(ValueError, match=name):
+        norm_bwd(grads=grads, **without)
+    assert grads == {name: t} and not world.calls
+
+
+def test_results_of_a_call_are_passed_to_the_next(world):
+    """With the None of what was not given, which stays, or is allocated where it is now."""
+    g = norm_bwd(z=None, scale=None)
+    assert g["dz"] is None
+    kept = {n: t for n, t in g.items() if t is not None}
+    assert norm_bwd(z=None, scale=None, grads=g) is g
+    assert all(g[n] is t for n, t in kept.items())
+    norm_bwd(grads=g)
+    assert g["dz"].shape == (2, 4, 24) and all(g[n] is t for n, t in kept.items())
