@@ -85,6 +85,10 @@ def _heads(t):
     return _strides(s[0], s[1], s[2])
 
 
+def _default_scale(m):
+    return max(m, 1) ** -0.5  # keys of no channel are the library's to refuse
+
+
 def _decay_setup(q, k, v, log_decay, S0, lengths, scale):
     dt = _dtype(q, "q")
     if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
@@ -99,7 +103,7 @@ def _decay_setup(q, k, v, log_decay, S0, lengths, scale):
         raise TypeError("log_decay must be a torch.Tensor")
     _dense(S0, "S0", torch.float32, (B, H, m, dv), dev)
     _dense(lengths, "lengths", torch.int32, (B,), dev)
-    scale = m ** -0.5 if scale is None else float(scale)
+    scale = _default_scale(m) if scale is None else float(scale)
     return (B, H, T, m, dv, _DTYPE[dt], scale), dt, dev
 
 
@@ -194,7 +198,8 @@ def falcon_decay_attn_step(q, k, v, log_decay, S, slots=None, fresh=None, scale=
     o = block._empty((N, H, dv), dt, dev) if o is None else _dense(o, "o", dt, (N, H, dv), dev)
     s, t, u = q.stride(), k.stride(), v.stride()
     rc = lib.falcon_decay_attn_step(
-        _decay_shape(N, H, 1, m, dv, _DTYPE[dt], m ** -0.5 if scale is None else float(scale)),
+        _decay_shape(N, H, 1, m, dv, _DTYPE[dt],
+                     _default_scale(m) if scale is None else float(scale)),
         q.data_ptr(), _strides(s[0], s[1], 0), k.data_ptr(), _strides(t[0], t[1], 0),
         v.data_ptr(), _strides(u[0], u[1], 0), log_decay.data_ptr(), S.data_ptr(), pool,
         _at(slots), _at(fresh), o.data_ptr(), block._raw_stream(dev.index))

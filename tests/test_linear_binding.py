@@ -163,3 +163,13 @@ def test_results_of_a_call_are_passed_to_the_next(world):
     assert all(g[n] is t for n, t in kept.items())
     norm_bwd(grads=g)
     assert g["dz"].shape == (2, 4, 24) and all(g[n] is t for n, t in kept.items())
+
+
+def test_keys_of_no_channel_are_refused_by_the_library(world):
+    """Not by a division of one by zero on the way there."""
+    wide = dict(q=_gpu(2, 3, 4, 0), k=_gpu(2, 3, 4, 0))
+    fwd(**wide)
+    bwd(**wide)
+    step(q=_gpu(2, 3, 0), k=_gpu(2, 3, 0), S=_gpu(2, 3, 0, 6))
+    assert [name for name, _ in world.calls] == [
+        "falcon_decay_attn_fwd", "falcon_decay_attn_bwd", "falcon_decay_attn_step"]
