@@ -440,12 +440,9 @@ cudaError_t launch_decay_bwd(const DecayCall& c, cudaStream_t stream) {
   const bool kept = tc_pass(c.s, v, &e, stream);  // its states serve dk too
   if (!kept) e = simt_pass(c.s, v, stream);
   if (e != cudaSuccess) return e;
-  if (kept) {
-    DecayPass shared = k;
-    shared.sums = false, shared.xi = 1, shared.xj = dv;
-    if (tc_pass(c.s, shared, &e, stream)) return e;
-  }
-  return simt_pass(c.s, k, stream);
+  DecayPass last = k;  // forms its own where dv's tensors did not fit
+  if (kept) last.sums = false, last.xi = 1, last.xj = dv;
+  return tc_pass(c.s, last, &e, stream) ? e : simt_pass(c.s, k, stream);
 }
 
 }  // namespace falcon

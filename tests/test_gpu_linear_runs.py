@@ -66,3 +66,22 @@ def test_norm_of_a_row_of_as_many_tokens_as_there_may_be(falcon):  # noqa: F811
         off = (out[0, at].double().cpu() - d * slope).abs()
         assert (off <= (d * slope).abs() * HALF[BF16] * 1.01 + 2.0 ** -18 * size).all()
     assert (room[:, :256] == 7).all() and (room[:, -256:] == 7).all()
+
+
+@pytest.mark.parametrize("m,dv", [(64, 64), (64, 128), (128, 64)])
+def test_keys_gradient_beside_values_off_their_boundary(falcon, m, dv):  # noqa: F811
+    """Only dv lies where TMA cannot be used: dk takes the tensor cores all the same.  The
+    gradient of the state in place forms dk's states by themselves too: the same bits."""
+    B, H, T = 2, 3, 700
+    c = decay_case(B, H, T, m, dv, BF16, seed=1, lengths=[T, 300])
+    dO, dS = randn(gen(2), B, H, T, dv, dtype=BF16), randn(gen(3), B, H, m, dv)
+    odd = torch.empty(B, H, T, dv + 1, dtype=BF16, device="cuda")[..., 1:]
+    got = falcon.falcon_decay_attn_bwd(**c, dO=dO, dS_T=dS, grads=dict(dv=odd))
+    held = dS.clone()
+    alone = falcon.falcon_decay_attn_bwd(**c, dO=dO, dS_T=held, grads=dict(dS0=held))
+    assert torch.equal(got["dk"], alone["dk"]) and torch.equal(got["dq"], alone["dq"])
+    want = ref.decay_gradient(**c, dO=dO, dS_T=dS)
+    size = ref.decay_gradient_size(**c, dO=dO, dS_T=dS)
+    for name in ("dq", "dk", "dv"):
+        near(got[name], want[name], size[name], HALF[BF16], m + dv + T + 256, name)
+    near(got["dS0"], want["dS0"], size["dS0"], 0.0, T + 256, "dS0")
