@@ -286,14 +286,15 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // `want` blocks take the runs of all heads in turn, a run costing its chunks and `extra`
 // of one: its set-up, and the state that is written, joined and read back.  96 heads of 16
 // chunks over 152 blocks: 3 runs of 6 chunks, of which a block takes up to two (10.1 chunks
-// a block would be even).
-void split_runs(DecayPass* p, int chunk, int64_t want, double extra) {
+// a block would be even).  No run has more than `longest` chunks.
+void split_runs(DecayPass* p, int chunk, int64_t want, double extra, int64_t longest) {
   const int64_t chunks = ceil_div(p->T, chunk), heads = p->B * p->H;
   int64_t best = chunks ? chunks : 1;
   double least = -1.;
   const int64_t first = ceil_div(heads, want);
   for (int64_t t = first; t < first + 4 && chunks; ++t) {
-    const int64_t most = t * want / heads, runs = most < chunks ? (most ? most : 1) : chunks;
+    const int64_t most = t * want / heads, few = ceil_div(chunks, longest);
+    const int64_t runs = most < few ? few : most < chunks ? most : chunks;
     const int64_t each = ceil_div(chunks, runs);
     const double cost =
         (double)ceil_div(heads * ceil_div(chunks, each), want) * ((double)each + extra);
@@ -310,9 +311,9 @@ DecayPass shape_pass(const falcon_decay_shape& s, int m, int dv, bool tc) {
   p.B = s.B, p.H = s.H, p.T = s.T;
   p.m = m, p.dv = dv, p.dtype = s.dtype;
   if (tc)
-    split_runs(&p, kDecayTcChunk, kDecayTcBlocks, 0.5);
+    split_runs(&p, kDecayTcChunk, kDecayTcBlocks, 0.5, kDecayTcRun);
   else
-    split_runs(&p, kChunk, kSimtBlocks, 1.);
+    split_runs(&p, kChunk, kSimtBlocks, 1., p.T);
   return p;
 }
 bool quads(const void* p, const falcon_strides& s, int dtype) {

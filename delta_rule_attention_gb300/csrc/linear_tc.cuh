@@ -9,6 +9,11 @@ namespace falcon {
 int* device_error_word_of_current();  // api.cu
 
 constexpr int kDecayTcChunk = 128;
+// Chunks of a run at most: the state that the reads carry through a run is added to by the
+// tensor cores, which round towards zero, and where nothing decays each chunk leaves it 1.4e-6
+// low (160 heads of one sign, runs of 512 chunks: o 7e-4 low, of 1024 1.4e-3; of 64 less
+// than 1e-4, where its rounding to bf16 is up to 4e-3).
+constexpr int kDecayTcRun = 64;
 constexpr int kDecayTcBlocks = 152;  // one for each SM, each taking runs in turn
 // One pass, p.runs in chunks of kDecayTcChunk; false where the tensors do not fit it.
 bool decay_tc_pass(const DecayPass& p, cudaError_t* status, cudaStream_t stream);
