@@ -634,9 +634,10 @@ typedef struct {
  *              nullable, may be S0
  *   workspace: at least falcon_decay_attn_workspace_bytes(shape) bytes, 256-byte
  *   aligned: a state for every run of tokens that is worked on by itself.
- * A NaN or infinity in a token reaches the tokens behind it, and may reach those before
- * it among the 128 that are worked on together; a token whose weight in a state is zero
- * in float32 (gamma^n below 2^-149) is left out of it, whatever it holds.
+ * A NaN or infinity in a token reaches the tokens behind it in its row and head, and
+ * may reach those before it among the 128 that are worked on together.  Whether it still
+ * reaches a state or a token where its weight is zero in float32 (gamma^n below 2^-149)
+ * depends on how the row is split.
  *   Behind a call's first kernel, an ordinary launch, the others are programmatic
  * dependent ones; they read the call's inputs, not what its kernels write, before they
  * wait for the one before them.  What is said above of a caller's kernel launched in

@@ -1,0 +1,41 @@
+"""Values out of the ordinary: how far a NaN or an infinity of one token reaches."""
+import pytest
+import torch
+
+from test_gpu_linear import BF16, F32, decay_case, falcon, gen, no_timeout, randn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T", [60, 700])
+def test_one_bad_token_stays_in_its_head(falcon, T, bad, name, dtype):  # noqa: F811
+    """Its own output is no number; what lies 128 tokens before it, in another head or in
+    another row is as it was.  The gradient's adjoint runs the other way."""
+    B, H, m = 2, 3, 64
+    c = decay_case(B, H, T, m, m, dtype, seed=T)
+    c["dO"], c["dS_T"] = randn(gen(1), B, H, T, m, dtype=dtype), randn(gen(2), B, H, m, m)
+    at = T // 2 + 3
+    dirty = {**c, name: c[name].clone()}
+    dirty[name][1, 2, at, 5] = bad
+
+    def run(c):
+        fwd = {n: t for n, t in c.items() if n not in ("dO", "dS_T")}
+        o, S = falcon.falcon_decay_attn_fwd(**fwd)
+        return dict(falcon.falcon_decay_attn_bwd(**c), o=o, S=S)
+
+    want, got = run(c), run(dirty)
+    for n, t in want.items():
+        rest = torch.ones(B, H, dtype=torch.bool, device="cuda")
+        rest[1, 2] = False
+        assert torch.equal(got[n][rest], t[rest]), n
+    last = max(at - 128, 0)
+    assert torch.equal(got["o"][1, 2, :last], want["o"][1, 2, :last])
+    assert not torch.isfinite(got["o"][1, 2, at]).all()
+    if name == "q":
+        assert torch.equal(got["S"], want["S"]) and torch.equal(got["dq"], want["dq"])
+    else:
+        assert not torch.isfinite(got["S"][1, 2]).all()
+        assert torch.equal(got["dS0"], want["dS0"])
