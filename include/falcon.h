@@ -700,7 +700,9 @@ typedef struct {
  * the next block, in one pass over the rows:
  *   out  = x + scale act(z) n(h) weight,   n(h) = h / sqrt(mean_head h^2 + eps)
  *   next = out / sqrt(mean out^2 + eps) next_weight
- * next is taken from out before its rounding.  Where h is NULL, out = x is not
+ * next is taken from out before its rounding.  Squares are summed in float32: where the
+ * sum leaves its range (values from about 1e19 on) n, or next, and what the gradient
+ * passes back through it are zero.  Where h is NULL, out = x is not
  * written, and next alone is the norm before the first block.
  *   h           [B,H,T,m] dtype, any strides (an attention's head-major output, or
  *               rows of channels: H = 1, or `head` = m)

@@ -1,4 +1,5 @@
-"""Values out of the ordinary: how far a NaN or an infinity of one token reaches."""
+"""Values out of the ordinary: how far a NaN or an infinity of one token reaches, and rows
+whose squares leave float32."""
 import pytest
 import torch
 
@@ -39,3 +40,25 @@ def test_one_bad_token_stays_in_its_head(falcon, T, bad, name, dtype):  # noqa: 
     else:
         assert not torch.isfinite(got["S"][1, 2]).all()
         assert torch.equal(got["dS0"], want["dS0"])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,m", [(1, 64), (3, 64), (2, 111), (1, 4096)])
+def test_rows_whose_squares_leave_float32(falcon, H, m, dtype):  # noqa: F811
+    """Counted as infinitely large: what is normalised is zero, and nothing is NaN."""
+    B, T = 2, 5
+    D = H * m
+    h = randn(gen(1), B, H, T, m, dtype=dtype)
+    h[1, H - 1, 3] = torch.tensor([3e19, -1e25], device="cuda").to(dtype).repeat(m)[:m]
+    x, z, d, e = (randn(gen(i), B, T, D, dtype=dtype) for i in range(2, 6))
+    x[0, 2] = 2e30
+    w = randn(gen(7), D)
+    out, nxt = falcon.falcon_gated_norm_fwd(h, weight=w, z=z, scale=w, x=x, next_weight=w)
+    assert torch.isfinite(out).all() and torch.isfinite(nxt).all()
+    assert torch.equal(out[1, 3, D - m:], x[1, 3, D - m:])
+    assert (nxt[0, 2] == 0).all() and (nxt[1, 3] != 0).any()
+    g = falcon.falcon_gated_norm_bwd(h, d, dnext=e, out=out, weight=w, z=z, scale=w,
+                                     next_weight=w)
+    assert all(torch.isfinite(t).all() for t in g.values())
+    assert (g["dh"][1, H - 1, 3] == 0).all() and (g["dz"][1, 3, D - m:] == 0).all()
+    assert torch.equal(g["dx"][0, 2], d[0, 2])
