@@ -870,6 +870,10 @@ __global__ void __launch_bounds__(kRevThreads)
         const int c = n - 1 - (k + kRevStages);
         rev_issue_load(s, st, hmaps + (size_t)c * kMapBytes, &tm_do, c * kBC, (int)bh);
       }
+      // what the MMAs of the last stages send, which no refill waits for: after the
+      // block's end its shared memory may be another's
+      for (int k = n > kRevStages ? n - kRevStages : 0; k < n && !*fail; ++k)
+        if (!mbar_wait(&s.empty[k % kRevStages], (uint32_t)(k / kRevStages) & 1u)) *fail = 1;
     }
     __syncwarp();
   } else if (state) {
