@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(V == 1 && K > 1 ? 512 : 256, V == 1 && K > 1 ?
                       at[k].live && r.in, r.held);
     }
   }
+  if (ahead) ahead_wait(0);  // the last turns' copies, zeros for rows that there are not
 }
 
 template <typename E, int V, int K>

@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(V == 1 ? (K > 1 ? 512 : 256) : K == 3 || K == 
     next.advance(a);
     slot = slot + 1 < ring ? slot + 1 : 0;
   }
+  if (ahead) ahead_wait(0);  // the last turns' copies, zeros for rows that there are not
   float* part = a.ws + ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * 2 * a.D;
 #pragma unroll
   for (int k = 0; k < K; ++k) {

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import linear_reference as ref
-from test_gpu_linear import (BF16, F32, HALF, decay_case, falcon, gen, near,  # noqa: F401
+from test_gpu_linear import (BF16, F32, HALF, decay_case, falcon, gen, near, once,  # noqa: F401
                              no_timeout, randn)
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +85,27 @@ def test_keys_gradient_beside_values_off_their_boundary(falcon, m, dv):  # noqa:
     for name in ("dq", "dk", "dv"):
         near(got[name], want[name], size[name], HALF[BF16], m + dv + T + 256, name)
     near(got["dS0"], want["dS0"], size["dS0"], 0.0, T + 256, "dS0")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 1024, 4096])
+def test_norms_of_few_and_of_many_rows_one_behind_another(falcon, D, dtype):  # noqa: F811
+    """Blocks that take fewer rows than they copy ahead, as many, and more, in calls that follow
+    one another without a pause: the same bits, and each row what it is by itself."""
+    g = gen(D)
+    w = randn(g, D)
+    h, z, x, d = (randn(g, 1, 3000, D, dtype=dtype) for _ in range(4))
+    rows = [1, 2, 151, 303, 609, 1217, 3000]
+    outs = [(falcon.falcon_gated_norm_fwd(h[:, :n], weight=w, z=z[:, :n], x=x[:, :n],
+                                          next_weight=w),
+             falcon.falcon_gated_norm_bwd(h[:, :n], d[:, :n], dnext=z[:, :n], out=x[:, :n],
+                                          weight=w, z=z[:, :n], next_weight=w))
+            for _ in range(3) for n in rows]
+    for i, ((y, u), gr) in enumerate(outs):
+        (y0, u0), g0 = outs[i % len(rows)]
+        assert torch.equal(y, y0) and torch.equal(u, u0)
+        assert all(t is None or torch.equal(t, g0[n]) for n, t in gr.items())
+        (want, wu), (size, su) = ref.norm_forward(h[:, :1], weight=w, z=z[:, :1], x=x[:, :1],
+                                                  next_weight=w)
+        once(y[:, :1], want, size, HALF[dtype], D + 64, "out")
+        once(u[:, :1], wu, su, HALF[dtype], D + 64, "next")
