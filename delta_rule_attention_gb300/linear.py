@@ -317,8 +317,8 @@ def falcon_gated_norm_bwd(h, dout, dnext=None, out=None, weight=None, z=None, ga
     given = dict(dx=residual or h is None, dh=h is not None, dz=z is not None,
                  dweight=weight is not None, dscale=scale is not None,
                  dnext_weight=next_weight is not None)
-    for name, on in given.items():
-        if not on and g.get(name) is not None:
+    for name in g:
+        if g[name] is not None and not given.get(name, True):
             raise ValueError(f"grads has {name}, whose argument was not given")
     for name, on in given.items():
         if not on:
