@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kThreads)
   const float g = decay_rate(a.log_decay, (int)(bh - b * (unsigned)a.H));
   const int64_t seat = (int64_t)bh * size + i * a.si + j * a.sj;
   float X = a.S_init ? a.S_init[seat] : 0.f;
+  const Carries carries(g, (unsigned)a.run_len, (unsigned)n);
   float* st = a.states + (int64_t)bh * a.runs * size + e;
   for (int s0 = 0; s0 < a.runs; s0 += kAhead) {
     float U[kAhead];
@@ -125,7 +126,8 @@ __global__ void __launch_bounds__(kThreads)
       if (s0 + s >= a.runs) break;
       const int r = a.rev ? a.runs - 1 - s0 - s : s0 + s;
       st[(int64_t)r * size] = X;
-      X = Carry(g, (float)run_tokens(n, r, a.run_len)).of(X) + U[s];
+      const int64_t len = run_tokens(n, r, a.run_len);
+      X = (len > 0 ? carries.after(len, a.run_len).of(X) : X) + U[s];
     }
   }
   if (a.S_out) a.S_out[seat] = X;

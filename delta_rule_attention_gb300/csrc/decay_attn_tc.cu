@@ -634,8 +634,14 @@ __global__ void __launch_bounds__(kReadThreads, 1)
         *reinterpret_cast<uint4*>(chunk_of(tile, row, 4 * (cb & 1) + e)) =
             tcu::pack8(x + 8 * e, 1.f);
       uint32_t w[32];
+      const float keep = carry.near ? 1.f : 0.f;
+      const f32x2 f2 = pack2(carry.f, carry.f), keep2 = pack2(keep, keep);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(carry.of(x[j]));
+      for (int j = 0; j < 16; ++j) {  // carry.of() of two at a time
+        const f32x2 y = pack2(x[2 * j], x[2 * j + 1]);
+        const float2 z = unpack2(fma2(f2, y, mul2(keep2, y)));
+        w[2 * j] = __float_as_uint(z.x), w[2 * j + 1] = __float_as_uint(z.y);
+      }
       tmem_st32(tmem + lanes + L::X + 32 * cb, w);
       if constexpr (L::kSide) {  // the second term's sum
 #pragma unroll
@@ -655,9 +661,10 @@ __global__ void __launch_bounds__(kReadThreads, 1)
       auto power = [&](int gap) { return exp2_approx(g2 * (float)gap); };
       __nv_bfloat16* out =
           static_cast<__nv_bfloat16*>(p.o) + it.b * p.os.batch + it.h * p.os.head;
+      const Carries carries(it.g, kC, (unsigned)max(min(it.n, it.end) - it.first, 0));
       if (it.chunks > 0) {
         if (state_row) {
-          const Carry carry(it.g, (float)Chunk(it, p, 0).have);
+          const Carry carry = carries.after(Chunk(it, p, 0).have, kC);
           const float* X = p.states + (it.bh * p.runs + it.run) * p.m * p.dv + row * p.xj;
 #pragma unroll 1
           for (int q = 0; q < M / 64; ++q) {
@@ -726,7 +733,7 @@ __global__ void __launch_bounds__(kReadThreads, 1)
           __syncwarp();
         }
         if (more) {
-          const Carry carry(it.g, (float)Chunk(it, p, i + 1).have);
+          const Carry carry = carries.after(Chunk(it, p, i + 1).have, kC);
           wait_warp(ctl, L::kC_, carried);
           ++carried;
           tc_fence_after();

@@ -61,6 +61,15 @@ struct Carry {
   }
   __device__ __forceinline__ float of(float X) const { return fmaf(f, X, near ? X : 0.f); }
 };
+// Those of a row's steps of `step` tokens each: n of them whole, then one of what is left.
+struct Carries {
+  Carry whole, rest;
+  __device__ __forceinline__ Carries(float g, unsigned step, unsigned n)
+      : whole(g, (float)step), rest(g, (float)(n % step)) {}
+  __device__ __forceinline__ Carry after(int64_t tokens, int64_t step) const {
+    return tokens == step ? whole : rest;
+  }
+};
 
 // Tokens of run r of a row of n.
 __device__ __forceinline__ int64_t run_tokens(int64_t n, int64_t r, int64_t run_len) {
