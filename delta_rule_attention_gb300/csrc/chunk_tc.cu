@@ -900,9 +900,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const uint32_t ch1 = (uint32_t)(((2 * qc + 1) ^ (row & 7)) << 4);
   const unsigned char* ws = reinterpret_cast<const unsigned char*>(a.workspace) +
                             ((size_t)bh * nchunks + c_begin) * kMapBytes;  // this range's maps
-  // A following map launch may start now; it waits for this grid to complete
-  // before it touches memory.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) tmem_alloc(&s.tmem_base, 128);
   if (tid == 0) {
     for (int st = 0; st < kSt; ++st) {
@@ -926,6 +923,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // A following map launch may start now; it waits for this grid to complete
+  // before it touches memory.  Not sooner: its blocks hold tensor memory while they
+  // wait, which this block has to have first.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // The maps are written by the preceding launch: wait for it to complete.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = s.tmem_base;
@@ -1147,9 +1148,6 @@ __global__ void __launch_bounds__(kScan128Threads)
   const int row = 32 * (warp & 3) + lane;  // TMEM lane
   const unsigned char* ws = reinterpret_cast<const unsigned char*>(a.workspace) +
                             ((size_t)bh * nchunks + c_begin) * kMap;  // this range's maps
-  // A following map launch may start now; it waits for this grid to complete
-  // before it touches memory.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) tmem_alloc(&s.tmem_base, 256);
   if (tid == 0) {
     for (int st = 0; st < kStages128; ++st) {
@@ -1176,6 +1174,10 @@ __global__ void __launch_bounds__(kScan128Threads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // A following map launch may start now; it waits for this grid to complete
+  // before it touches memory.  Not sooner: its blocks hold tensor memory while they
+  // wait, which this block has to have first.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = s.tmem_base;
 

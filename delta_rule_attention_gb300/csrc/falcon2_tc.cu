@@ -277,10 +277,12 @@ __global__ void __launch_bounds__(kF2Threads, 1)
   // Launched behind the preceding kernel (programmatic dependent launch):
   // nothing is read or written before it has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Not before this block has its tensor memory: a block of the launch behind holds its
+  // own while it waits.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = sc.tmem_base;
   const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 

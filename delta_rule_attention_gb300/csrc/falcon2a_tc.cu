@@ -386,9 +386,6 @@ __global__ void __launch_bounds__(k2Threads, 1)
   const int row = 32 * (warp & 3) + lane, h = warp >> 2;
   const unsigned char* hmaps = reinterpret_cast<const unsigned char*>(a.workspace) +
                                (size_t)bh * nchunks * kMap2ABytes;
-  // A following map launch may start now; it waits for this grid to complete
-  // before it touches memory.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) tmem_alloc(&s.tmem_base, 64);
   if (tid == 0) {
     for (int st = 0; st < kS2Stages; ++st) mbar_init(&s.full[st], 1);
@@ -404,6 +401,10 @@ __global__ void __launch_bounds__(k2Threads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // A following map launch may start now; it waits for this grid to complete
+  // before it touches memory.  Not sooner: its blocks hold tensor memory while they
+  // wait, which this block has to have first.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the maps of the preceding launch
   const uint32_t tmem = s.tmem_base;
   if (issuer)
