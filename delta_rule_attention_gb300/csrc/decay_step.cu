@@ -43,7 +43,9 @@ __global__ void __launch_bounds__(kMostThreads)
     k[i] = load_vec<E, 1>(kp + i).v[0];
   }
   const float4 v = widen(load_quad<E>(vp, false, have < 4 ? have : 4));
-  const float g = decay_power(decay_rate(a.log_decay, h), 1.f);
+  // what a token loses is subtracted: gamma's own rounding would repeat itself token after
+  // token (off by 2^-25 a step, 1e-4 of a slow head's state after 4096)
+  const Carry carry(decay_rate(a.log_decay, h), 1.f);
   __syncthreads();
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -51,8 +53,8 @@ __global__ void __launch_bounds__(kMostThreads)
     const int i = grp + r * groups;
     if (i < a.m) {
       const float ki = k[i], qi = q[i];
-      s[r].x = fmaf(g, s[r].x, ki * v.x), s[r].y = fmaf(g, s[r].y, ki * v.y);
-      s[r].z = fmaf(g, s[r].z, ki * v.z), s[r].w = fmaf(g, s[r].w, ki * v.w);
+      s[r].x = fmaf(ki, v.x, carry.of(s[r].x)), s[r].y = fmaf(ki, v.y, carry.of(s[r].y));
+      s[r].z = fmaf(ki, v.z, carry.of(s[r].z)), s[r].w = fmaf(ki, v.w, carry.of(s[r].w));
       o.x = fmaf(qi, s[r].x, o.x), o.y = fmaf(qi, s[r].y, o.y);
       o.z = fmaf(qi, s[r].z, o.z), o.w = fmaf(qi, s[r].w, o.w);
       if (has) {

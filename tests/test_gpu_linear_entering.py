@@ -74,3 +74,36 @@ def test_terms_after_a_large_state(falcon, dtype):  # noqa: F811
     size, size_S = ref.decay_forward_size(q, k, v, g, S0)
     near(o, want, size, HALF[dtype], m + T + 256, "o")
     near(S, want_S, size_S, 0.0, T + 256, "S")
+
+
+def rounded_rates(n):
+    """n rates near -1e-4, -2e-4, ... whose gamma lies close to the middle between two floats."""
+    out = []
+    for i in range(n):
+        g = -1e-4 * (1 + i) - 1e-8 * torch.arange(400, dtype=torch.float32)
+        gamma = torch.exp(g.double())
+        off = (gamma.float().double() - gamma).abs()
+        out.append(g[off.argmax()])
+    return torch.stack(out).cuda()
+
+
+def test_states_that_lose_a_little_token_by_token(falcon):  # noqa: F811
+    """4096 tokens that add nothing.  A token rounds a state's value by at most half a step of
+    it, either way: the mean over 64 x 64 values stays within 2^-24 of a step, 64 / 64 of them
+    (4096 tokens, 4096 values) and five times that; what a token loses, 4e-4 at most, is off
+    by 2^-23 of itself: 2e-7.  gamma rounded would be off by up to 2^-25 a token: 1.2e-4."""
+    H, m, N = 4, 64, 4096
+    g = rounded_rates(H)
+    S0 = randn(gen(1), 1, H, m, m)
+    S = S0.clone()
+    zero = torch.zeros(1, H, m, device="cuda")
+    q = randn(gen(2), 1, H, m)
+    for _ in range(N):
+        falcon.falcon_decay_attn_step(q, zero, zero, g, S)
+    left = torch.exp(N * g.double())[:, None, None]
+    off = S[0].double() / (S0[0].double() * left) - 1
+    assert float(off.mean((1, 2)).abs().max()) <= 5 * 2.0 ** -24 + 2e-7 + 2.0 ** -24
+    assert float(off.abs().max()) <= N * 2.0 ** -24
+    # and one prompt of as many tokens leaves the same
+    _, P = falcon.falcon_decay_attn_fwd(*(torch.zeros(1, H, N, m, device="cuda"),) * 3, g, S0=S0)
+    assert float((P[0].double() / (S0[0].double() * left) - 1).abs().max()) <= 1e-5
