@@ -13,7 +13,7 @@
 //
 // Bound by the CUDA cores and the shared memory that feeds them: a thread's 4 x 4 corner
 // takes two 16-byte reads for 16 multiply-adds.  fp32, 96 heads of 64 channels and 2048
-// tokens: 319 us, 25 TFLOP/s of the 80 that the cores have (gradient 943 us); 32 heads of 128
+// tokens: 323 us, 25 TFLOP/s of the 80 that the cores have (gradient 945 us); 32 heads of 128
 // and 4096 tokens 607 us (1820).  64 keys a step, all loads of a chunk under way at once:
 // 319 for 336 us with 32 keys, 607 for 715.
 #include "linear.cuh"

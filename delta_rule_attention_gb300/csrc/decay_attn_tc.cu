@@ -26,11 +26,13 @@
 // second half of V^T as an A operand is the tile behind it in shared memory, which lands
 // in lanes 64..127 that nobody reads.
 //
-// Measured (96 heads of 64, 2048 tokens; 16 heads of 128, 65536 tokens): a call 50 us, of
-// which the states take 19 and the reads 29 (floor of the call's bytes: 15); 293 us, 99 and
+// Measured (96 heads of 64, 2048 tokens; 16 heads of 128, 65536 tokens): a call 51 us, of
+// which the states take 18 and the reads 28 (floor of the call's bytes: 15); 291 us, 99 and
 // 175 (158).  The states are bound by shared memory, through which three terms of every
-// key go to the tensor cores, the reads by the chain from one chunk's state to the next
-// (3300 cycles a chunk of 64 channels).  One block an SM whose warps have roles took the place
+// key go to the tensor cores.  The reads of 64 channels take 8 us for the launch's start and
+// end, 1.7 us (3500 cycles) a chunk, where memory needs 1.5, and 1.1 for a block's second
+// run: the chain from one chunk's state to the next is about as long as memory takes.
+// One block an SM whose warps have roles took the place
 // of two blocks an SM that went through the phases together: 68 us and 609.
 #include <cuda_bf16.h>
 

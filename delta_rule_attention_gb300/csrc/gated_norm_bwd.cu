@@ -3,10 +3,13 @@
 // the sums over rows of its channels for the parameters; a second kernel adds the blocks'
 // sums in a fixed order.
 //
-// Bound by instructions, about 45 a value: 16384 rows of 2048 channels (bf16, 403 MB) 110 us,
-// 3.7 TB/s, of which the blocks' sums take 6 (8 with a block for every 32 channels).  The
-// plan's limit of two vectors a thread: with four, 384 threads an SM hold the registers and
-// the same rows take 118 us; one instruction for two values (112 us before: 114).
+// Bound by latency: 16384 rows of 2048 channels (bf16, 403 MB) 110 us, 3.7 TB/s, of which the
+// blocks' sums take 6 (8 with a block for every 32 channels).  63 instructions a value go
+// through half of the issue slots (54%): 125 registers leave 15 warps an SM, and a warp issues
+// once in 6.9 cycles, waiting for fixed latencies (1.6) and shared memory (1.7) most.  12
+// heads of 64 with a gate (16384 rows): 61 us, 168 registers, 11 warps, 49%.  The plan's limit
+// of two vectors a thread: with four, 384 threads an SM hold the registers and the same rows
+// take 118 us; one instruction for two values (112 us before: 114).
 #include "gated_norm.cuh"
 
 namespace falcon {
