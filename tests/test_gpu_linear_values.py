@@ -44,14 +44,16 @@ def test_one_bad_token_stays_in_its_head(falcon, T, bad, name, dtype):  # noqa: 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("H,m", [(1, 64), (3, 64), (2, 111), (1, 4096)])
-def test_rows_whose_squares_leave_float32(falcon, H, m, dtype):  # noqa: F811
-    """Counted as infinitely large: what is normalised is zero, and nothing is NaN."""
+@pytest.mark.parametrize("large", [3e19, 3e38])
+def test_rows_whose_squares_leave_float32(falcon, large, H, m, dtype):  # noqa: F811
+    """Counted as infinitely large: what is normalised is zero, and nothing is NaN, not where
+    the gradient's own sums leave float32 too."""
     B, T = 2, 5
     D = H * m
     h = randn(gen(1), B, H, T, m, dtype=dtype)
-    h[1, H - 1, 3] = torch.tensor([3e19, -1e25], device="cuda").to(dtype).repeat(m)[:m]
+    h[1, H - 1, 3] = torch.tensor([large, -1e25], device="cuda").to(dtype).repeat(m)[:m]
     x, z, d, e = (randn(gen(i), B, T, D, dtype=dtype) for i in range(2, 6))
-    x[0, 2] = 2e30
+    x[0, 2] = large
     w = randn(gen(7), D)
     out, nxt = falcon.falcon_gated_norm_fwd(h, weight=w, z=z, scale=w, x=x, next_weight=w)
     assert torch.isfinite(out).all() and torch.isfinite(nxt).all()
