@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(V == 1 ? (K > 1 ? 512 : 256) : K == 3 || K == 
       const Sums<2> s = row_sum<2>({yy.sum(), ey.sum()}, blockDim.x, red, turn);
       const float rn = rsqrtf(s.v[0] / (float)a.D + a.eps);
       // zero where rn is, whatever the other sum has come to
-      const float back = rn > 0.f ? -rn * rn * s.v[1] / (float)a.D : 0.f;
+      const float back = rn > 0.f ? -rn * (rn * s.v[1] / (float)a.D) : 0.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const FloatV<V> y = in_y(k), er = times<V>(in_e(k), rn);
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(V == 1 ? (K > 1 ? 512 : 256) : K == 3 || K == 
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const float rn = rsqrtf(s[k].v[0] / (float)a.m + a.eps);
-        const float back = rn > 0.f ? -rn * rn * s[k].v[1] / (float)a.m : 0.f;
+        const float back = rn > 0.f ? -rn * (rn * s[k].v[1] / (float)a.m) : 0.f;
         const FloatV<V> h = in_h(k), n = times<V>(h, rn);
         FloatV<V> f = mul_of<V>(d[k], ws(k));
         if (a.z) {

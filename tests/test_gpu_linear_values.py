@@ -64,3 +64,25 @@ def test_rows_whose_squares_leave_float32(falcon, large, H, m, dtype):  # noqa: 
     assert all(torch.isfinite(t).all() for t in g.values())
     assert (g["dh"][1, H - 1, 3] == 0).all() and (g["dz"][1, 3, D - m:] == 0).all()
     assert torch.equal(g["dx"][0, 2], d[0, 2])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_of_zeros_beside_the_smallest_stabiliser(falcon, dtype):  # noqa: F811
+    """1 / eps leaves float32, 1 / sqrt(eps) does not: rows of zeros stay zeros, and so do
+    their gradients' second parts."""
+    B, T, D, eps = 1, 6, 64, 1e-40
+    h = torch.zeros(B, T, D, dtype=dtype, device="cuda")
+    h[0, 3:] = randn(gen(1), 3, D, dtype=dtype)
+    d, w = randn(gen(2), B, T, D, dtype=dtype) * 1e-3, randn(gen(3), D)
+    out, nxt = falcon.falcon_gated_norm_fwd(h, weight=w, next_weight=w, eps=eps)
+    assert (out[0, :3] == 0).all() and (nxt[0, :3] == 0).all()
+    g = falcon.falcon_gated_norm_bwd(h, d, dnext=d, out=out, weight=w, next_weight=w, eps=eps,
+                                     residual=False)
+    r = torch.rsqrt(torch.tensor(eps, dtype=torch.float32).double()).cuda()
+    # dnext comes back through both norms of a row of zeros: d w r, then w r again
+    want = (d[0, :3].double() + d[0, :3].double() * w * r) * w * r
+    within = want.abs() < 3e38
+    off = (g["dh"][0, :3].double() - want).abs()
+    assert (off[within] <= (2.0 ** -8 if dtype is BF16 else 2.0 ** -20) * 1.02 * want.abs()[within]).all()
+    assert all(torch.isfinite(g["dh"][0, 3:]).flatten()) and torch.isfinite(g["dweight"]).all()
+    assert torch.isfinite(g["dnext_weight"]).all()
